@@ -129,6 +129,85 @@ PA_API pa_status pa_reshape_and_cache(const void* k, const void* v, void* k_cach
                                pa_stream_t stream);
 
 /*
+ * Rotary positions (no counterpart on the pages, which take q and k as already
+ * positioned): a head's first rot_dim components are turned in pairs by angles that
+ * grow with the token's position p,
+ *   u = a cos(p f_i) - b sin(p f_i),  v = b cos(p f_i) + a sin(p f_i),
+ * with the pairs (i, i + rot_dim / 2) or (2i, 2i + 1), i < rot_dim / 2.
+ *
+ * pa_rope_frequencies: the f_i, on the host (no GPU work).
+ *   PA_ROPE_UNSCALED  f_i = base^(-2 i / rot_dim)
+ *   PA_ROPE_LINEAR    f_i / factor: positions interpolated into the trained range
+ *   PA_ROPE_BY_PARTS  f_i blended with f_i / factor by the turns t = trained f_i / 2 pi
+ *                     it makes over the trained length: kept for t >= high_turns, divided
+ *                     for t <= low_turns, keep = (t - low_turns) / (high_turns - low_turns)
+ *                     between (YaRN's frequencies, "YaRN: Efficient Context Window
+ *                     Extension of Large Language Models", s.3.2)
+ *   freqs             host, [rot_dim / 2]
+ *   rot_dim           a multiple of 16, 16 .. 128
+ *   base, factor      > 0 and finite; factor is read by the scaled forms
+ *   trained, low_turns, high_turns
+ *                     read by PA_ROPE_BY_PARTS: trained > 0, high_turns > low_turns >= 0
+ */
+typedef enum { PA_ROPE_UNSCALED = 0, PA_ROPE_LINEAR = 1, PA_ROPE_BY_PARTS = 2 } pa_rope_scaling;
+
+PA_API pa_status pa_rope_frequencies(double* freqs, int rot_dim, double base, pa_rope_scaling scaling, double factor,
+                                     double trained, double low_turns, double high_turns);
+
+/*
+ * The table of a set of frequencies: for p < max_positions and i < rot_dim / 2
+ *   cos_sin[p][i] = attention cos(p f_i),  cos_sin[p][rot_dim / 2 + i] = attention sin(p f_i)
+ * to about one unit in the last place of float32 at every position (angles are held
+ * modulo one turn in 64-bit fixed point).  Built once; any table of this layout serves
+ * pa_rope_and_cache.
+ *   cos_sin    device, float32 [max_positions][rot_dim], 16-byte aligned
+ *   freqs      host, [rot_dim / 2], finite (read during the call)
+ *   attention  factor on both (YaRN's scaling of the logits; 1 for none)
+ * max_positions == 0 does nothing.
+ */
+PA_API pa_status pa_rope_table(float* cos_sin, int max_positions, int rot_dim, const double* freqs, float attention,
+                               pa_stream_t stream);
+
+/*
+ * Rotation of a step's queries and keys with the slot write in one pass: q_out[t] =
+ * q[t] turned by positions[t], and k[t] turned likewise and v[t] as it is stored at
+ * slot_mapping[t] as pa_reshape_and_cache stores them.  Positions and slots are
+ * separate: after pa_evict a token's place in the cache is no longer its position.
+ *
+ * Each product and sum of the rotation is rounded to float32, its result once to the
+ * type stored (for an FP8 cache: divided by the scale in float32, then rounded; a NaN
+ * there becomes 0.1111.111).  Components from rot_dim on are copied.
+ *
+ *   q_out          device, [num_tokens][num_q_heads][128] of src_dtype; may be q itself
+ *                  (same pointer and stride), otherwise must not overlap the inputs
+ *   q, k, v        device, [num_tokens][heads][128] of src_dtype
+ *   *_stride       elements from one token to the next (a multiple of 8; the heads of a
+ *                  token are contiguous), so that q, k and v can be parts of one
+ *                  [num_tokens][num_q_heads + 2 num_kv_heads][128] projection; an output
+ *                  stride is at least num_q_heads * 128
+ *   positions      device, int64 [num_tokens]; a negative position is padding (nothing of
+ *                  the token is written); a position >= max_positions is recorded as
+ *                  PA_ERR_OUT_OF_RANGE and nothing of the token is written
+ *   slot_mapping   device, int64 [num_tokens]; a negative slot writes no K or V (q is
+ *                  turned all the same); a slot beyond the pool is recorded as
+ *                  PA_ERR_OUT_OF_RANGE and not written
+ *   cos_sin        device, float32 [max_positions][rot_dim], 16-byte aligned (pa_rope_table)
+ *   rot_dim        a multiple of 16, 16 .. 128 (others: PA_ERR_UNSUPPORTED)
+ *   workspace      NULL (nothing is recorded), or a workspace whose status word records errors
+ * Other arguments as pa_reshape_and_cache.
+ */
+typedef enum { PA_ROPE_HALF = 0, PA_ROPE_INTERLEAVED = 1 } pa_rope_layout;
+
+PA_API pa_status pa_rope_and_cache(void* q_out, long long q_out_stride, const void* q, long long q_stride,
+                                   const void* k, long long k_stride, const void* v, long long v_stride,
+                                   void* k_cache, void* v_cache, const int64_t* slot_mapping,
+                                   const int64_t* positions, const float* cos_sin, int max_positions, int rot_dim,
+                                   pa_rope_layout layout, int num_tokens, int num_q_heads, int num_kv_heads,
+                                   int head_dim, int block_size, int num_blocks, pa_dtype src_dtype,
+                                   pa_dtype cache_dtype, const float* k_scale, const float* v_scale, void* workspace,
+                                   pa_stream_t stream);
+
+/*
  * Bytes of workspace pa_decode / pa_mixed need on the CURRENT device for
  * num_seqs sequences (the default worker count depends on the device's SM
  * count).  The workspace is caller-owned device memory, 256-byte aligned.  Its

@@ -18,6 +18,7 @@ from . import build_ext
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_CUDA, PA_ERR_TIMEOUT, PA_ERR_OUT_OF_RANGE, \
     PA_ERR_WORKSPACE = range(7)
 PA_BF16, PA_FP16, PA_FP8_E4M3, PA_FP8_E4M3_PER_HEAD = 0, 1, 2, 3
+PA_ROPE_UNSCALED, PA_ROPE_LINEAR, PA_ROPE_BY_PARTS = 0, 1, 2
 
 _DTYPE = {torch.bfloat16: PA_BF16, torch.float16: PA_FP16, torch.uint8: PA_FP8_E4M3,
           torch.float8_e4m3fn: PA_FP8_E4M3}
@@ -59,6 +60,14 @@ def _lib():
     lib.pa_last_error.restype = ctypes.c_char_p
     lib.pa_reshape_and_cache.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, P, P, P]
     lib.pa_reshape_and_cache.restype = I
+    LL, DB = ctypes.c_longlong, ctypes.c_double
+    lib.pa_rope_frequencies.argtypes = [P, I, DB, I, DB, DB, DB, DB]
+    lib.pa_rope_frequencies.restype = I
+    lib.pa_rope_table.argtypes = [P, I, I, P, F, P]
+    lib.pa_rope_table.restype = I
+    lib.pa_rope_and_cache.argtypes = [P, LL, P, LL, P, LL, P, LL, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, I, P, P,
+                                      P, P]
+    lib.pa_rope_and_cache.restype = I
     lib.pa_workspace_size.argtypes = [I, I, I, I]
     lib.pa_workspace_size.restype = Z
     lib.pa_workspace_size_shared_prefix.argtypes = [I, I, I, I]
@@ -124,6 +133,53 @@ def _need(t: torch.Tensor, name: str, dtypes=None):
         raise ValueError(f"{name} must be contiguous")
     if dtypes is not None and t.dtype not in dtypes:
         raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
+
+
+def _need_rows(t: torch.Tensor, name: str, dtypes):
+    """[tokens, heads, 128] on a GPU with each token's heads contiguous (any stride between tokens)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    if t.numel() and not t[0].is_contiguous():
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+
+
+def _token_stride(t: torch.Tensor) -> int:
+    """Elements between two tokens (of a single one: its own size, its stride means nothing)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _need_scales(code: int, k_scale, v_scale, num_kv_heads: int) -> None:
+    """FP8 scales: float32, one per tensor or one per KV head, K and V alike."""
+    if code not in (PA_FP8_E4M3, PA_FP8_E4M3_PER_HEAD):
+        return
+    want = num_kv_heads if code == PA_FP8_E4M3_PER_HEAD else 1
+    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        _need(t, n, (torch.float32,))
+        if t.numel() != want:
+            raise ValueError(f"{n}: {t.numel()} scales where {want} are expected")
+
+
+def _need_workspace(workspace) -> None:
+    if workspace is not None:
+        _need(workspace, "workspace", (torch.uint8,))
+        if workspace.numel() < 256:
+            raise ValueError("workspace: at least 256 bytes")
+
+
+def _same_device(first: torch.Tensor, **others) -> None:
+    for n, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{n} is on {t.device}, not on {first.device}")
+
+
+def _on(t: torch.Tensor):
+    """The tensor's device as the current one: the library works on the current device, and the
+    default stream is the current stream of that device."""
+    return torch.cuda.device(t.device)
 
 
 def _cache_code(cache, k_scale, num_kv_heads: int) -> int:
@@ -193,6 +249,65 @@ def pa_reshape_and_cache(k, v, k_cache, v_cache, slot_mapping, k_scale=None, v_s
                                      bs, nb, _DTYPE[k.dtype], _cache_code(k_cache, k_scale, k_cache.shape[1]), _ptr(k_scale),
                                      _ptr(v_scale), _stream(stream))
     _check(st, "pa_reshape_and_cache")
+
+
+def pa_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = PA_ROPE_UNSCALED, factor: float = 1.0,
+                        trained: float = 0.0, low_turns: float = 1.0, high_turns: float = 32.0):
+    """Rotary frequencies, float64 numpy [rot_dim / 2]; scaling PA_ROPE_LINEAR or PA_ROPE_BY_PARTS
+    (trained: the length the model was trained for) stretches them by factor."""
+    import numpy as np
+    f = np.zeros(max(int(rot_dim) // 2, 1), dtype=np.float64)
+    _check(_lib().pa_rope_frequencies(f.ctypes.data, int(rot_dim), float(base), int(scaling), float(factor),
+                                      float(trained), float(low_turns), float(high_turns)), "pa_rope_frequencies")
+    return f
+
+
+def pa_rope_table(cos_sin, freqs, attention: float = 1.0, stream=None):
+    """Table of a set of frequencies (host float64 [rot / 2]): cos_sin float32 [max_positions, rot],
+    cosines then sines of position x frequency, both times attention."""
+    import numpy as np
+    _need(cos_sin, "cos_sin", (torch.float32,))
+    f = np.ascontiguousarray(np.asarray(freqs, dtype=np.float64))
+    if cos_sin.dim() != 2 or f.ndim != 1 or cos_sin.shape[1] != 2 * f.size:
+        raise ValueError("cos_sin must be [max_positions, 2 * len(freqs)]")
+    with _on(cos_sin):
+        st = _lib().pa_rope_table(_ptr(cos_sin), cos_sin.shape[0], cos_sin.shape[1], f.ctypes.data, float(attention),
+                                  _stream(stream))
+    _check(st, "pa_rope_table")
+
+
+def pa_rope_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, interleaved: bool = False,
+                      k_scale=None, v_scale=None, workspace=None, stream=None):
+    """Slot write with rotary positions: q_out [T, H_q, 128] = q turned by positions[T] (int64), k [T, H_kv, 128]
+    turned and v stored at slot_mapping[T] (int64).  q, k and v may be views of one projection (the heads of a
+    token contiguous, any stride between tokens); cos_sin float32 [max_positions, rot] as pa_rope_table builds it."""
+    for t, n in ((q, "q"), (k, "k"), (v, "v"), (q_out, "q_out")):
+        _need_rows(t, n, (torch.bfloat16, torch.float16))
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _need(t, n, tuple(_DTYPE))
+    _need(slot_mapping, "slot_mapping", (torch.int64,))
+    _need(positions, "positions", (torch.int64,))
+    _need(cos_sin, "cos_sin", (torch.float32,))
+    T, Hq, d = q.shape
+    H = k.shape[1]
+    nb, H2, bs, d2 = k_cache.shape
+    if (q_out.shape != q.shape or k.shape != (T, H, d) or v.shape != k.shape or v_cache.shape != k_cache.shape or
+            H2 != H or d2 != d or slot_mapping.shape != (T,) or positions.shape != (T,) or cos_sin.dim() != 2):
+        raise ValueError("shape mismatch")
+    if not (q.dtype == k.dtype == v.dtype == q_out.dtype) or v_cache.dtype != k_cache.dtype:
+        raise TypeError("q, k, v and q_out must have one type, and the caches one")
+    code = _cache_code(k_cache, k_scale, H)
+    _need_scales(code, k_scale, v_scale, H)
+    _need_workspace(workspace)
+    _same_device(q, q_out=q_out, k=k, v=v, k_cache=k_cache, v_cache=v_cache, slot_mapping=slot_mapping,
+                 positions=positions, cos_sin=cos_sin, k_scale=k_scale, v_scale=v_scale, workspace=workspace)
+    with _on(q):
+        st = _lib().pa_rope_and_cache(_ptr(q_out), _token_stride(q_out), _ptr(q), _token_stride(q), _ptr(k),
+                                      _token_stride(k), _ptr(v), _token_stride(v), _ptr(k_cache), _ptr(v_cache),
+                                      _ptr(slot_mapping), _ptr(positions), _ptr(cos_sin), cos_sin.shape[0],
+                                      cos_sin.shape[1], int(bool(interleaved)), T, Hq, H, d, bs, nb, _DTYPE[q.dtype],
+                                      code, _ptr(k_scale), _ptr(v_scale), _ptr(workspace), _stream(stream))
+    _check(st, "pa_rope_and_cache")
 
 
 def pa_decode(out, q, k_cache, v_cache, block_tables, seq_lens, scale, workspace, k_scale=None, v_scale=None,

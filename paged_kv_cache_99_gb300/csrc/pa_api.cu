@@ -475,6 +475,98 @@ pa_status pa_reshape_and_cache(const void* k, const void* v, void* k_cache, void
                        "launch(reshape_and_cache)");
 }
 
+pa_status pa_rope_frequencies(double* freqs, int rot_dim, double base, pa_rope_scaling scaling, double factor,
+                              double trained, double low_turns, double high_turns) {
+    if (rot_dim < 16 || rot_dim > kHeadDim || rot_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
+    if (scaling != PA_ROPE_UNSCALED && scaling != PA_ROPE_LINEAR && scaling != PA_ROPE_BY_PARTS)
+        return PA_ERR_UNSUPPORTED;
+    if (!freqs || !std::isfinite(base) || !(base > 0.0)) return PA_ERR_INVALID_ARG;
+    if (scaling != PA_ROPE_UNSCALED && (!std::isfinite(factor) || !(factor > 0.0))) return PA_ERR_INVALID_ARG;
+    if (scaling == PA_ROPE_BY_PARTS &&
+        (!std::isfinite(trained) || !(trained > 0.0) || !(low_turns >= 0.0) || !(high_turns > low_turns) ||
+         !std::isfinite(high_turns)))
+        return PA_ERR_INVALID_ARG;
+    rope_frequencies(freqs, rot_dim, base, scaling, factor, trained, low_turns, high_turns);
+    return PA_OK;
+}
+
+pa_status pa_rope_table(float* cos_sin, int max_positions, int rot_dim, const double* freqs, float attention,
+                        pa_stream_t stream) {
+    if (rot_dim < 16 || rot_dim > kHeadDim || rot_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
+    if (max_positions < 0 || !freqs || !std::isfinite(attention)) return PA_ERR_INVALID_ARG;
+    for (int i = 0; i < rot_dim / 2; ++i)
+        if (!std::isfinite(freqs[i])) return PA_ERR_INVALID_ARG;
+    if (max_positions == 0) return PA_OK;
+    if (!cos_sin || !aligned(cos_sin, 16)) return PA_ERR_INVALID_ARG;
+    DeviceState* st = device_state(nullptr);
+    if (!st) return PA_ERR_CUDA;
+    return launched(launch_rope_table(cos_sin, max_positions, rot_dim, freqs, attention, st->sms,
+                                      reinterpret_cast<cudaStream_t>(stream)),
+                    "launch(rope_table)");
+}
+
+pa_status pa_rope_and_cache(void* q_out, long long q_out_stride, const void* q, long long q_stride, const void* k,
+                            long long k_stride, const void* v, long long v_stride, void* k_cache, void* v_cache,
+                            const int64_t* slot_mapping, const int64_t* positions, const float* cos_sin,
+                            int max_positions, int rot_dim, pa_rope_layout layout, int num_tokens, int num_q_heads,
+                            int num_kv_heads, int head_dim, int block_size, int num_blocks, pa_dtype src_dtype,
+                            pa_dtype cache_dtype, const float* k_scale, const float* v_scale, void* workspace,
+                            pa_stream_t stream) {
+    if (head_dim != kHeadDim || !block_size_ok(block_size)) return PA_ERR_UNSUPPORTED;
+    if (src_dtype != PA_BF16 && src_dtype != PA_FP16) return PA_ERR_UNSUPPORTED;
+    if (cache_dtype != src_dtype && !is_fp8(cache_dtype)) return PA_ERR_UNSUPPORTED;
+    if (rot_dim < 16 || rot_dim > kHeadDim || rot_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
+    if (layout != PA_ROPE_HALF && layout != PA_ROPE_INTERLEAVED) return PA_ERR_UNSUPPORTED;
+    if (num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_blocks <= 0 || max_positions <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (num_tokens == 0) return PA_OK;
+    if (!q_out || !q || !k || !v || !k_cache || !v_cache || !slot_mapping || !positions || !cos_sin)
+        return PA_ERR_INVALID_ARG;
+    if (is_fp8(cache_dtype) && (!k_scale || !v_scale)) return PA_ERR_INVALID_ARG;
+    if (!aligned(q_out, 16) || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) ||
+        !aligned(v_cache, 16) || !aligned(cos_sin, 16) || !aligned(slot_mapping, 8) || !aligned(positions, 8) ||
+        (workspace && !aligned(workspace, 256)))
+        return PA_ERR_INVALID_ARG;
+    if (q_out_stride % 8 || q_stride % 8 || k_stride % 8 || v_stride % 8 || q_stride < 0 || k_stride < 0 || v_stride < 0 ||
+        (num_tokens > 1 && q_out_stride < static_cast<long long>(num_q_heads) * kHeadDim) ||
+        (q_out == q && num_tokens > 1 && q_out_stride != q_stride))
+        return PA_ERR_INVALID_ARG;
+    // thread groups are numbered in 32 bits
+    if (static_cast<long long>(num_tokens) * (static_cast<long long>(num_q_heads) + 2ll * num_kv_heads) >= (1ll << 31))
+        return PA_ERR_UNSUPPORTED;
+    DeviceState* st = device_state(nullptr);
+    if (!st) return PA_ERR_CUDA;
+    RopeParams p;
+    p.q_out = static_cast<uint16_t*>(q_out);
+    p.q = static_cast<const uint16_t*>(q);
+    p.k = static_cast<const uint16_t*>(k);
+    p.v = static_cast<const uint16_t*>(v);
+    p.q_out_stride = q_out_stride;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.slots = slot_mapping;
+    p.positions = positions;
+    p.cos_sin = cos_sin;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.scale_stride = scale_stride_of(cache_dtype);
+    p.status = static_cast<int*>(workspace);
+    p.max_positions = max_positions;
+    p.rot_dim = rot_dim;
+    p.num_tokens = num_tokens;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.num_blocks = num_blocks;
+    p.block_shift = block_shift_of(block_size);
+    p.groups = 0;
+    return launched(launch_rope_cache(p, src_dtype == PA_BF16, is_fp8(cache_dtype), layout == PA_ROPE_INTERLEAVED,
+                                      st->sms, reinterpret_cast<cudaStream_t>(stream)),
+                    "launch(rope_and_cache)");
+}
+
 size_t pa_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim) {
     if (num_seqs < 0 || num_seqs > kMaxSeqs || head_dim != kHeadDim || num_kv_heads <= 0 || num_q_heads <= 0 ||
         num_q_heads % num_kv_heads != 0)

@@ -188,6 +188,41 @@ cudaError_t launch_reshape(const void* k, const void* v, void* k_cache, void* v_
                            int block_shift, bool src_bf16, bool cache_fp8, const float* k_scale,
                            const float* v_scale, int scale_stride, cudaStream_t stream);
 
+// Rotary positions: frequency scalings (as pa_rope_scaling), the table, and the
+// rotation fused with the slot write.
+enum RopeScaling { kRopeUnscaled = 0, kRopeLinear = 1, kRopeByParts = 2 };
+
+struct RopeParams {
+    uint16_t* q_out;
+    const uint16_t* q;
+    const uint16_t* k;
+    const uint16_t* v;
+    long long q_out_stride, q_stride, k_stride, v_stride;   // elements from one token to the next
+    void* k_cache;
+    void* v_cache;
+    const int64_t* slots;
+    const int64_t* positions;
+    const float* cos_sin;             // [max_positions][rot_dim]: cosines, then sines
+    const float* k_scale;
+    const float* v_scale;
+    int scale_stride;                 // FP8 scales: 0 one per tensor, 1 one per KV head
+    int* status;                      // device status word, or null
+    int max_positions;
+    int rot_dim;                      // a multiple of 16, 16 .. 128
+    int num_tokens;
+    int num_q_heads;
+    int num_kv_heads;
+    int num_blocks;
+    int block_shift;
+    int groups;                       // thread groups per token (set by the launch)
+};
+
+void rope_frequencies(double* freqs, int rot_dim, double base, int scaling, double factor, double trained,
+                      double low_turns, double high_turns);
+cudaError_t launch_rope_table(float* cos_sin, int max_positions, int rot_dim, const double* freqs, float attention,
+                              int sms, cudaStream_t stream);
+cudaError_t launch_rope_cache(RopeParams p, bool src_bf16, bool fp8, bool interleaved, int sms, cudaStream_t stream);
+
 // Prefill chunks.
 size_t chunk_smem_bytes(CacheKind kind, int num_seqs);
 int chunk_rows();           // MMA rows of one query tile
