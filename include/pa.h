@@ -455,6 +455,51 @@ PA_API pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int32_t* src
                                 pa_dtype cache_dtype, void* workspace, pa_stream_t stream);
 
 /*
+ * Eviction: brings every sequence to at most `budget` cached tokens, keeping for each KV
+ * head the tokens that were attended to most (no counterpart on the pages, whose cache
+ * only grows until a request is preempted [P1 s.6]; P1 s.2's sizing is what it bounds).
+ *
+ * For sequence s with n = seq_lens[s] tokens and KV head h:
+ *   n <= budget: every token stays;
+ *   n >  budget: tokens t < sinks and t >= n - recent stay, and of the others the
+ *     budget - sinks - recent with the largest weights[s][h][t]; of equal weights the lower t;
+ *     -0 counts as 0, a NaN as less than everything.
+ * Each head keeps tokens of its own, all the same number left = min(n, budget) of them, in
+ * their order.  The j-th kept token of head h moves to place j of the new table: its K and
+ * V rows are copied to block new_tables[s][j / block_size], offset j % block_size, and
+ *   kept[s][h][j] = its place t before (j < left), -1 (left <= j < budget)
+ *   weights_out[s][h][j] = weights[s][h][t] (j < left), 0 (left <= j < n), else as it was
+ *   seq_lens_out[s] = left.
+ * The source blocks are only read (they may be shared with other sequences); the caller
+ * frees the old table afterwards.  The copied keys keep the rotation of the positions they
+ * were written with; the next token's position goes on counting all tokens ever written.
+ *
+ *   weights        device, float32 [num_seqs][num_kv_heads][weight_stride] (pa_decode_weights
+ *                  adds to it), 16-byte aligned; weight_stride a multiple of 4 and at least
+ *                  max_blocks_per_seq * block_size
+ *   weights_out    the same layout; may be weights itself (up to 393216 tokens of table:
+ *                  beyond that PA_ERR_UNSUPPORTED), otherwise must not overlap it
+ *   kept           device, int32 [num_seqs][num_kv_heads][budget]
+ *   seq_lens_out   device, int32 [num_seqs]; not seq_lens itself
+ *   new_tables     device, int32 [num_seqs][max_new_blocks_per_seq] with
+ *                  max_new_blocks_per_seq * block_size >= min(budget, max_blocks_per_seq *
+ *                  block_size); entries past ceil(left / block_size) are never read.  Its
+ *                  blocks must be distinct and none may be read by the call (the result is
+ *                  otherwise unspecified).
+ *   budget         >= 1; sinks, recent >= 0 and sinks + recent <= budget
+ *   workspace      NULL, or a workspace whose status word records PA_ERR_OUT_OF_RANGE: a
+ *                  length beyond the table (cut to it), a source block outside the pool (block 0
+ *                  is read instead), a new block outside it (its rows are not copied)
+ * Cache layout and types as pa_decode (the FP8 scales do not change).
+ */
+PA_API pa_status pa_evict(int32_t* kept, int32_t* seq_lens_out, float* weights_out, const float* weights,
+                          long long weight_stride, void* k_cache, void* v_cache, const int32_t* block_tables,
+                          int max_blocks_per_seq, const int32_t* seq_lens, const int32_t* new_tables,
+                          int max_new_blocks_per_seq, int num_seqs, int budget, int sinks, int recent,
+                          int num_kv_heads, int head_dim, int block_size, int num_blocks, pa_dtype cache_dtype,
+                          void* workspace, pa_stream_t stream);
+
+/*
  * Block pool (host memory, no GPU work) [P1 s.4 "PagedAttention and Block
  * Management", s.5 "Prefix Caching"; P3 "The block pool", "Prefix caching is the
  * second win"].

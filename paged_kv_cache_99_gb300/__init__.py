@@ -68,6 +68,8 @@ def _lib():
     lib.pa_rope_and_cache.argtypes = [P, LL, P, LL, P, LL, P, LL, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, I, P, P,
                                       P, P]
     lib.pa_rope_and_cache.restype = I
+    lib.pa_evict.argtypes = [P, P, P, P, LL, P, P, P, I, P, P, I, I, I, I, I, I, I, I, I, I, P, P]
+    lib.pa_evict.restype = I
     lib.pa_workspace_size.argtypes = [I, I, I, I]
     lib.pa_workspace_size.restype = Z
     lib.pa_workspace_size_shared_prefix.argtypes = [I, I, I, I]
@@ -453,6 +455,39 @@ def pa_copy_blocks(k_cache, v_cache, src, dst, workspace=None, stream=None):
     st = _lib().pa_copy_blocks(_ptr(k_cache), _ptr(v_cache), _ptr(src), _ptr(dst), int(src.numel()), Hkv, d, bs,
                                nb, _DTYPE[k_cache.dtype], _ptr(workspace), _stream(stream))
     _check(st, "pa_copy_blocks")
+
+
+def pa_evict(kept, seq_lens_out, weights_out, weights, k_cache, v_cache, block_tables, seq_lens, new_tables,
+             budget: int, sinks: int = 0, recent: int = 0, workspace=None, stream=None):
+    """Brings every sequence to at most budget tokens: the first sinks and last recent tokens stay, and for
+    each KV head those of the largest weights ([B, H_kv, >= tokens of the table] float32) between them; their
+    K and V rows move to the blocks of new_tables, their places before go to kept [B, H_kv, budget] (int32)."""
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _need(t, n, tuple(_DTYPE))
+    for t, n in ((weights, "weights"), (weights_out, "weights_out")):
+        _need(t, n, (torch.float32,))
+    for t, n in ((kept, "kept"), (seq_lens_out, "seq_lens_out"), (block_tables, "block_tables"), (seq_lens, "seq_lens"),
+                 (new_tables, "new_tables")):
+        _need(t, n, (torch.int32,))
+    nb, H, bs, d = k_cache.shape
+    B = seq_lens.shape[0]
+    if (v_cache.shape != k_cache.shape or weights.dim() != 3 or weights.shape[:2] != (B, H) or
+            weights_out.shape != weights.shape or kept.shape != (B, H, budget) or seq_lens.shape != (B,) or
+            seq_lens_out.shape != (B,) or block_tables.dim() != 2 or block_tables.shape[0] != B or
+            new_tables.dim() != 2 or new_tables.shape[0] != B):
+        raise ValueError("shape mismatch")
+    if v_cache.dtype != k_cache.dtype:
+        raise TypeError("the caches must have one type")
+    _need_workspace(workspace)
+    _same_device(k_cache, v_cache=v_cache, weights=weights, weights_out=weights_out, kept=kept,
+                 seq_lens_out=seq_lens_out, block_tables=block_tables, seq_lens=seq_lens, new_tables=new_tables,
+                 workspace=workspace)
+    with _on(k_cache):
+        st = _lib().pa_evict(_ptr(kept), _ptr(seq_lens_out), _ptr(weights_out), _ptr(weights), weights.shape[2],
+                             _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens),
+                             _ptr(new_tables), new_tables.shape[1], B, int(budget), int(sinks), int(recent), H, d, bs,
+                             nb, _DTYPE[k_cache.dtype], _ptr(workspace), _stream(stream))
+    _check(st, "pa_evict")
 
 
 class BlockPool:

@@ -12,7 +12,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 SOURCES = ["pa_api.cu", "decode.cu", "chunk_tc.cu", "reshape_and_cache.cu", "selftest.cu", "copy_blocks.cu",
-           "rope.cu", "pool.cpp"]
+           "rope.cu", "evict.cu", "pool.cpp"]
 HEADERS = ["pa_device.cuh", "pa_internal.h"]
 BUILD_DIR = os.path.join(HERE, "_build", platform.machine())
 LIB_PATH = os.path.join(BUILD_DIR, "libpa.so")

@@ -26,6 +26,7 @@ struct DeviceState {
     size_t max_smem_optin = 0;
     bool decode_prepared[3][2][2][2][2] = {};
     bool chunk_prepared[3][2] = {};
+    bool evict_prepared = false;
 };
 
 std::mutex g_mu;
@@ -811,6 +812,74 @@ pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int32_t* src, const
     return launched(launch_copy_blocks(k_cache, v_cache, src, dst, num_pairs, num_blocks, block_bytes,
                                           static_cast<int*>(workspace), reinterpret_cast<cudaStream_t>(stream)),
                        "launch(copy_blocks)");
+}
+
+pa_status pa_evict(int32_t* kept, int32_t* seq_lens_out, float* weights_out, const float* weights,
+                   long long weight_stride, void* k_cache, void* v_cache, const int32_t* block_tables,
+                   int max_blocks_per_seq, const int32_t* seq_lens, const int32_t* new_tables,
+                   int max_new_blocks_per_seq, int num_seqs, int budget, int sinks, int recent, int num_kv_heads,
+                   int head_dim, int block_size, int num_blocks, pa_dtype cache_dtype, void* workspace,
+                   pa_stream_t stream) {
+    if (head_dim != kHeadDim || !block_size_ok(block_size)) return PA_ERR_UNSUPPORTED;
+    if (cache_dtype != PA_BF16 && cache_dtype != PA_FP16 && !is_fp8(cache_dtype)) return PA_ERR_UNSUPPORTED;
+    if (num_seqs < 0 || num_kv_heads <= 0 || num_blocks <= 0 || max_blocks_per_seq <= 0 || max_new_blocks_per_seq <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (budget < 1 || sinks < 0 || recent < 0 || static_cast<long long>(sinks) + recent > budget)
+        return PA_ERR_INVALID_ARG;
+    const long long cap = static_cast<long long>(max_blocks_per_seq) * block_size;
+    const int max_left = static_cast<int>(cap < budget ? cap : budget);
+    if (static_cast<long long>(max_new_blocks_per_seq) * block_size < max_left) return PA_ERR_INVALID_ARG;
+    if (weight_stride < cap || weight_stride % 4) return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0) return PA_OK;
+    if (!kept || !seq_lens_out || !weights_out || !weights || !k_cache || !v_cache || !block_tables || !seq_lens ||
+        !new_tables || seq_lens_out == seq_lens)
+        return PA_ERR_INVALID_ARG;
+    if (!aligned(weights, 16) || !aligned(weights_out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        !aligned(kept, 4) || !aligned(seq_lens_out, 4) || !aligned(seq_lens, 4) || !aligned(block_tables, 4) ||
+        !aligned(new_tables, 4) || (workspace && !aligned(workspace, 256)))
+        return PA_ERR_INVALID_ARG;
+    // cache rows, tokens of a table and the grids are numbered in 32 bits
+    const long long rows = static_cast<long long>(num_seqs) * num_kv_heads;
+    if (static_cast<long long>(num_blocks) * num_kv_heads * block_size >= (1ll << 31) || cap >= (1ll << 30) ||
+        rows >= (1ll << 27) || rows * ((static_cast<long long>(max_left) + 7) / 8) >= (1ll << 33))
+        return PA_ERR_UNSUPPORTED;
+    DeviceState* st = device_state(nullptr);
+    if (!st) return PA_ERR_CUDA;
+    const EvictPlan plan = evict_plan(num_seqs, num_kv_heads, cap, st->sms);
+    if (!plan.staged && weights_out == weights) return PA_ERR_UNSUPPORTED;
+    {
+        std::lock_guard<std::mutex> lock(g_mu);
+        if (!st->evict_prepared) {
+            cudaError_t e = evict_prepare();
+            if (e != cudaSuccess) return fail("cudaFuncSetAttribute(evict)", e);
+            st->evict_prepared = true;
+        }
+    }
+    EvictParams p;
+    p.kept = kept;
+    p.seq_lens_out = seq_lens_out;
+    p.weights_out = weights_out;
+    p.weights = weights;
+    p.weight_stride = weight_stride;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.block_tables = block_tables;
+    p.seq_lens = seq_lens;
+    p.new_tables = new_tables;
+    p.status = static_cast<int*>(workspace);
+    p.max_blocks = max_blocks_per_seq;
+    p.max_new_blocks = max_new_blocks_per_seq;
+    p.num_seqs = num_seqs;
+    p.budget = budget;
+    p.sinks = sinks;
+    p.recent = recent;
+    p.num_kv_heads = num_kv_heads;
+    p.num_blocks = num_blocks;
+    p.block_shift = block_shift_of(block_size);
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    const pa_status s = launched(launch_evict_select(p, plan, cs), "launch(evict_select)");
+    if (s != PA_OK) return s;
+    return launched(launch_evict_copy(p, is_fp8(cache_dtype), max_left, st->sms, cs), "launch(evict_copy)");
 }
 
 pa_status pa_read_device_status(void* workspace, pa_stream_t stream) {

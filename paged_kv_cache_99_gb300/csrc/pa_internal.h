@@ -223,6 +223,42 @@ cudaError_t launch_rope_table(float* cos_sin, int max_positions, int rot_dim, co
                               int sms, cudaStream_t stream);
 cudaError_t launch_rope_cache(RopeParams p, bool src_bf16, bool fp8, bool interleaved, int sms, cudaStream_t stream);
 
+// Eviction: selection of the places that stay (a cluster of `parts` CTAs per sequence
+// and KV head), then the copy of their rows.
+struct EvictParams {
+    int32_t* kept;                    // [num_seqs][num_kv_heads][budget]
+    int32_t* seq_lens_out;
+    float* weights_out;               // rows of weight_stride
+    const float* weights;
+    long long weight_stride;
+    void* k_cache;
+    void* v_cache;
+    const int32_t* block_tables;
+    const int32_t* seq_lens;
+    const int32_t* new_tables;
+    int* status;                      // device status word, or null
+    int max_blocks;
+    int max_new_blocks;
+    int num_seqs;
+    int budget;
+    int sinks;
+    int recent;
+    int num_kv_heads;
+    int num_blocks;
+    int block_shift;
+};
+
+struct EvictPlan {
+    int parts;                        // CTAs per row
+    bool staged;                      // a CTA's part of the row fits its shared memory
+    size_t smem;
+};
+
+EvictPlan evict_plan(int num_seqs, int num_kv_heads, long long cap, int sms);
+cudaError_t evict_prepare();
+cudaError_t launch_evict_select(const EvictParams& p, const EvictPlan& plan, cudaStream_t stream);
+cudaError_t launch_evict_copy(const EvictParams& p, bool fp8, int max_left, int sms, cudaStream_t stream);
+
 // Prefill chunks.
 size_t chunk_smem_bytes(CacheKind kind, int num_seqs);
 int chunk_rows();           // MMA rows of one query tile
