@@ -228,6 +228,16 @@ PA_API size_t pa_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
  */
 PA_API size_t pa_workspace_size_shared_prefix(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim);
 
+/*
+ * Bytes of workspace for pa_decode_weights: pa_workspace_size and the scores of up to
+ * max_tokens cached tokens (the sum over the batch of each sequence's length rounded up
+ * to 16), 4 bytes per token, KV head and query head of its group (a group counted up to
+ * an even number, groups of more than 8 up to a multiple of 8).  Same rules as
+ * pa_workspace_size.  Returns 0 for invalid arguments.
+ */
+PA_API size_t pa_workspace_size_weights(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                        long long max_tokens);
+
 /* Default number of decode workers (warps) on the current device for a 16-bit
  * cache: two 4-warp CTAs per SM.  An FP8 cache defaults to twice as many (four
  * CTAs per SM: its warps are bound by the latency of the work on each block, not
@@ -324,6 +334,31 @@ PA_API pa_status pa_decode_ex(void* out, const void* q, const void* k_cache, con
                        pa_dtype q_dtype, pa_dtype cache_dtype, const float* k_scale,
                        const float* v_scale, void* workspace, size_t workspace_bytes,
                        int num_workers, pa_stream_t stream);
+
+/*
+ * pa_decode that also adds up how much each cached token is attended to (no counterpart on
+ * the pages; pa_evict chooses by these sums): out as pa_decode, and for every sequence s,
+ * KV head h and token t < seq_lens[s]
+ *   weights_out[s][h][t] = weights_in[s][h][t] + sum over the query heads of h's group of
+ *                          their softmax weight of token t, in float32.
+ * Entries of weights_out from seq_lens[s] on are left as they were.
+ *
+ *   weights_in     device, float32 [num_seqs][num_kv_heads][weight_stride], or NULL for
+ *                  zeros (weights_out is then this step's weights alone)
+ *   weights_out    device, the same layout; may be weights_in, otherwise must not overlap it
+ *   weight_stride  at least max_blocks_per_seq * block_size
+ *   workspace      pa_workspace_size_weights bytes.  A batch with more tokens than the
+ *                  workspace holds scores for is recorded as PA_ERR_WORKSPACE in its status
+ *                  word: out is computed, weights_out is left as it was
+ * Other arguments as pa_decode; out agrees with pa_decode's exactly.
+ */
+PA_API pa_status pa_decode_weights(void* out, float* weights_out, const float* weights_in, long long weight_stride,
+                                   const void* q, const void* k_cache, const void* v_cache,
+                                   const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                                   int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                   int num_blocks, float scale, pa_dtype q_dtype, pa_dtype cache_dtype,
+                                   const float* k_scale, const float* v_scale, void* workspace,
+                                   size_t workspace_bytes, pa_stream_t stream);
 
 /*
  * Decode for a batch whose block tables share their leading blocks: the same
@@ -553,8 +588,8 @@ PA_API pa_status pa_pool_copy_on_write(pa_block_pool* pool, int32_t* blocks, int
 
 /*
  * Reads (and clears) the device-side status word of a workspace.  Synchronises
- * `stream`.  Returns PA_OK, PA_ERR_OUT_OF_RANGE or PA_ERR_TIMEOUT (the first
- * recorded, timeouts first), or PA_ERR_CUDA if the copy failed.
+ * `stream`.  Returns PA_OK, PA_ERR_TIMEOUT, PA_ERR_OUT_OF_RANGE or PA_ERR_WORKSPACE
+ * (of several recorded the first in this order), or PA_ERR_CUDA if the copy failed.
  */
 PA_API pa_status pa_read_device_status(void* workspace, pa_stream_t stream);
 

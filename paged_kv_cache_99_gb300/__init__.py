@@ -70,6 +70,10 @@ def _lib():
     lib.pa_rope_and_cache.restype = I
     lib.pa_evict.argtypes = [P, P, P, P, LL, P, P, P, I, P, P, I, I, I, I, I, I, I, I, I, I, P, P]
     lib.pa_evict.restype = I
+    lib.pa_workspace_size_weights.argtypes = [I, I, I, I, LL]
+    lib.pa_workspace_size_weights.restype = Z
+    lib.pa_decode_weights.argtypes = [P, P, P, LL, P, P, P, P, I, P, I, I, I, I, I, I, F, I, I, P, P, P, Z, P]
+    lib.pa_decode_weights.restype = I
     lib.pa_workspace_size.argtypes = [I, I, I, I]
     lib.pa_workspace_size.restype = Z
     lib.pa_workspace_size_shared_prefix.argtypes = [I, I, I, I]
@@ -225,6 +229,20 @@ def pa_workspace_size_shared_prefix(num_seqs: int, num_q_heads: int, num_kv_head
     return int(_lib().pa_workspace_size_shared_prefix(num_seqs, num_q_heads, num_kv_heads, head_dim))
 
 
+def pa_workspace_size_weights(num_seqs: int, num_q_heads: int, num_kv_heads: int, max_tokens: int,
+                              head_dim: int = 128) -> int:
+    return int(_lib().pa_workspace_size_weights(num_seqs, num_q_heads, num_kv_heads, head_dim, int(max_tokens)))
+
+
+def new_workspace_weights(num_seqs: int, num_q_heads: int, num_kv_heads: int, max_tokens: int, device=None) -> torch.Tensor:
+    """Zeroed workspace for pa_decode_weights with up to max_tokens cached tokens in all
+    (each sequence's length rounded up to 16)."""
+    n = pa_workspace_size_weights(num_seqs, num_q_heads, num_kv_heads, max_tokens)
+    if n == 0:
+        raise ValueError("invalid workspace arguments")
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
 def new_workspace(num_seqs: int, num_q_heads: int, num_kv_heads: int, device=None,
                   shared_prefix: bool = False) -> torch.Tensor:
     """Workspace of pa_workspace_size bytes (zeroed, so the status word starts clear);
@@ -331,6 +349,40 @@ def pa_decode(out, q, k_cache, v_cache, block_tables, seq_lens, scale, workspace
                              _DTYPE[q.dtype], _cache_code(k_cache, k_scale, k_cache.shape[1]), _ptr(k_scale), _ptr(v_scale),
                              _ptr(workspace), workspace.numel(), int(num_workers), _stream(stream))
     _check(st, "pa_decode")
+
+
+def pa_decode_weights(out, weights_out, q, k_cache, v_cache, block_tables, seq_lens, scale, workspace, weights_in=None,
+                      k_scale=None, v_scale=None, stream=None):
+    """pa_decode that also writes weights_out [B, H_kv, >= tokens of the table] (float32) = weights_in (or
+    zeros) + the step's softmax weights summed over each group's query heads; weights_in may be weights_out."""
+    _need(q, "q", (torch.bfloat16, torch.float16))
+    _need(out, "out", (q.dtype,))
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _need(t, n, tuple(_DTYPE))
+    _need(block_tables, "block_tables", (torch.int32,))
+    _need(seq_lens, "seq_lens", (torch.int32,))
+    _need(workspace, "workspace", (torch.uint8,))
+    _need(weights_out, "weights_out", (torch.float32,))
+    if weights_in is not None:
+        _need(weights_in, "weights_in", (torch.float32,))
+    B, Hq, d = q.shape
+    nb, Hkv, bs, _ = k_cache.shape
+    if (out.shape != q.shape or v_cache.shape != k_cache.shape or block_tables.dim() != 2 or
+            block_tables.shape[0] != B or seq_lens.shape != (B,) or weights_out.dim() != 3 or
+            weights_out.shape[:2] != (B, Hkv) or (weights_in is not None and weights_in.shape != weights_out.shape)):
+        raise ValueError("shape mismatch")
+    if v_cache.dtype != k_cache.dtype:
+        raise TypeError("the caches must have one type")
+    code = _cache_code(k_cache, k_scale, Hkv)
+    _need_scales(code, k_scale, v_scale, Hkv)
+    _same_device(q, out=out, weights_out=weights_out, weights_in=weights_in, k_cache=k_cache, v_cache=v_cache,
+                 block_tables=block_tables, seq_lens=seq_lens, workspace=workspace, k_scale=k_scale, v_scale=v_scale)
+    with _on(q):
+        st = _lib().pa_decode_weights(_ptr(out), _ptr(weights_out), _ptr(weights_in), weights_out.shape[2], _ptr(q),
+                                      _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), block_tables.shape[1],
+                                      _ptr(seq_lens), B, Hq, Hkv, d, bs, nb, float(scale), _DTYPE[q.dtype], code,
+                                      _ptr(k_scale), _ptr(v_scale), _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(st, "pa_decode_weights")
 
 
 def pa_decode_append(out, q, k_new, v_new, slot_mapping, k_cache, v_cache, block_tables, seq_lens, scale, workspace,

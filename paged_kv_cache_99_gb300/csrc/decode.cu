@@ -151,7 +151,7 @@ __device__ __forceinline__ T shfl(T v, int src) {
 
 }  // namespace
 
-template <int Kind, bool QBf16, bool Append, bool Dyn, int Stages = 3>
+template <int Kind, bool QBf16, bool Append, bool Dyn, int Stages = 3, bool Weights = false>
 __device__ __forceinline__ void decode_body(const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeParams& p) {
     using Cfg = DecodeCfg<Kind, Stages>;
     constexpr bool kFp8 = Cfg::kFp8;
@@ -254,6 +254,8 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kmap, const CUten
 
     const int T = cum[B];
     if (T == 0) return;
+    if (Weights && T > p.score_units && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.status, kDevErrWorkspace);
+    const bool keep_scores = Weights && T <= p.score_units;
     const Split sp = make_split(T, p.num_workers, p.dyn256);
     const int wid = blockIdx.x * kDecodeWarps + warp;
     // With static ranges the warps of a CTA, whose ranges follow one another, merge
@@ -600,6 +602,15 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kmap, const CUten
             if (g + 8 >= valid) s2 = s3 = -INFINITY;
         }
 
+        // the scores of this unit, for the weights once the softmax's sum is known: [16 keys][pitch]
+        if constexpr (Weights) {
+            if (keep_scores && 2 * t < p.score_pitch) {
+                float* sc = p.scores + static_cast<size_t>(c_f) * (kBlockSize * p.score_pitch) + g * p.score_pitch + 2 * t;
+                *reinterpret_cast<float2*>(sc) = make_float2(s0, s1);
+                *reinterpret_cast<float2*>(sc + 8 * p.score_pitch) = make_float2(s2, s3);
+            }
+        }
+
         // ---- online softmax over keys (lanes with equal t share heads) ----
         float x0 = fmaxf(s0, s2), x1 = fmaxf(s1, s3);
 #pragma unroll
@@ -698,6 +709,13 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kmap, const CUten
                 if (stage) my_staged = u;
             }
             if (write) {
+                if constexpr (Weights) {
+                    if (lane < 4) {
+                        float* um = p.unit_ml + static_cast<size_t>(u) * 16 + 2 * t;
+                        *reinterpret_cast<float2*>(um) = make_float2(m0, m1);
+                        *reinterpret_cast<float2*>(um + 8) = make_float2(1.0f / l0, 1.0f / l1);
+                    }
+                }
                 const int h = C.uh / p.head_groups;
                 const int hg = C.uh % p.head_groups;
                 const float inv0 = vscale / l0, inv1 = vscale / l1;
@@ -811,6 +829,15 @@ __global__ void __maxnreg__(decode_max_regs<Kind>())
     decode_body<Kind, QBf16, true, Dyn>(kmap, vmap, p);
 }
 
+
+// Decode that also leaves every score and, per unit, the softmax's maximum and sum, for
+// weights_kernel (pa_decode_weights).
+template <int Kind, bool QBf16, bool Dyn>
+__global__ void __maxnreg__(decode_max_regs<Kind>())
+    decode_scores_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                         const DecodeParams p) {
+    decode_body<Kind, QBf16, false, Dyn, 3, true>(kmap, vmap, p);
+}
 
 // Log-sum-exp combine of the units split across workers:
 //   out = sum_i e^{m_i - M} o_i / sum_i e^{m_i - M} l_i,   M = max_i m_i,
@@ -952,6 +979,11 @@ __device__ __forceinline__ void combine_unit(const DecodeParams& p, int u, const
             lv[k] = __ldcg(reinterpret_cast<const float2*>(p.ml + static_cast<size_t>(sl) * 16 + 8 + 2 * t));
         }
         fold(v, mv, lv, min(kBatch, nseg - base));
+    }
+    if (!Cascade && p.unit_ml && threadIdx.x < 4) {      // the unit's maximum and 1 / sum, for weights_kernel
+        float* um = p.unit_ml + static_cast<size_t>(u) * 16 + 2 * t;
+        *reinterpret_cast<float2*>(um) = make_float2(M0, M1);
+        *reinterpret_cast<float2*>(um + 8) = make_float2(1.0f / L0, 1.0f / L1);
     }
     const float vscale = Fp8Layout ? __ldg(p.v_scale + h * p.scale_stride) : 1.0f;
 #pragma unroll
@@ -1193,6 +1225,63 @@ __global__ void __maxnreg__(112) combine_cascade_kernel(const DecodeParams p) {
     }
 }
 
+// Attention weights of a decode step: for every cached token t of sequence s and KV head h
+//   weights_out[s][h][t] = weights_in[s][h][t] + sum over the group's heads of 2^(score - M) / L
+// from the scores the decode kernel left (in log2 units, [16 keys][pitch heads] per 16-key
+// unit, in the flattened order) and the units' final (M, 1 / L).  HBM- and L2-bound: a
+// score is 4 bytes per query head, written and read once, against 512 bytes of K and V (256
+// for FP8) per token and KV head; reading K a second time instead would cost 256 (128).
+// 16 lanes take a unit (one key each), a CTA 16 consecutive units at a time.
+template <int Pitch>
+__global__ void __launch_bounds__(256) weights_kernel(const DecodeParams p) {
+    __shared__ int pre_sum[kCombineScanSeqs + 1];
+    __shared__ int warp_sum[8];
+    grid_launch_dependents();
+    const int B = p.num_seqs;
+    const int UH = p.num_kv_heads * p.head_groups;
+    const int* cum = pre_sum;
+    if (B <= kCombineScanSeqs) combine_block_prefix(p, pre_sum, warp_sum);
+    else cum = p.plan;
+    grid_dependency_wait();
+    const int T = cum[B];
+    if (T > p.score_units) return;               // recorded by the decode grid
+    const int F = T / p.head_groups;             // units of KV heads
+    const int key = threadIdx.x & 15;
+    for (int f = blockIdx.x * 16 + (threadIdx.x >> 4); f < F; f += gridDim.x * 16) {
+        // sequence s with cum[s] <= f head_groups < cum[s + 1]
+        int lo = 0, hi = B;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (cum[mid] <= f * p.head_groups) lo = mid; else hi = mid;
+        }
+        const int first = cum[lo], nb = (cum[lo + 1] - first) / UH;
+        const int rem = f - first / p.head_groups;
+        const int h = rem / nb, j = rem % nb;
+        const int t = j * kBlockSize + key;
+        float w = 0.f;
+        for (int hg = 0; hg < p.head_groups; ++hg) {
+            const int uh = h * p.head_groups + hg;
+            const float* sc = p.scores + (static_cast<size_t>(first + uh * nb + j) * kBlockSize + key) * Pitch;
+            const float* um = p.unit_ml + static_cast<size_t>(lo * UH + uh) * 16;
+            const int live = p.group - hg * kHeadsPerGroup;      // heads of this unit
+            float x[Pitch], m[Pitch], r[Pitch];
+#pragma unroll
+            for (int e = 0; e < Pitch; e += 2) {
+                *reinterpret_cast<float2*>(x + e) = __ldcg(reinterpret_cast<const float2*>(sc + e));
+                *reinterpret_cast<float2*>(m + e) = __ldcg(reinterpret_cast<const float2*>(um + e));
+                *reinterpret_cast<float2*>(r + e) = __ldcg(reinterpret_cast<const float2*>(um + 8 + e));
+            }
+#pragma unroll
+            for (int e = 0; e < Pitch; ++e)
+                if (e < live) w += exp2f(x[e] - m[e]) * r[e];
+        }
+        if (t < min(p.seq_lens[lo], p.max_blocks * p.block_size)) {
+            const size_t at = (static_cast<size_t>(lo) * p.num_kv_heads + h) * p.weight_stride + t;
+            p.weights_out[at] = (p.weights_in ? p.weights_in[at] : 0.f) + w;
+        }
+    }
+}
+
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
@@ -1213,7 +1302,22 @@ void* kernel_ptr(bool append, bool dyn, bool narrow) {
                   : reinterpret_cast<void*>(&decode_kernel<Kind, QBf16, false, 3>);
 }
 
-void* decode_fn(CacheKind kind, bool q_bf16, bool append, bool dyn, bool narrow) {
+template <int Kind, bool QBf16>
+void* scores_ptr(bool dyn) {
+    return dyn ? reinterpret_cast<void*>(&decode_scores_kernel<Kind, QBf16, true>)
+               : reinterpret_cast<void*>(&decode_scores_kernel<Kind, QBf16, false>);
+}
+
+void* decode_fn(CacheKind kind, bool q_bf16, DecodeForm form, bool dyn, bool narrow) {
+    if (form == kDecodeScores) {
+        switch (kind) {
+            case kKindBf16: return scores_ptr<kKindBf16, true>(dyn);
+            case kKindFp16: return scores_ptr<kKindFp16, false>(dyn);
+            case kKindFp8: return q_bf16 ? scores_ptr<kKindFp8, true>(dyn) : scores_ptr<kKindFp8, false>(dyn);
+        }
+        return nullptr;
+    }
+    const bool append = form == kDecodeAppend;
     switch (kind) {
         case kKindBf16: return kernel_ptr<kKindBf16, true>(append, dyn, narrow);
         case kKindFp16: return kernel_ptr<kKindFp16, false>(append, dyn, narrow);
@@ -1243,22 +1347,22 @@ size_t decode_smem_bytes(CacheKind kind, int num_seqs, bool narrow) {
     return 1024 + static_cast<size_t>(tile_area_bytes(kind, narrow)) + static_cast<size_t>(num_seqs + 1) * 4;
 }
 
-cudaError_t decode_prepare(CacheKind kind, bool q_bf16, bool append, bool dyn, bool narrow, size_t max_smem) {
+cudaError_t decode_prepare(CacheKind kind, bool q_bf16, DecodeForm form, bool dyn, bool narrow, size_t max_smem) {
     // the largest request a call can make (kMaxSeqs sequences), within what the
     // device allows next to the kernel's static shared memory
     cudaFuncAttributes fa;
-    cudaError_t e = cudaFuncGetAttributes(&fa, decode_fn(kind, q_bf16, append, dyn, narrow));
+    cudaError_t e = cudaFuncGetAttributes(&fa, decode_fn(kind, q_bf16, form, dyn, narrow));
     if (e != cudaSuccess) return e;
     size_t want = decode_smem_bytes(kind, kMaxSeqs, narrow);
     const size_t cap = max_smem > fa.sharedSizeBytes ? max_smem - fa.sharedSizeBytes : 0;
     if (want > cap) want = cap;
-    return cudaFuncSetAttribute(decode_fn(kind, q_bf16, append, dyn, narrow),
+    return cudaFuncSetAttribute(decode_fn(kind, q_bf16, form, dyn, narrow),
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(want));
 }
 
-cudaError_t decode_occupancy(CacheKind kind, bool q_bf16, bool append, bool dyn, bool narrow, size_t smem,
+cudaError_t decode_occupancy(CacheKind kind, bool q_bf16, DecodeForm form, bool dyn, bool narrow, size_t smem,
                              int* ctas_per_sm) {
-    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas_per_sm, decode_fn(kind, q_bf16, append, dyn, narrow),
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas_per_sm, decode_fn(kind, q_bf16, form, dyn, narrow),
                                                          kDecodeWarps * 32, smem);
 }
 
@@ -1275,7 +1379,8 @@ cudaError_t launch_decode(CacheKind kind, bool q_bf16, const CUtensorMap& kmap, 
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     void* args[] = {const_cast<CUtensorMap*>(&kmap), const_cast<CUtensorMap*>(&vmap), const_cast<DecodeParams*>(&p)};
-    const void* fn = decode_fn(kind, q_bf16, p.append != 0, p.dyn256 > 0, p.narrow != 0);
+    const void* fn = decode_fn(kind, q_bf16, p.scores ? kDecodeScores : p.append ? kDecodeAppend : kDecodePlain, p.dyn256 > 0,
+                               p.narrow != 0);
     if (!fn) return cudaErrorInvalidValue;
     return cudaLaunchKernelExC(&cfg, fn, args);
 }
@@ -1316,6 +1421,29 @@ cudaError_t launch_combine(bool out_bf16, bool fp8_cache, const DecodeParams& p,
                               : (fp8_cache ? kernel(Fa{}, T{}) : kernel(Fa{}, Fa{}));
     void* args[] = {const_cast<DecodeParams*>(&p)};
     return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+cudaError_t launch_weights(const DecodeParams& p, int sms, cudaStream_t stream) {
+    // 16 units per CTA and turn, up to the resident CTAs
+    const long long per_seq = (static_cast<long long>(p.max_blocks) * p.block_size + kBlockSize - 1) / kBlockSize;
+    const long long want = (static_cast<long long>(p.num_seqs) * p.num_kv_heads * per_seq + 15) / 16;
+    const long long cap = 6ll * sms;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(want < cap ? want : cap));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    switch (p.score_pitch) {
+        case 2: return cudaLaunchKernelEx(&cfg, weights_kernel<2>, p);
+        case 4: return cudaLaunchKernelEx(&cfg, weights_kernel<4>, p);
+        case 6: return cudaLaunchKernelEx(&cfg, weights_kernel<6>, p);
+        case 8: return cudaLaunchKernelEx(&cfg, weights_kernel<8>, p);
+    }
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace pa

@@ -24,7 +24,7 @@ struct DeviceState {
     bool ready = false;
     int sms = 0;
     size_t max_smem_optin = 0;
-    bool decode_prepared[3][2][2][2][2] = {};
+    bool decode_prepared[3][2][3][2][2] = {};
     bool chunk_prepared[3][2] = {};
     bool evict_prepared = false;
 };
@@ -171,6 +171,17 @@ CacheKind kind_of(pa_dtype cache_dtype) {
     return is_fp8(cache_dtype) ? kKindFp8 : (cache_dtype == PA_FP16 ? kKindFp16 : kKindBf16);
 }
 
+// The weights' part of a decode call: where they go, and the scores' part of the workspace.
+struct WeightsArgs {
+    const float* weights_in;
+    float* weights_out;
+    long long weight_stride;
+    float* scores;
+    float* unit_ml;
+    long long score_units;
+    int score_pitch;
+};
+
 pa_status decode_impl(void* out, const void* q, const int32_t* query_start_loc, const void* k_cache,
                       const void* v_cache, const int32_t* block_tables, int max_blocks_per_seq,
                       const int32_t* seq_lens, int num_seqs, int num_q_heads, int num_kv_heads, float scale,
@@ -179,13 +190,15 @@ pa_status decode_impl(void* out, const void* q, const int32_t* query_start_loc, 
                       int total_rows, cudaStream_t stream, bool overlap_prior = false, bool cascade = false,
                       int first_block = 0, int prefix_splits = 1, const float* prefix_o_extra = nullptr,
                       const float* prefix_ml_extra = nullptr, const void* k_new = nullptr,
-                      const void* v_new = nullptr, const int64_t* slots = nullptr) {
+                      const void* v_new = nullptr, const int64_t* slots = nullptr,
+                      const WeightsArgs* weights = nullptr) {
     int dev = 0;
     DeviceState* st = device_state(&dev);
     if (!st) return PA_ERR_CUDA;
     const CacheKind kind = kind_of(cache_dtype);
     const bool q_bf16 = q_dtype == PA_BF16;
     const bool append = slots != nullptr;
+    const DecodeForm form = weights ? kDecodeScores : append ? kDecodeAppend : kDecodePlain;
     // claimed pieces balance SMs that stream at different rates; they pay only where
     // workers' ranges are long (judged from the table width: the decode grid decides
     // from the lengths) and the warps keep HBM busy: FP8 warps, and 16-bit warps with
@@ -211,16 +224,16 @@ pa_status decode_impl(void* out, const void* q, const int32_t* query_start_loc, 
     int ctas = 0;
     {
         std::lock_guard<std::mutex> lock(g_mu);
-        if (!st->decode_prepared[kind][q_bf16][append][dyn][narrow]) {
-            cudaError_t e = decode_prepare(kind, q_bf16, append, dyn, narrow, st->max_smem_optin);
+        if (!st->decode_prepared[kind][q_bf16][form][dyn][narrow]) {
+            cudaError_t e = decode_prepare(kind, q_bf16, form, dyn, narrow, st->max_smem_optin);
             if (e != cudaSuccess) return fail("cudaFuncSetAttribute(decode)", e);
-            st->decode_prepared[kind][q_bf16][append][dyn][narrow] = true;
+            st->decode_prepared[kind][q_bf16][form][dyn][narrow] = true;
         }
-        auto key = std::make_tuple(dev, static_cast<int>(kind), static_cast<int>(q_bf16), static_cast<int>(append),
+        auto key = std::make_tuple(dev, static_cast<int>(kind), static_cast<int>(q_bf16), static_cast<int>(form),
                                    static_cast<int>(dyn) + 2 * static_cast<int>(narrow), smem);
         auto it = g_occupancy.find(key);
         if (it == g_occupancy.end()) {
-            cudaError_t e = decode_occupancy(kind, q_bf16, append, dyn, narrow, smem, &ctas);
+            cudaError_t e = decode_occupancy(kind, q_bf16, form, dyn, narrow, smem, &ctas);
             if (e != cudaSuccess) return fail("cudaOccupancyMaxActiveBlocksPerMultiprocessor(decode)", e);
             if (ctas <= 0) return fail_msg("decode kernel does not fit on an SM");
             g_occupancy[key] = ctas;
@@ -286,12 +299,23 @@ pa_status decode_impl(void* out, const void* q, const int32_t* query_start_loc, 
     p.slots = slots;
     p.k_cache_w = const_cast<void*>(k_cache);
     p.v_cache_w = const_cast<void*>(v_cache);
+    const WeightsArgs none = {};
+    const WeightsArgs& wa = weights ? *weights : none;
+    p.scores = wa.scores;
+    p.unit_ml = wa.unit_ml;
+    p.score_units = wa.score_units;
+    p.score_pitch = wa.score_pitch;
+    p.weights_in = wa.weights_in;
+    p.weights_out = wa.weights_out;
+    p.weight_stride = wa.weight_stride;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.timeout_ns = kDefaultTimeoutNs;
     const int grid = (W + kDecodeWarps - 1) / kDecodeWarps;
     s = launched(launch_decode(kind, q_bf16, kmap, vmap, p, grid, smem, stream), "launch(decode)");
     if (s != PA_OK) return s;
-    return launched(launch_combine(q_bf16, kind == kKindFp8, p, 2 * st->sms, stream), "launch(combine)");
+    s = launched(launch_combine(q_bf16, kind == kKindFp8, p, 2 * st->sms, stream), "launch(combine)");
+    if (s != PA_OK || !weights) return s;
+    return launched(launch_weights(p, st->sms, stream), "launch(weights)");
 }
 
 pa_status chunk_impl(void* out, const void* q, const int32_t* query_start_loc, const void* k_cache,
@@ -378,6 +402,25 @@ WorkspaceLayout decode_workspace_layout(int num_seqs, int num_q_heads, int num_k
     l.ml_off = l.prefix_ml_off + round_up(rows * 2 * sizeof(float), 256);
     l.partial_off = l.ml_off + round_up(slots * 16 * 4, 256);
     l.total = l.partial_off + slots * 8 * 32 * sizeof(float4);
+    return l;
+}
+
+// The attention weights' part of a workspace, after the base: (maximum, 1 / sum) of 8
+// heads per unit, then the scores.
+struct ScoresLayout {
+    size_t ml_off, scores_off;
+    int pitch;                        // heads kept per key
+    size_t unit_bytes;                // scores of one 16-key unit
+};
+
+ScoresLayout scores_layout(size_t base, int num_seqs, int num_q_heads, int num_kv_heads) {
+    ScoresLayout l;
+    const int group = num_q_heads / num_kv_heads;
+    const size_t units = static_cast<size_t>(num_seqs) * num_kv_heads * head_groups_of(num_q_heads, num_kv_heads);
+    l.ml_off = round_up(base, 256);
+    l.scores_off = l.ml_off + round_up(units * 16 * sizeof(float), 256);
+    l.pitch = group >= kHeadsPerGroup ? kHeadsPerGroup : (group + 1) / 2 * 2;
+    l.unit_bytes = static_cast<size_t>(kBlockSize) * l.pitch * sizeof(float);
     return l;
 }
 
@@ -588,6 +631,15 @@ size_t pa_workspace_size_shared_prefix(int num_seqs, int num_q_heads, int num_kv
     return prefix_extra_layout(base, static_cast<size_t>(num_seqs) * num_q_heads, kMaxPrefixSplits).end;
 }
 
+size_t pa_workspace_size_weights(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, long long max_tokens) {
+    const size_t base = pa_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim);
+    if (base == 0 || max_tokens < 0 || max_tokens >= (1ll << 40)) return 0;
+    const ScoresLayout l = scores_layout(base, num_seqs, num_q_heads, num_kv_heads);
+    const size_t units = static_cast<size_t>((max_tokens + kBlockSize - 1) / kBlockSize) * num_kv_heads *
+                         head_groups_of(num_q_heads, num_kv_heads);
+    return l.scores_off + units * l.unit_bytes;
+}
+
 int pa_default_workers(void) {
     DeviceState* st = device_state(nullptr);
     return st ? max_workers(*st) : 0;
@@ -687,6 +739,38 @@ pa_status pa_decode_shared_prefix(void* out, const void* q, const void* k_cache,
                        num_q_heads, num_kv_heads, scale, q_dtype, cache_dtype, k_scale, v_scale, workspace,
                        workspace_bytes, workers, num_blocks, block_size, num_seqs, cs, prefix_units > 0, true,
                        prefix_units, splits, o_extra, ml_extra);
+}
+
+pa_status pa_decode_weights(void* out, float* weights_out, const float* weights_in, long long weight_stride,
+                            const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                            int max_blocks_per_seq, const int32_t* seq_lens, int num_seqs, int num_q_heads,
+                            int num_kv_heads, int head_dim, int block_size, int num_blocks, float scale,
+                            pa_dtype q_dtype, pa_dtype cache_dtype, const float* k_scale, const float* v_scale,
+                            void* workspace, size_t workspace_bytes, pa_stream_t stream) {
+    pa_status s = check_attention_args(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens,
+                                       num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                                       scale, q_dtype, cache_dtype, k_scale, v_scale, workspace);
+    if (s != PA_OK) return s;
+    if (weight_stride < static_cast<long long>(max_blocks_per_seq) * block_size) return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0) return PA_OK;
+    if (!weights_out || !aligned(weights_out, 4) || !aligned(weights_in, 4)) return PA_ERR_INVALID_ARG;
+    const size_t base = pa_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim);
+    if (base == 0) return PA_ERR_CUDA;
+    const ScoresLayout l = scores_layout(base, num_seqs, num_q_heads, num_kv_heads);
+    if (workspace_bytes < l.scores_off) return PA_ERR_WORKSPACE;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    WeightsArgs wa;
+    wa.weights_in = weights_in;
+    wa.weights_out = weights_out;
+    wa.weight_stride = weight_stride;
+    wa.scores = reinterpret_cast<float*>(ws + l.scores_off);
+    wa.unit_ml = reinterpret_cast<float*>(ws + l.ml_off);
+    wa.score_units = static_cast<long long>((workspace_bytes - l.scores_off) / l.unit_bytes);
+    wa.score_pitch = l.pitch;
+    return decode_impl(out, q, nullptr, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, num_seqs,
+                       num_q_heads, num_kv_heads, scale, q_dtype, cache_dtype, k_scale, v_scale, workspace,
+                       workspace_bytes, 0, num_blocks, block_size, num_seqs, reinterpret_cast<cudaStream_t>(stream),
+                       false, false, 0, 1, nullptr, nullptr, nullptr, nullptr, nullptr, &wa);
 }
 
 pa_status pa_decode_append_ex(void* out, const void* q, const void* k_new, const void* v_new,
@@ -896,6 +980,7 @@ pa_status pa_read_device_status(void* workspace, pa_stream_t stream) {
     }
     if (word & kDevErrTimeout) return PA_ERR_TIMEOUT;
     if (word & kDevErrRange) return PA_ERR_OUT_OF_RANGE;
+    if (word & kDevErrWorkspace) return PA_ERR_WORKSPACE;
     return PA_OK;
 }
 

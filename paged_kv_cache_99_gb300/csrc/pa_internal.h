@@ -48,6 +48,11 @@ constexpr int kMaxPrefixSplits = 16;
 // Bits of the device-side status word (first word of the workspace).
 constexpr int kDevErrTimeout = 1;
 constexpr int kDevErrRange = 2;
+constexpr int kDevErrWorkspace = 4;
+
+// Forms of the decode kernel: plain, with the slot write of the new tokens, and leaving
+// the scores for the attention weights.
+enum DecodeForm { kDecodePlain = 0, kDecodeAppend = 1, kDecodeScores = 2 };
 
 // Decode: one "unit" = (sequence, KV head, group of up to 8 query heads).  The
 // cached blocks of all units are laid end to end and cut into ranges: equal
@@ -105,6 +110,16 @@ struct DecodeParams {
     const int64_t* slots;
     void* k_cache_w;
     void* v_cache_w;
+    // Attention weights (pa_decode_weights): the scores of every 16-key unit, in the
+    // flattened order, [16 keys][score_pitch heads] in log2 units, and per unit the
+    // softmax's maximum and 1 / sum of its 8 heads.  Null: a decode without them.
+    float* scores;
+    float* unit_ml;
+    long long score_units;            // units the scores' part of the workspace holds
+    int score_pitch;                  // heads of a unit, rounded up to an even number
+    const float* weights_in;          // null: zeros
+    float* weights_out;               // rows of weight_stride
+    long long weight_stride;
     float scale_log2;                 // softmax scale * log2(e)
     unsigned long long timeout_ns;    // bound of every barrier wait
 };
@@ -169,8 +184,8 @@ WorkspaceLayout decode_workspace_layout(int num_seqs, int num_q_heads, int num_k
 // Decode kernels: dynamic shared memory for num_seqs sequences.
 // narrow: the 16-bit kernel with a two-stage ring per warp (three CTAs per SM)
 size_t decode_smem_bytes(CacheKind kind, int num_seqs, bool narrow);
-cudaError_t decode_prepare(CacheKind kind, bool q_bf16, bool append, bool dyn, bool narrow, size_t max_smem);
-cudaError_t decode_occupancy(CacheKind kind, bool q_bf16, bool append, bool dyn, bool narrow, size_t smem,
+cudaError_t decode_prepare(CacheKind kind, bool q_bf16, DecodeForm form, bool dyn, bool narrow, size_t max_smem);
+cudaError_t decode_occupancy(CacheKind kind, bool q_bf16, DecodeForm form, bool dyn, bool narrow, size_t smem,
                              int* ctas_per_sm);
 cudaError_t launch_decode(CacheKind kind, bool q_bf16, const CUtensorMap& kmap,
                           const CUtensorMap& vmap, const DecodeParams& p, int grid, size_t smem,
@@ -178,6 +193,9 @@ cudaError_t launch_decode(CacheKind kind, bool q_bf16, const CUtensorMap& kmap,
 // Block copies (copy-on-write): dst[i] <- src[i] in both caches.
 cudaError_t launch_copy_blocks(void* k_cache, void* v_cache, const int32_t* src, const int32_t* dst, int num_pairs,
                                int num_blocks, size_t block_bytes, int* status, cudaStream_t stream);
+
+// Adds the step's attention weights up from the scores (after the combine).
+cudaError_t launch_weights(const DecodeParams& p, int sms, cudaStream_t stream);
 
 cudaError_t launch_combine(bool out_bf16, bool fp8_cache, const DecodeParams& p, int max_ctas,
                            cudaStream_t stream);
