@@ -512,7 +512,7 @@ PA_API pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int32_t* src
  *   weights        device, float32 [num_seqs][num_kv_heads][weight_stride] (pa_decode_weights
  *                  adds to it), 16-byte aligned; weight_stride a multiple of 4 and at least
  *                  max_blocks_per_seq * block_size
- *   weights_out    the same layout; may be weights itself (up to 393216 tokens of table:
+ *   weights_out    the same layout; may be weights itself (up to 131072 tokens of table:
  *                  beyond that PA_ERR_UNSUPPORTED), otherwise must not overlap it
  *   kept           device, int32 [num_seqs][num_kv_heads][budget]
  *   seq_lens_out   device, int32 [num_seqs]; not seq_lens itself

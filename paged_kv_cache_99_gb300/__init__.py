@@ -141,51 +141,80 @@ def _need(t: torch.Tensor, name: str, dtypes=None):
         raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
 
 
-def _need_rows(t: torch.Tensor, name: str, dtypes):
-    """[tokens, heads, 128] on a GPU with each token's heads contiguous (any stride between tokens)."""
+# The calls below check a dozen tensors each and launch kernels of a few microseconds, so
+# their checks take one pass over the tensors and few attribute reads.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
+_16BIT = (torch.bfloat16, torch.float16)
+_CACHE = (torch.bfloat16, torch.float16, torch.uint8, torch.float8_e4m3fn)
+_F32, _I32, _I64, _U8 = (torch.float32,), (torch.int32,), (torch.int64,), (torch.uint8,)
+
+
+def _device_of(t, name: str) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
+    return t.get_device()
+
+
+def _pointers(device: int, *tensors) -> list:
+    """Addresses of (tensor or None, name, dtypes): contiguous tensors of one of the types on the device."""
+    out = []
+    for t, name, dtypes in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.dtype not in dtypes:
+            raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
+        if t.get_device() != device:
+            raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        out.append(t.data_ptr())
+    return out
+
+
+def _rows(device: int, t, name: str, dtype):
+    """(address, elements between tokens, tokens, heads, head_dim) of [tokens, heads, head_dim] with each
+    token's heads contiguous and any stride between tokens."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: dtype {t.dtype} is not {dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
     if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens, heads, head_dim]")
-    if t.numel() and not t[0].is_contiguous():
+    n, heads, d = t.shape
+    st, sh, sd = t.stride()
+    if n and ((sd != 1 and d > 1) or (sh != d and heads > 1)):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-
-
-def _token_stride(t: torch.Tensor) -> int:
-    """Elements between two tokens (of a single one: its own size, its stride means nothing)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return t.data_ptr(), st if n > 1 else heads * d, n, heads, d     # a single token's stride means nothing
 
 
 def _need_scales(code: int, k_scale, v_scale, num_kv_heads: int) -> None:
-    """FP8 scales: float32, one per tensor or one per KV head, K and V alike."""
-    if code not in (PA_FP8_E4M3, PA_FP8_E4M3_PER_HEAD):
+    """An FP8 cache has float32 scales for K and V, both one per tensor or both one per KV head."""
+    if code < PA_FP8_E4M3:
         return
     want = num_kv_heads if code == PA_FP8_E4M3_PER_HEAD else 1
     for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        _need(t, n, (torch.float32,))
+        if t is None:
+            raise TypeError(f"{n}: an FP8 cache needs its scales")
         if t.numel() != want:
             raise ValueError(f"{n}: {t.numel()} scales where {want} are expected")
 
 
-def _need_workspace(workspace) -> None:
-    if workspace is not None:
-        _need(workspace, "workspace", (torch.uint8,))
-        if workspace.numel() < 256:
-            raise ValueError("workspace: at least 256 bytes")
-
-
-def _same_device(first: torch.Tensor, **others) -> None:
-    for n, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{n} is on {t.device}, not on {first.device}")
-
-
-def _on(t: torch.Tensor):
-    """The tensor's device as the current one: the library works on the current device, and the
-    default stream is the current stream of that device."""
-    return torch.cuda.device(t.device)
+def _invoke(what: str, device: int, stream, fn, *args) -> None:
+    """fn(*args, stream) with the tensors' device current; the default stream is that device's current one."""
+    raw = _raw_stream(device) if stream is None else stream.cuda_stream
+    if device == torch.cuda.current_device():
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, raw)
+    if status != PA_OK:
+        raise PagedAttentionError(status, what)
 
 
 def _cache_code(cache, k_scale, num_kv_heads: int) -> int:
@@ -286,14 +315,13 @@ def pa_rope_table(cos_sin, freqs, attention: float = 1.0, stream=None):
     """Table of a set of frequencies (host float64 [rot / 2]): cos_sin float32 [max_positions, rot],
     cosines then sines of position x frequency, both times attention."""
     import numpy as np
-    _need(cos_sin, "cos_sin", (torch.float32,))
-    f = np.ascontiguousarray(np.asarray(freqs, dtype=np.float64))
+    device = _device_of(cos_sin, "cos_sin")
+    ptr, = _pointers(device, (cos_sin, "cos_sin", _F32))
+    f = np.ascontiguousarray(freqs, dtype=np.float64)
     if cos_sin.dim() != 2 or f.ndim != 1 or cos_sin.shape[1] != 2 * f.size:
         raise ValueError("cos_sin must be [max_positions, 2 * len(freqs)]")
-    with _on(cos_sin):
-        st = _lib().pa_rope_table(_ptr(cos_sin), cos_sin.shape[0], cos_sin.shape[1], f.ctypes.data, float(attention),
-                                  _stream(stream))
-    _check(st, "pa_rope_table")
+    _invoke("pa_rope_table", device, stream, _lib().pa_rope_table, ptr, cos_sin.shape[0], cos_sin.shape[1],
+            f.ctypes.data, attention)
 
 
 def pa_rope_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, interleaved: bool = False,
@@ -301,33 +329,29 @@ def pa_rope_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions,
     """Slot write with rotary positions: q_out [T, H_q, 128] = q turned by positions[T] (int64), k [T, H_kv, 128]
     turned and v stored at slot_mapping[T] (int64).  q, k and v may be views of one projection (the heads of a
     token contiguous, any stride between tokens); cos_sin float32 [max_positions, rot] as pa_rope_table builds it."""
-    for t, n in ((q, "q"), (k, "k"), (v, "v"), (q_out, "q_out")):
-        _need_rows(t, n, (torch.bfloat16, torch.float16))
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _need(t, n, tuple(_DTYPE))
-    _need(slot_mapping, "slot_mapping", (torch.int64,))
-    _need(positions, "positions", (torch.int64,))
-    _need(cos_sin, "cos_sin", (torch.float32,))
-    T, Hq, d = q.shape
-    H = k.shape[1]
-    nb, H2, bs, d2 = k_cache.shape
-    if (q_out.shape != q.shape or k.shape != (T, H, d) or v.shape != k.shape or v_cache.shape != k_cache.shape or
-            H2 != H or d2 != d or slot_mapping.shape != (T,) or positions.shape != (T,) or cos_sin.dim() != 2):
+    device = _device_of(q, "q")
+    dt = q.dtype
+    if dt not in _16BIT:
+        raise TypeError(f"q: dtype {dt} not in {_16BIT}")
+    po, so, To, Ho, do = _rows(device, q_out, "q_out", dt)
+    pq, sq, T, Hq, d = _rows(device, q, "q", dt)
+    pk, sk, Tk, H, dk = _rows(device, k, "k", dt)
+    pv, sv, Tv, Hv, dv = _rows(device, v, "v", dt)
+    kc, vc, slots, pos, table, ks, vs, ws = _pointers(
+        device, (k_cache, "k_cache", _CACHE), (v_cache, "v_cache", (k_cache.dtype,)),
+        (slot_mapping, "slot_mapping", _I64), (positions, "positions", _I64), (cos_sin, "cos_sin", _F32),
+        (k_scale, "k_scale", _F32), (v_scale, "v_scale", _F32), (workspace, "workspace", _U8))
+    nb, Hc, bs, dc = shape = k_cache.shape
+    max_positions, rot = cos_sin.shape
+    if ((To, Ho, do) != (T, Hq, d) or (Tk, dk) != (T, d) or (Tv, Hv, dv) != (T, H, d) or v_cache.shape != shape or
+            (Hc, dc) != (H, d) or slot_mapping.shape != (T,) or positions.shape != (T,)):
         raise ValueError("shape mismatch")
-    if not (q.dtype == k.dtype == v.dtype == q_out.dtype) or v_cache.dtype != k_cache.dtype:
-        raise TypeError("q, k, v and q_out must have one type, and the caches one")
+    if workspace is not None and workspace.numel() < 256:
+        raise ValueError("workspace: at least 256 bytes")
     code = _cache_code(k_cache, k_scale, H)
     _need_scales(code, k_scale, v_scale, H)
-    _need_workspace(workspace)
-    _same_device(q, q_out=q_out, k=k, v=v, k_cache=k_cache, v_cache=v_cache, slot_mapping=slot_mapping,
-                 positions=positions, cos_sin=cos_sin, k_scale=k_scale, v_scale=v_scale, workspace=workspace)
-    with _on(q):
-        st = _lib().pa_rope_and_cache(_ptr(q_out), _token_stride(q_out), _ptr(q), _token_stride(q), _ptr(k),
-                                      _token_stride(k), _ptr(v), _token_stride(v), _ptr(k_cache), _ptr(v_cache),
-                                      _ptr(slot_mapping), _ptr(positions), _ptr(cos_sin), cos_sin.shape[0],
-                                      cos_sin.shape[1], int(bool(interleaved)), T, Hq, H, d, bs, nb, _DTYPE[q.dtype],
-                                      code, _ptr(k_scale), _ptr(v_scale), _ptr(workspace), _stream(stream))
-    _check(st, "pa_rope_and_cache")
+    _invoke("pa_rope_and_cache", device, stream, _lib().pa_rope_and_cache, po, so, pq, sq, pk, sk, pv, sv, kc, vc, slots,
+            pos, table, max_positions, rot, 1 if interleaved else 0, T, Hq, H, d, bs, nb, _DTYPE[dt], code, ks, vs, ws)
 
 
 def pa_decode(out, q, k_cache, v_cache, block_tables, seq_lens, scale, workspace, k_scale=None, v_scale=None,
@@ -355,34 +379,25 @@ def pa_decode_weights(out, weights_out, q, k_cache, v_cache, block_tables, seq_l
                       k_scale=None, v_scale=None, stream=None):
     """pa_decode that also writes weights_out [B, H_kv, >= tokens of the table] (float32) = weights_in (or
     zeros) + the step's softmax weights summed over each group's query heads; weights_in may be weights_out."""
-    _need(q, "q", (torch.bfloat16, torch.float16))
-    _need(out, "out", (q.dtype,))
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _need(t, n, tuple(_DTYPE))
-    _need(block_tables, "block_tables", (torch.int32,))
-    _need(seq_lens, "seq_lens", (torch.int32,))
-    _need(workspace, "workspace", (torch.uint8,))
-    _need(weights_out, "weights_out", (torch.float32,))
-    if weights_in is not None:
-        _need(weights_in, "weights_in", (torch.float32,))
-    B, Hq, d = q.shape
-    nb, Hkv, bs, _ = k_cache.shape
-    if (out.shape != q.shape or v_cache.shape != k_cache.shape or block_tables.dim() != 2 or
-            block_tables.shape[0] != B or seq_lens.shape != (B,) or weights_out.dim() != 3 or
-            weights_out.shape[:2] != (B, Hkv) or (weights_in is not None and weights_in.shape != weights_out.shape)):
+    device = _device_of(q, "q")
+    po, pw, pi, pq, kc, vc, bt, sl, ks, vs, ws = _pointers(
+        device, (out, "out", (q.dtype,)), (weights_out, "weights_out", _F32), (weights_in, "weights_in", _F32),
+        (q, "q", _16BIT), (k_cache, "k_cache", _CACHE), (v_cache, "v_cache", (k_cache.dtype,)),
+        (block_tables, "block_tables", _I32), (seq_lens, "seq_lens", _I32), (k_scale, "k_scale", _F32),
+        (v_scale, "v_scale", _F32), (workspace, "workspace", _U8))
+    if pw is None or po is None or ws is None:
+        raise TypeError("out, weights_out and workspace are needed")
+    B, Hq, d = shape = q.shape
+    nb, Hkv, bs, _ = cache = k_cache.shape
+    rows, width = block_tables.shape
+    wB, wH, stride = wshape = weights_out.shape
+    if (out.shape != shape or v_cache.shape != cache or rows != B or seq_lens.shape != (B,) or (wB, wH) != (B, Hkv) or
+            (weights_in is not None and weights_in.shape != wshape)):
         raise ValueError("shape mismatch")
-    if v_cache.dtype != k_cache.dtype:
-        raise TypeError("the caches must have one type")
     code = _cache_code(k_cache, k_scale, Hkv)
     _need_scales(code, k_scale, v_scale, Hkv)
-    _same_device(q, out=out, weights_out=weights_out, weights_in=weights_in, k_cache=k_cache, v_cache=v_cache,
-                 block_tables=block_tables, seq_lens=seq_lens, workspace=workspace, k_scale=k_scale, v_scale=v_scale)
-    with _on(q):
-        st = _lib().pa_decode_weights(_ptr(out), _ptr(weights_out), _ptr(weights_in), weights_out.shape[2], _ptr(q),
-                                      _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), block_tables.shape[1],
-                                      _ptr(seq_lens), B, Hq, Hkv, d, bs, nb, float(scale), _DTYPE[q.dtype], code,
-                                      _ptr(k_scale), _ptr(v_scale), _ptr(workspace), workspace.numel(), _stream(stream))
-    _check(st, "pa_decode_weights")
+    _invoke("pa_decode_weights", device, stream, _lib().pa_decode_weights, po, pw, pi, stride, pq, kc, vc, bt, width, sl, B,
+            Hq, Hkv, d, bs, nb, scale, _DTYPE[q.dtype], code, ks, vs, ws, workspace.numel())
 
 
 def pa_decode_append(out, q, k_new, v_new, slot_mapping, k_cache, v_cache, block_tables, seq_lens, scale, workspace,
@@ -514,32 +529,23 @@ def pa_evict(kept, seq_lens_out, weights_out, weights, k_cache, v_cache, block_t
     """Brings every sequence to at most budget tokens: the first sinks and last recent tokens stay, and for
     each KV head those of the largest weights ([B, H_kv, >= tokens of the table] float32) between them; their
     K and V rows move to the blocks of new_tables, their places before go to kept [B, H_kv, budget] (int32)."""
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _need(t, n, tuple(_DTYPE))
-    for t, n in ((weights, "weights"), (weights_out, "weights_out")):
-        _need(t, n, (torch.float32,))
-    for t, n in ((kept, "kept"), (seq_lens_out, "seq_lens_out"), (block_tables, "block_tables"), (seq_lens, "seq_lens"),
-                 (new_tables, "new_tables")):
-        _need(t, n, (torch.int32,))
-    nb, H, bs, d = k_cache.shape
-    B = seq_lens.shape[0]
-    if (v_cache.shape != k_cache.shape or weights.dim() != 3 or weights.shape[:2] != (B, H) or
-            weights_out.shape != weights.shape or kept.shape != (B, H, budget) or seq_lens.shape != (B,) or
-            seq_lens_out.shape != (B,) or block_tables.dim() != 2 or block_tables.shape[0] != B or
-            new_tables.dim() != 2 or new_tables.shape[0] != B):
+    device = _device_of(k_cache, "k_cache")
+    kc, vc, pw, pwo, pk, plo, bt, sl, nt, ws = _pointers(
+        device, (k_cache, "k_cache", _CACHE), (v_cache, "v_cache", (k_cache.dtype,)), (weights, "weights", _F32),
+        (weights_out, "weights_out", _F32), (kept, "kept", _I32), (seq_lens_out, "seq_lens_out", _I32),
+        (block_tables, "block_tables", _I32), (seq_lens, "seq_lens", _I32), (new_tables, "new_tables", _I32),
+        (workspace, "workspace", _U8))
+    nb, H, bs, d = shape = k_cache.shape
+    B, wH, stride = wshape = weights.shape
+    rows, width = block_tables.shape
+    new_rows, new_width = new_tables.shape
+    if (v_cache.shape != shape or wH != H or weights_out.shape != wshape or kept.shape != (B, H, budget) or
+            seq_lens.shape != (B,) or seq_lens_out.shape != (B,) or rows != B or new_rows != B):
         raise ValueError("shape mismatch")
-    if v_cache.dtype != k_cache.dtype:
-        raise TypeError("the caches must have one type")
-    _need_workspace(workspace)
-    _same_device(k_cache, v_cache=v_cache, weights=weights, weights_out=weights_out, kept=kept,
-                 seq_lens_out=seq_lens_out, block_tables=block_tables, seq_lens=seq_lens, new_tables=new_tables,
-                 workspace=workspace)
-    with _on(k_cache):
-        st = _lib().pa_evict(_ptr(kept), _ptr(seq_lens_out), _ptr(weights_out), _ptr(weights), weights.shape[2],
-                             _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens),
-                             _ptr(new_tables), new_tables.shape[1], B, int(budget), int(sinks), int(recent), H, d, bs,
-                             nb, _DTYPE[k_cache.dtype], _ptr(workspace), _stream(stream))
-    _check(st, "pa_evict")
+    if workspace is not None and workspace.numel() < 256:
+        raise ValueError("workspace: at least 256 bytes")
+    _invoke("pa_evict", device, stream, _lib().pa_evict, pk, plo, pwo, pw, stride, kc, vc, bt, width, sl, nt, new_width, B,
+            budget, sinks, recent, H, d, bs, nb, _DTYPE[k_cache.dtype], ws)
 
 
 class BlockPool:

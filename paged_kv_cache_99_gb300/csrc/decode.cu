@@ -322,8 +322,9 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kmap, const CUten
     uint4 pf_x = make_uint4(0, 0, 0, 0);
     // A cascade's private blocks are read once, beside partials (the prefix grid's and
     // this grid's) that the combine reads back: the stream leaves L2 first, the
-    // partials stay in it
-    const bool stream_first = p.cascade != 0;
+    // partials stay in it.  So do the scores of a decode with attention weights, which
+    // weights_kernel reads back (64 sequences of up to 4096, 12/2 heads: 49.5 -> 43.8 us)
+    const bool stream_first = Weights || p.cascade != 0;
     const uint64_t pol = stream_first ? l2_policy_evict_first() : 0ull;
     auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
         if (stream_first) tma_load_2d_hint(dst, map, x, y, bar, pol);
@@ -1231,53 +1232,105 @@ __global__ void __maxnreg__(112) combine_cascade_kernel(const DecodeParams p) {
 // unit, in the flattened order) and the units' final (M, 1 / L).  HBM- and L2-bound: a
 // score is 4 bytes per query head, written and read once, against 512 bytes of K and V (256
 // for FP8) per token and KV head; reading K a second time instead would cost 256 (128).
-// 16 lanes take a unit (one key each), a CTA 16 consecutive units at a time.
+// A warp takes up to kWeightUnits consecutive units (fewer while that keeps every warp at
+// work): it finds its place in the flattened order once, loads the heads' (M, 1 / L) once per (sequence, KV head), and then only streams, a
+// key per lane with kKeys of them in flight (their scores are contiguous).
+constexpr int kWeightUnits = 16;
+
 template <int Pitch>
 __global__ void __launch_bounds__(256) weights_kernel(const DecodeParams p) {
+    constexpr int kKeys = Pitch <= 4 ? 4 : 2;    // keys of a lane in flight
     __shared__ int pre_sum[kCombineScanSeqs + 1];
     __shared__ int warp_sum[8];
     grid_launch_dependents();
     const int B = p.num_seqs;
-    const int UH = p.num_kv_heads * p.head_groups;
+    const int HG = p.head_groups;
+    const int UH = p.num_kv_heads * HG;
     const int* cum = pre_sum;
     if (B <= kCombineScanSeqs) combine_block_prefix(p, pre_sum, warp_sum);
     else cum = p.plan;
     grid_dependency_wait();
     const int T = cum[B];
     if (T > p.score_units) return;               // recorded by the decode grid
-    const int F = T / p.head_groups;             // units of KV heads
-    const int key = threadIdx.x & 15;
-    for (int f = blockIdx.x * 16 + (threadIdx.x >> 4); f < F; f += gridDim.x * 16) {
-        // sequence s with cum[s] <= f head_groups < cum[s + 1]
-        int lo = 0, hi = B;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (cum[mid] <= f * p.head_groups) lo = mid; else hi = mid;
+    const int F = T / HG;                        // units of KV heads
+    const int lane = threadIdx.x & 31;
+    const int warps = gridDim.x * 8;
+    const int take = min(kWeightUnits, ((F + warps - 1) / warps + 1) & ~1);
+    for (long long f0 = (static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * take; f0 < F;
+         f0 += static_cast<long long>(warps) * take) {
+        int f = static_cast<int>(f0);
+        const int f1 = min(F, f + take);
+        // sequence s with cum[s] <= f HG < cum[s + 1]
+        int s = 0, hi = B;
+        while (hi - s > 1) {
+            const int mid = (s + hi) >> 1;
+            if (cum[mid] <= f * HG) s = mid; else hi = mid;
         }
-        const int first = cum[lo], nb = (cum[lo + 1] - first) / UH;
-        const int rem = f - first / p.head_groups;
-        const int h = rem / nb, j = rem % nb;
-        const int t = j * kBlockSize + key;
-        float w = 0.f;
-        for (int hg = 0; hg < p.head_groups; ++hg) {
-            const int uh = h * p.head_groups + hg;
-            const float* sc = p.scores + (static_cast<size_t>(first + uh * nb + j) * kBlockSize + key) * Pitch;
-            const float* um = p.unit_ml + static_cast<size_t>(lo * UH + uh) * 16;
-            const int live = p.group - hg * kHeadsPerGroup;      // heads of this unit
-            float x[Pitch], m[Pitch], r[Pitch];
+        int first = cum[s], nb = (cum[s + 1] - first) / UH;
+        int h = (f - first / HG) / nb, j = (f - first / HG) % nb;
+        while (true) {
+            // units [j, je) of (s, h)
+            const int je = min(nb, j + f1 - f);
+            const int end = min(je * kBlockSize, min(p.seq_lens[s], p.max_blocks * p.block_size));
+            const size_t at = (static_cast<size_t>(s) * p.num_kv_heads + h) * p.weight_stride;
+            for (int t0 = j * kBlockSize + lane; t0 - lane < end; t0 += 32 * kKeys) {
+                float w[kKeys];
 #pragma unroll
-            for (int e = 0; e < Pitch; e += 2) {
-                *reinterpret_cast<float2*>(x + e) = __ldcg(reinterpret_cast<const float2*>(sc + e));
-                *reinterpret_cast<float2*>(m + e) = __ldcg(reinterpret_cast<const float2*>(um + e));
-                *reinterpret_cast<float2*>(r + e) = __ldcg(reinterpret_cast<const float2*>(um + 8 + e));
+                for (int i = 0; i < kKeys; ++i)
+                    w[i] = p.weights_in && t0 + 32 * i < end ? __ldcg(p.weights_in + at + t0 + 32 * i) : 0.f;
+                for (int hg = 0; hg < HG; ++hg) {
+                    const int uh = h * HG + hg;
+                    const float* um = p.unit_ml + static_cast<size_t>(s * UH + uh) * 16;
+                    const float* sc = p.scores + static_cast<size_t>(first + uh * nb) * (kBlockSize * Pitch);
+                    const int live = p.group - hg * kHeadsPerGroup;      // heads of this unit
+                    float m[Pitch], r[Pitch], x[kKeys][Pitch];
+#pragma unroll
+                    for (int i = 0; i < kKeys; ++i) {
+                        const float* q = sc + static_cast<size_t>(min(t0 + 32 * i, end - 1)) * Pitch;
+                        if constexpr (Pitch % 4 == 0) {
+#pragma unroll
+                            for (int e = 0; e < Pitch; e += 4) {
+                                const float4 v = __ldcg(reinterpret_cast<const float4*>(q + e));
+                                x[i][e] = v.x;
+                                x[i][e + 1] = v.y;
+                                x[i][e + 2] = v.z;
+                                x[i][e + 3] = v.w;
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < Pitch; e += 2) {
+                                const float2 v = __ldcg(reinterpret_cast<const float2*>(q + e));
+                                x[i][e] = v.x;
+                                x[i][e + 1] = v.y;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < Pitch; ++e) {
+                        m[e] = um[e];
+                        r[e] = e < live ? um[8 + e] : 0.f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < kKeys; ++i)
+#pragma unroll
+                        for (int e = 0; e < Pitch; ++e)
+                            if (e < live) w[i] = fmaf(ex2_approx(x[i][e] - m[e]), r[e], w[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < kKeys; ++i)
+                    if (t0 + 32 * i < end) p.weights_out[at + t0 + 32 * i] = w[i];
             }
-#pragma unroll
-            for (int e = 0; e < Pitch; ++e)
-                if (e < live) w += exp2f(x[e] - m[e]) * r[e];
-        }
-        if (t < min(p.seq_lens[lo], p.max_blocks * p.block_size)) {
-            const size_t at = (static_cast<size_t>(lo) * p.num_kv_heads + h) * p.weight_stride + t;
-            p.weights_out[at] = (p.weights_in ? p.weights_in[at] : 0.f) + w;
+            f += je - j;
+            if (f >= f1) break;
+            j = 0;
+            if (++h == p.num_kv_heads) {
+                h = 0;
+                do {
+                    ++s;
+                } while (cum[s + 1] == cum[s]);
+                first = cum[s];
+                nb = (cum[s + 1] - first) / UH;
+            }
         }
     }
 }
@@ -1424,10 +1477,10 @@ cudaError_t launch_combine(bool out_bf16, bool fp8_cache, const DecodeParams& p,
 }
 
 cudaError_t launch_weights(const DecodeParams& p, int sms, cudaStream_t stream) {
-    // 16 units per CTA and turn, up to the resident CTAs
+    // 8 warps of at least two units per CTA, up to the resident CTAs
     const long long per_seq = (static_cast<long long>(p.max_blocks) * p.block_size + kBlockSize - 1) / kBlockSize;
     const long long want = (static_cast<long long>(p.num_seqs) * p.num_kv_heads * per_seq + 15) / 16;
-    const long long cap = 6ll * sms;
+    const long long cap = 4ll * sms;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(want < cap ? want : cap));
     cfg.blockDim = dim3(256);

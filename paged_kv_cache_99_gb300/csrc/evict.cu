@@ -26,46 +26,48 @@ constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;                  // 11 bits of a key at a time: 11 + 11 + 10
 constexpr int kMaxCluster = 8;
-// tokens of one CTA's part of a row that fit its shared memory beside the histograms
-constexpr int kMaxStaged = 48 * 1024;
+constexpr uint32_t kNone = 0u;               // key of a place past the end: never kept
+constexpr uint32_t kSure = 0xffffffffu;      // key of a token that stays whatever its weight
 
 // Weights in an order of unsigned integers: larger weight, larger key; -0 counts as 0,
-// NaN lies below everything (even -inf).
+// NaN (1) lies below everything (-inf is 0x007fffff), +inf is 0xff800000.
 __device__ __forceinline__ uint32_t key_of(uint32_t bits) {
-    if ((bits & 0x7fffffffu) > 0x7f800000u) return 0u;
+    if ((bits & 0x7fffffffu) > 0x7f800000u) return 1u;
     if (bits == 0x80000000u) bits = 0u;
     return bits & 0x80000000u ? ~bits : bits | 0x80000000u;
 }
 
-// One cluster per (sequence, KV head), its CTAs taking equal parts of the row.  Staged:
-// each CTA reads its part once into shared memory (the weights may then be compacted in
-// place); rows too long for that are read from L2 in every pass.
+// One cluster per (sequence, KV head), its CTAs taking equal parts of the row and their
+// warps contiguous segments.  With Keys > 0 a thread holds the (at most Keys) weights of
+// its places and their keys in registers: the row is read once, and may be compacted in
+// place.  Keys = 0 takes rows of any length and reads them again (from L2) in each pass.
 //
-// Radix select: a histogram of the top 11 bits of the keys (shared-memory atomics, the
-// CTAs' histograms added up through distributed shared memory) gives the bin that holds
-// the k-th largest; two more passes over the keys in that bin give the key itself and
-// how many of the keys equal to it are kept.  Latency-bound: three passes over a few
-// thousand keys per CTA, so a row is spread over more CTAs while the device has room.
-template <bool Staged>
+// Radix select: a histogram of the top 11 bits of the keys (shared-memory atomics; the
+// CTAs' histograms are added up in the first one through distributed shared memory, which
+// hands the result to all) gives the bin that holds the k-th largest; two more passes over
+// the keys of that bin give the key itself and how many of the keys equal to it stay.  A
+// bin that stays as a whole ends the search early: 22 bits tell most weights apart.
+// Bound by instruction issue and barrier latency (the row itself is small): keys are
+// computed once, a pass costs about four instructions per key.
+template <int Keys>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p) {
-    extern __shared__ uint32_t staged[];
-    __shared__ unsigned hist[kBins];
-    __shared__ unsigned total[kBins];
+    __shared__ alignas(16) unsigned hist[kBins];
+    __shared__ alignas(16) unsigned total[kBins];
     __shared__ int warp_sum[kSelWarps];
-    __shared__ int warp_gt[kSelWarps], warp_eq[kSelWarps];
-    __shared__ int part_gt[kMaxCluster], part_eq[kMaxCluster];
-    __shared__ unsigned found_digit;
-    __shared__ int found_left;
+    __shared__ int warp_sure[kSelWarps], warp_eq[kSelWarps];
+    __shared__ int part_sure[kMaxCluster], part_eq[kMaxCluster];
+    __shared__ int found[3];                     // digit, tokens still to take, tokens of that bin
 
     cg::cluster_group cluster = cg::this_cluster();
     const int parts = static_cast<int>(cluster.num_blocks());
     const int rank = static_cast<int>(cluster.block_rank());
-    grid_dependency_wait();
-    grid_launch_dependents();
-    if (parts > 1) cluster.sync();               // every CTA runs before its shared memory is written
     const int row = blockIdx.x / parts;
     const int s = row / p.num_kv_heads, h = row % p.num_kv_heads;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    *reinterpret_cast<uint4*>(hist + 4 * tid) = make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(total + 4 * tid) = make_uint4(0, 0, 0, 0);
+    grid_dependency_wait();
+    grid_launch_dependents();
 
     const int cap = p.max_blocks << p.block_shift;
     const int len = p.seq_lens[s];
@@ -75,154 +77,202 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
         p.seq_lens_out[s] = left;
         if (len > cap && p.status) atomicOr(p.status, kDevErrRange);
     }
-    const int per = ((n + parts - 1) / parts + 3) & ~3;
-    const int t0 = min(n, rank * per), t1 = min(n, t0 + per);
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(p.weights) + static_cast<size_t>(row) * p.weight_stride;
-    if (Staged) {
-        const uint4* src = reinterpret_cast<const uint4*>(w + t0);
-        for (int i = tid; i < (t1 - t0) / 4; i += kSelThreads) reinterpret_cast<uint4*>(staged)[i] = src[i];
-        for (int i = ((t1 - t0) & ~3) + tid; i < t1 - t0; i += kSelThreads) staged[i] = w[t0 + i];
-    }
-    auto bits_at = [&](int t) -> uint32_t { return Staged ? staged[t - t0] : w[t]; };
-
-    // the tokens to choose from, and how many of them stay
+    // the tokens to choose from: [lo, hi)
     const int lo = min(n, p.sinks), hi = max(lo, n - p.recent);
-    int k = left - lo - (n - hi);
-    uint32_t threshold = 0u;                     // keys above it stay ...
-    int take_eq = 0x7fffffff;                    // ... and this many of those equal to it
+    const int per = (n + parts - 1) / parts;
+    const int t0 = min(n, rank * per), t1 = min(n, t0 + per);
+    const int seg = ((per + kSelWarps - 1) / kSelWarps + 31) & ~31;
+    const int w0 = min(t1, t0 + warp * seg), w1 = min(t1, w0 + seg);
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(p.weights) + static_cast<size_t>(row) * p.weight_stride;
+    auto classify = [&](int t, uint32_t bits) -> uint32_t {
+        return t >= w1 ? kNone : t < lo || t >= hi ? kSure : key_of(bits);
+    };
+    uint32_t raw[Keys > 0 ? Keys : 1], key[Keys > 0 ? Keys : 1];
+    if constexpr (Keys > 0) {
+#pragma unroll
+        for (int i = 0; i < Keys; ++i) raw[i] = w0 + 32 * i + lane < w1 ? w[w0 + 32 * i + lane] : 0u;
+#pragma unroll
+        for (int i = 0; i < Keys; ++i) key[i] = classify(w0 + 32 * i + lane, raw[i]);
+    }
+    // f(key, weight's bits, place) for the warp's places, 32 at a time
+    auto each = [&](auto&& f) {
+        if constexpr (Keys > 0) {
+#pragma unroll
+            for (int i = 0; i < Keys; ++i)
+                if (32 * i < seg) f(key[i], raw[i], w0 + 32 * i + lane);
+        } else {
+#pragma unroll 1
+            for (int b = w0; b < w1; b += 32) {
+                const uint32_t x = b + lane < w1 ? w[b + lane] : 0u;
+                f(classify(b + lane, x), x, b + lane);
+            }
+        }
+    };
+    // every CTA runs, its histograms cleared, before another adds to them
+    if (parts > 1) cluster.sync();
+    else __syncthreads();
+
+    int k = left - lo - (n - hi);                // tokens of [lo, hi) that stay
+    uint32_t threshold = kNone;                  // keys above it stay ...
+    int take_eq = 0;                             // ... and this many of those equal to it
     if (n > p.budget) {
-        threshold = 0xffffffffu;
-        take_eq = 0;
+        threshold = kSure - 1u;
         if (k > 0) {
             uint32_t prefix = 0u;
-            const int a = max(t0, lo), b = min(t1, hi);
 #pragma unroll 1
             for (int pass = 0; pass < 3; ++pass) {
-                const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
-                const int above = pass == 0 ? 32 : (pass == 1 ? 21 : 10);    // bits fixed so far end here
-                for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0u;
-                __syncthreads();
-                for (int t = a + tid; t < b; t += kSelThreads) {
-                    const uint32_t key = key_of(bits_at(t));
-                    if (pass == 0 || (key >> above) == prefix)
-                        atomicAdd(&hist[(key >> shift) & (pass == 2 ? 1023u : 2047u)], 1u);
-                }
-                if (parts > 1) {
-                    // the cluster's histogram: each CTA adds up its share of the bins for all
-                    cluster.sync();
-                    const int share = kBins / parts;
-                    for (int i = tid; i < share; i += kSelThreads) {
-                        const int bin = rank * share + i;
-                        unsigned sum = 0u;
-                        for (int r = 0; r < parts; ++r) sum += *cluster.map_shared_rank(&hist[bin], r);
-                        for (int r = 0; r < parts; ++r) *cluster.map_shared_rank(&total[bin], r) = sum;
-                    }
-                    cluster.sync();
+                if (pass == 0) {
+                    each([&](uint32_t x, uint32_t, int) {
+                        if (x - 1u < kSure - 1u) atomicAdd(&hist[x >> 21], 1u);
+                    });
+                } else if (pass == 1) {
+                    each([&](uint32_t x, uint32_t, int) {
+                        if ((x >> 21) == prefix && x != kNone) atomicAdd(&hist[(x >> 10) & 2047u], 1u);
+                    });
                 } else {
-                    __syncthreads();
+                    each([&](uint32_t x, uint32_t, int) {
+                        if ((x >> 10) == prefix && x != kNone) atomicAdd(&hist[x & 1023u], 1u);
+                    });
                 }
-                // the bin in which the k-th largest lies: a scan from the top, four bins a thread
-                const unsigned* from = parts > 1 ? total : hist;
-                const int top = kBins - 1 - 4 * tid;
-                const int c0 = from[top], c1 = from[top - 1], c2 = from[top - 2], c3 = from[top - 3];
-                int incl = c0 + c1 + c2 + c3;
-                const int own = incl;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, incl, o);
-                    if (lane >= o) incl += y;
-                }
-                if (lane == 31) warp_sum[warp] = incl;
                 __syncthreads();
-                for (int v = 0; v < warp; ++v) incl += warp_sum[v];
-                int before = incl - own;
-                if (before < k && k <= incl) {
-                    int d = top;
-                    if (before + c0 < k) {
-                        before += c0;
-                        --d;
-                        if (before + c1 < k) {
-                            before += c1;
+                // a thread owns four bins, from the top down: it adds them to the cluster's
+                // (or takes them as they are) and clears them for the next pass
+                const int bin = kBins - 4 - 4 * tid;
+                uint4 c = *reinterpret_cast<uint4*>(hist + bin);
+                *reinterpret_cast<uint4*>(hist + bin) = make_uint4(0, 0, 0, 0);
+                if (parts > 1) {
+                    unsigned* to = cluster.map_shared_rank(total, 0) + bin;
+                    if (c.x) atomicAdd(to, c.x);
+                    if (c.y) atomicAdd(to + 1, c.y);
+                    if (c.z) atomicAdd(to + 2, c.z);
+                    if (c.w) atomicAdd(to + 3, c.w);
+                    cluster.sync();
+                    if (rank == 0) {
+                        c = *reinterpret_cast<uint4*>(total + bin);
+                        *reinterpret_cast<uint4*>(total + bin) = make_uint4(0, 0, 0, 0);
+                    }
+                }
+                if (rank == 0) {
+                    // the bin in which the k-th largest lies: a scan over the threads
+                    const int own = static_cast<int>(c.x + c.y + c.z + c.w);
+                    int incl = own;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                        if (lane >= o) incl += y;
+                    }
+                    if (lane == 31) warp_sum[warp] = incl;
+                    __syncthreads();
+                    int other = lane < warp ? warp_sum[lane & (kSelWarps - 1)] : 0;
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) other += __shfl_xor_sync(0xffffffffu, other, o);
+                    int before = incl - own + other;
+                    if (before < k && k <= before + own) {
+                        int d = bin + 3, in = static_cast<int>(c.w);
+                        if (before + in < k) {
+                            before += in;
                             --d;
-                            if (before + c2 < k) {
-                                before += c2;
+                            in = static_cast<int>(c.z);
+                            if (before + in < k) {
+                                before += in;
                                 --d;
+                                in = static_cast<int>(c.y);
+                                if (before + in < k) {
+                                    before += in;
+                                    --d;
+                                    in = static_cast<int>(c.x);
+                                }
                             }
                         }
+                        for (int r = 0; r < parts; ++r) {
+                            int* to = parts > 1 ? cluster.map_shared_rank(found, r) : found;
+                            to[0] = d;
+                            to[1] = k - before;
+                            to[2] = in;
+                        }
                     }
-                    found_digit = static_cast<unsigned>(d);
-                    found_left = k - before;
                 }
-                __syncthreads();
-                prefix = (prefix << (pass == 2 ? 10 : 11)) | found_digit;
-                k = found_left;
+                if (parts > 1) cluster.sync();
+                else __syncthreads();
+                const int bits = pass == 2 ? 10 : 11;
+                prefix = (prefix << bits) | static_cast<uint32_t>(found[0]);
+                k = found[1];
+                if (pass == 2) {
+                    threshold = prefix;
+                    take_eq = k;
+                } else if (k == found[2]) {
+                    // the whole bin stays: everything above the key before its first
+                    threshold = prefix == 0u ? kNone : (prefix << (pass == 0 ? 21 : 10)) - 1u;
+                    break;
+                }
             }
-            threshold = prefix;
-            take_eq = k;
         }
     }
-    __syncthreads();
 
-    // counts of the tokens that surely stay and of those equal to the threshold: per warp
-    // (each a contiguous segment), per CTA, per cluster
-    const int seg = ((t1 - t0 + kSelWarps - 1) / kSelWarps + 31) & ~31;
-    const int w0 = min(t1, t0 + warp * seg), w1 = min(t1, w0 + seg);
-    auto classify = [&](int t, bool& sure, bool& eq) {
-        const bool in = t < w1;
-        const bool fixed = in && (t < lo || t >= hi);
-        const uint32_t key = in && !fixed ? key_of(bits_at(t)) : 0u;
-        sure = fixed || (in && key > threshold);
-        eq = in && !fixed && key == threshold;
-    };
+    // counts of the tokens that surely stay and of those equal to the threshold: per warp,
+    // per CTA, per cluster
     int n_sure = 0, n_eq = 0;
-    for (int b = w0; b < w1; b += 32) {
-        bool sure, eq;
-        classify(b + lane, sure, eq);
-        n_sure += __popc(__ballot_sync(0xffffffffu, sure));
-        n_eq += __popc(__ballot_sync(0xffffffffu, eq));
-    }
+    each([&](uint32_t x, uint32_t, int) {
+        n_sure += x > threshold;
+        n_eq += x == threshold;
+    });
+    if (take_eq == 0) n_eq = 0;
+    n_sure = __reduce_add_sync(0xffffffffu, n_sure);
+    n_eq = __reduce_add_sync(0xffffffffu, n_eq);
     if (lane == 0) {
-        warp_gt[warp] = n_sure;
+        warp_sure[warp] = n_sure;
         warp_eq[warp] = n_eq;
     }
     __syncthreads();
-    if (tid < parts) {
-        int g = 0, e = 0;
-        for (int v = 0; v < kSelWarps; ++v) {
-            g += warp_gt[v];
-            e += warp_eq[v];
-        }
-        *cluster.map_shared_rank(&part_gt[rank], tid) = g;
-        *cluster.map_shared_rank(&part_eq[rank], tid) = e;
-    }
-    // after this no CTA touches another's shared memory, and every weight of the row has
-    // been read (staged rows): places and weights can be written
-    cluster.sync();
     int sure_before = 0, eq_before = 0;
-    for (int r = 0; r < rank; ++r) {
-        sure_before += part_gt[r];
-        eq_before += part_eq[r];
+    if (parts > 1) {
+        if (tid < parts) {
+            int g = 0, e = 0;
+            for (int v = 0; v < kSelWarps; ++v) {
+                g += warp_sure[v];
+                e += warp_eq[v];
+            }
+            *cluster.map_shared_rank(&part_sure[rank], tid) = g;
+            *cluster.map_shared_rank(&part_eq[rank], tid) = e;
+        }
+        // after this no CTA touches another's shared memory, and (Keys > 0) every weight of
+        // the row has been read: places and weights can be written
+        cluster.sync();
+        for (int r = 0; r < rank; ++r) {
+            sure_before += part_sure[r];
+            eq_before += part_eq[r];
+        }
     }
     for (int v = 0; v < warp; ++v) {
-        sure_before += warp_gt[v];
+        sure_before += warp_sure[v];
         eq_before += warp_eq[v];
     }
     int32_t* kept = p.kept + static_cast<size_t>(row) * p.budget;
     uint32_t* wo = reinterpret_cast<uint32_t*>(p.weights_out) + static_cast<size_t>(row) * p.weight_stride;
     const unsigned below = (1u << lane) - 1u;
-    for (int b = w0; b < w1; b += 32) {
-        bool sure, eq;
-        const int t = b + lane;
-        classify(t, sure, eq);
-        const unsigned ms = __ballot_sync(0xffffffffu, sure), me = __ballot_sync(0xffffffffu, eq);
-        const int eq_rank = eq_before + __popc(me & below);
-        if (sure || (eq && eq_rank < take_eq)) {
-            const int at = sure_before + __popc(ms & below) + min(eq_rank, take_eq);
-            kept[at] = t;
-            wo[at] = bits_at(t);
-        }
-        sure_before += __popc(ms);
-        eq_before += __popc(me);
+    if (take_eq == 0) {
+        each([&](uint32_t x, uint32_t bits, int t) {
+            const unsigned ms = __ballot_sync(0xffffffffu, x > threshold);
+            if (x > threshold) {
+                const int at = sure_before + __popc(ms & below);
+                kept[at] = t;
+                wo[at] = bits;
+            }
+            sure_before += __popc(ms);
+        });
+    } else {
+        each([&](uint32_t x, uint32_t bits, int t) {
+            const bool sure = x > threshold, eq = x == threshold;
+            const unsigned ms = __ballot_sync(0xffffffffu, sure), me = __ballot_sync(0xffffffffu, eq);
+            const int eq_rank = eq_before + __popc(me & below);
+            if (sure || (eq && eq_rank < take_eq)) {
+                const int at = sure_before + __popc(ms & below) + min(eq_rank, take_eq);
+                kept[at] = t;
+                wo[at] = bits;
+            }
+            sure_before += __popc(ms);
+            eq_before += __popc(me);
+        });
     }
     // what the row no longer holds: weights of 0, places of -1
     for (int t = left + rank * kSelThreads + tid; t < n; t += parts * kSelThreads) wo[t] = 0u;
@@ -295,30 +345,21 @@ __global__ void __launch_bounds__(256) evict_copy_kernel(const EvictParams p, in
 
 }  // namespace
 
-// CTAs per row: as few as hold its weights in shared memory (Staged), then more while
-// the device has room and each has over 1024 tokens to look at.
-EvictPlan evict_plan(int num_seqs, int num_kv_heads, long long cap, int sms) {
-    const long long rows = static_cast<long long>(num_seqs) * num_kv_heads;
+// CTAs per row and weights per thread: parts of at most 4096 tokens (8 per thread)
+// while a cluster reaches, then 8192 and 16384; longer rows are read again in each pass.
+EvictPlan evict_plan(long long cap) {
     EvictPlan e;
     e.parts = 1;
-    while (e.parts < kMaxCluster && (cap > static_cast<long long>(e.parts) * kMaxStaged ||
-                                     (rows * e.parts * 2 <= 2ll * sms && cap > 2048ll * e.parts)))
-        e.parts *= 2;
-    e.staged = cap <= static_cast<long long>(e.parts) * kMaxStaged;
-    e.smem = e.staged ? static_cast<size_t>(((cap + e.parts - 1) / e.parts + 3) & ~3ll) * 4 : 0;
+    while (e.parts < kMaxCluster && cap > 4096ll * e.parts) e.parts *= 2;
+    const long long per = (cap + e.parts - 1) / e.parts;
+    e.keys = per <= 2048 ? 4 : per <= 4096 ? 8 : per <= 8192 ? 16 : per <= 16384 ? 32 : 0;
     return e;
-}
-
-cudaError_t evict_prepare() {
-    return cudaFuncSetAttribute(reinterpret_cast<const void*>(&evict_select_kernel<true>),
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxStaged * 4);
 }
 
 cudaError_t launch_evict_select(const EvictParams& p, const EvictPlan& plan, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(p.num_seqs) * p.num_kv_heads * plan.parts));
     cfg.blockDim = dim3(kSelThreads);
-    cfg.dynamicSmemBytes = plan.smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -329,8 +370,13 @@ cudaError_t launch_evict_select(const EvictParams& p, const EvictPlan& plan, cud
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return plan.staged ? cudaLaunchKernelEx(&cfg, evict_select_kernel<true>, p)
-                       : cudaLaunchKernelEx(&cfg, evict_select_kernel<false>, p);
+    switch (plan.keys) {
+        case 4: return cudaLaunchKernelEx(&cfg, evict_select_kernel<4>, p);
+        case 8: return cudaLaunchKernelEx(&cfg, evict_select_kernel<8>, p);
+        case 16: return cudaLaunchKernelEx(&cfg, evict_select_kernel<16>, p);
+        case 32: return cudaLaunchKernelEx(&cfg, evict_select_kernel<32>, p);
+    }
+    return cudaLaunchKernelEx(&cfg, evict_select_kernel<0>, p);
 }
 
 cudaError_t launch_evict_copy(const EvictParams& p, bool fp8, int max_left, int sms, cudaStream_t stream) {

@@ -26,7 +26,6 @@ struct DeviceState {
     size_t max_smem_optin = 0;
     bool decode_prepared[3][2][3][2][2] = {};
     bool chunk_prepared[3][2] = {};
-    bool evict_prepared = false;
 };
 
 std::mutex g_mu;
@@ -929,16 +928,8 @@ pa_status pa_evict(int32_t* kept, int32_t* seq_lens_out, float* weights_out, con
         return PA_ERR_UNSUPPORTED;
     DeviceState* st = device_state(nullptr);
     if (!st) return PA_ERR_CUDA;
-    const EvictPlan plan = evict_plan(num_seqs, num_kv_heads, cap, st->sms);
-    if (!plan.staged && weights_out == weights) return PA_ERR_UNSUPPORTED;
-    {
-        std::lock_guard<std::mutex> lock(g_mu);
-        if (!st->evict_prepared) {
-            cudaError_t e = evict_prepare();
-            if (e != cudaSuccess) return fail("cudaFuncSetAttribute(evict)", e);
-            st->evict_prepared = true;
-        }
-    }
+    const EvictPlan plan = evict_plan(cap);
+    if (plan.keys == 0 && weights_out == weights) return PA_ERR_UNSUPPORTED;
     EvictParams p;
     p.kept = kept;
     p.seq_lens_out = seq_lens_out;

@@ -268,12 +268,10 @@ struct EvictParams {
 
 struct EvictPlan {
     int parts;                        // CTAs per row
-    bool staged;                      // a CTA's part of the row fits its shared memory
-    size_t smem;
+    int keys;                         // weights a thread holds; 0: read again in each pass
 };
 
-EvictPlan evict_plan(int num_seqs, int num_kv_heads, long long cap, int sms);
-cudaError_t evict_prepare();
+EvictPlan evict_plan(long long cap);
 cudaError_t launch_evict_select(const EvictParams& p, const EvictPlan& plan, cudaStream_t stream);
 cudaError_t launch_evict_copy(const EvictParams& p, bool fp8, int max_left, int sms, cudaStream_t stream);
 

@@ -295,9 +295,11 @@ cudaError_t launch_rope_table(float* cos_sin, int max_positions, int rot_dim, co
 
 cudaError_t launch_rope_cache(RopeParams p, bool src_bf16, bool fp8, bool interleaved, int sms, cudaStream_t stream) {
     const int rows = p.num_q_heads + 2 * p.num_kv_heads;
-    // one row per thread group while that leaves the device's thread slots unfilled
-    const bool few = static_cast<long long>(p.num_tokens) * rows <= 256ll * sms;
-    p.groups = few ? rows : (rows + 3) / 4;
+    // one row per thread group up to a few waves of CTAs, where a call is as long as its
+    // chains of loads (1040 tokens of 64/8 heads: 12.7 us, with four rows 16.9); four rows
+    // beyond, for the loads in flight (16384 tokens of 32/8 heads: 64.0 us, with one 70.0)
+    const int per = static_cast<long long>(p.num_tokens) * rows <= 2048ll * sms ? 1 : 4;
+    p.groups = (rows + per - 1) / per;
     const long long ctas = (static_cast<long long>(p.num_tokens) * p.groups + 31) / 32;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
@@ -309,7 +311,7 @@ cudaError_t launch_rope_cache(RopeParams p, bool src_bf16, bool fp8, bool interl
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     void* args[] = {&p};
-    const void* fn = few ? rope_cache_fn<1>(src_bf16, fp8, interleaved) : rope_cache_fn<4>(src_bf16, fp8, interleaved);
+    const void* fn = per == 1 ? rope_cache_fn<1>(src_bf16, fp8, interleaved) : rope_cache_fn<4>(src_bf16, fp8, interleaved);
     return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
