@@ -503,7 +503,8 @@ PA_API pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int32_t* src
  * their order.  The j-th kept token of head h moves to place j of the new table: its K and
  * V rows are copied to block new_tables[s][j / block_size], offset j % block_size, and
  *   kept[s][h][j] = its place t before (j < left), -1 (left <= j < budget)
- *   weights_out[s][h][j] = weights[s][h][t] (j < left), 0 (left <= j < n), else as it was
+ *   weights_out[s][h][j] = weights[s][h][t] (j < left; -0 becomes 0, a NaN some NaN),
+ *                          0 (left <= j < n), else as it was
  *   seq_lens_out[s] = left.
  * The source blocks are only read (they may be shared with other sequences); the caller
  * frees the old table afterwards.  The copied keys keep the rotation of the positions they
@@ -512,7 +513,7 @@ PA_API pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int32_t* src
  *   weights        device, float32 [num_seqs][num_kv_heads][weight_stride] (pa_decode_weights
  *                  adds to it), 16-byte aligned; weight_stride a multiple of 4 and at least
  *                  max_blocks_per_seq * block_size
- *   weights_out    the same layout; may be weights itself (up to 131072 tokens of table:
+ *   weights_out    the same layout; may be weights itself (up to 393216 tokens of table:
  *                  beyond that PA_ERR_UNSUPPORTED), otherwise must not overlap it
  *   kept           device, int32 [num_seqs][num_kv_heads][budget]
  *   seq_lens_out   device, int32 [num_seqs]; not seq_lens itself

@@ -22,12 +22,9 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;                  // 11 bits of a key at a time: 11 + 11 + 10
 constexpr int kMaxCluster = 8;
-constexpr uint32_t kNone = 0u;               // key of a place past the end: never kept
-constexpr uint32_t kSure = 0xffffffffu;      // key of a token that stays whatever its weight
+constexpr int kMaxStaged = 48 * 1024;        // keys of a CTA's part of a row in shared memory
 
 // Weights in an order of unsigned integers: larger weight, larger key; -0 counts as 0,
 // NaN (1) lies below everything (-inf is 0x007fffff), +inf is 0xff800000.
@@ -37,24 +34,34 @@ __device__ __forceinline__ uint32_t key_of(uint32_t bits) {
     return bits & 0x80000000u ? ~bits : bits | 0x80000000u;
 }
 
+// The weight of a key (of -0: 0, of a NaN: a NaN).
+__device__ __forceinline__ uint32_t bits_of(uint32_t key) { return key & 0x80000000u ? key ^ 0x80000000u : ~key; }
+
 // One cluster per (sequence, KV head), its CTAs taking equal parts of the row and their
-// warps contiguous segments.  With Keys > 0 a thread holds the (at most Keys) weights of
-// its places and their keys in registers: the row is read once, and may be compacted in
-// place.  Keys = 0 takes rows of any length and reads them again (from L2) in each pass.
+// warps contiguous segments.  Staged: a CTA keeps the keys of its part in shared memory, so
+// that the row is read once and may be compacted in place (the weights are read back from
+// the keys).  Otherwise (rows too long for a cluster's shared memory) it is read again, from
+// L2, in each pass.
 //
 // Radix select: a histogram of the top 11 bits of the keys (shared-memory atomics; the
 // CTAs' histograms are added up in the first one through distributed shared memory, which
 // hands the result to all) gives the bin that holds the k-th largest; two more passes over
 // the keys of that bin give the key itself and how many of the keys equal to it stay.  A
 // bin that stays as a whole ends the search early: 22 bits tell most weights apart.
-// Bound by instruction issue and barrier latency (the row itself is small): keys are
-// computed once, a pass costs about four instructions per key.
-template <int Keys>
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p) {
+// Bound by the latency of loads, barriers and scans and by instruction issue (stamps in a
+// row of 4096 on one CTA: load 1.5 us, a pass 0.5 and its scan 0.4, counts and writes 1.0; a
+// cluster adds 1 us per exchange): keys are computed once, a pass costs three or four
+// instructions per key, and the keys live in shared memory rather than in registers so
+// that all rows of a batch of 320 are resident at once (registers: 22 us, three waves).
+template <int Threads, bool Staged>
+__global__ void __launch_bounds__(Threads, Threads == 1024 ? 1 : 1536 / Threads) evict_select_kernel(const EvictParams p) {
+    constexpr int kWarps = Threads / 32;
+    constexpr int kOwn = kBins / Threads;        // bins a thread owns
+    extern __shared__ uint4 staged[];            // keys of the CTA's part, from t0 on
     __shared__ alignas(16) unsigned hist[kBins];
     __shared__ alignas(16) unsigned total[kBins];
-    __shared__ int warp_sum[kSelWarps];
-    __shared__ int warp_sure[kSelWarps], warp_eq[kSelWarps];
+    __shared__ int warp_sum[kWarps];
+    __shared__ int warp_sure[kWarps], warp_eq[kWarps];
     __shared__ int part_sure[kMaxCluster], part_eq[kMaxCluster];
     __shared__ int found[3];                     // digit, tokens still to take, tokens of that bin
 
@@ -64,8 +71,10 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
     const int row = blockIdx.x / parts;
     const int s = row / p.num_kv_heads, h = row % p.num_kv_heads;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    *reinterpret_cast<uint4*>(hist + 4 * tid) = make_uint4(0, 0, 0, 0);
-    *reinterpret_cast<uint4*>(total + 4 * tid) = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < kBins / 4; i += Threads) {
+        reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
+        reinterpret_cast<uint4*>(total)[i] = make_uint4(0, 0, 0, 0);
+    }
     grid_dependency_wait();
     grid_launch_dependents();
 
@@ -79,33 +88,42 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
     }
     // the tokens to choose from: [lo, hi)
     const int lo = min(n, p.sinks), hi = max(lo, n - p.recent);
-    const int per = (n + parts - 1) / parts;
+    const int per = ((n + parts - 1) / parts + 3) & ~3;
     const int t0 = min(n, rank * per), t1 = min(n, t0 + per);
-    const int seg = ((per + kSelWarps - 1) / kSelWarps + 31) & ~31;
-    const int w0 = min(t1, t0 + warp * seg), w1 = min(t1, w0 + seg);
     const uint32_t* w = reinterpret_cast<const uint32_t*>(p.weights) + static_cast<size_t>(row) * p.weight_stride;
-    auto classify = [&](int t, uint32_t bits) -> uint32_t {
-        return t >= w1 ? kNone : t < lo || t >= hi ? kSure : key_of(bits);
-    };
-    uint32_t raw[Keys > 0 ? Keys : 1], key[Keys > 0 ? Keys : 1];
-    if constexpr (Keys > 0) {
-#pragma unroll
-        for (int i = 0; i < Keys; ++i) raw[i] = w0 + 32 * i + lane < w1 ? w[w0 + 32 * i + lane] : 0u;
-#pragma unroll
-        for (int i = 0; i < Keys; ++i) key[i] = classify(w0 + 32 * i + lane, raw[i]);
+    uint32_t* keys = reinterpret_cast<uint32_t*>(staged);
+    if constexpr (Staged) {
+        // whole quads: a row holds a multiple of four weights
+        const uint4* from = reinterpret_cast<const uint4*>(w + t0);
+#pragma unroll 2
+        for (int q = tid; 4 * q < t1 - t0; q += Threads) {
+            const uint4 x = from[q];
+            staged[q] = make_uint4(key_of(x.x), key_of(x.y), key_of(x.z), key_of(x.w));
+        }
     }
-    // f(key, weight's bits, place) for the warp's places, 32 at a time
+    auto key_at = [&](int t) -> uint32_t { return Staged ? keys[t - t0] : key_of(w[t]); };
+    // f(key) for every token of the part to choose from, in any order
+    const int a = max(t0, lo), b = min(t1, hi);
     auto each = [&](auto&& f) {
-        if constexpr (Keys > 0) {
-#pragma unroll
-            for (int i = 0; i < Keys; ++i)
-                if (32 * i < seg) f(key[i], raw[i], w0 + 32 * i + lane);
-        } else {
-#pragma unroll 1
-            for (int b = w0; b < w1; b += 32) {
-                const uint32_t x = b + lane < w1 ? w[b + lane] : 0u;
-                f(classify(b + lane, x), x, b + lane);
+        if constexpr (Staged) {
+#pragma unroll 2
+            for (int q = (a - t0) / 4 + tid; 4 * q < b - t0; q += Threads) {
+                const uint4 x = staged[q];
+                const int t = t0 + 4 * q;
+                if (t >= a && t + 4 <= b) {
+                    f(x.x);
+                    f(x.y);
+                    f(x.z);
+                    f(x.w);
+                } else {
+                    if (t >= a) f(x.x);
+                    if (t + 1 >= a && t + 1 < b) f(x.y);
+                    if (t + 2 >= a && t + 2 < b) f(x.z);
+                    if (t + 3 < b) f(x.w);
+                }
             }
+        } else {
+            for (int t = a + tid; t < b; t += Threads) f(key_of(w[t]));
         }
     };
     // every CTA runs, its histograms cleared, before another adds to them
@@ -113,48 +131,53 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
     else __syncthreads();
 
     int k = left - lo - (n - hi);                // tokens of [lo, hi) that stay
-    uint32_t threshold = kNone;                  // keys above it stay ...
+    uint32_t threshold = 0u;                     // keys above it stay (all, so far) ...
     int take_eq = 0;                             // ... and this many of those equal to it
     if (n > p.budget) {
-        threshold = kSure - 1u;
+        threshold = 0xffffffffu;
         if (k > 0) {
             uint32_t prefix = 0u;
 #pragma unroll 1
             for (int pass = 0; pass < 3; ++pass) {
                 if (pass == 0) {
-                    each([&](uint32_t x, uint32_t, int) {
-                        if (x - 1u < kSure - 1u) atomicAdd(&hist[x >> 21], 1u);
-                    });
+                    each([&](uint32_t x) { atomicAdd(&hist[x >> 21], 1u); });
                 } else if (pass == 1) {
-                    each([&](uint32_t x, uint32_t, int) {
-                        if ((x >> 21) == prefix && x != kNone) atomicAdd(&hist[(x >> 10) & 2047u], 1u);
+                    each([&](uint32_t x) {
+                        if ((x >> 21) == prefix) atomicAdd(&hist[(x >> 10) & 2047u], 1u);
                     });
                 } else {
-                    each([&](uint32_t x, uint32_t, int) {
-                        if ((x >> 10) == prefix && x != kNone) atomicAdd(&hist[x & 1023u], 1u);
+                    each([&](uint32_t x) {
+                        if ((x >> 10) == prefix) atomicAdd(&hist[x & 1023u], 1u);
                     });
                 }
                 __syncthreads();
-                // a thread owns four bins, from the top down: it adds them to the cluster's
-                // (or takes them as they are) and clears them for the next pass
-                const int bin = kBins - 4 - 4 * tid;
-                uint4 c = *reinterpret_cast<uint4*>(hist + bin);
-                *reinterpret_cast<uint4*>(hist + bin) = make_uint4(0, 0, 0, 0);
+                // a thread owns kOwn bins, the first thread the highest: it adds them to the
+                // cluster's (or takes them as they are) and clears them for the next pass
+                const int bin = kBins - kOwn * (tid + 1);
+                int c[kOwn];
+                auto take = [&](unsigned* from) {
+#pragma unroll
+                    for (int e = 0; e < kOwn; e += 2) {
+                        const uint2 x = *reinterpret_cast<uint2*>(from + bin + e);
+                        *reinterpret_cast<uint2*>(from + bin + e) = make_uint2(0, 0);
+                        c[e] = static_cast<int>(x.x);
+                        c[e + 1] = static_cast<int>(x.y);
+                    }
+                };
+                take(hist);
                 if (parts > 1) {
                     unsigned* to = cluster.map_shared_rank(total, 0) + bin;
-                    if (c.x) atomicAdd(to, c.x);
-                    if (c.y) atomicAdd(to + 1, c.y);
-                    if (c.z) atomicAdd(to + 2, c.z);
-                    if (c.w) atomicAdd(to + 3, c.w);
+#pragma unroll
+                    for (int e = 0; e < kOwn; ++e)
+                        if (c[e]) atomicAdd(to + e, static_cast<unsigned>(c[e]));
                     cluster.sync();
-                    if (rank == 0) {
-                        c = *reinterpret_cast<uint4*>(total + bin);
-                        *reinterpret_cast<uint4*>(total + bin) = make_uint4(0, 0, 0, 0);
-                    }
+                    if (rank == 0) take(total);
                 }
                 if (rank == 0) {
                     // the bin in which the k-th largest lies: a scan over the threads
-                    const int own = static_cast<int>(c.x + c.y + c.z + c.w);
+                    int own = 0;
+#pragma unroll
+                    for (int e = 0; e < kOwn; ++e) own += c[e];
                     int incl = own;
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) {
@@ -163,30 +186,23 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
                     }
                     if (lane == 31) warp_sum[warp] = incl;
                     __syncthreads();
-                    int other = lane < warp ? warp_sum[lane & (kSelWarps - 1)] : 0;
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) other += __shfl_xor_sync(0xffffffffu, other, o);
+                    const int other = __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[lane & (kWarps - 1)] : 0);
                     int before = incl - own + other;
                     if (before < k && k <= before + own) {
-                        int d = bin + 3, in = static_cast<int>(c.w);
-                        if (before + in < k) {
-                            before += in;
-                            --d;
-                            in = static_cast<int>(c.z);
-                            if (before + in < k) {
-                                before += in;
-                                --d;
-                                in = static_cast<int>(c.y);
+                        int d = kOwn - 1, in = 0;
+#pragma unroll
+                        for (int e = kOwn - 1; e >= 0; --e) {
+                            if (e == d) {
+                                in = c[e];
                                 if (before + in < k) {
                                     before += in;
                                     --d;
-                                    in = static_cast<int>(c.x);
                                 }
                             }
                         }
                         for (int r = 0; r < parts; ++r) {
                             int* to = parts > 1 ? cluster.map_shared_rank(found, r) : found;
-                            to[0] = d;
+                            to[0] = bin + d;
                             to[1] = k - before;
                             to[2] = in;
                         }
@@ -202,7 +218,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
                     take_eq = k;
                 } else if (k == found[2]) {
                     // the whole bin stays: everything above the key before its first
-                    threshold = prefix == 0u ? kNone : (prefix << (pass == 0 ? 21 : 10)) - 1u;
+                    threshold = prefix == 0u ? 0u : (prefix << (pass == 0 ? 21 : 10)) - 1u;
                     break;
                 }
             }
@@ -211,11 +227,16 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
 
     // counts of the tokens that surely stay and of those equal to the threshold: per warp,
     // per CTA, per cluster
-    int n_sure = 0, n_eq = 0;
-    each([&](uint32_t x, uint32_t, int) {
+    const int seg = ((per + kWarps - 1) / kWarps + 31) & ~31;
+    const int w0 = min(t1, t0 + warp * seg), w1 = min(t1, w0 + seg);
+    const int m0 = max(w0, lo), m1 = min(w1, hi);          // to choose from
+    int n_sure = lane == 0 ? w1 - w0 - max(m1 - m0, 0) : 0, n_eq = 0;
+#pragma unroll 4
+    for (int t = m0 + lane; t < m1; t += 32) {
+        const uint32_t x = key_at(t);
         n_sure += x > threshold;
         n_eq += x == threshold;
-    });
+    }
     if (take_eq == 0) n_eq = 0;
     n_sure = __reduce_add_sync(0xffffffffu, n_sure);
     n_eq = __reduce_add_sync(0xffffffffu, n_eq);
@@ -228,15 +249,15 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
     if (parts > 1) {
         if (tid < parts) {
             int g = 0, e = 0;
-            for (int v = 0; v < kSelWarps; ++v) {
+            for (int v = 0; v < kWarps; ++v) {
                 g += warp_sure[v];
                 e += warp_eq[v];
             }
             *cluster.map_shared_rank(&part_sure[rank], tid) = g;
             *cluster.map_shared_rank(&part_eq[rank], tid) = e;
         }
-        // after this no CTA touches another's shared memory, and (Keys > 0) every weight of
-        // the row has been read: places and weights can be written
+        // after this no CTA touches another's shared memory, and (Staged) every weight of the
+        // row has been read: places and weights can be written
         cluster.sync();
         for (int r = 0; r < rank; ++r) {
             sure_before += part_sure[r];
@@ -250,44 +271,46 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
     int32_t* kept = p.kept + static_cast<size_t>(row) * p.budget;
     uint32_t* wo = reinterpret_cast<uint32_t*>(p.weights_out) + static_cast<size_t>(row) * p.weight_stride;
     const unsigned below = (1u << lane) - 1u;
-    if (take_eq == 0) {
-        each([&](uint32_t x, uint32_t bits, int t) {
-            const unsigned ms = __ballot_sync(0xffffffffu, x > threshold);
-            if (x > threshold) {
-                const int at = sure_before + __popc(ms & below);
-                kept[at] = t;
-                wo[at] = bits;
-            }
-            sure_before += __popc(ms);
-        });
-    } else {
-        each([&](uint32_t x, uint32_t bits, int t) {
-            const bool sure = x > threshold, eq = x == threshold;
-            const unsigned ms = __ballot_sync(0xffffffffu, sure), me = __ballot_sync(0xffffffffu, eq);
+#pragma unroll 2
+    for (int t = w0 + lane; t - lane < w1; t += 32) {
+        const uint32_t x = t < w1 ? key_at(t) : 0u;
+        const bool choose = t >= lo && t < hi;
+        const bool sure = t < w1 && (!choose || x > threshold);
+        const unsigned ms = __ballot_sync(0xffffffffu, sure);
+        int at = sure_before + __popc(ms & below);
+        bool stays = sure;
+        if (take_eq > 0) {
+            const bool eq = t < w1 && choose && x == threshold;
+            const unsigned me = __ballot_sync(0xffffffffu, eq);
             const int eq_rank = eq_before + __popc(me & below);
-            if (sure || (eq && eq_rank < take_eq)) {
-                const int at = sure_before + __popc(ms & below) + min(eq_rank, take_eq);
-                kept[at] = t;
-                wo[at] = bits;
-            }
-            sure_before += __popc(ms);
+            stays = sure || (eq && eq_rank < take_eq);
+            at += min(eq_rank, take_eq);
             eq_before += __popc(me);
-        });
+        }
+        if (stays) {
+            kept[at] = t;
+            wo[at] = bits_of(x);
+        }
+        sure_before += __popc(ms);
     }
     // what the row no longer holds: weights of 0, places of -1
-    for (int t = left + rank * kSelThreads + tid; t < n; t += parts * kSelThreads) wo[t] = 0u;
-    for (int j = left + rank * kSelThreads + tid; j < p.budget; j += parts * kSelThreads) kept[j] = -1;
+    for (int t = left + rank * Threads + tid; t < n; t += parts * Threads) wo[t] = 0u;
+    for (int j = left + rank * Threads + tid; j < p.budget; j += parts * Threads) kept[j] = -1;
 }
 
-// Copy of the kept rows to the new blocks.  A warp takes kRows consecutive places of one
+// Copy of the kept rows to the new blocks.  A warp takes kTile consecutive places of one
 // (sequence, KV head): its lanes look up a place's source and destination rows at once
 // (three dependent loads for all of them together), then 16 lanes (8 for FP8) move a row
-// of K and one of V, 16 bytes each, with kBatch such pairs in flight per lane.
-template <bool Fp8, int kRows>
+// of K and one of V, 16 bytes each, kBatch such pairs in flight per lane.  HBM-bound: 40
+// sequences of 8192 tokens to 2048 in fp16, 0.67 GB, take 105 us (6.4 TB/s); tiles of 16
+// and 32 places took 117, eight pairs in flight 130.
+constexpr int kTile = 8;
+
+template <bool Fp8>
 __global__ void __launch_bounds__(256) evict_copy_kernel(const EvictParams p, int tiles) {
     constexpr int kLanes = Fp8 ? 8 : 16;                   // lanes per row
     constexpr int kPer = 32 / kLanes;                      // rows a warp moves at a time
-    constexpr int kBatch = kRows / kPer < 4 ? kRows / kPer : 4;
+    constexpr int kBatch = kTile / kPer;
     constexpr int kRowBytes = kLanes * 16;
     grid_dependency_wait();
     grid_launch_dependents();
@@ -296,13 +319,13 @@ __global__ void __launch_bounds__(256) evict_copy_kernel(const EvictParams p, in
     const long long row = unit / tiles;
     if (row >= static_cast<long long>(p.num_seqs) * p.num_kv_heads) return;
     const int s = static_cast<int>(row / p.num_kv_heads), h = static_cast<int>(row % p.num_kv_heads);
-    const int j0 = static_cast<int>(unit % tiles) * kRows;
+    const int j0 = static_cast<int>(unit % tiles) * kTile;
     const int left = __ldcg(p.seq_lens_out + s);
     if (j0 >= left) return;
     const int bs = 1 << p.block_shift;
     int src = -1, dst = -1;                                // rows of the cache; -1: nothing to move
     const int j = j0 + lane;
-    if (lane < kRows && j < left) {
+    if (lane < kTile && j < left) {
         const int t = __ldcg(p.kept + static_cast<size_t>(row) * p.budget + j);
         int from = __ldg(p.block_tables + static_cast<size_t>(s) * p.max_blocks + (t >> p.block_shift));
         const int to = __ldg(p.new_tables + static_cast<size_t>(s) * p.max_new_blocks + (j >> p.block_shift));
@@ -318,48 +341,66 @@ __global__ void __launch_bounds__(256) evict_copy_kernel(const EvictParams p, in
     const int sub = lane / kLanes, off = (lane % kLanes) * 16;
     uint8_t* kc = static_cast<uint8_t*>(p.k_cache) + off;
     uint8_t* vc = static_cast<uint8_t*>(p.v_cache) + off;
-    const int rows = min(kRows, left - j0);
-#pragma unroll 1
-    for (int r0 = 0; r0 < rows; r0 += kPer * kBatch) {
-        uint4 kx[kBatch], vx[kBatch];
-        int to[kBatch];
+    uint4 kx[kBatch], vx[kBatch];
+    int to[kBatch];
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int r = (r0 + u * kPer + sub) & 31;
-            const int from = __shfl_sync(0xffffffffu, src, r);
-            to[u] = __shfl_sync(0xffffffffu, dst, r);
-            if (to[u] >= 0) {
-                kx[u] = __ldcs(reinterpret_cast<const uint4*>(kc + static_cast<size_t>(from) * kRowBytes));
-                vx[u] = __ldcs(reinterpret_cast<const uint4*>(vc + static_cast<size_t>(from) * kRowBytes));
-            }
+    for (int u = 0; u < kBatch; ++u) {
+        const int from = __shfl_sync(0xffffffffu, src, u * kPer + sub);
+        to[u] = __shfl_sync(0xffffffffu, dst, u * kPer + sub);
+        if (to[u] >= 0) {
+            kx[u] = __ldcg(reinterpret_cast<const uint4*>(kc + static_cast<size_t>(from) * kRowBytes));
+            vx[u] = __ldcg(reinterpret_cast<const uint4*>(vc + static_cast<size_t>(from) * kRowBytes));
         }
+    }
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            if (to[u] >= 0) {
-                *reinterpret_cast<uint4*>(kc + static_cast<size_t>(to[u]) * kRowBytes) = kx[u];
-                *reinterpret_cast<uint4*>(vc + static_cast<size_t>(to[u]) * kRowBytes) = vx[u];
-            }
+    for (int u = 0; u < kBatch; ++u) {
+        if (to[u] >= 0) {
+            *reinterpret_cast<uint4*>(kc + static_cast<size_t>(to[u]) * kRowBytes) = kx[u];
+            *reinterpret_cast<uint4*>(vc + static_cast<size_t>(to[u]) * kRowBytes) = vx[u];
         }
     }
 }
 
 }  // namespace
 
-// CTAs per row and weights per thread: parts of at most 4096 tokens (8 per thread)
-// while a cluster reaches, then 8192 and 16384; longer rows are read again in each pass.
-EvictPlan evict_plan(long long cap) {
+// CTAs per row and threads per CTA: one CTA up to 8192 tokens, a cluster beyond, or for
+// long rows while they leave most of the device idle; 1024 threads where there is an SM for
+// every CTA, else 512, and 256 for short rows.
+EvictPlan evict_plan(long long rows, long long cap, int sms) {
     EvictPlan e;
     e.parts = 1;
-    while (e.parts < kMaxCluster && cap > 4096ll * e.parts) e.parts *= 2;
-    const long long per = (cap + e.parts - 1) / e.parts;
-    e.keys = per <= 2048 ? 4 : per <= 4096 ? 8 : per <= 8192 ? 16 : per <= 16384 ? 32 : 0;
+    while (e.parts < kMaxCluster && (cap > 8192ll * e.parts || (rows * e.parts <= sms / 2 && cap > 4096ll * e.parts)))
+        e.parts *= 2;
+    const long long per = ((cap + e.parts - 1) / e.parts + 3) & ~3ll;
+    e.staged = per <= kMaxStaged;
+    e.smem = e.staged ? static_cast<size_t>(per) * 4 : 0;
+    e.threads = per <= 1024 ? 256 : rows * e.parts <= sms ? 1024 : 512;
     return e;
+}
+
+namespace {
+const void* select_fn(const EvictPlan& plan) {
+    if (!plan.staged) return reinterpret_cast<const void*>(&evict_select_kernel<1024, false>);
+    return plan.threads == 256   ? reinterpret_cast<const void*>(&evict_select_kernel<256, true>)
+           : plan.threads == 512 ? reinterpret_cast<const void*>(&evict_select_kernel<512, true>)
+                                 : reinterpret_cast<const void*>(&evict_select_kernel<1024, true>);
+}
+}  // namespace
+
+cudaError_t evict_prepare() {
+    for (int threads : {512, 1024}) {            // 256 threads: at most 1024 tokens
+        EvictPlan plan = {1, threads, true, 0};
+        cudaError_t e = cudaFuncSetAttribute(select_fn(plan), cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxStaged * 4);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 cudaError_t launch_evict_select(const EvictParams& p, const EvictPlan& plan, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(p.num_seqs) * p.num_kv_heads * plan.parts));
-    cfg.blockDim = dim3(kSelThreads);
+    cfg.blockDim = dim3(static_cast<unsigned>(plan.staged ? plan.threads : 1024));
+    cfg.dynamicSmemBytes = plan.smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -370,21 +411,13 @@ cudaError_t launch_evict_select(const EvictParams& p, const EvictPlan& plan, cud
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    switch (plan.keys) {
-        case 4: return cudaLaunchKernelEx(&cfg, evict_select_kernel<4>, p);
-        case 8: return cudaLaunchKernelEx(&cfg, evict_select_kernel<8>, p);
-        case 16: return cudaLaunchKernelEx(&cfg, evict_select_kernel<16>, p);
-        case 32: return cudaLaunchKernelEx(&cfg, evict_select_kernel<32>, p);
-    }
-    return cudaLaunchKernelEx(&cfg, evict_select_kernel<0>, p);
+    void* args[] = {const_cast<EvictParams*>(&p)};
+    return cudaLaunchKernelExC(&cfg, select_fn(plan), args);
 }
 
-cudaError_t launch_evict_copy(const EvictParams& p, bool fp8, int max_left, int sms, cudaStream_t stream) {
+cudaError_t launch_evict_copy(const EvictParams& p, bool fp8, int max_left, cudaStream_t stream) {
     const long long rows = static_cast<long long>(p.num_seqs) * p.num_kv_heads;
-    // tiles of 32 places where that fills the device's warp slots, else of 8
-    const bool wide = rows * ((max_left + 31) / 32) >= 64ll * sms;
-    const int tile = wide ? 32 : 8;
-    int tiles = (max_left + tile - 1) / tile;
+    int tiles = (max_left + kTile - 1) / kTile;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((rows * tiles + 7) / 8));
     cfg.blockDim = dim3(256);
@@ -394,11 +427,8 @@ cudaError_t launch_evict_copy(const EvictParams& p, bool fp8, int max_left, int 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (fp8)
-        return wide ? cudaLaunchKernelEx(&cfg, evict_copy_kernel<true, 32>, p, tiles)
-                    : cudaLaunchKernelEx(&cfg, evict_copy_kernel<true, 8>, p, tiles);
-    return wide ? cudaLaunchKernelEx(&cfg, evict_copy_kernel<false, 32>, p, tiles)
-                : cudaLaunchKernelEx(&cfg, evict_copy_kernel<false, 8>, p, tiles);
+    return fp8 ? cudaLaunchKernelEx(&cfg, evict_copy_kernel<true>, p, tiles)
+               : cudaLaunchKernelEx(&cfg, evict_copy_kernel<false>, p, tiles);
 }
 
 }  // namespace pa

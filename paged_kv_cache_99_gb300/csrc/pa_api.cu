@@ -26,6 +26,7 @@ struct DeviceState {
     size_t max_smem_optin = 0;
     bool decode_prepared[3][2][3][2][2] = {};
     bool chunk_prepared[3][2] = {};
+    bool evict_prepared = false;
 };
 
 std::mutex g_mu;
@@ -928,8 +929,16 @@ pa_status pa_evict(int32_t* kept, int32_t* seq_lens_out, float* weights_out, con
         return PA_ERR_UNSUPPORTED;
     DeviceState* st = device_state(nullptr);
     if (!st) return PA_ERR_CUDA;
-    const EvictPlan plan = evict_plan(cap);
-    if (plan.keys == 0 && weights_out == weights) return PA_ERR_UNSUPPORTED;
+    const EvictPlan plan = evict_plan(rows, cap, st->sms);
+    if (!plan.staged && weights_out == weights) return PA_ERR_UNSUPPORTED;
+    {
+        std::lock_guard<std::mutex> lock(g_mu);
+        if (!st->evict_prepared) {
+            cudaError_t e = evict_prepare();
+            if (e != cudaSuccess) return fail("cudaFuncSetAttribute(evict)", e);
+            st->evict_prepared = true;
+        }
+    }
     EvictParams p;
     p.kept = kept;
     p.seq_lens_out = seq_lens_out;
@@ -954,7 +963,7 @@ pa_status pa_evict(int32_t* kept, int32_t* seq_lens_out, float* weights_out, con
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     const pa_status s = launched(launch_evict_select(p, plan, cs), "launch(evict_select)");
     if (s != PA_OK) return s;
-    return launched(launch_evict_copy(p, is_fp8(cache_dtype), max_left, st->sms, cs), "launch(evict_copy)");
+    return launched(launch_evict_copy(p, is_fp8(cache_dtype), max_left, cs), "launch(evict_copy)");
 }
 
 pa_status pa_read_device_status(void* workspace, pa_stream_t stream) {

@@ -268,12 +268,15 @@ struct EvictParams {
 
 struct EvictPlan {
     int parts;                        // CTAs per row
-    int keys;                         // weights a thread holds; 0: read again in each pass
+    int threads;                      // threads per CTA
+    bool staged;                      // a CTA's part of the row fits its shared memory
+    size_t smem;
 };
 
-EvictPlan evict_plan(long long cap);
+EvictPlan evict_plan(long long rows, long long cap, int sms);
+cudaError_t evict_prepare();
 cudaError_t launch_evict_select(const EvictParams& p, const EvictPlan& plan, cudaStream_t stream);
-cudaError_t launch_evict_copy(const EvictParams& p, bool fp8, int max_left, int sms, cudaStream_t stream);
+cudaError_t launch_evict_copy(const EvictParams& p, bool fp8, int max_left, cudaStream_t stream);
 
 // Prefill chunks.
 size_t chunk_smem_bytes(CacheKind kind, int num_seqs);

@@ -87,7 +87,7 @@ class Case:
         if in_place:
             for s, n in enumerate(self.lens):
                 want[s, :, n:] = self.w[s, :, n:]
-        assert np.array_equal(got.view(np.int32), want.view(np.int32))
+        np.testing.assert_array_equal(got, want)             # NaN where NaN, -0 as 0
         as_bits = lambda x: x.cpu().numpy() if self.cache == "fp8" else x.cpu().view(torch.int16).numpy().view(np.uint16)  # noqa: E731
         assert np.array_equal(as_bits(self.kc), k) and np.array_equal(as_bits(self.vc), v)
 
