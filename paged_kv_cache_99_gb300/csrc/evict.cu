@@ -7,9 +7,9 @@
 // go, in order, to the blocks of a new table; the source blocks are only read, so they
 // may be shared with other sequences.
 //
-// Two launches.  The selection finds the k-th largest weight of each row by radix
-// select and writes the kept places in order; the copy is pure data movement
-// (HBM-bound) over those places.
+// One launch.  A cluster of CTAs (one CTA for rows of up to 8192 tokens) takes a row, that
+// is, a sequence and KV head: it finds the k-th largest weight by radix select, writes the
+// kept places in order, and copies their rows.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -37,6 +37,68 @@ __device__ __forceinline__ uint32_t key_of(uint32_t bits) {
 // The weight of a key (of -0: 0, of a NaN: a NaN).
 __device__ __forceinline__ uint32_t bits_of(uint32_t key) { return key & 0x80000000u ? key ^ 0x80000000u : ~key; }
 
+// The copy of a row's kept places to the new blocks, by all warps of its cluster, each
+// taking kTile consecutive places at a time: its lanes look up a place's source and
+// destination rows at once (three dependent loads for all of them together), then 16 lanes
+// (8 for FP8) move a row of K and one of V, 16 bytes each, kBatch such pairs in flight per
+// lane.  HBM-bound: 40 sequences of 8192 tokens to 2048 in fp16, 0.67 GB in and out, about
+// 105 us (6.4 TB/s).  The warps of a row work side by side on short tiles, which keeps the
+// rows in flight close together in the blocks they come from: tiles of 16 and 32 places
+// took 117, eight pairs in flight 130.
+constexpr int kTile = 8;
+
+template <bool Fp8, int kBatch>
+__device__ __forceinline__ void copy_kept(const EvictParams& p, int s, int h, const int32_t* kept, int left, int warp,
+                                          int warps) {
+    constexpr int kLanes = Fp8 ? 8 : 16;                   // lanes per row
+    constexpr int kPer = 32 / kLanes;                      // rows a warp moves at a time
+    constexpr int kRowBytes = kLanes * 16;
+    const int lane = threadIdx.x & 31;
+    const int bs = 1 << p.block_shift;
+    const int sub = lane / kLanes, off = (lane % kLanes) * 16;
+    uint8_t* kc = static_cast<uint8_t*>(p.k_cache) + off;
+    uint8_t* vc = static_cast<uint8_t*>(p.v_cache) + off;
+#pragma unroll 1
+    for (int j0 = kTile * warp; j0 < left; j0 += kTile * warps) {
+        int src = -1, dst = -1;                            // rows of the cache; -1: nothing to move
+        const int j = j0 + lane;
+        if (lane < kTile && j < left) {
+            const int t = __ldcg(kept + j);
+            int from = __ldg(p.block_tables + static_cast<size_t>(s) * p.max_blocks + (t >> p.block_shift));
+            const int to = __ldg(p.new_tables + static_cast<size_t>(s) * p.max_new_blocks + (j >> p.block_shift));
+            const bool bad_from = static_cast<unsigned>(from) >= static_cast<unsigned>(p.num_blocks);
+            const bool bad_to = static_cast<unsigned>(to) >= static_cast<unsigned>(p.num_blocks);
+            if ((bad_from || bad_to) && p.status) atomicOr(p.status, kDevErrRange);
+            if (bad_from) from = 0;
+            if (!bad_to) {
+                src = ((from * p.num_kv_heads + h) << p.block_shift) + (t & (bs - 1));
+                dst = ((to * p.num_kv_heads + h) << p.block_shift) + (j & (bs - 1));
+            }
+        }
+#pragma unroll 1
+        for (int r0 = 0; r0 < kTile; r0 += kPer * kBatch) {
+            uint4 kx[kBatch], vx[kBatch];
+            int to[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int from = __shfl_sync(0xffffffffu, src, r0 + u * kPer + sub);
+                to[u] = __shfl_sync(0xffffffffu, dst, r0 + u * kPer + sub);
+                if (to[u] >= 0) {
+                    kx[u] = __ldcg(reinterpret_cast<const uint4*>(kc + static_cast<size_t>(from) * kRowBytes));
+                    vx[u] = __ldcg(reinterpret_cast<const uint4*>(vc + static_cast<size_t>(from) * kRowBytes));
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                if (to[u] >= 0) {
+                    *reinterpret_cast<uint4*>(kc + static_cast<size_t>(to[u]) * kRowBytes) = kx[u];
+                    *reinterpret_cast<uint4*>(vc + static_cast<size_t>(to[u]) * kRowBytes) = vx[u];
+                }
+            }
+        }
+    }
+}
+
 // One cluster per (sequence, KV head), its CTAs taking equal parts of the row and their
 // warps contiguous segments.  Staged: a CTA keeps the keys of its part in shared memory, so
 // that the row is read once and may be compacted in place (the weights are read back from
@@ -52,9 +114,11 @@ __device__ __forceinline__ uint32_t bits_of(uint32_t key) { return key & 0x80000
 // row of 4096 on one CTA: load 1.5 us, a pass 0.5 and its scan 0.4, counts and writes 1.0; a
 // cluster adds 1 us per exchange): keys are computed once, a pass costs three or four
 // instructions per key, and the keys live in shared memory rather than in registers so
-// that all rows of a batch of 320 are resident at once (registers: 22 us, three waves).
-template <int Threads, bool Staged>
-__global__ void __launch_bounds__(Threads, Threads == 1024 ? 1 : 1536 / Threads) evict_select_kernel(const EvictParams p) {
+// that all rows of a batch of 320 are resident at once (registers: 22 us of selection, now
+// about 15).  With the copy a launch of its own, 64 sequences of up to 4096 tokens took
+// 20.5 us, now 18.4; the largest batches take the same.
+template <int Threads, bool Staged, bool Fp8>
+__global__ void __launch_bounds__(Threads, Threads == 1024 ? 1 : 1536 / Threads) evict_kernel(const EvictParams p) {
     constexpr int kWarps = Threads / 32;
     constexpr int kOwn = kBins / Threads;        // bins a thread owns
     extern __shared__ uint4 staged[];            // keys of the CTA's part, from t0 on
@@ -296,69 +360,10 @@ __global__ void __launch_bounds__(Threads, Threads == 1024 ? 1 : 1536 / Threads)
     // what the row no longer holds: weights of 0, places of -1
     for (int t = left + rank * Threads + tid; t < n; t += parts * Threads) wo[t] = 0u;
     for (int j = left + rank * Threads + tid; j < p.budget; j += parts * Threads) kept[j] = -1;
-}
-
-// Copy of the kept rows to the new blocks.  A warp takes kTile consecutive places of one
-// (sequence, KV head): its lanes look up a place's source and destination rows at once
-// (three dependent loads for all of them together), then 16 lanes (8 for FP8) move a row
-// of K and one of V, 16 bytes each, kBatch such pairs in flight per lane.  HBM-bound: 40
-// sequences of 8192 tokens to 2048 in fp16, 0.67 GB, take 105 us (6.4 TB/s); tiles of 16
-// and 32 places took 117, eight pairs in flight 130.
-constexpr int kTile = 8;
-
-template <bool Fp8>
-__global__ void __launch_bounds__(256) evict_copy_kernel(const EvictParams p, int tiles) {
-    constexpr int kLanes = Fp8 ? 8 : 16;                   // lanes per row
-    constexpr int kPer = 32 / kLanes;                      // rows a warp moves at a time
-    constexpr int kBatch = kTile / kPer;
-    constexpr int kRowBytes = kLanes * 16;
-    grid_dependency_wait();
-    grid_launch_dependents();
-    const int lane = threadIdx.x & 31;
-    const long long unit = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const long long row = unit / tiles;
-    if (row >= static_cast<long long>(p.num_seqs) * p.num_kv_heads) return;
-    const int s = static_cast<int>(row / p.num_kv_heads), h = static_cast<int>(row % p.num_kv_heads);
-    const int j0 = static_cast<int>(unit % tiles) * kTile;
-    const int left = __ldcg(p.seq_lens_out + s);
-    if (j0 >= left) return;
-    const int bs = 1 << p.block_shift;
-    int src = -1, dst = -1;                                // rows of the cache; -1: nothing to move
-    const int j = j0 + lane;
-    if (lane < kTile && j < left) {
-        const int t = __ldcg(p.kept + static_cast<size_t>(row) * p.budget + j);
-        int from = __ldg(p.block_tables + static_cast<size_t>(s) * p.max_blocks + (t >> p.block_shift));
-        const int to = __ldg(p.new_tables + static_cast<size_t>(s) * p.max_new_blocks + (j >> p.block_shift));
-        const bool bad_from = static_cast<unsigned>(from) >= static_cast<unsigned>(p.num_blocks);
-        const bool bad_to = static_cast<unsigned>(to) >= static_cast<unsigned>(p.num_blocks);
-        if ((bad_from || bad_to) && p.status) atomicOr(p.status, kDevErrRange);
-        if (bad_from) from = 0;
-        if (!bad_to) {
-            src = ((from * p.num_kv_heads + h) << p.block_shift) + (t & (bs - 1));
-            dst = ((to * p.num_kv_heads + h) << p.block_shift) + (j & (bs - 1));
-        }
-    }
-    const int sub = lane / kLanes, off = (lane % kLanes) * 16;
-    uint8_t* kc = static_cast<uint8_t*>(p.k_cache) + off;
-    uint8_t* vc = static_cast<uint8_t*>(p.v_cache) + off;
-    uint4 kx[kBatch], vx[kBatch];
-    int to[kBatch];
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-        const int from = __shfl_sync(0xffffffffu, src, u * kPer + sub);
-        to[u] = __shfl_sync(0xffffffffu, dst, u * kPer + sub);
-        if (to[u] >= 0) {
-            kx[u] = __ldcg(reinterpret_cast<const uint4*>(kc + static_cast<size_t>(from) * kRowBytes));
-            vx[u] = __ldcg(reinterpret_cast<const uint4*>(vc + static_cast<size_t>(from) * kRowBytes));
-        }
-    }
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-        if (to[u] >= 0) {
-            *reinterpret_cast<uint4*>(kc + static_cast<size_t>(to[u]) * kRowBytes) = kx[u];
-            *reinterpret_cast<uint4*>(vc + static_cast<size_t>(to[u]) * kRowBytes) = vx[u];
-        }
-    }
+    // every place is written, and visible to the cluster: the rows can move
+    if (parts > 1) cluster.sync();
+    else __syncthreads();
+    copy_kept<Fp8, Fp8 ? 2 : (Threads == 512 ? 2 : 4)>(p, s, h, kept, left, rank * kWarps + warp, parts * kWarps);
 }
 
 }  // namespace
@@ -379,24 +384,26 @@ EvictPlan evict_plan(long long rows, long long cap, int sms) {
 }
 
 namespace {
-const void* select_fn(const EvictPlan& plan) {
-    if (!plan.staged) return reinterpret_cast<const void*>(&evict_select_kernel<1024, false>);
-    return plan.threads == 256   ? reinterpret_cast<const void*>(&evict_select_kernel<256, true>)
-           : plan.threads == 512 ? reinterpret_cast<const void*>(&evict_select_kernel<512, true>)
-                                 : reinterpret_cast<const void*>(&evict_select_kernel<1024, true>);
+template <bool Fp8>
+const void* evict_fn(const EvictPlan& plan) {
+    if (!plan.staged) return reinterpret_cast<const void*>(&evict_kernel<1024, false, Fp8>);
+    return plan.threads == 256   ? reinterpret_cast<const void*>(&evict_kernel<256, true, Fp8>)
+           : plan.threads == 512 ? reinterpret_cast<const void*>(&evict_kernel<512, true, Fp8>)
+                                 : reinterpret_cast<const void*>(&evict_kernel<1024, true, Fp8>);
 }
 }  // namespace
 
 cudaError_t evict_prepare() {
     for (int threads : {512, 1024}) {            // 256 threads: at most 1024 tokens
         EvictPlan plan = {1, threads, true, 0};
-        cudaError_t e = cudaFuncSetAttribute(select_fn(plan), cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxStaged * 4);
+        cudaError_t e = cudaFuncSetAttribute(evict_fn<true>(plan), cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxStaged * 4);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(evict_fn<false>(plan), cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxStaged * 4);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
 
-cudaError_t launch_evict_select(const EvictParams& p, const EvictPlan& plan, cudaStream_t stream) {
+cudaError_t launch_evict(const EvictParams& p, const EvictPlan& plan, bool fp8, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(p.num_seqs) * p.num_kv_heads * plan.parts));
     cfg.blockDim = dim3(static_cast<unsigned>(plan.staged ? plan.threads : 1024));
@@ -412,23 +419,7 @@ cudaError_t launch_evict_select(const EvictParams& p, const EvictPlan& plan, cud
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     void* args[] = {const_cast<EvictParams*>(&p)};
-    return cudaLaunchKernelExC(&cfg, select_fn(plan), args);
-}
-
-cudaError_t launch_evict_copy(const EvictParams& p, bool fp8, int max_left, cudaStream_t stream) {
-    const long long rows = static_cast<long long>(p.num_seqs) * p.num_kv_heads;
-    int tiles = (max_left + kTile - 1) / kTile;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((rows * tiles + 7) / 8));
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return fp8 ? cudaLaunchKernelEx(&cfg, evict_copy_kernel<true>, p, tiles)
-               : cudaLaunchKernelEx(&cfg, evict_copy_kernel<false>, p, tiles);
+    return cudaLaunchKernelExC(&cfg, fp8 ? evict_fn<true>(plan) : evict_fn<false>(plan), args);
 }
 
 }  // namespace pa

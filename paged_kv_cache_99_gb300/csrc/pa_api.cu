@@ -922,10 +922,10 @@ pa_status pa_evict(int32_t* kept, int32_t* seq_lens_out, float* weights_out, con
         !aligned(kept, 4) || !aligned(seq_lens_out, 4) || !aligned(seq_lens, 4) || !aligned(block_tables, 4) ||
         !aligned(new_tables, 4) || (workspace && !aligned(workspace, 256)))
         return PA_ERR_INVALID_ARG;
-    // cache rows, tokens of a table and the grids are numbered in 32 bits
+    // cache rows, tokens of a table and the grid are numbered in 32 bits
     const long long rows = static_cast<long long>(num_seqs) * num_kv_heads;
     if (static_cast<long long>(num_blocks) * num_kv_heads * block_size >= (1ll << 31) || cap >= (1ll << 30) ||
-        rows >= (1ll << 27) || rows * ((static_cast<long long>(max_left) + 7) / 8) >= (1ll << 33))
+        rows >= (1ll << 27))
         return PA_ERR_UNSUPPORTED;
     DeviceState* st = device_state(nullptr);
     if (!st) return PA_ERR_CUDA;
@@ -960,10 +960,7 @@ pa_status pa_evict(int32_t* kept, int32_t* seq_lens_out, float* weights_out, con
     p.num_kv_heads = num_kv_heads;
     p.num_blocks = num_blocks;
     p.block_shift = block_shift_of(block_size);
-    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    const pa_status s = launched(launch_evict_select(p, plan, cs), "launch(evict_select)");
-    if (s != PA_OK) return s;
-    return launched(launch_evict_copy(p, is_fp8(cache_dtype), max_left, cs), "launch(evict_copy)");
+    return launched(launch_evict(p, plan, is_fp8(cache_dtype), reinterpret_cast<cudaStream_t>(stream)), "launch(evict)");
 }
 
 pa_status pa_read_device_status(void* workspace, pa_stream_t stream) {

@@ -241,8 +241,8 @@ cudaError_t launch_rope_table(float* cos_sin, int max_positions, int rot_dim, co
                               int sms, cudaStream_t stream);
 cudaError_t launch_rope_cache(RopeParams p, bool src_bf16, bool fp8, bool interleaved, int sms, cudaStream_t stream);
 
-// Eviction: selection of the places that stay (a cluster of `parts` CTAs per sequence
-// and KV head), then the copy of their rows.
+// Eviction: selection of the places that stay and the copy of their rows, by a cluster of
+// `parts` CTAs per sequence and KV head.
 struct EvictParams {
     int32_t* kept;                    // [num_seqs][num_kv_heads][budget]
     int32_t* seq_lens_out;
@@ -275,8 +275,7 @@ struct EvictPlan {
 
 EvictPlan evict_plan(long long rows, long long cap, int sms);
 cudaError_t evict_prepare();
-cudaError_t launch_evict_select(const EvictParams& p, const EvictPlan& plan, cudaStream_t stream);
-cudaError_t launch_evict_copy(const EvictParams& p, bool fp8, int max_left, cudaStream_t stream);
+cudaError_t launch_evict(const EvictParams& p, const EvictPlan& plan, bool fp8, cudaStream_t stream);
 
 // Prefill chunks.
 size_t chunk_smem_bytes(CacheKind kind, int num_seqs);

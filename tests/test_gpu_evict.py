@@ -133,7 +133,7 @@ def test_ties_and_odd_weights(weights, budget, sinks, recent):
     c.check()
 
 
-@pytest.mark.parametrize("lens,budget", [([20000], 3000), ([20000, 9], 4096), ([60000, 30000], 777), ([130000], 16384)])
+@pytest.mark.parametrize("lens,budget", [([20000], 3000), ([20000, 9], 4096), ([60000, 30000], 777), ([130000], 16384), ([390000], 5000)])
 @pytest.mark.parametrize("weights", [None, _few_values])
 def test_long_rows_over_several_ctas(lens, budget, weights):
     c = Case(11, lens, 2, "fp8", 16, budget, 4, 256, weights=weights).device()
