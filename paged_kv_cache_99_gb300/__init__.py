@@ -156,41 +156,43 @@ def _device_of(t, name: str) -> int:
     return t.get_device()
 
 
+def _refuse(device: int, t, name: str, dtypes) -> None:
+    """Why a tensor is not a contiguous one of these types on the device."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
+    raise ValueError(f"{name} must be contiguous")
+
+
 def _pointers(device: int, *tensors) -> list:
     """Addresses of (tensor or None, name, dtypes): contiguous tensors of one of the types on the device."""
     out = []
     for t, name, dtypes in tensors:
         if t is None:
             out.append(None)
-            continue
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError(f"{name} must be a CUDA tensor")
-        if t.dtype not in dtypes:
-            raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
-        if t.get_device() != device:
-            raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        out.append(t.data_ptr())
+        elif isinstance(t, torch.Tensor) and t.get_device() == device and t.dtype in dtypes and t.is_contiguous():
+            out.append(t.data_ptr())
+        else:
+            _refuse(device, t, name, dtypes)
     return out
 
 
 def _rows(device: int, t, name: str, dtype):
-    """(address, elements between tokens, tokens, heads, head_dim) of [tokens, heads, head_dim] with each
-    token's heads contiguous and any stride between tokens."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name}: dtype {t.dtype} is not {dtype}")
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
-    if t.dim() != 3:
+    """(address, elements between tokens, shape) of [tokens, heads, head_dim] with each token's heads
+    contiguous and any stride between tokens."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != device or t.dtype is not dtype:
+        _refuse(device, t, name, (dtype,))
+    shape = t.shape
+    if len(shape) != 3:
         raise ValueError(f"{name} must be [tokens, heads, head_dim]")
-    n, heads, d = t.shape
+    n, heads, d = shape
     st, sh, sd = t.stride()
     if n and ((sd != 1 and d > 1) or (sh != d and heads > 1)):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), st if n > 1 else heads * d, n, heads, d     # a single token's stride means nothing
+    return t.data_ptr(), st if n > 1 else heads * d, shape          # a single token's stride means nothing
 
 
 def _need_scales(code: int, k_scale, v_scale, num_kv_heads: int) -> None:
@@ -333,18 +335,20 @@ def pa_rope_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions,
     dt = q.dtype
     if dt not in _16BIT:
         raise TypeError(f"q: dtype {dt} not in {_16BIT}")
-    po, so, To, Ho, do = _rows(device, q_out, "q_out", dt)
-    pq, sq, T, Hq, d = _rows(device, q, "q", dt)
-    pk, sk, Tk, H, dk = _rows(device, k, "k", dt)
-    pv, sv, Tv, Hv, dv = _rows(device, v, "v", dt)
+    po, so, out_shape = _rows(device, q_out, "q_out", dt)
+    pq, sq, q_shape = _rows(device, q, "q", dt)
+    pk, sk, k_shape = _rows(device, k, "k", dt)
+    pv, sv, v_shape = _rows(device, v, "v", dt)
+    T, Hq, d = q_shape
+    Tk, H, dk = k_shape
     kc, vc, slots, pos, table, ks, vs, ws = _pointers(
         device, (k_cache, "k_cache", _CACHE), (v_cache, "v_cache", (k_cache.dtype,)),
         (slot_mapping, "slot_mapping", _I64), (positions, "positions", _I64), (cos_sin, "cos_sin", _F32),
         (k_scale, "k_scale", _F32), (v_scale, "v_scale", _F32), (workspace, "workspace", _U8))
     nb, Hc, bs, dc = shape = k_cache.shape
     max_positions, rot = cos_sin.shape
-    if ((To, Ho, do) != (T, Hq, d) or (Tk, dk) != (T, d) or (Tv, Hv, dv) != (T, H, d) or v_cache.shape != shape or
-            (Hc, dc) != (H, d) or slot_mapping.shape != (T,) or positions.shape != (T,)):
+    if (out_shape != q_shape or Tk != T or dk != d or v_shape != k_shape or v_cache.shape != shape or Hc != H or
+            dc != d or slot_mapping.shape != (T,) or positions.shape != (T,)):
         raise ValueError("shape mismatch")
     if workspace is not None and workspace.numel() < 256:
         raise ValueError("workspace: at least 256 bytes")
