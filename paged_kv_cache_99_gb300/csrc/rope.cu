@@ -51,7 +51,9 @@ __device__ __forceinline__ void sincos_quarter(float y, float& sn, float& cs) {
 }
 
 // A thread owns four frequencies and every `step`-th position, so that it writes 16
-// bytes of cosines and 16 of sines at a time and a row goes out in whole lines.
+// bytes of cosines and 16 of sines at a time and a row goes out in whole lines.  Bound by
+// the stores: 524288 positions of 128 (268 MB) take 37.2 us, 7.2 TB/s; 32768 (16.8 MB, it
+// stays in L2) 4.2.  Two CTAs per SM store as fast as more (eight: 38.6 and 6.8 us).
 __global__ void __launch_bounds__(256) rope_table_kernel(float* __restrict__ cos_sin, int max_positions, int rot_dim,
                                                          const __grid_constant__ RopeTurns turns, float attention) {
     grid_dependency_wait();
@@ -107,7 +109,8 @@ __device__ __forceinline__ uint32_t e4m3_of(float a, float b, float scale) {
     return c_lo | (c_hi << 8);
 }
 
-// HBM-bound: q is read and written once, k and v are read once and written once.
+// HBM-bound: q is read and written once, k and v are read once and written once (16384
+// tokens of 32/8 heads in bf16, 0.41 GB, take 62.3 us: 6.6 TB/s).
 // Eight threads own a row (one head of one token): each holds two 16-byte pieces of it,
 // the two whose components are paired with one another (half layout: pieces 8c and
 // rot / 2 + 8c; interleaved: 16c and 16c + 8; past the rotated part: what is left, two
@@ -116,12 +119,14 @@ __device__ __forceinline__ uint32_t e4m3_of(float a, float b, float scale) {
 // their loads all in flight together).  With few tokens a thread takes one row, so
 // that the call is as short as its chain of loads (position, table row).
 // The rotation is two products and a sum, each rounded to 32 bits, then one rounding to
-// the type stored.
+// the type stored: what separate 32-bit operations give, bit for bit.
+constexpr int kRopeThreads = 128;           // 256: 64.0 us on the 16384 tokens, 12.7 on 1040 (below)
+
 template <bool SrcBf16, bool Fp8, bool Interleaved, int Rows>
-__global__ void __launch_bounds__(256) rope_cache_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads) rope_cache_kernel(const RopeParams p) {
     grid_dependency_wait();
     grid_launch_dependents();
-    const unsigned grp = blockIdx.x * 32u + (threadIdx.x >> 3);
+    const unsigned grp = blockIdx.x * (kRopeThreads / 8) + (threadIdx.x >> 3);
     const unsigned tok = grp / static_cast<unsigned>(p.groups);
     const int gi = static_cast<int>(grp % static_cast<unsigned>(p.groups));
     if (tok >= static_cast<unsigned>(p.num_tokens)) return;
@@ -280,7 +285,7 @@ cudaError_t launch_rope_table(float* cos_sin, int max_positions, int rot_dim, co
     }
     const int rows = 256 / (rot_dim / 8);
     const long long want = (static_cast<long long>(max_positions) + rows - 1) / rows;
-    const long long cap = 8ll * sms;                // resident CTAs
+    const long long cap = 2ll * sms;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(want < cap ? want : cap));
     cfg.blockDim = dim3(256);
@@ -296,14 +301,16 @@ cudaError_t launch_rope_table(float* cos_sin, int max_positions, int rot_dim, co
 cudaError_t launch_rope_cache(RopeParams p, bool src_bf16, bool fp8, bool interleaved, int sms, cudaStream_t stream) {
     const int rows = p.num_q_heads + 2 * p.num_kv_heads;
     // one row per thread group up to a few waves of CTAs, where a call is as long as its
-    // chains of loads (1040 tokens of 64/8 heads: 12.7 us, with four rows 16.9); four rows
-    // beyond, for the loads in flight (16384 tokens of 32/8 heads: 64.0 us, with one 70.0)
+    // chains of loads (1040 tokens of 64/8 heads into an FP8 cache: 12.0 us, with four rows
+    // 13.5); four rows beyond, for the loads in flight (16384 tokens of 32/8 heads: 62.3 us,
+    // with one 66.8, with two 65.9)
     const int per = static_cast<long long>(p.num_tokens) * rows <= 2048ll * sms ? 1 : 4;
     p.groups = (rows + per - 1) / per;
-    const long long ctas = (static_cast<long long>(p.num_tokens) * p.groups + 31) / 32;
+    constexpr int kPerCta = kRopeThreads / 8;
+    const long long ctas = (static_cast<long long>(p.num_tokens) * p.groups + kPerCta - 1) / kPerCta;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3(kRopeThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
