@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 
+import numpy as np
 import torch
 
 from . import build_ext
@@ -148,6 +149,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 _16BIT = (torch.bfloat16, torch.float16)
 _CACHE = (torch.bfloat16, torch.float16, torch.uint8, torch.float8_e4m3fn)
 _F32, _I32, _I64, _U8 = (torch.float32,), (torch.int32,), (torch.int64,), (torch.uint8,)
+_F32_OR_NONE, _U8_OR_NONE = (torch.float32, None), (torch.uint8, None)
 
 
 def _device_of(t, name: str) -> int:
@@ -168,10 +170,11 @@ def _refuse(device: int, t, name: str, dtypes) -> None:
 
 
 def _pointers(device: int, *tensors) -> list:
-    """Addresses of (tensor or None, name, dtypes): contiguous tensors of one of the types on the device."""
+    """Addresses of (tensor, name, dtypes): contiguous tensors of one of the types on the device (None
+    where that is among the types: an argument that may be left out)."""
     out = []
     for t, name, dtypes in tensors:
-        if t is None:
+        if t is None and None in dtypes:
             out.append(None)
         elif isinstance(t, torch.Tensor) and t.get_device() == device and t.dtype in dtypes and t.is_contiguous():
             out.append(t.data_ptr())
@@ -306,7 +309,6 @@ def pa_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = PA_R
                         trained: float = 0.0, low_turns: float = 1.0, high_turns: float = 32.0):
     """Rotary frequencies, float64 numpy [rot_dim / 2]; scaling PA_ROPE_LINEAR or PA_ROPE_BY_PARTS
     (trained: the length the model was trained for) stretches them by factor."""
-    import numpy as np
     f = np.zeros(max(int(rot_dim) // 2, 1), dtype=np.float64)
     _check(_lib().pa_rope_frequencies(f.ctypes.data, int(rot_dim), float(base), int(scaling), float(factor),
                                       float(trained), float(low_turns), float(high_turns)), "pa_rope_frequencies")
@@ -316,14 +318,13 @@ def pa_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = PA_R
 def pa_rope_table(cos_sin, freqs, attention: float = 1.0, stream=None):
     """Table of a set of frequencies (host float64 [rot / 2]): cos_sin float32 [max_positions, rot],
     cosines then sines of position x frequency, both times attention."""
-    import numpy as np
     device = _device_of(cos_sin, "cos_sin")
     ptr, = _pointers(device, (cos_sin, "cos_sin", _F32))
     f = np.ascontiguousarray(freqs, dtype=np.float64)
     if cos_sin.dim() != 2 or f.ndim != 1 or cos_sin.shape[1] != 2 * f.size:
         raise ValueError("cos_sin must be [max_positions, 2 * len(freqs)]")
     _invoke("pa_rope_table", device, stream, _lib().pa_rope_table, ptr, cos_sin.shape[0], cos_sin.shape[1],
-            f.ctypes.data, attention)
+            f.ctypes.data, float(attention))
 
 
 def pa_rope_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, interleaved: bool = False,
@@ -344,7 +345,8 @@ def pa_rope_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions,
     kc, vc, slots, pos, table, ks, vs, ws = _pointers(
         device, (k_cache, "k_cache", _CACHE), (v_cache, "v_cache", (k_cache.dtype,)),
         (slot_mapping, "slot_mapping", _I64), (positions, "positions", _I64), (cos_sin, "cos_sin", _F32),
-        (k_scale, "k_scale", _F32), (v_scale, "v_scale", _F32), (workspace, "workspace", _U8))
+        (k_scale, "k_scale", _F32_OR_NONE), (v_scale, "v_scale", _F32_OR_NONE),
+        (workspace, "workspace", _U8_OR_NONE))
     nb, Hc, bs, dc = shape = k_cache.shape
     max_positions, rot = cos_sin.shape
     if (out_shape != q_shape or Tk != T or dk != d or v_shape != k_shape or v_cache.shape != shape or Hc != H or
@@ -385,12 +387,10 @@ def pa_decode_weights(out, weights_out, q, k_cache, v_cache, block_tables, seq_l
     zeros) + the step's softmax weights summed over each group's query heads; weights_in may be weights_out."""
     device = _device_of(q, "q")
     po, pw, pi, pq, kc, vc, bt, sl, ks, vs, ws = _pointers(
-        device, (out, "out", (q.dtype,)), (weights_out, "weights_out", _F32), (weights_in, "weights_in", _F32),
+        device, (out, "out", (q.dtype,)), (weights_out, "weights_out", _F32), (weights_in, "weights_in", _F32_OR_NONE),
         (q, "q", _16BIT), (k_cache, "k_cache", _CACHE), (v_cache, "v_cache", (k_cache.dtype,)),
-        (block_tables, "block_tables", _I32), (seq_lens, "seq_lens", _I32), (k_scale, "k_scale", _F32),
-        (v_scale, "v_scale", _F32), (workspace, "workspace", _U8))
-    if pw is None or po is None or ws is None:
-        raise TypeError("out, weights_out and workspace are needed")
+        (block_tables, "block_tables", _I32), (seq_lens, "seq_lens", _I32), (k_scale, "k_scale", _F32_OR_NONE),
+        (v_scale, "v_scale", _F32_OR_NONE), (workspace, "workspace", _U8))
     B, Hq, d = shape = q.shape
     nb, Hkv, bs, _ = cache = k_cache.shape
     rows, width = block_tables.shape
@@ -401,7 +401,7 @@ def pa_decode_weights(out, weights_out, q, k_cache, v_cache, block_tables, seq_l
     code = _cache_code(k_cache, k_scale, Hkv)
     _need_scales(code, k_scale, v_scale, Hkv)
     _invoke("pa_decode_weights", device, stream, _lib().pa_decode_weights, po, pw, pi, stride, pq, kc, vc, bt, width, sl, B,
-            Hq, Hkv, d, bs, nb, scale, _DTYPE[q.dtype], code, ks, vs, ws, workspace.numel())
+            Hq, Hkv, d, bs, nb, float(scale), _DTYPE[q.dtype], code, ks, vs, ws, workspace.numel())
 
 
 def pa_decode_append(out, q, k_new, v_new, slot_mapping, k_cache, v_cache, block_tables, seq_lens, scale, workspace,
@@ -538,7 +538,7 @@ def pa_evict(kept, seq_lens_out, weights_out, weights, k_cache, v_cache, block_t
         device, (k_cache, "k_cache", _CACHE), (v_cache, "v_cache", (k_cache.dtype,)), (weights, "weights", _F32),
         (weights_out, "weights_out", _F32), (kept, "kept", _I32), (seq_lens_out, "seq_lens_out", _I32),
         (block_tables, "block_tables", _I32), (seq_lens, "seq_lens", _I32), (new_tables, "new_tables", _I32),
-        (workspace, "workspace", _U8))
+        (workspace, "workspace", _U8_OR_NONE))
     nb, H, bs, d = shape = k_cache.shape
     B, wH, stride = wshape = weights.shape
     rows, width = block_tables.shape
@@ -549,7 +549,7 @@ def pa_evict(kept, seq_lens_out, weights_out, weights, k_cache, v_cache, block_t
     if workspace is not None and workspace.numel() < 256:
         raise ValueError("workspace: at least 256 bytes")
     _invoke("pa_evict", device, stream, _lib().pa_evict, pk, plo, pwo, pw, stride, kc, vc, bt, width, sl, nt, new_width, B,
-            budget, sinks, recent, H, d, bs, nb, _DTYPE[k_cache.dtype], ws)
+            int(budget), int(sinks), int(recent), H, d, bs, nb, _DTYPE[k_cache.dtype], ws)
 
 
 class BlockPool:

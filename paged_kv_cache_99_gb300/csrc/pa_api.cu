@@ -492,7 +492,7 @@ const char* pa_status_string(int status) {
     }
 }
 
-int pa_version(void) { return 101; }
+int pa_version(void) { return 102; }
 
 unsigned long long pa_kernel_launches(void) { return g_launches.load(std::memory_order_relaxed); }
 

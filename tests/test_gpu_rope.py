@@ -209,7 +209,8 @@ def test_refusals():
                                 positions=c.positions, cos_sin=c.cos_sin, k_scale=c.ks, v_scale=c.vs), **kw}
     for bad in (dict(positions=c.positions[:-1]), dict(slot_mapping=c.slots[1:]), dict(k=k[:, :1]), dict(q_out=c.q_out[:-1]),
                 dict(q=q.transpose(0, 1).contiguous().transpose(0, 1)), dict(k_scale=c.ks.repeat(3)),
-                dict(workspace=torch.zeros(64, dtype=torch.uint8, device=DEV)), dict(positions=c.positions.cpu())):
+                dict(workspace=torch.zeros(64, dtype=torch.uint8, device=DEV)), dict(positions=c.positions.cpu()),
+                dict(positions=None), dict(v_cache=None)):
         with pytest.raises((ValueError, TypeError)):
             pa.pa_rope_and_cache(**args(**bad))
     for bad in (dict(positions=c.positions.int()), dict(q_out=c.q_out.half()), dict(k_scale=None, v_scale=None),
