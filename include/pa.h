@@ -522,7 +522,7 @@ PA_API pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int32_t* src
  *                  block_size); entries past ceil(left / block_size) are never read.  Its
  *                  blocks must be distinct and none may be read by the call (the result is
  *                  otherwise unspecified).
- *   budget         >= 1; sinks, recent >= 0 and sinks + recent <= budget
+ *   budget         1 .. 2^30 - 1; sinks, recent >= 0 and sinks + recent <= budget
  *   workspace      NULL, or a workspace whose status word records PA_ERR_OUT_OF_RANGE: a
  *                  length beyond the table (cut to it), a source block outside the pool (block 0
  *                  is read instead), a new block outside it (its rows are not copied)

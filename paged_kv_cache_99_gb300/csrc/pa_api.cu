@@ -922,10 +922,10 @@ pa_status pa_evict(int32_t* kept, int32_t* seq_lens_out, float* weights_out, con
         !aligned(kept, 4) || !aligned(seq_lens_out, 4) || !aligned(seq_lens, 4) || !aligned(block_tables, 4) ||
         !aligned(new_tables, 4) || (workspace && !aligned(workspace, 256)))
         return PA_ERR_INVALID_ARG;
-    // cache rows, tokens of a table and the grid are numbered in 32 bits
+    // cache rows, places of a row and the grid are numbered in 32 bits
     const long long rows = static_cast<long long>(num_seqs) * num_kv_heads;
     if (static_cast<long long>(num_blocks) * num_kv_heads * block_size >= (1ll << 31) || cap >= (1ll << 30) ||
-        rows >= (1ll << 27))
+        budget >= (1 << 30) || rows >= (1ll << 27))
         return PA_ERR_UNSUPPORTED;
     DeviceState* st = device_state(nullptr);
     if (!st) return PA_ERR_CUDA;

@@ -38,5 +38,6 @@ def test_refusals(lib):
                 dict(recent=-1), dict(sinks=10, recent=11), dict(sinks=2**31 - 1, recent=2**31 - 1), dict(stride=60),
                 dict(stride=66), dict(maxn=1), dict(lens=FAKE), dict(ws=ctypes.c_void_p(0x10010))):
         assert _evict(lib, **bad) == INVALID, bad
-    for bad in (dict(nb=1 << 27), dict(B=1 << 27), dict(maxb=1 << 26, stride=1 << 30)):
+    for bad in (dict(nb=1 << 27), dict(B=1 << 27), dict(maxb=1 << 26, stride=1 << 30), dict(budget=1 << 30, maxn=4),
+                dict(budget=2**31 - 1, maxn=4)):
         assert _evict(lib, **bad) == UNSUPPORTED, bad

@@ -171,3 +171,85 @@ def test_prompt_decode_evict_decode(cache, interleaved, graph):
                 np.testing.assert_allclose(running[s, h, :host_lens[s]], sums[s][h], rtol=2e-4, atol=1e-9)
                 assert np.all(running[s, h, host_lens[s]:] == 0)
     assert max(seen) > max(host_lens)                # positions ran on past the cache
+
+
+def test_blocks_beyond_four_gigabytes():
+    # every row the calls touch lies past 2^32 bytes into the caches
+    nb, bs = 1_200_000, 16                       # 4096 bytes a block and head: 4.9 GB per cache
+    far = 1_100_000
+    kc = torch.empty(nb, 1, bs, 128, dtype=torch.bfloat16, device=DEV)
+    vc = torch.empty_like(kc)
+    kc[far:], vc[far:] = float("nan"), float("nan")
+    T = 100
+    blocks = torch.randperm(nb - far, generator=torch.Generator().manual_seed(3))[:14] + far
+    qkv = torch.randn(T, 6, 128, generator=torch.Generator().manual_seed(4)).bfloat16().to(DEV)
+    slots = (blocks[torch.arange(T) // bs] * bs + torch.arange(T) % bs).to(DEV)
+    cos_sin = torch.empty(T, 64, device=DEV)
+    pa.pa_rope_table(cos_sin, pa.pa_rope_frequencies(64))
+    q = torch.empty(T, 4, 128, dtype=torch.bfloat16, device=DEV)
+    pa.pa_rope_and_cache(q, qkv[:, :4], qkv[:, 4:5], qkv[:, 5:], kc, vc, slots, torch.arange(T, device=DEV), cos_sin)
+    # the same into a small cache
+    kn, vn = (torch.empty(7, 1, bs, 128, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    qn = torch.empty_like(q)
+    pa.pa_rope_and_cache(qn, qkv[:, :4], qkv[:, 4:5], qkv[:, 5:], kn, vn, torch.arange(T, device=DEV),
+                         torch.arange(T, device=DEV), cos_sin)
+    assert torch.equal(q, qn)
+    at = blocks[:7].to(DEV)
+    rows = lambda c: c.reshape(-1, 128)[:T]  # noqa: E731
+    assert torch.equal(rows(kc[at]), rows(kn)) and torch.equal(rows(vc[at]), rows(vn))
+    lens = torch.tensor([T], dtype=torch.int32, device=DEV)
+    ws = pa.new_workspace_weights(1, 4, 1, 112)
+    tables = [blocks[None, :7].int().to(DEV), torch.arange(7, dtype=torch.int32, device=DEV)[None]]
+    out, w = [], []
+    for (k, v), t in zip(((kc, vc), (kn, vn)), tables):
+        out.append(torch.empty(1, 4, 128, dtype=torch.bfloat16, device=DEV))
+        w.append(torch.zeros(1, 1, 112, device=DEV))
+        pa.pa_decode_weights(out[-1], w[-1], q[-1:], k, v, t, lens, 0.088, ws)
+    assert torch.equal(out[0], out[1]) and torch.equal(w[0], w[1])
+    kept = torch.empty(1, 1, 40, dtype=torch.int32, device=DEV)
+    new_lens = torch.empty_like(lens)
+    new = blocks[7:10]
+    pa.pa_evict(kept, new_lens, w[1], w[0], kc, vc, tables[0], lens, new[None].int().to(DEV), 40, 2, 8, workspace=ws)
+    pick = torch.topk(w[0][0, 0, 2:92], 30).indices.sort().values.cpu() + 2
+    pick = torch.cat((torch.arange(2), pick, torch.arange(92, 100)))
+    assert torch.equal(kept[0, 0].cpu(), pick.int())
+    assert torch.equal(kc[new.to(DEV)].reshape(-1, 128)[:40], rows(kn)[pick.to(DEV)])
+    assert torch.equal(vc[new.to(DEV)].reshape(-1, 128)[:40], rows(vn)[pick.to(DEV)])
+    assert pa.pa_read_device_status(ws) == pa.PA_OK
+
+
+def test_two_graphs_share_a_workspace():
+    # two captured decode steps over one workspace, replayed in turns beside eager calls
+    g = torch.Generator(device=DEV).manual_seed(9)
+    lens = [[300, 17, 2000, 1], [64, 900]]
+    ws = pa.new_workspace_weights(4, 8, 2, 4 * 2000)
+    calls = []
+    for n in lens:
+        nb = [-(-x // BS) for x in n]
+        t = torch.full((len(n), max(nb)), -1, dtype=torch.int32)
+        perm = torch.randperm(sum(nb), generator=torch.Generator().manual_seed(len(n))).int()
+        for s, b in enumerate(nb):
+            t[s, :b] = perm[sum(nb[:s]):sum(nb[:s]) + b]
+        kc, vc = (torch.randn(sum(nb), 2, BS, 128, generator=g, device=DEV).bfloat16() for _ in range(2))
+        q = torch.randn(len(n), 8, 128, generator=g, device=DEV).bfloat16()
+        calls.append(dict(q=q, k_cache=kc, v_cache=vc, block_tables=t.to(DEV), scale=0.088, workspace=ws,
+                          seq_lens=torch.tensor(n, dtype=torch.int32, device=DEV),
+                          out=torch.empty_like(q), weights_out=torch.zeros(len(n), 2, max(nb) * BS, device=DEV)))
+    want, graphs = [], []
+    for c in calls:
+        pa.pa_decode_weights(**c)
+        want.append((c["out"].clone(), c["weights_out"].clone()))
+    torch.cuda.synchronize()
+    for c in calls:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            pa.pa_decode_weights(**c)
+    for i in (0, 1, 1, 0, 0, 1):
+        for c in calls:
+            c["out"].zero_()
+            c["weights_out"].zero_()
+        graphs[i].replay()
+        pa.pa_decode_weights(**calls[1 - i])
+        for c, (o, w) in zip(calls, want):
+            assert torch.equal(c["out"], o) and torch.equal(c["weights_out"], w)
+    assert pa.pa_read_device_status(ws) == pa.PA_OK
