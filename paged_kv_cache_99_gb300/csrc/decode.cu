@@ -326,6 +326,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kmap, const CUten
     // weights_kernel reads back (64 sequences of up to 4096, 12/2 heads: 49.5 -> 43.8 us)
     const bool stream_first = Weights || p.cascade != 0;
     const uint64_t pol = stream_first ? l2_policy_evict_first() : 0ull;
+    const uint64_t keep = Weights ? l2_policy_evict_last() : 0ull;
     auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
         if (stream_first) tma_load_2d_hint(dst, map, x, y, bar, pol);
         else tma_load_2d(dst, map, x, y, bar);
@@ -607,8 +608,8 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kmap, const CUten
         if constexpr (Weights) {
             if (keep_scores && 2 * t < p.score_pitch) {
                 float* sc = p.scores + static_cast<size_t>(c_f) * (kBlockSize * p.score_pitch) + g * p.score_pitch + 2 * t;
-                *reinterpret_cast<float2*>(sc) = make_float2(s0, s1);
-                *reinterpret_cast<float2*>(sc + 8 * p.score_pitch) = make_float2(s2, s3);
+                st_global_hint(sc, s0, s1, keep);
+                st_global_hint(sc + 8 * p.score_pitch, s2, s3, keep);
             }
         }
 
@@ -1325,6 +1326,14 @@ __global__ void __launch_bounds__(256) weights_kernel(const DecodeParams p) {
 #pragma unroll
                 for (int i = 0; i < kKeys; ++i)
                     if (t0 + 32 * i < end) p.weights_out[at + t0 + 32 * i] = w[i];
+            }
+            // the scores are done with: their lines need not be written back
+            __syncwarp();
+            for (int hg = 0; hg < HG; ++hg) {
+                const char* lines = reinterpret_cast<const char*>(
+                    p.scores + static_cast<size_t>(first + (h * HG + hg) * nb + j) * (kBlockSize * Pitch));
+                for (int i = lane; i < (je - j) * (kBlockSize * Pitch * 4 / 128); i += 32)
+                    l2_discard_line(lines + 128 * i);
             }
             f += je - j;
             if (f >= f1) break;
