@@ -1235,15 +1235,10 @@ __global__ void __maxnreg__(112) combine_cascade_kernel(const DecodeParams p) {
 // for FP8) per token and KV head; reading K a second time instead would cost 256 (128).
 // Scores stay in 32 bits: a 16-bit score or exponential would cost the weights 2^-9 of
 // themselves.
-// A warp takes up to kWeightUnits consecutive units (fewer while that keeps every warp at
-// work): it finds its place in the flattened order once, loads the heads' (M, 1 / L) once
+// Every warp takes one run of consecutive units, all of the same size: it finds its place
+// in the flattened order while it waits for the combine, loads the heads' (M, 1 / L) once
 // per (sequence, KV head), and then only streams, a key per lane with kKeys of them in
-// flight (their scores are contiguous).  On top of the decode and its combine it adds
-// 11 us of 237 (40 x 8192 tokens, 32/8 heads, fp16), 5.4 of 41 (64 of up to 4096, 12/2,
-// bf16) and 2.7 of 10.7 (four short sequences).  In one launch with the combine, whose 112
-// registers leave half the warps, the largest takes 247 us and the others about the same.
-constexpr int kWeightUnits = 16;
-
+// flight (their scores are contiguous).
 template <int Pitch>
 __global__ void __launch_bounds__(256) weights_kernel(const DecodeParams p) {
     constexpr int kKeys = Pitch <= 4 ? 4 : 2;    // keys of a lane in flight
@@ -1254,98 +1249,109 @@ __global__ void __launch_bounds__(256) weights_kernel(const DecodeParams p) {
     const int HG = p.head_groups;
     const int UH = p.num_kv_heads * HG;
     const int* cum = pre_sum;
-    if (B <= kCombineScanSeqs) combine_block_prefix(p, pre_sum, warp_sum);
-    else cum = p.plan;
-    grid_dependency_wait();
+    if (B <= kCombineScanSeqs) {
+        combine_block_prefix(p, pre_sum, warp_sum);
+    } else {
+        grid_dependency_wait();                  // the decode grid publishes the plan
+        cum = p.plan;
+    }
     const int T = cum[B];
-    if (T > p.score_units) return;               // recorded by the decode grid
     const int F = T / HG;                        // units of KV heads
     const int lane = threadIdx.x & 31;
     const int warps = gridDim.x * 8;
-    const int take = min(kWeightUnits, ((F + warps - 1) / warps + 1) & ~1);
-    for (long long f0 = (static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * take; f0 < F;
-         f0 += static_cast<long long>(warps) * take) {
-        int f = static_cast<int>(f0);
-        const int f1 = min(F, f + take);
+    const int take = ((F + warps - 1) / warps + 1) & ~1;       // whole warps: two units of 16 keys
+    const long long f0 = (static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * take;
+    // too many tokens for the workspace: recorded by the decode grid
+    const bool any = f0 < F && T <= p.score_units;
+    int f = any ? static_cast<int>(f0) : 0;
+    const int f1 = min(F, f + take);
+    int s = 0, first = 0, nb = 1, h = 0, j = 0, n = 0;
+    if (any) {
         // sequence s with cum[s] <= f HG < cum[s + 1]
-        int s = 0, hi = B;
+        int hi = B;
         while (hi - s > 1) {
             const int mid = (s + hi) >> 1;
             if (cum[mid] <= f * HG) s = mid; else hi = mid;
         }
-        int first = cum[s], nb = (cum[s + 1] - first) / UH;
-        int h = (f - first / HG) / nb, j = (f - first / HG) % nb;
-        while (true) {
-            // units [j, je) of (s, h)
-            const int je = min(nb, j + f1 - f);
-            const int end = min(je * kBlockSize, min(p.seq_lens[s], p.max_blocks * p.block_size));
-            const size_t at = (static_cast<size_t>(s) * p.num_kv_heads + h) * p.weight_stride;
-            for (int t0 = j * kBlockSize + lane; t0 - lane < end; t0 += 32 * kKeys) {
-                float w[kKeys];
+        first = cum[s];
+        nb = (cum[s + 1] - first) / UH;
+        h = (f - first / HG) / nb;
+        j = (f - first / HG) % nb;
+        n = min(p.seq_lens[s], p.max_blocks * p.block_size);
+    }
+    grid_dependency_wait();
+    if (!any) return;
+    while (true) {
+        // units [j, je) of (s, h)
+        const int je = min(nb, j + f1 - f);
+        const int end = min(je * kBlockSize, n);
+        const size_t at = (static_cast<size_t>(s) * p.num_kv_heads + h) * p.weight_stride;
+        for (int t0 = j * kBlockSize + lane; t0 - lane < end; t0 += 32 * kKeys) {
+            float w[kKeys];
 #pragma unroll
-                for (int i = 0; i < kKeys; ++i)
-                    w[i] = p.weights_in && t0 + 32 * i < end ? __ldcg(p.weights_in + at + t0 + 32 * i) : 0.f;
-                for (int hg = 0; hg < HG; ++hg) {
-                    const int uh = h * HG + hg;
-                    const float* um = p.unit_ml + static_cast<size_t>(s * UH + uh) * 16;
-                    const float* sc = p.scores + static_cast<size_t>(first + uh * nb) * (kBlockSize * Pitch);
-                    const int live = p.group - hg * kHeadsPerGroup;      // heads of this unit
-                    float m[Pitch], r[Pitch], x[kKeys][Pitch];
+            for (int i = 0; i < kKeys; ++i)
+                w[i] = p.weights_in && t0 + 32 * i < end ? __ldcg(p.weights_in + at + t0 + 32 * i) : 0.f;
+            for (int hg = 0; hg < HG; ++hg) {
+                const int uh = h * HG + hg;
+                const float* um = p.unit_ml + static_cast<size_t>(s * UH + uh) * 16;
+                const float* sc = p.scores + static_cast<size_t>(first + uh * nb) * (kBlockSize * Pitch);
+                const int live = p.group - hg * kHeadsPerGroup;      // heads of this unit
+                float m[Pitch], r[Pitch], x[kKeys][Pitch];
 #pragma unroll
-                    for (int i = 0; i < kKeys; ++i) {
-                        const float* q = sc + static_cast<size_t>(min(t0 + 32 * i, end - 1)) * Pitch;
-                        if constexpr (Pitch % 4 == 0) {
+                for (int i = 0; i < kKeys; ++i) {
+                    const float* q = sc + static_cast<size_t>(min(t0 + 32 * i, end - 1)) * Pitch;
+                    if constexpr (Pitch % 4 == 0) {
 #pragma unroll
-                            for (int e = 0; e < Pitch; e += 4) {
-                                const float4 v = __ldcg(reinterpret_cast<const float4*>(q + e));
-                                x[i][e] = v.x;
-                                x[i][e + 1] = v.y;
-                                x[i][e + 2] = v.z;
-                                x[i][e + 3] = v.w;
-                            }
-                        } else {
+                        for (int e = 0; e < Pitch; e += 4) {
+                            const float4 v = __ldcg(reinterpret_cast<const float4*>(q + e));
+                            x[i][e] = v.x;
+                            x[i][e + 1] = v.y;
+                            x[i][e + 2] = v.z;
+                            x[i][e + 3] = v.w;
+                        }
+                    } else {
 #pragma unroll
-                            for (int e = 0; e < Pitch; e += 2) {
-                                const float2 v = __ldcg(reinterpret_cast<const float2*>(q + e));
-                                x[i][e] = v.x;
-                                x[i][e + 1] = v.y;
-                            }
+                        for (int e = 0; e < Pitch; e += 2) {
+                            const float2 v = __ldcg(reinterpret_cast<const float2*>(q + e));
+                            x[i][e] = v.x;
+                            x[i][e + 1] = v.y;
                         }
                     }
+                }
 #pragma unroll
-                    for (int e = 0; e < Pitch; ++e) {
-                        m[e] = um[e];
-                        r[e] = e < live ? um[8 + e] : 0.f;
-                    }
-#pragma unroll
-                    for (int i = 0; i < kKeys; ++i)
-#pragma unroll
-                        for (int e = 0; e < Pitch; ++e)
-                            if (e < live) w[i] = fmaf(ex2_approx(x[i][e] - m[e]), r[e], w[i]);
+                for (int e = 0; e < Pitch; ++e) {
+                    m[e] = um[e];
+                    r[e] = e < live ? um[8 + e] : 0.f;
                 }
 #pragma unroll
                 for (int i = 0; i < kKeys; ++i)
-                    if (t0 + 32 * i < end) p.weights_out[at + t0 + 32 * i] = w[i];
+#pragma unroll
+                    for (int e = 0; e < Pitch; ++e)
+                        if (e < live) w[i] = fmaf(ex2_approx(x[i][e] - m[e]), r[e], w[i]);
             }
-            // the scores are done with: their lines need not be written back
-            __syncwarp();
-            for (int hg = 0; hg < HG; ++hg) {
-                const char* lines = reinterpret_cast<const char*>(
-                    p.scores + static_cast<size_t>(first + (h * HG + hg) * nb + j) * (kBlockSize * Pitch));
-                for (int i = lane; i < (je - j) * (kBlockSize * Pitch * 4 / 128); i += 32)
-                    l2_discard_line(lines + 128 * i);
-            }
-            f += je - j;
-            if (f >= f1) break;
-            j = 0;
-            if (++h == p.num_kv_heads) {
-                h = 0;
-                do {
-                    ++s;
-                } while (cum[s + 1] == cum[s]);
-                first = cum[s];
-                nb = (cum[s + 1] - first) / UH;
-            }
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i)
+                if (t0 + 32 * i < end) p.weights_out[at + t0 + 32 * i] = w[i];
+        }
+        // the scores are done with: their lines need not be written back
+        __syncwarp();
+        for (int hg = 0; hg < HG; ++hg) {
+            const char* lines = reinterpret_cast<const char*>(
+                p.scores + static_cast<size_t>(first + (h * HG + hg) * nb + j) * (kBlockSize * Pitch));
+            for (int i = lane; i < (je - j) * (kBlockSize * Pitch * 4 / 128); i += 32)
+                l2_discard_line(lines + 128 * i);
+        }
+        f += je - j;
+        if (f >= f1) break;
+        j = 0;
+        if (++h == p.num_kv_heads) {
+            h = 0;
+            do {
+                ++s;
+            } while (cum[s + 1] == cum[s]);
+            first = cum[s];
+            nb = (cum[s + 1] - first) / UH;
+            n = min(p.seq_lens[s], p.max_blocks * p.block_size);
         }
     }
 }
