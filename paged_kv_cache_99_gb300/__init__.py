@@ -146,6 +146,7 @@ def _need(t: torch.Tensor, name: str, dtypes=None):
 # their checks take one pass over the tensors and few attribute reads.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _16BIT = (torch.bfloat16, torch.float16)
 _CACHE = (torch.bfloat16, torch.float16, torch.uint8, torch.float8_e4m3fn)
 _F32, _I32, _I64, _U8 = (torch.float32,), (torch.int32,), (torch.int64,), (torch.uint8,)
@@ -173,13 +174,16 @@ def _pointers(device: int, *tensors) -> list:
     """Addresses of (tensor, name, dtypes): contiguous tensors of one of the types on the device (None
     where that is among the types: an argument that may be left out)."""
     out = []
-    for t, name, dtypes in tensors:
-        if t is None and None in dtypes:
-            out.append(None)
-        elif isinstance(t, torch.Tensor) and t.get_device() == device and t.dtype in dtypes and t.is_contiguous():
-            out.append(t.data_ptr())
-        else:
-            _refuse(device, t, name, dtypes)
+    try:
+        for t, name, dtypes in tensors:
+            if t is None and None in dtypes:
+                out.append(None)
+            elif t.get_device() == device and t.dtype in dtypes and t.is_contiguous():
+                out.append(t.data_ptr())
+            else:
+                _refuse(device, t, name, dtypes)
+    except AttributeError:                       # not a tensor
+        _refuse(device, t, name, dtypes)
     return out
 
 
@@ -200,8 +204,6 @@ def _rows(device: int, t, name: str, dtype):
 
 def _need_scales(code: int, k_scale, v_scale, num_kv_heads: int) -> None:
     """An FP8 cache has float32 scales for K and V, both one per tensor or both one per KV head."""
-    if code < PA_FP8_E4M3:
-        return
     want = num_kv_heads if code == PA_FP8_E4M3_PER_HEAD else 1
     for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
         if t is None:
@@ -213,7 +215,7 @@ def _need_scales(code: int, k_scale, v_scale, num_kv_heads: int) -> None:
 def _invoke(what: str, device: int, stream, fn, *args) -> None:
     """fn(*args, stream) with the tensors' device current; the default stream is that device's current one."""
     raw = _raw_stream(device) if stream is None else stream.cuda_stream
-    if device == torch.cuda.current_device():
+    if device == _current_device():
         status = fn(*args, raw)
     else:
         with torch.cuda.device(device):
@@ -354,8 +356,10 @@ def pa_rope_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions,
         raise ValueError("shape mismatch")
     if workspace is not None and workspace.numel() < 256:
         raise ValueError("workspace: at least 256 bytes")
-    code = _cache_code(k_cache, k_scale, H)
-    _need_scales(code, k_scale, v_scale, H)
+    code = _DTYPE[k_cache.dtype]
+    if code >= PA_FP8_E4M3:
+        code = _cache_code(k_cache, k_scale, H)
+        _need_scales(code, k_scale, v_scale, H)
     _invoke("pa_rope_and_cache", device, stream, _lib().pa_rope_and_cache, po, so, pq, sq, pk, sk, pv, sv, kc, vc, slots,
             pos, table, max_positions, rot, 1 if interleaved else 0, T, Hq, H, d, bs, nb, _DTYPE[dt], code, ks, vs, ws)
 
@@ -398,8 +402,10 @@ def pa_decode_weights(out, weights_out, q, k_cache, v_cache, block_tables, seq_l
     if (out.shape != shape or v_cache.shape != cache or rows != B or seq_lens.shape != (B,) or (wB, wH) != (B, Hkv) or
             (weights_in is not None and weights_in.shape != wshape)):
         raise ValueError("shape mismatch")
-    code = _cache_code(k_cache, k_scale, Hkv)
-    _need_scales(code, k_scale, v_scale, Hkv)
+    code = _DTYPE[k_cache.dtype]
+    if code >= PA_FP8_E4M3:
+        code = _cache_code(k_cache, k_scale, Hkv)
+        _need_scales(code, k_scale, v_scale, Hkv)
     _invoke("pa_decode_weights", device, stream, _lib().pa_decode_weights, po, pw, pi, stride, pq, kc, vc, bt, width, sl, B,
             Hq, Hkv, d, bs, nb, float(scale), _DTYPE[q.dtype], code, ks, vs, ws, workspace.numel())
 

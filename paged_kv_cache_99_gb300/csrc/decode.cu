@@ -1234,11 +1234,17 @@ __global__ void __maxnreg__(112) combine_cascade_kernel(const DecodeParams p) {
 // score is 4 bytes per query head, written and read once, against 512 bytes of K and V (256
 // for FP8) per token and KV head; reading K a second time instead would cost 256 (128).
 // Scores stay in 32 bits: a 16-bit score or exponential would cost the weights 2^-9 of
-// themselves.
+// themselves.  They stay in L2 too (stored with evict_last behind a K/V stream that leaves
+// first), and a warp drops the lines it has used, so that they are not written back: 16
+// sequences of up to 32768 over FP8 took 131 us with plain stores, 119 so.
 // Every warp takes one run of consecutive units, all of the same size: it finds its place
 // in the flattened order while it waits for the combine, loads the heads' (M, 1 / L) once
 // per (sequence, KV head), and then only streams, a key per lane with kKeys of them in
-// flight (their scores are contiguous).
+// flight (their scores are contiguous).  The two kernels of a call beside pa_decode's own
+// times: 226 us against 212 (40 x 8192 tokens, 32/8 heads, fp16), 113 against 99 (16 of up
+// to 32768, 64/8, FP8), 39 against 36 (64 of up to 4096, 12/2, bf16), 10.3 against 7.7 (four
+// short sequences).  In one launch with the combine, whose 112 registers leave half the
+// warps, the first takes 10 us more.
 template <int Pitch>
 __global__ void __launch_bounds__(256) weights_kernel(const DecodeParams p) {
     constexpr int kKeys = Pitch <= 4 ? 4 : 2;    // keys of a lane in flight
