@@ -517,7 +517,7 @@ PA_API pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int32_t* src
  *                  beyond that PA_ERR_UNSUPPORTED), otherwise must not overlap it
  *   kept           device, int32 [num_seqs][num_kv_heads][budget]
  *   seq_lens_out   device, int32 [num_seqs]; not seq_lens itself
- *   new_tables     device, int32 [num_seqs][max_new_blocks_per_seq] with
+ *   new_tables     device, int32 [num_seqs][max_new_blocks_per_seq], not block_tables itself, with
  *                  max_new_blocks_per_seq * block_size >= min(budget, max_blocks_per_seq *
  *                  block_size); entries past ceil(left / block_size) are never read.  Its
  *                  blocks must be distinct and none may be read by the call (the result is

@@ -916,7 +916,7 @@ pa_status pa_evict(int32_t* kept, int32_t* seq_lens_out, float* weights_out, con
     if (weight_stride < cap || weight_stride % 4) return PA_ERR_INVALID_ARG;
     if (num_seqs == 0) return PA_OK;
     if (!kept || !seq_lens_out || !weights_out || !weights || !k_cache || !v_cache || !block_tables || !seq_lens ||
-        !new_tables || seq_lens_out == seq_lens)
+        !new_tables || seq_lens_out == seq_lens || new_tables == block_tables)
         return PA_ERR_INVALID_ARG;
     if (!aligned(weights, 16) || !aligned(weights_out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
         !aligned(kept, 4) || !aligned(seq_lens_out, 4) || !aligned(seq_lens, 4) || !aligned(block_tables, 4) ||

@@ -150,6 +150,13 @@ def test_in_place(weights):
     c.check(wout=c.dw, in_place=True)
 
 
+def test_many_long_rows():
+    # more CTAs than SMs, each with more keys than shared memory holds without asking
+    c = Case(19, [100000] * 20, 1, "fp8", 32, 300, 4, 64).device()
+    c.call(wout=c.dw)
+    c.check(wout=c.dw, in_place=True)
+
+
 def test_a_row_too_long_to_stage():
     c = Case(13, [400000], 1, "fp8", 32, 1000, 4, 64, weights=_few_values).device()
     with pytest.raises(pa.PagedAttentionError):

@@ -202,6 +202,34 @@ def test_graph_replay_and_another_stream():
     c.check(False, k0, v0)
 
 
+def test_no_tokens_and_one_token_of_any_stride():
+    c = Case(11, 5, 8, 2, 64, "bf16", "bf16", 16)
+    q, k, v = c.parts()
+    k0, v0 = c.kc.clone(), c.vc.clone()
+    args = (c.kc, c.vc, c.slots[:0], c.positions[:0], c.cos_sin)
+    pa.pa_rope_and_cache(c.q_out[:0], q[:0], k[:0], v[:0], *args)
+    assert torch.equal(c.kc, k0) and torch.equal(c.vc, v0) and bool((c.q_out == 3.0).all())
+    # a single token: its stride means nothing, an odd one included
+    one = torch.empty(4096, dtype=torch.bfloat16, device=DEV)
+    views = [one[i:i + h * 128].as_strided((1, h, 128), (7, 128, 1)) for i, h in ((0, 8), (1024, 2), (1280, 2))]
+    for view, part in zip(views, (q, k, v)):
+        view.copy_(part[3:4])
+    pa.pa_rope_and_cache(c.q_out[:1], *views, c.kc, c.vc, c.slots[3:4], c.positions[3:4], c.cos_sin)
+    got = c.q_out[0].clone()
+    pa.pa_rope_and_cache(c.q_out, q, k, v, k0, v0, c.slots, c.positions, c.cos_sin)
+    assert torch.equal(got, c.q_out[3])
+    at = int(c.slots[3])
+    assert torch.equal(c.kc[at // 16, :, at % 16], k0[at // 16, :, at % 16])
+
+
+def test_the_tensors_device_is_made_current(monkeypatch):
+    c = Case(12, 40, 8, 2, 128, "bf16", "bf16", 16)
+    k0, v0 = c.kc.clone(), c.vc.clone()
+    monkeypatch.setattr(pa, "_current_device", lambda: -1)        # as if another device were
+    c.call(True)
+    c.check(True, k0, v0)
+
+
 def test_refusals():
     c = Case(10, 6, 8, 2, 64, "bf16", "fp8", 16)
     q, k, v = c.parts()

@@ -201,6 +201,16 @@ def test_graph_replay_and_another_stream():
     _check(w, wout, torch.zeros_like(wout), ref, base)
 
 
+def test_no_sequences_and_only_empty_ones():
+    w = _case(39, 4, lens=[0, 0, 0])
+    wout = torch.full((3, 2, _stride(w)), 2.0, device=DEV)
+    out = _call(w, _workspace(w), wout)
+    assert bool((out == 0).all()) and bool((wout == 2.0).all())
+    e = lambda t: t[:0]  # noqa: E731
+    pa.pa_decode_weights(e(out), e(wout), e(w.q[0]), w.k_cache[0], w.v_cache[0], e(w.block_tables), e(w.seq_lens),
+                         w.scale, pa.new_workspace_weights(0, 8, 2, 0))
+
+
 def test_refusals():
     w = _case(38, 4, "fp8", lens=[20, 30])
     ws = _workspace(w)
