@@ -350,7 +350,10 @@ PA_API pa_status pa_decode_ex(void* out, const void* q, const void* k_cache, con
  *   workspace      pa_workspace_size_weights bytes.  A batch with more tokens than the
  *                  workspace holds scores for is recorded as PA_ERR_WORKSPACE in its status
  *                  word: out is computed, weights_out is left as it was
- * Other arguments as pa_decode; out agrees with pa_decode's exactly.
+ * Other arguments as pa_decode; out agrees with pa_decode's exactly.  The last queries of a
+ * prompt can be observed the same way before an eviction: one row for each, all with the
+ * prompt's block table, seq_lens = its position + 1, and a row of weights_out of its own
+ * (added up afterwards).
  */
 PA_API pa_status pa_decode_weights(void* out, float* weights_out, const float* weights_in, long long weight_stride,
                                    const void* q, const void* k_cache, const void* v_cache,

@@ -271,12 +271,14 @@ def pa_workspace_size_weights(num_seqs: int, num_q_heads: int, num_kv_heads: int
 
 
 def new_workspace_weights(num_seqs: int, num_q_heads: int, num_kv_heads: int, max_tokens: int, device=None) -> torch.Tensor:
-    """Zeroed workspace for pa_decode_weights with up to max_tokens cached tokens in all
-    (each sequence's length rounded up to 16)."""
+    """Workspace for pa_decode_weights with up to max_tokens cached tokens in all (each sequence's
+    length rounded up to 16); only its head is zeroed, the scores need not be."""
     n = pa_workspace_size_weights(num_seqs, num_q_heads, num_kv_heads, max_tokens)
     if n == 0:
         raise ValueError("invalid workspace arguments")
-    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+    ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    ws[:256].zero_()
+    return ws
 
 
 def new_workspace(num_seqs: int, num_q_heads: int, num_kv_heads: int, device=None,

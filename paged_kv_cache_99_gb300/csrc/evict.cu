@@ -118,7 +118,7 @@ __device__ __forceinline__ void copy_kept(const EvictParams& p, int s, int h, co
 // about 15).  With the copy a launch of its own, 64 sequences of up to 4096 tokens took
 // 20.5 us, now 18.4; the largest batches take the same.
 template <int Threads, bool Staged, bool Fp8>
-__global__ void __launch_bounds__(Threads, Threads == 1024 ? 1 : 1536 / Threads) evict_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(Threads, Threads == 1024 ? 1 : Threads == 512 ? 3 : 4) evict_kernel(const EvictParams p) {
     constexpr int kWarps = Threads / 32;
     constexpr int kOwn = kBins / Threads;        // bins a thread owns
     extern __shared__ uint4 staged[];            // keys of the CTA's part, from t0 on

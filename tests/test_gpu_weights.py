@@ -201,6 +201,18 @@ def test_graph_replay_and_another_stream():
     _check(w, wout, torch.zeros_like(wout), ref, base)
 
 
+def test_observing_the_last_queries_of_a_prompt():
+    # one row per query over the same table, each up to its own position; the sums added up
+    w = _case(40, 4, lens=[300] + [7] * 5)
+    n = torch.arange(295, 301, device=DEV, dtype=torch.int32)
+    w.block_tables = w.block_tables[:1].repeat(6, 1).contiguous()
+    w.seq_lens = n
+    wout = torch.zeros(6, 2, _stride(w), device=DEV)
+    _call(w, _workspace(w), wout)
+    _check(w, wout, torch.zeros_like(wout), _reference(w, range(6)))
+    assert float((wout.double().sum((0, 2)) - 24).abs().max()) < 1e-4        # 6 rows of 4 heads per KV head
+
+
 def test_no_sequences_and_only_empty_ones():
     w = _case(39, 4, lens=[0, 0, 0])
     wout = torch.full((3, 2, _stride(w)), 2.0, device=DEV)
