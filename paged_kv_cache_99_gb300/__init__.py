@@ -1,14 +1,17 @@
-"""Paged-KV-cache attention on one GB300 (sm_103a): a thin ctypes binding of libpa.so.
+"""Paged-KV-cache attention on one GB300 (sm_103a): a thin binding of libpa.so.
 
 Every function here only marshals torch tensors into the C ABI declared in
 ``include/pa.h`` (pointers, sizes, dtypes, the current CUDA stream) and raises
 ``PagedAttentionError`` on a non-zero status; all the work runs in the
-library's CUDA kernels.  There is no CPU fallback: if libpa.so is missing the
+library's CUDA kernels.  Most go through ctypes; those that are called many
+times a step and check many tensors go through a small extension module
+(csrc/binding.c).  There is no CPU fallback: if libpa.so is missing the
 import of the binding fails loudly.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import numpy as np
@@ -142,86 +145,30 @@ def _need(t: torch.Tensor, name: str, dtypes=None):
         raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
 
 
-# The calls below check a dozen tensors each and launch kernels of a few microseconds, so
-# their checks take one pass over the tensors and few attribute reads.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda device: torch.cuda.current_stream(device).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-_16BIT = (torch.bfloat16, torch.float16)
-_CACHE = (torch.bfloat16, torch.float16, torch.uint8, torch.float8_e4m3fn)
-_F32, _I32, _I64, _U8 = (torch.float32,), (torch.int32,), (torch.int64,), (torch.uint8,)
-_F32_OR_NONE, _U8_OR_NONE = (torch.float32, None), (torch.uint8, None)
+_BINDING = None
 
 
-def _device_of(t, name: str) -> int:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    return t.get_device()
+def _calls():
+    """The extension module of csrc/binding.c."""
+    global _BINDING
+    if _BINDING is None:
+        _lib()
+        path = build_ext.BINDING_PATH
+        if not os.path.exists(path):
+            raise ImportError(f"{path} is not built; run __graft_entry__.build() "
+                              "or python -m paged_kv_cache_99_gb300.build_ext")
+        spec = importlib.util.spec_from_file_location("_binding", path)
+        _BINDING = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_BINDING)
+    return _BINDING
 
 
-def _refuse(device: int, t, name: str, dtypes) -> None:
-    """Why a tensor is not a contiguous one of these types on the device."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
-    raise ValueError(f"{name} must be contiguous")
-
-
-def _pointers(device: int, *tensors) -> list:
-    """Addresses of (tensor, name, dtypes): contiguous tensors of one of the types on the device (None
-    where that is among the types: an argument that may be left out)."""
-    out = []
-    try:
-        for t, name, dtypes in tensors:
-            if t is None and None in dtypes:
-                out.append(None)
-            elif t.get_device() == device and t.dtype in dtypes and t.is_contiguous():
-                out.append(t.data_ptr())
-            else:
-                _refuse(device, t, name, dtypes)
-    except AttributeError:                       # not a tensor
-        _refuse(device, t, name, dtypes)
-    return out
-
-
-def _rows(device: int, t, name: str, dtype):
-    """(address, elements between tokens, shape) of [tokens, heads, head_dim] with each token's heads
-    contiguous and any stride between tokens."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != device or t.dtype is not dtype:
-        _refuse(device, t, name, (dtype,))
-    shape = t.shape
-    if len(shape) != 3:
-        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
-    n, heads, d = shape
-    st, sh, sd = t.stride()
-    if n and ((sd != 1 and d > 1) or (sh != d and heads > 1)):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), st if n > 1 else heads * d, shape          # a single token's stride means nothing
-
-
-def _need_scales(code: int, k_scale, v_scale, num_kv_heads: int) -> None:
-    """An FP8 cache has float32 scales for K and V, both one per tensor or both one per KV head."""
-    want = num_kv_heads if code == PA_FP8_E4M3_PER_HEAD else 1
-    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if t is None:
-            raise TypeError(f"{n}: an FP8 cache needs its scales")
-        if t.numel() != want:
-            raise ValueError(f"{n}: {t.numel()} scales where {want} are expected")
-
-
-def _invoke(what: str, device: int, stream, fn, *args) -> None:
-    """fn(*args, stream) with the tensors' device current; the default stream is that device's current one."""
-    raw = _raw_stream(device) if stream is None else stream.cuda_stream
-    if device == _current_device():
-        status = fn(*args, raw)
-    else:
-        with torch.cuda.device(device):
-            status = fn(*args, raw)
-    if status != PA_OK:
-        raise PagedAttentionError(status, what)
+def _raw(stream):
+    """A stream's handle; None: the current one of the tensors' device."""
+    return None if stream is None else stream.cuda_stream
 
 
 def _cache_code(cache, k_scale, num_kv_heads: int) -> int:
@@ -322,13 +269,19 @@ def pa_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = PA_R
 def pa_rope_table(cos_sin, freqs, attention: float = 1.0, stream=None):
     """Table of a set of frequencies (host float64 [rot / 2]): cos_sin float32 [max_positions, rot],
     cosines then sines of position x frequency, both times attention."""
-    device = _device_of(cos_sin, "cos_sin")
-    ptr, = _pointers(device, (cos_sin, "cos_sin", _F32))
+    _need(cos_sin, "cos_sin", (torch.float32,))
     f = np.ascontiguousarray(freqs, dtype=np.float64)
     if cos_sin.dim() != 2 or f.ndim != 1 or cos_sin.shape[1] != 2 * f.size:
         raise ValueError("cos_sin must be [max_positions, 2 * len(freqs)]")
-    _invoke("pa_rope_table", device, stream, _lib().pa_rope_table, ptr, cos_sin.shape[0], cos_sin.shape[1],
-            f.ctypes.data, float(attention))
+    device = cos_sin.get_device()
+    args = (cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], f.ctypes.data, float(attention),
+            _raw_stream(device) if stream is None else stream.cuda_stream)
+    if device == _current_device():
+        status = _lib().pa_rope_table(*args)
+    else:
+        with torch.cuda.device(device):
+            status = _lib().pa_rope_table(*args)
+    _check(status, "pa_rope_table")
 
 
 def pa_rope_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, interleaved: bool = False,
@@ -336,34 +289,8 @@ def pa_rope_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions,
     """Slot write with rotary positions: q_out [T, H_q, 128] = q turned by positions[T] (int64), k [T, H_kv, 128]
     turned and v stored at slot_mapping[T] (int64).  q, k and v may be views of one projection (the heads of a
     token contiguous, any stride between tokens); cos_sin float32 [max_positions, rot] as pa_rope_table builds it."""
-    device = _device_of(q, "q")
-    dt = q.dtype
-    if dt not in _16BIT:
-        raise TypeError(f"q: dtype {dt} not in {_16BIT}")
-    po, so, out_shape = _rows(device, q_out, "q_out", dt)
-    pq, sq, q_shape = _rows(device, q, "q", dt)
-    pk, sk, k_shape = _rows(device, k, "k", dt)
-    pv, sv, v_shape = _rows(device, v, "v", dt)
-    T, Hq, d = q_shape
-    Tk, H, dk = k_shape
-    kc, vc, slots, pos, table, ks, vs, ws = _pointers(
-        device, (k_cache, "k_cache", _CACHE), (v_cache, "v_cache", (k_cache.dtype,)),
-        (slot_mapping, "slot_mapping", _I64), (positions, "positions", _I64), (cos_sin, "cos_sin", _F32),
-        (k_scale, "k_scale", _F32_OR_NONE), (v_scale, "v_scale", _F32_OR_NONE),
-        (workspace, "workspace", _U8_OR_NONE))
-    nb, Hc, bs, dc = shape = k_cache.shape
-    max_positions, rot = cos_sin.shape
-    if (out_shape != q_shape or Tk != T or dk != d or v_shape != k_shape or v_cache.shape != shape or Hc != H or
-            dc != d or slot_mapping.shape != (T,) or positions.shape != (T,)):
-        raise ValueError("shape mismatch")
-    if workspace is not None and workspace.numel() < 256:
-        raise ValueError("workspace: at least 256 bytes")
-    code = _DTYPE[k_cache.dtype]
-    if code >= PA_FP8_E4M3:
-        code = _cache_code(k_cache, k_scale, H)
-        _need_scales(code, k_scale, v_scale, H)
-    _invoke("pa_rope_and_cache", device, stream, _lib().pa_rope_and_cache, po, so, pq, sq, pk, sk, pv, sv, kc, vc, slots,
-            pos, table, max_positions, rot, 1 if interleaved else 0, T, Hq, H, d, bs, nb, _DTYPE[dt], code, ks, vs, ws)
+    _check(_calls().rope_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, interleaved,
+                                   k_scale, v_scale, workspace, _raw(stream)), "pa_rope_and_cache")
 
 
 def pa_decode(out, q, k_cache, v_cache, block_tables, seq_lens, scale, workspace, k_scale=None, v_scale=None,
@@ -391,25 +318,8 @@ def pa_decode_weights(out, weights_out, q, k_cache, v_cache, block_tables, seq_l
                       k_scale=None, v_scale=None, stream=None):
     """pa_decode that also writes weights_out [B, H_kv, >= tokens of the table] (float32) = weights_in (or
     zeros) + the step's softmax weights summed over each group's query heads; weights_in may be weights_out."""
-    device = _device_of(q, "q")
-    po, pw, pi, pq, kc, vc, bt, sl, ks, vs, ws = _pointers(
-        device, (out, "out", (q.dtype,)), (weights_out, "weights_out", _F32), (weights_in, "weights_in", _F32_OR_NONE),
-        (q, "q", _16BIT), (k_cache, "k_cache", _CACHE), (v_cache, "v_cache", (k_cache.dtype,)),
-        (block_tables, "block_tables", _I32), (seq_lens, "seq_lens", _I32), (k_scale, "k_scale", _F32_OR_NONE),
-        (v_scale, "v_scale", _F32_OR_NONE), (workspace, "workspace", _U8))
-    B, Hq, d = shape = q.shape
-    nb, Hkv, bs, _ = cache = k_cache.shape
-    rows, width = block_tables.shape
-    wB, wH, stride = wshape = weights_out.shape
-    if (out.shape != shape or v_cache.shape != cache or rows != B or seq_lens.shape != (B,) or (wB, wH) != (B, Hkv) or
-            (weights_in is not None and weights_in.shape != wshape)):
-        raise ValueError("shape mismatch")
-    code = _DTYPE[k_cache.dtype]
-    if code >= PA_FP8_E4M3:
-        code = _cache_code(k_cache, k_scale, Hkv)
-        _need_scales(code, k_scale, v_scale, Hkv)
-    _invoke("pa_decode_weights", device, stream, _lib().pa_decode_weights, po, pw, pi, stride, pq, kc, vc, bt, width, sl, B,
-            Hq, Hkv, d, bs, nb, float(scale), _DTYPE[q.dtype], code, ks, vs, ws, workspace.numel())
+    _check(_calls().decode_weights(out, weights_out, q, k_cache, v_cache, block_tables, seq_lens, scale, workspace,
+                                   weights_in, k_scale, v_scale, _raw(stream)), "pa_decode_weights")
 
 
 def pa_decode_append(out, q, k_new, v_new, slot_mapping, k_cache, v_cache, block_tables, seq_lens, scale, workspace,
@@ -541,23 +451,8 @@ def pa_evict(kept, seq_lens_out, weights_out, weights, k_cache, v_cache, block_t
     """Brings every sequence to at most budget tokens: the first sinks and last recent tokens stay, and for
     each KV head those of the largest weights ([B, H_kv, >= tokens of the table] float32) between them; their
     K and V rows move to the blocks of new_tables, their places before go to kept [B, H_kv, budget] (int32)."""
-    device = _device_of(k_cache, "k_cache")
-    kc, vc, pw, pwo, pk, plo, bt, sl, nt, ws = _pointers(
-        device, (k_cache, "k_cache", _CACHE), (v_cache, "v_cache", (k_cache.dtype,)), (weights, "weights", _F32),
-        (weights_out, "weights_out", _F32), (kept, "kept", _I32), (seq_lens_out, "seq_lens_out", _I32),
-        (block_tables, "block_tables", _I32), (seq_lens, "seq_lens", _I32), (new_tables, "new_tables", _I32),
-        (workspace, "workspace", _U8_OR_NONE))
-    nb, H, bs, d = shape = k_cache.shape
-    B, wH, stride = wshape = weights.shape
-    rows, width = block_tables.shape
-    new_rows, new_width = new_tables.shape
-    if (v_cache.shape != shape or wH != H or weights_out.shape != wshape or kept.shape != (B, H, budget) or
-            seq_lens.shape != (B,) or seq_lens_out.shape != (B,) or rows != B or new_rows != B):
-        raise ValueError("shape mismatch")
-    if workspace is not None and workspace.numel() < 256:
-        raise ValueError("workspace: at least 256 bytes")
-    _invoke("pa_evict", device, stream, _lib().pa_evict, pk, plo, pwo, pw, stride, kc, vc, bt, width, sl, nt, new_width, B,
-            int(budget), int(sinks), int(recent), H, d, bs, nb, _DTYPE[k_cache.dtype], ws)
+    _check(_calls().evict(kept, seq_lens_out, weights_out, weights, k_cache, v_cache, block_tables, seq_lens, new_tables,
+                          budget, sinks, recent, workspace, _raw(stream)), "pa_evict")
 
 
 class BlockPool:

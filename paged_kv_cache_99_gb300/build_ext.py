@@ -1,4 +1,5 @@
-"""Builds libpa.so in-tree with nvcc for sm_103a (parallel compiles, no cmake)."""
+"""Builds libpa.so in-tree with nvcc for sm_103a (parallel compiles, no cmake), and the Python
+calls over it (csrc/binding.c) with the C compiler."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -6,6 +7,7 @@ import os
 import platform
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -16,6 +18,8 @@ SOURCES = ["pa_api.cu", "decode.cu", "chunk_tc.cu", "reshape_and_cache.cu", "sel
 HEADERS = ["pa_device.cuh", "pa_internal.h"]
 BUILD_DIR = os.path.join(HERE, "_build", platform.machine())
 LIB_PATH = os.path.join(BUILD_DIR, "libpa.so")
+BINDING = "binding.c"
+BINDING_PATH = os.path.join(BUILD_DIR, "_binding" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -27,10 +31,10 @@ def _nvcc() -> str:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
         return True
-    t = os.path.getmtime(LIB_PATH)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(INCLUDE, "pa.h"), __file__]
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
+    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + [BINDING]] + [os.path.join(INCLUDE, "pa.h"), __file__]
     return any(os.path.getmtime(p) > t for p in deps)
 
 
@@ -63,7 +67,20 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB_PATH)
+    _build_binding()
     return LIB_PATH
+
+
+def _build_binding() -> None:
+    """The extension module of the calls in csrc/binding.c, beside libpa.so and linked to it."""
+    tmp = BINDING_PATH + f".{os.getpid()}.tmp"
+    cmd = [shutil.which("gcc") or shutil.which("cc") or "cc", "-O2", "-shared", "-fPIC", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, BINDING), "-o", tmp,
+           "-L", BUILD_DIR, "-l:libpa.so", "-Wl,-rpath,$ORIGIN"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"building {BINDING} failed:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, BINDING_PATH)
 
 
 if __name__ == "__main__":

@@ -223,11 +223,12 @@ def test_no_tokens_and_one_token_of_any_stride():
 
 
 def test_the_tensors_device_is_made_current(monkeypatch):
-    c = Case(12, 40, 8, 2, 128, "bf16", "bf16", 16)
-    k0, v0 = c.kc.clone(), c.vc.clone()
+    f = pa.pa_rope_frequencies(64)
+    t, u = torch.zeros(500, 64, device=DEV), torch.zeros(500, 64, device=DEV)
+    pa.pa_rope_table(t, f)
     monkeypatch.setattr(pa, "_current_device", lambda: -1)        # as if another device were
-    c.call(True)
-    c.check(True, k0, v0)
+    pa.pa_rope_table(u, f)
+    assert torch.equal(t, u) and torch.cuda.current_device() == t.get_device()
 
 
 def test_refusals():
