@@ -145,9 +145,6 @@ def _need(t: torch.Tensor, name: str, dtypes=None):
         raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
 
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-    (lambda device: torch.cuda.current_stream(device).cuda_stream)
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _BINDING = None
 
 
@@ -269,19 +266,10 @@ def pa_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = PA_R
 def pa_rope_table(cos_sin, freqs, attention: float = 1.0, stream=None):
     """Table of a set of frequencies (host float64 [rot / 2]): cos_sin float32 [max_positions, rot],
     cosines then sines of position x frequency, both times attention."""
-    _need(cos_sin, "cos_sin", (torch.float32,))
     f = np.ascontiguousarray(freqs, dtype=np.float64)
-    if cos_sin.dim() != 2 or f.ndim != 1 or cos_sin.shape[1] != 2 * f.size:
-        raise ValueError("cos_sin must be [max_positions, 2 * len(freqs)]")
-    device = cos_sin.get_device()
-    args = (cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], f.ctypes.data, float(attention),
-            _raw_stream(device) if stream is None else stream.cuda_stream)
-    if device == _current_device():
-        status = _lib().pa_rope_table(*args)
-    else:
-        with torch.cuda.device(device):
-            status = _lib().pa_rope_table(*args)
-    _check(status, "pa_rope_table")
+    if f.ndim != 1:
+        raise ValueError("freqs must have one dimension")
+    _check(_calls().rope_table(cos_sin, f, attention, _raw(stream)), "pa_rope_table")
 
 
 def pa_rope_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, interleaved: bool = False,

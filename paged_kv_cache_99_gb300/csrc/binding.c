@@ -3,8 +3,8 @@
  * graph: they check a dozen tensors each and launch kernels of a few microseconds, so the
  * checks are made here rather than in Python and the arguments passed without ctypes (host
  * time of a call on the Grace cores: the rotation 11.0 -> 5.2 us, the decode with attention
- * weights, three launches, 13.5 -> 8, the eviction 10 -> 4.5).  Same rules as the package's
- * other calls: TypeError for what is no CUDA tensor or of another type, ValueError
+ * weights, three launches, 13.5 -> 8, the eviction 10 -> 4.5, the table 6 -> 3).  Same rules
+ * as the package's other calls: TypeError for what is no CUDA tensor or of another type, ValueError
  * for a wrong shape, layout or device; the tensors' device is current for the call, the
  * default stream is that device's current one.  Each returns the library's status.
  */
@@ -22,7 +22,7 @@ static const char* const type_names[NUM_TYPES] = {"bfloat16", "float16", "uint8"
 static PyObject* types[NUM_TYPES];
 static PyTypeObject* tensor_type;
 static PyObject *s_dtype, *s_shape, *s_stride, *s_get_device, *s_data_ptr, *s_is_contiguous;
-static PyObject *f_raw_stream, *f_get_device, *f_set_device;
+static PyObject *torch_c, *s_raw_stream, *s_current_device, *s_set_device;   /* torch._C and its functions */
 
 typedef struct {
     void* ptr;
@@ -166,15 +166,15 @@ static int enter(long long device, PyObject* stream, void** raw, long long* back
     long long s, current;
     PyObject* dev = PyLong_FromLongLong(device);
     if (!dev) return -1;
-    if (as_int(stream == Py_None ? PyObject_CallOneArg(f_raw_stream, dev) : Py_NewRef(stream), &s) ||
-        as_int(PyObject_CallNoArgs(f_get_device), &current)) {
+    if (as_int(stream == Py_None ? PyObject_CallMethodOneArg(torch_c, s_raw_stream, dev) : Py_NewRef(stream), &s) ||
+        as_int(PyObject_CallMethodNoArgs(torch_c, s_current_device), &current)) {
         Py_DECREF(dev);
         return -1;
     }
     *raw = (void*)s;
     *back = -1;
     if (current != device) {
-        PyObject* r = PyObject_CallOneArg(f_set_device, dev);
+        PyObject* r = PyObject_CallMethodOneArg(torch_c, s_set_device, dev);
         if (!r) {
             Py_DECREF(dev);
             return -1;
@@ -188,7 +188,9 @@ static int enter(long long device, PyObject* stream, void** raw, long long* back
 
 static PyObject* leave(long long back, pa_status status) {
     if (back >= 0) {
-        PyObject* r = PyObject_CallFunction(f_set_device, "L", back);
+        PyObject* dev = PyLong_FromLongLong(back);
+        PyObject* r = dev ? PyObject_CallMethodOneArg(torch_c, s_set_device, dev) : NULL;
+        Py_XDECREF(dev);
         if (!r) return NULL;
         Py_DECREF(r);
     }
@@ -199,6 +201,28 @@ static int want_args(Py_ssize_t n, Py_ssize_t want) {
     if (n == want) return 0;
     PyErr_Format(PyExc_TypeError, "%zd arguments, not %zd", want, n);
     return -1;
+}
+
+/* cos_sin, freqs (a buffer of float64), attention, stream */
+static PyObject* rope_table(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    Tensor t;
+    long long dev, back;
+    void* stream;
+    if (want_args(n, 4) || device_of(a[0], "cos_sin", &dev) || take(a[0], "cos_sin", F32, 2, dev, 0, &t)) return NULL;
+    const double attention = PyFloat_AsDouble(a[2]);
+    if (attention == -1.0 && PyErr_Occurred()) return NULL;
+    Py_buffer f;
+    if (PyObject_GetBuffer(a[1], &f, PyBUF_SIMPLE)) return NULL;
+    PyObject* res = NULL;
+    if (f.len % sizeof(double) || t.shape[1] != 2 * (long long)(f.len / sizeof(double))) {
+        PyErr_SetString(PyExc_ValueError, "cos_sin must be [max_positions, 2 * len(freqs)]");
+    } else if (!enter(dev, a[3], &stream, &back)) {
+        res = leave(back, pa_rope_table(t.ptr, (int)t.shape[0], (int)t.shape[1], f.buf, (float)attention,
+                                        (pa_stream_t)stream));
+    }
+    PyBuffer_Release(&f);
+    return res;
 }
 
 /* q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, interleaved, k_scale, v_scale,
@@ -299,6 +323,7 @@ static PyObject* evict(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 }
 
 static PyMethodDef methods[] = {
+    {"rope_table", (PyCFunction)(void (*)(void))rope_table, METH_FASTCALL, NULL},
     {"rope_and_cache", (PyCFunction)(void (*)(void))rope_and_cache, METH_FASTCALL, NULL},
     {"decode_weights", (PyCFunction)(void (*)(void))decode_weights, METH_FASTCALL, NULL},
     {"evict", (PyCFunction)(void (*)(void))evict, METH_FASTCALL, NULL},
@@ -309,21 +334,19 @@ static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", NULL, -1,
 
 PyMODINIT_FUNC PyInit__binding(void) {
     PyObject* torch = PyImport_ImportModule("torch");
-    PyObject* c = torch ? PyObject_GetAttrString(torch, "_C") : NULL;
-    if (!c) return NULL;
+    if (!torch || !(torch_c = PyObject_GetAttrString(torch, "_C"))) return NULL;
     for (int i = 0; i < NUM_TYPES; ++i)
         if (!(types[i] = PyObject_GetAttrString(torch, type_names[i]))) return NULL;
     if (!(tensor_type = (PyTypeObject*)PyObject_GetAttrString(torch, "Tensor")) ||
-        !(f_raw_stream = PyObject_GetAttrString(c, "_cuda_getCurrentRawStream")) ||
-        !(f_get_device = PyObject_GetAttrString(c, "_cuda_getDevice")) ||
-        !(f_set_device = PyObject_GetAttrString(c, "_cuda_setDevice")) ||
+        !(s_raw_stream = PyUnicode_InternFromString("_cuda_getCurrentRawStream")) ||
+        !(s_current_device = PyUnicode_InternFromString("_cuda_getDevice")) ||
+        !(s_set_device = PyUnicode_InternFromString("_cuda_setDevice")) ||
         !(s_dtype = PyUnicode_InternFromString("dtype")) || !(s_shape = PyUnicode_InternFromString("shape")) ||
         !(s_stride = PyUnicode_InternFromString("stride")) ||
         !(s_get_device = PyUnicode_InternFromString("get_device")) ||
         !(s_data_ptr = PyUnicode_InternFromString("data_ptr")) ||
         !(s_is_contiguous = PyUnicode_InternFromString("is_contiguous")))
         return NULL;
-    Py_DECREF(c);
     Py_DECREF(torch);
     return PyModule_Create(&module);
 }

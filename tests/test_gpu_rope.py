@@ -223,12 +223,17 @@ def test_no_tokens_and_one_token_of_any_stride():
 
 
 def test_the_tensors_device_is_made_current(monkeypatch):
-    f = pa.pa_rope_frequencies(64)
-    t, u = torch.zeros(500, 64, device=DEV), torch.zeros(500, 64, device=DEV)
-    pa.pa_rope_table(t, f)
-    monkeypatch.setattr(pa, "_current_device", lambda: -1)        # as if another device were
-    pa.pa_rope_table(u, f)
-    assert torch.equal(t, u) and torch.cuda.current_device() == t.get_device()
+    # as if device 1 were the current one: device 0 is set for the call, and 1 again behind it
+    c = Case(12, 40, 8, 2, 128, "bf16", "bf16", 16)
+    k0, v0 = c.kc.clone(), c.vc.clone()
+    torch.cuda.synchronize()
+    seen = []
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    monkeypatch.setattr(torch._C, "_cuda_setDevice", seen.append)
+    c.call(True)
+    monkeypatch.undo()
+    assert seen == [0, 1]
+    c.check(True, k0, v0)
 
 
 def test_refusals():
@@ -246,5 +251,14 @@ def test_refusals():
                 dict(cos_sin=c.cos_sin.double())):
         with pytest.raises((TypeError, pa.PagedAttentionError)):
             pa.pa_rope_and_cache(**args(**bad))
+    f = pa.pa_rope_frequencies(64)
+    for table, freqs in ((c.cos_sin, f[:-1]), (c.cos_sin, f.reshape(2, -1)), (c.cos_sin[:, ::2], f[:16]), (c.cos_sin[0], f)):
+        with pytest.raises(ValueError):
+            pa.pa_rope_table(table, freqs)
+    for table in (c.cos_sin.half(), c.cos_sin.cpu(), None):
+        with pytest.raises(TypeError):
+            pa.pa_rope_table(table, f)
+    with pytest.raises(pa.PagedAttentionError):
+        pa.pa_rope_table(c.cos_sin, f * float("inf"))
     with pytest.raises(pa.PagedAttentionError):
         pa.pa_rope_and_cache(**args(cos_sin=c.cos_sin[:, :40].contiguous()))      # 40 components: not a multiple of 16
