@@ -7,9 +7,9 @@
 // go, in order, to the blocks of a new table; the source blocks are only read, so they
 // may be shared with other sequences.
 //
-// One launch.  A cluster of CTAs (one CTA for rows of up to 8192 tokens) takes a row, that
-// is, a sequence and KV head: it finds the k-th largest weight by radix select, writes the
-// kept places in order, and copies their rows.
+// One launch.  A cluster of CTAs (one CTA for rows of up to 8192 tokens, 4096 where there
+// are few rows) takes a row, that is, a sequence and KV head: it finds the k-th largest
+// weight by radix select, writes the kept places in order, and copies their rows.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
