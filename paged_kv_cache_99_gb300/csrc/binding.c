@@ -273,8 +273,8 @@ static PyObject* decode_weights(PyObject* self, PyObject* const* a, Py_ssize_t n
         take_or_none(a[10], "k_scale", F32, 0, dev, &ks) || take_or_none(a[11], "v_scale", F32, 0, dev, &vs))
         return NULL;
     const long long B = q.shape[0], H = kc.shape[1];
-    if (!same_shape(&out, &q) || !same_shape(&vc, &kc) || bt.shape[0] != B || !is(&sl, B, -1, -1) ||
-        !is(&wo, B, H, -1) || (a[9] != Py_None && !same_shape(&wi, &wo)))
+    if (!same_shape(&out, &q) || !same_shape(&vc, &kc) || kc.shape[3] != q.shape[2] || bt.shape[0] != B ||
+        !is(&sl, B, -1, -1) || !is(&wo, B, H, -1) || (a[9] != Py_None && !same_shape(&wi, &wo)))
         return mismatch(), NULL;
     const int code = cache_code(&kc, &ks, &vs, H);
     const double scale = PyFloat_AsDouble(a[7]);
