@@ -292,8 +292,9 @@ def pa_decode(out, q, k_cache, v_cache, block_tables, seq_lens, scale, workspace
     _need(seq_lens, "seq_lens", (torch.int32,))
     _need(workspace, "workspace", (torch.uint8,))
     B, Hq, d = q.shape
-    nb, Hkv, bs, _ = k_cache.shape
-    if out.shape != q.shape or block_tables.shape[0] != B or seq_lens.shape != (B,):
+    nb, Hkv, bs, dk = k_cache.shape
+    if (out.shape != q.shape or dk != d or v_cache.shape != k_cache.shape or
+            block_tables.shape[0] != B or seq_lens.shape != (B,)):
         raise ValueError("shape mismatch")
     st = _lib().pa_decode_ex(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
                              block_tables.shape[1], _ptr(seq_lens), B, Hq, Hkv, d, bs, nb, float(scale),
@@ -326,8 +327,9 @@ def pa_decode_append(out, q, k_new, v_new, slot_mapping, k_cache, v_cache, block
     _need(seq_lens, "seq_lens", (torch.int32,))
     _need(workspace, "workspace", (torch.uint8,))
     B, Hq, d = q.shape
-    nb, Hkv, bs, _ = k_cache.shape
-    if (out.shape != q.shape or block_tables.shape[0] != B or seq_lens.shape != (B,) or
+    nb, Hkv, bs, dk = k_cache.shape
+    if (out.shape != q.shape or dk != d or v_cache.shape != k_cache.shape or
+            block_tables.shape[0] != B or seq_lens.shape != (B,) or
             k_new.shape != (B, Hkv, d) or v_new.shape != k_new.shape or slot_mapping.shape != (B,)):
         raise ValueError("shape mismatch")
     args = (_ptr(out), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(slot_mapping), _ptr(k_cache), _ptr(v_cache),
@@ -353,8 +355,9 @@ def pa_decode_shared_prefix(out, q, k_cache, v_cache, block_tables, seq_lens, pr
     _need(seq_lens, "seq_lens", (torch.int32,))
     _need(workspace, "workspace", (torch.uint8,))
     B, Hq, d = q.shape
-    nb, Hkv, bs, _ = k_cache.shape
-    if out.shape != q.shape or block_tables.shape[0] != B or seq_lens.shape != (B,):
+    nb, Hkv, bs, dk = k_cache.shape
+    if (out.shape != q.shape or dk != d or v_cache.shape != k_cache.shape or
+            block_tables.shape[0] != B or seq_lens.shape != (B,)):
         raise ValueError("shape mismatch")
     st = _lib().pa_decode_shared_prefix(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
                                         block_tables.shape[1], _ptr(seq_lens), B, int(prefix_blocks), Hq, Hkv, d,
@@ -376,9 +379,10 @@ def pa_mixed(out, q, query_start_loc, k_cache, v_cache, block_tables, seq_lens, 
     _need(seq_lens, "seq_lens", (torch.int32,))
     _need(workspace, "workspace", (torch.uint8,))
     total_q, Hq, d = q.shape
-    nb, Hkv, bs, _ = k_cache.shape
+    nb, Hkv, bs, dk = k_cache.shape
     B = seq_lens.shape[0]
-    if out.shape != q.shape or block_tables.shape[0] != B or query_start_loc.shape != (B + 1,):
+    if (out.shape != q.shape or dk != d or v_cache.shape != k_cache.shape or
+            block_tables.shape[0] != B or query_start_loc.shape != (B + 1,)):
         raise ValueError("shape mismatch")
     st = _lib().pa_mixed(_ptr(out), _ptr(q), _ptr(query_start_loc), _ptr(k_cache), _ptr(v_cache),
                          _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), B, total_q, int(max_q_len), Hq,
@@ -398,8 +402,9 @@ def pa_decode_noalloc(out, q, k_cache, v_cache, block_tables, seq_lens, scale, k
     _need(block_tables, "block_tables", (torch.int32,))
     _need(seq_lens, "seq_lens", (torch.int32,))
     B, Hq, d = q.shape
-    nb, Hkv, bs, _ = k_cache.shape
-    if out.shape != q.shape or block_tables.shape[0] != B or seq_lens.shape != (B,):
+    nb, Hkv, bs, dk = k_cache.shape
+    if (out.shape != q.shape or dk != d or v_cache.shape != k_cache.shape or
+            block_tables.shape[0] != B or seq_lens.shape != (B,)):
         raise ValueError("shape mismatch")
     st = _lib().pa_decode_noalloc(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
                                   block_tables.shape[1], _ptr(seq_lens), B, Hq, Hkv, d, bs, nb, float(scale),
@@ -428,6 +433,8 @@ def pa_copy_blocks(k_cache, v_cache, src, dst, workspace=None, stream=None):
     _need(dst, "dst", (torch.int32,))
     if src.shape != dst.shape or src.dim() != 1:
         raise ValueError("src and dst must be 1-D and of equal length")
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("shape mismatch")
     nb, Hkv, bs, d = k_cache.shape
     st = _lib().pa_copy_blocks(_ptr(k_cache), _ptr(v_cache), _ptr(src), _ptr(dst), int(src.numel()), Hkv, d, bs,
                                nb, _DTYPE[k_cache.dtype], _ptr(workspace), _stream(stream))

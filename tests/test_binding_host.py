@@ -57,3 +57,42 @@ def test_decode_weights_wants_a_cache_of_the_querys_head_dimension():
         _weights(v_cache=_t(10, 2, 16, 64))
     with pytest.raises(ValueError):
         _weights(k_cache=_t(10, 2, 16, 256), v_cache=_t(10, 2, 16, 256))
+
+
+def _q(B=2):
+    return dict(out=_t(B, 8, 128), q=_t(B, 8, 128), scale=0.088)
+
+
+def _batch(B=2):
+    return dict(block_tables=_t(B, 4, dtype=torch.int32), seq_lens=_t(B, dtype=torch.int32))
+
+
+def _calls():
+    ws = dict(workspace=_t(1 << 10, dtype=torch.uint8))
+    new = dict(k_new=_t(2, 2, 128), v_new=_t(2, 2, 128), slot_mapping=_t(2, dtype=torch.int64))
+    return {
+        "pa_decode": dict(**_q(), **_batch(), **ws),
+        "pa_decode_append": dict(**_q(), **_batch(), **ws, **new),
+        "pa_decode_shared_prefix": dict(**_q(), **_batch(), **ws, prefix_blocks=1),
+        "pa_mixed": dict(**_q(), **_batch(), **ws, query_start_loc=_t(3, dtype=torch.int32), max_q_len=1),
+        "pa_decode_noalloc": dict(**_q(), **_batch()),
+        "pa_copy_blocks": dict(src=_t(1, dtype=torch.int32), dst=_t(1, dtype=torch.int32)),
+    }
+
+
+@pytest.mark.parametrize("name", list(_calls()))
+def test_both_caches_have_one_shape_and_the_querys_head_dimension(name):
+    def call(k, v):
+        getattr(pa, name)(k_cache=k, v_cache=v, **_calls()[name])
+
+    good = _t(10, 2, 16, 128)
+    with pytest.raises(_Reached):
+        call(good, good)
+    for other in (_t(5, 2, 16, 128), _t(10, 1, 16, 128), _t(10, 2, 8, 128), _t(10, 2, 16, 64)):
+        with pytest.raises(ValueError):
+            call(good, other)
+        with pytest.raises(ValueError):
+            call(other, good)
+    if name != "pa_copy_blocks":          # no query: the library checks its head dimension
+        with pytest.raises(ValueError):
+            call(_t(10, 2, 16, 64), _t(10, 2, 16, 64))
