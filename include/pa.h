@@ -264,7 +264,9 @@ PA_API int pa_default_workers(void);
  *   q              device, [num_seqs][num_q_heads][128], q_dtype bf16|fp16, 16-byte aligned
  *   k_cache,v_cache device, layout above; cache_dtype == q_dtype, PA_FP8_E4M3 or
  *                  PA_FP8_E4M3_PER_HEAD
- *   block_tables   device, int32 [num_seqs][max_blocks_per_seq]
+ *   block_tables   device, int32 [num_seqs][max_blocks_per_seq]; a table's width in tokens
+ *                  (block_size * max_blocks_per_seq) at most 2^31 - 1024, else
+ *                  PA_ERR_UNSUPPORTED
  *   seq_lens       device, int32 [num_seqs]; each <= block_size * max_blocks_per_seq
  *   scale          softmax scale (e.g. 1/sqrt(128))
  *   k_scale,v_scale device float32 scalars, required iff cache is FP8 (dequant

@@ -159,11 +159,13 @@ pa_status check_attention_args(const void* out, const void* q, const void* k_cac
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
         !aligned(workspace, 256))
         return PA_ERR_INVALID_ARG;
-    // tensor-map rows and flattened 16-key unit counts must fit in 32 bits
+    // tensor-map rows, flattened 16-key unit counts and a sequence's tokens (rounded up to
+    // the steps they are taken in) must fit in 32 bits
     const long long rows = static_cast<long long>(num_blocks) * num_kv_heads * block_size;
     const long long units = static_cast<long long>(num_seqs) * num_kv_heads * head_groups_of(num_q_heads, num_kv_heads);
     const long long per_seq = (static_cast<long long>(max_blocks_per_seq) * block_size + kBlockSize - 1) / kBlockSize;
-    if (rows >= (1ll << 31) || units * per_seq >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
+    if (rows >= (1ll << 31) || units * per_seq >= (1ll << 31) || per_seq * kBlockSize > (1ll << 31) - 1024)
+        return PA_ERR_UNSUPPORTED;
     return PA_OK;
 }
 

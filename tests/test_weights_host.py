@@ -37,3 +37,12 @@ def test_workspace_size_refusals(lib):
     assert f(2, 8, 2, 64, 100) == 0
     assert f(2, 7, 2, 128, 100) == 0
     assert f(2, 8, 2, 128, -1) == 0
+
+
+def test_tables_of_more_tokens_than_32_bits_number(lib):
+    # one KV head: few enough 16-key units, but the kernels number a sequence's tokens in 32 bits
+    one = dict(B=1, Hq=1, Hkv=1)
+    for bs, maxb in ((8, 1 << 28), (16, 1 << 27), (32, 1 << 26), (16, (1 << 27) - 1)):
+        assert _weights(lib, **one, bs=bs, maxb=maxb, stride=bs * maxb) == UNSUPPORTED, (bs, maxb)
+        a = [FAKE, FAKE, FAKE, FAKE, FAKE, maxb, FAKE, 1, 1, 1, 128, bs, 10, 0.088, 0, 0, None, None, FAKE, 1 << 20, None]
+        assert lib.pa_decode(*a) == UNSUPPORTED, (bs, maxb)
