@@ -157,9 +157,10 @@ PA_API pa_status pa_rope_frequencies(double* freqs, int rot_dim, double base, pa
 /*
  * The table of a set of frequencies: for p < max_positions and i < rot_dim / 2
  *   cos_sin[p][i] = attention cos(p f_i),  cos_sin[p][rot_dim / 2 + i] = attention sin(p f_i)
- * to about one unit in the last place of float32 at every position (angles are held
- * modulo one turn in 64-bit fixed point).  Built once; any table of this layout serves
- * pa_rope_and_cache.
+ * each entry to within 3.5 x 2^-24 of itself (two to three units in the last place of
+ * float32 at most, small sines included), but for what the angle itself is off by: it is
+ * held modulo one turn in 64-bit fixed point, up to 2^-54 + p 2^-61 + p |f_i| 2^-52 radians.
+ * Built once; any table of this layout serves pa_rope_and_cache.
  *   cos_sin    device, float32 [max_positions][rot_dim], 16-byte aligned
  *   freqs      host, [rot_dim / 2], finite (read during the call)
  *   attention  factor on both (YaRN's scaling of the logits; 1 for none)

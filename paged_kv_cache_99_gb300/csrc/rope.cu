@@ -26,34 +26,42 @@ namespace {
 // the whole turns fall off the top by themselves, the product with a position is an
 // integer product, and the next position of a thread is one 64-bit addition.  The
 // nearest quarter turn (two bits) picks sine or cosine and sign; the rest, in
-// [-1/2, 1/2) quarter turns, keeps 32 bits and goes to a polynomial in 32-bit floats.
+// [-1/2, 1/2) quarter turns, goes to polynomials in 32-bit floats as the sum of two, so
+// that a sine near zero (a slow component at the first positions) is as exact relative
+// to itself as any other.
 struct RopeTurns {
     unsigned long long turn[kHeadDim / 2];     // f_i / 2 pi in units of 2^-64 turns
 };
 
-// sine and cosine of y quarter turns, |y| <= 1/2: Taylor polynomials in y with
-// (pi / 2)^n / n! folded into the coefficients, to y^9 and y^10 (the first terms left
-// out are under 3e-9 and 5e-11 of the result).
-__device__ __forceinline__ void sincos_quarter(float y, float& sn, float& cs) {
+// sine and cosine of y = a + b quarter turns, |a| <= 1/2 a multiple of 2^-23 and |b| at
+// most half of one: Taylor polynomials in y with (pi / 2)^n / n! folded into the
+// coefficients, to y^9 and y^10 (the first terms left out are under 2.5e-9 and 1.7e-10 of
+// the result).  pi / 2 times a, most of the sine, is added last and so rounded once, with
+// pi / 2 itself in two floats: both results are within 2.2 x 2^-24 of themselves (in one
+// float, with 32 bits of y, the rest cut off: 28 units in the last place at the slowest
+// component of base 10^4, thousands for slower ones).
+__device__ __forceinline__ void sincos_quarter(float a, float b, float& sn, float& cs) {
+    const float y = a + b;
     const float z = y * y;
-    float a = 1.6044118e-4f;                    // (pi/2)^9 / 9!
-    a = fmaf(a, z, -4.6817541e-3f);             // (pi/2)^7 / 7!
-    a = fmaf(a, z, 7.9692626e-2f);              // (pi/2)^5 / 5!
-    a = fmaf(a, z, -6.4596410e-1f);             // (pi/2)^3 / 3!
-    a = fmaf(a, z, 1.5707963e+0f);              // pi/2
-    sn = a * y;
-    float b = -2.5202042e-5f;                   // (pi/2)^10 / 10!
-    b = fmaf(b, z, 9.1926027e-4f);              // (pi/2)^8 / 8!
-    b = fmaf(b, z, -2.0863481e-2f);             // (pi/2)^6 / 6!
-    b = fmaf(b, z, 2.5366951e-1f);              // (pi/2)^4 / 4!
-    b = fmaf(b, z, -1.2337006e+0f);             // (pi/2)^2 / 2!
-    cs = fmaf(b, z, 1.0f);
+    float p = 1.6044118e-4f;                    // (pi/2)^9 / 9!
+    p = fmaf(p, z, -4.6817541e-3f);             // (pi/2)^7 / 7!
+    p = fmaf(p, z, 7.9692626e-2f);              // (pi/2)^5 / 5!
+    p = fmaf(p, z, -6.4596410e-1f);             // (pi/2)^3 / 3!
+    const float rest = fmaf(p, y * z, fmaf(b, 1.5707964f, a * -4.3711388e-8f));
+    sn = fmaf(a, 1.5707964f, rest);             // 1.5707964f - 4.3711388e-8 = pi/2
+    float q = -2.5202042e-5f;                   // (pi/2)^10 / 10!
+    q = fmaf(q, z, 9.1926027e-4f);              // (pi/2)^8 / 8!
+    q = fmaf(q, z, -2.0863481e-2f);             // (pi/2)^6 / 6!
+    q = fmaf(q, z, 2.5366951e-1f);              // (pi/2)^4 / 4!
+    q = fmaf(q, z, -1.2337006e+0f);             // (pi/2)^2 / 2!
+    cs = fmaf(q, z, 1.0f);
 }
 
 // A thread owns four frequencies and every `step`-th position, so that it writes 16
 // bytes of cosines and 16 of sines at a time and a row goes out in whole lines.  Bound by
-// the stores: 524288 positions of 128 (268 MB) take 37.2 us, 7.2 TB/s; 32768 (16.8 MB, it
-// stays in L2) 4.2.  Two CTAs per SM store as fast as more (eight: 38.6 and 6.8 us).
+// the stores and, as closely, by instruction issue: 524288 positions of 128 (268 MB) take
+// 41.0 us, 6.5 TB/s; 32768 (16.8 MB, it stays in L2) 4.5.  (With the rest of a quarter turn
+// in one float, cut to 32 bits, 37.2 and 4.2.)  Two CTAs per SM: four take 40.6 and 5.5.
 __global__ void __launch_bounds__(256) rope_table_kernel(float* __restrict__ cos_sin, int max_positions, int rot_dim,
                                                          const __grid_constant__ RopeTurns turns, float attention) {
     grid_dependency_wait();
@@ -75,16 +83,20 @@ __global__ void __launch_bounds__(256) rope_table_kernel(float* __restrict__ cos
         float c[4], s[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const unsigned long long ph = phase[e] + (1ull << 61);       // half a quarter turn up
-            const unsigned quarter = static_cast<unsigned>(ph >> 62);
-            const int rest = static_cast<int>(static_cast<unsigned>((phase[e] << 2) >> 32));
+            const unsigned hi = static_cast<unsigned>(phase[e] >> 32), lo = static_cast<unsigned>(phase[e]);
+            // half a quarter turn up, and half of 2^-23 more: the top two bits are the quarter,
+            // the next 23 the nearest multiple of 2^-23 quarter turns to the rest (a float
+            // exactly), and of what is left 32 bits are kept
+            const unsigned quarter = hi + (1u << 29) + 64u;
+            const int left = static_cast<int>(__funnelshift_r(lo, hi, 7));
             float sn, cs;
-            sincos_quarter(static_cast<float>(rest) * 0x1p-32f, sn, cs);
-            const bool swap = quarter & 1u;
+            sincos_quarter(fmaf(static_cast<float>(quarter & 0x3fffff80u), 0x1p-30f, -0.5f),
+                           static_cast<float>(left) * 0x1p-55f, sn, cs);
+            const bool swap = quarter & (1u << 30);
             const float x = swap ? sn : cs, y = swap ? cs : sn;
             // cosine is negative in quarters 1 and 2, sine in 2 and 3
-            c[e] = ((quarter + 1u) & 2u ? -x : x) * attention;
-            s[e] = (quarter & 2u ? -y : y) * attention;
+            c[e] = __uint_as_float(__float_as_uint(x) ^ ((quarter + (1u << 30)) & 0x80000000u)) * attention;
+            s[e] = __uint_as_float(__float_as_uint(y) ^ (quarter & 0x80000000u)) * attention;
             phase[e] += inc[e];
         }
         float* row = cos_sin + static_cast<size_t>(p) * rot_dim + 4 * i;
@@ -277,11 +289,12 @@ cudaError_t launch_rope_table(float* cos_sin, int max_positions, int rot_dim, co
                               int sms, cudaStream_t stream) {
     RopeTurns turns = {};
     for (int i = 0; i < rot_dim / 2; ++i) {
-        // f / 2 pi modulo one turn: the quotient is rounded once (2^-53, as an angle p f in
-        // 64 bits would be), its fraction and the product with 2^64 are exact
-        const double t = freqs[i] / kTwoPi;
-        const double frac = t - std::floor(t);
-        turns.turn[i] = frac < 1.0 ? static_cast<unsigned long long>(frac * 0x1p64) : 0ull;
+        // |f| / 2 pi modulo one turn: the quotient is rounded once (2^-53, as an angle p f in
+        // 64 bits would be), its fraction is exact (of a negative quotient it would not be:
+        // 1 - 2^-60 is no double), and the product with 2^64 is cut; the sign comes last
+        const double t = std::fabs(freqs[i]) / kTwoPi;
+        const unsigned long long turn = static_cast<unsigned long long>((t - std::floor(t)) * 0x1p64);
+        turns.turn[i] = std::signbit(freqs[i]) ? 0ull - turn : turn;
     }
     const int rows = 256 / (rot_dim / 8);
     const long long want = (static_cast<long long>(max_positions) + rows - 1) / rows;

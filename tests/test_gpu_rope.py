@@ -41,6 +41,26 @@ def test_table_of_negative_and_zero_frequencies():
     assert float((t.double() - torch.cat((angle.cos(), angle.sin()), 1)).abs().max()) <= 2.0 ** -22
 
 
+@pytest.mark.parametrize("base,factor", [(1e4, 1.0), (5e5, 1.0), (1e6, 16.0), (1e6, -64.0)])
+@pytest.mark.parametrize("rot,positions,attention", [(128, 200, 1.0), (128, 70000, 1.25), (16, 3001, 0.75)])
+def test_table_entries_near_zero(base, factor, rot, positions, attention):
+    """Every entry relative to itself, a slow component's sine at the first positions and
+    a cosine beside a quarter turn included.  Tolerance: the sine and cosine are within
+    2.2 x 2^-24 of themselves (what the polynomials' roundings add up to), the attention
+    factor's product rounds once more; the angle is cut to 2^-55 quarter turns and the
+    component to 2^-64 turns per position (2 pi 2^-64 < 2^-61); its quotient by 2 pi here,
+    and the product with the position in the reference, round to 2^-53 of the angle, the
+    constant 2 pi as well."""
+    f = pa.pa_rope_frequencies(rot, base) / factor
+    t = torch.empty(positions, rot, device=DEV)
+    pa.pa_rope_table(t, f, attention)
+    p = torch.arange(positions, dtype=torch.float64, device=DEV)[:, None]
+    angle = p * torch.from_numpy(f).to(DEV)
+    want = torch.cat((angle.cos(), angle.sin()), 1) * attention
+    off = (2.0 ** -54 + p * 2.0 ** -61 + 3 * 2.0 ** -53 * angle.abs()).repeat(1, 2)
+    assert bool(((t.double() - want).abs() <= 3.5 * 2.0 ** -24 * want.abs() + attention * off).all())
+
+
 class Case:
     def __init__(self, seed, T, Hq, Hkv, rot, src, cache, bs, context=4096):
         g = torch.Generator().manual_seed(seed)
