@@ -148,6 +148,8 @@ PA_API pa_status pa_reshape_and_cache(const void* k, const void* v, void* k_cach
  *   base, factor      > 0 and finite; factor is read by the scaled forms
  *   trained, low_turns, high_turns
  *                     read by PA_ROPE_BY_PARTS: trained > 0, high_turns > low_turns >= 0
+ * Arguments whose frequencies are not all finite are PA_ERR_INVALID_ARG (freqs is left as
+ * it was).
  */
 typedef enum { PA_ROPE_UNSCALED = 0, PA_ROPE_LINEAR = 1, PA_ROPE_BY_PARTS = 2 } pa_rope_scaling;
 

@@ -532,7 +532,11 @@ pa_status pa_rope_frequencies(double* freqs, int rot_dim, double base, pa_rope_s
         (!std::isfinite(trained) || !(trained > 0.0) || !(low_turns >= 0.0) || !(high_turns > low_turns) ||
          !std::isfinite(high_turns)))
         return PA_ERR_INVALID_ARG;
-    rope_frequencies(freqs, rot_dim, base, scaling, factor, trained, low_turns, high_turns);
+    double f[kHeadDim / 2];
+    rope_frequencies(f, rot_dim, base, scaling, factor, trained, low_turns, high_turns);
+    for (int i = 0; i < rot_dim / 2; ++i)
+        if (!std::isfinite(f[i])) return PA_ERR_INVALID_ARG;
+    for (int i = 0; i < rot_dim / 2; ++i) freqs[i] = f[i];
     return PA_OK;
 }
 
