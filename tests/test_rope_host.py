@@ -66,10 +66,13 @@ def test_frequencies_refusals(lib):
 def test_frequencies_that_are_not_finite_are_refused(lib):
     # finite arguments whose formula leaves the range of doubles
     out = np.full(64, 7.0)
-    for base, kind, factor, trained in ((5e-324, 0, 1.0, 0.0), (1e4, 1, 1e-310, 0.0), (1e4, 2, 1e-310, 8192.0)):
+    for base, kind, factor, trained in ((5e-324, 0, 1.0, 0.0), (1e4, 1, 1e-310, 0.0), (1e4, 2, 5e-324, 8192.0)):
         assert lib.pa_rope_frequencies(out.ctypes.data, 128, base, kind, factor, trained, 1.0, 32.0) == INVALID
         assert np.all(out == 7.0)                # nothing is written
     assert lib.pa_rope_frequencies(out.ctypes.data, 128, 1e-300, 0, 1.0, 0.0, 1.0, 32.0) == 0 and np.isfinite(out).all()
+    # the largest blended frequency is 0.0063 / 1e-310: still a double
+    assert lib.pa_rope_frequencies(out.ctypes.data, 128, 1e4, 2, 1e-310, 8192.0, 1.0, 32.0) == 0
+    assert np.isfinite(out).all() and 6e307 < out.max() < 7e307
     # every component turns more than 32 times over 8192 positions: all are kept, factor does not enter
     assert lib.pa_rope_frequencies(out.ctypes.data, 128, 1e-310, 2, 1e-310, 8192.0, 1.0, 32.0) == 0
     np.testing.assert_allclose(out, 1e-310 ** (-2.0 * np.arange(64) / 128), rtol=1e-14)
