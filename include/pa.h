@@ -141,8 +141,15 @@ PA_API pa_status pa_reshape_and_cache(const void* k, const void* v, void* k_cach
  *   PA_ROPE_BY_PARTS  f_i blended with f_i / factor by the turns t = trained f_i / 2 pi
  *                     it makes over the trained length: kept for t >= high_turns, divided
  *                     for t <= low_turns, keep = (t - low_turns) / (high_turns - low_turns)
- *                     between (YaRN's frequencies, "YaRN: Efficient Context Window
- *                     Extension of Large Language Models", s.3.2)
+ *                     between: the ramp in turns of the paper "YaRN: Efficient
+ *                     Context Window Extension of Large Language Models", s.3.2.
+ *                     NOT what most checkpoints released as YaRN were trained with:
+ *                     those blend linearly over the component i, between two bounds
+ *                     rounded to whole components, and differ from this by up to 1.7
+ *                     times (base 10^6, trained 32768, factor 4) or 4.3 times (10^4,
+ *                     4096, 40) between the ends of the ramp.  Compute such
+ *                     frequencies by the checkpoint's own rule and pass them to
+ *                     pa_rope_table, which takes any
  *   freqs             host, [rot_dim / 2]
  *   rot_dim           a multiple of 16, 16 .. 128
  *   base, factor      > 0 and finite; factor is read by the scaled forms

@@ -256,7 +256,9 @@ def pa_reshape_and_cache(k, v, k_cache, v_cache, slot_mapping, k_scale=None, v_s
 def pa_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = PA_ROPE_UNSCALED, factor: float = 1.0,
                         trained: float = 0.0, low_turns: float = 1.0, high_turns: float = 32.0):
     """Rotary frequencies, float64 numpy [rot_dim / 2]; scaling PA_ROPE_LINEAR or PA_ROPE_BY_PARTS
-    (trained: the length the model was trained for) stretches them by factor."""
+    (trained: the length the model was trained for) stretches them by factor.  By parts blends by the
+    turns a component makes; checkpoints that blend over the component's index (most of those released
+    as YaRN) need their own frequencies, which pa_rope_table takes as any others."""
     f = np.zeros(max(int(rot_dim) // 2, 1), dtype=np.float64)
     _check(_lib().pa_rope_frequencies(f.ctypes.data, int(rot_dim), float(base), int(scaling), float(factor),
                                       float(trained), float(low_turns), float(high_turns)), "pa_rope_frequencies")

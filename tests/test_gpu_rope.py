@@ -61,6 +61,21 @@ def test_table_entries_near_zero(base, factor, rot, positions, attention):
     assert bool(((t.double() - want).abs() <= 3.5 * 2.0 ** -24 * want.abs() + attention * off).all())
 
 
+def test_table_of_a_callers_own_frequencies():
+    # a blend over the component's index between two whole components, which by-parts scaling is not
+    base, factor, lo, hi = 1e6, 4.0, 23, 39
+    i = np.arange(64)
+    f = base ** (-2.0 * i / 128)
+    keep = 1 - np.clip((i - lo) / (hi - lo), 0, 1)
+    f = keep * f + (1 - keep) * f / factor
+    by_parts = pa.pa_rope_frequencies(128, base, pa.PA_ROPE_BY_PARTS, factor, 32768)
+    assert int((np.maximum(f / by_parts, by_parts / f) > 1.01).sum()) >= 8
+    t = torch.empty(5000, 128, device=DEV)
+    pa.pa_rope_table(t, f)
+    angle = torch.arange(5000, dtype=torch.float64, device=DEV)[:, None] * torch.from_numpy(f).to(DEV)
+    assert float((t.double() - torch.cat((angle.cos(), angle.sin()), 1)).abs().max()) <= 2.0 ** -22
+
+
 class Case:
     def __init__(self, seed, T, Hq, Hkv, rot, src, cache, bs, context=4096):
         g = torch.Generator().manual_seed(seed)
