@@ -8,6 +8,7 @@ import platform
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -30,18 +31,31 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
+def _stale(path: str, sources) -> bool:
+    if not os.path.exists(path):
         return True
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + [BINDING]] + [os.path.join(INCLUDE, "pa.h"), __file__]
+    t = os.path.getmtime(path)
+    deps = [os.path.join(CSRC, f) for f in sources] + [os.path.join(INCLUDE, "pa.h"), __file__]
     return any(os.path.getmtime(p) > t for p in deps)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every CUDA source and link libpa.so; returns its path."""
-    if not force and not _stale():
-        return LIB_PATH
+    """Compile what is out of date: libpa.so, whose path it returns, and the extension module over
+    it.  Without the latter (no C compiler or no Python headers) there is a warning, and the calls
+    that go through it raise ImportError; the library and all other calls do not need it."""
+    if force or _stale(LIB_PATH, SOURCES + HEADERS):
+        _build_lib(verbose)
+    if force or _stale(BINDING_PATH, [BINDING]):
+        try:
+            _build_binding()
+        except (OSError, RuntimeError) as e:
+            if os.path.exists(BINDING_PATH):
+                os.remove(BINDING_PATH)        # of an older source: not to be called
+            warnings.warn(f"{BINDING} was not built: {e}", RuntimeWarning, stacklevel=2)
+    return LIB_PATH
+
+
+def _build_lib(verbose: bool) -> None:
     os.makedirs(BUILD_DIR, exist_ok=True)
     nvcc = _nvcc()
     common = ARCH_FLAGS + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE,
@@ -67,8 +81,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB_PATH)
-    _build_binding()
-    return LIB_PATH
 
 
 def _build_binding() -> None:
