@@ -14,7 +14,6 @@ import ctypes
 import importlib.util
 import os
 
-import numpy as np
 import torch
 
 from . import build_ext
@@ -259,6 +258,7 @@ def pa_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = PA_R
     (trained: the length the model was trained for) stretches them by factor.  By parts blends by the
     turns a component makes; checkpoints that blend over the component's index (most of those released
     as YaRN) need their own frequencies, which pa_rope_table takes as any others."""
+    import numpy as np
     f = np.zeros(max(int(rot_dim) // 2, 1), dtype=np.float64)
     _check(_lib().pa_rope_frequencies(f.ctypes.data, int(rot_dim), float(base), int(scaling), float(factor),
                                       float(trained), float(low_turns), float(high_turns)), "pa_rope_frequencies")
@@ -268,6 +268,7 @@ def pa_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = PA_R
 def pa_rope_table(cos_sin, freqs, attention: float = 1.0, stream=None):
     """Table of a set of frequencies (host float64 [rot / 2]): cos_sin float32 [max_positions, rot],
     cosines then sines of position x frequency, both times attention."""
+    import numpy as np
     f = np.ascontiguousarray(freqs, dtype=np.float64)
     if f.ndim != 1:
         raise ValueError("freqs must have one dimension")

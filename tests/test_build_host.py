@@ -1,5 +1,7 @@
 """The library builds without what only the extension module of the Python calls needs."""
 import os
+import subprocess
+import sys
 import sysconfig
 
 import pytest
@@ -37,3 +39,11 @@ def test_a_module_that_cannot_be_rebuilt_does_not_stay(no_python_headers):
     with pytest.warns(RuntimeWarning):
         build_ext.build()
     assert not os.path.exists(build_ext.BINDING_PATH)
+
+
+def test_the_package_imports_without_numpy():
+    # only the calls that take or give host arrays need it
+    code = ("import sys; sys.modules['numpy'] = None; import paged_kv_cache_99_gb300 as pa; "
+            "assert pa.pa_version() >= 102; print('imported')")
+    res = subprocess.run([sys.executable, "-W", "ignore", "-c", code], cwd=build_ext.ROOT, capture_output=True, text=True)
+    assert res.stdout.strip().endswith("imported"), res.stderr
