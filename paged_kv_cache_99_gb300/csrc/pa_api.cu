@@ -641,9 +641,11 @@ size_t pa_workspace_size_weights(int num_seqs, int num_q_heads, int num_kv_heads
     const size_t base = pa_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim);
     if (base == 0 || max_tokens < 0 || max_tokens >= (1ll << 40)) return 0;
     const ScoresLayout l = scores_layout(base, num_seqs, num_q_heads, num_kv_heads);
-    const size_t units = static_cast<size_t>((max_tokens + kBlockSize - 1) / kBlockSize) * num_kv_heads *
-                         head_groups_of(num_q_heads, num_kv_heads);
-    return l.scores_off + units * l.unit_bytes;
+    // heads and tokens each fit 64 bits with room; their product may not
+    const size_t per_step = static_cast<size_t>(num_kv_heads) * head_groups_of(num_q_heads, num_kv_heads) * l.unit_bytes;
+    const size_t steps = static_cast<size_t>((max_tokens + kBlockSize - 1) / kBlockSize);
+    if (steps > (SIZE_MAX - l.scores_off) / per_step) return 0;
+    return l.scores_off + steps * per_step;
 }
 
 int pa_default_workers(void) {

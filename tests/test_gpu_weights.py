@@ -235,3 +235,9 @@ def test_refusals():
     with pytest.raises(pa.PagedAttentionError):
         _call(w, ws, good[..., :-1].contiguous())
     assert math.isfinite(float(good.sum()))
+
+
+def test_a_workspace_beyond_64_bits_has_no_size():
+    assert pa.pa_workspace_size_weights(1, 1 << 24, 1 << 24, (1 << 40) - 1) == 0
+    a, b = (pa.pa_workspace_size_weights(1, 1 << 24, 1 << 24, n) for n in (16, 1 << 20))
+    assert b - a == ((1 << 16) - 1) * (1 << 24) * 16 * 2 * 4
