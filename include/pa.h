@@ -282,6 +282,10 @@ PA_API int pa_default_workers(void);
  *   k_scale,v_scale device float32 scalars, required iff cache is FP8 (dequant
  *                  is code * scale)
  *   workspace      see pa_workspace_size
+ * Scores, the softmax and the sums over keys are float32; the probabilities are
+ * rounded to the cache's 16-bit type (fp16 for an FP8 cache) for the product
+ * with V, and with an FP8 cache the query to fp16 (a bf16 query's components
+ * beyond 65504 become infinite).
  * num_seqs <= 8192.  The work is split evenly over the workers by cached
  * blocks; a sequence split across workers is merged by a log-sum-exp combine
  * launched behind the decode kernel on the same stream.  The result does not
@@ -362,7 +366,8 @@ PA_API pa_status pa_decode_ex(void* out, const void* q, const void* k_cache, con
  *   workspace      pa_workspace_size_weights bytes.  A batch with more tokens than the
  *                  workspace holds scores for is recorded as PA_ERR_WORKSPACE in its status
  *                  word: out is computed, weights_out is left as it was
- * Other arguments as pa_decode; out agrees with pa_decode's exactly.  The last queries of a
+ * Other arguments as pa_decode; out agrees with pa_decode's exactly, its 16-bit
+ * probabilities included (the weights are of the unrounded ones).  The last queries of a
  * prompt can be observed the same way before an eviction: one row for each, all with the
  * prompt's block table, seq_lens = its position + 1, and a row of weights_out of its own
  * (added up afterwards).
@@ -541,7 +546,9 @@ PA_API pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int32_t* src
  *   workspace      NULL, or a workspace whose status word records PA_ERR_OUT_OF_RANGE: a
  *                  length beyond the table (cut to it), a source block outside the pool (block 0
  *                  is read instead), a new block outside it (its rows are not copied)
- * Cache layout and types as pa_decode (the FP8 scales do not change).
+ * Cache layout and types as pa_decode (the FP8 scales do not change).  The call's shape goes
+ * by the table's width, the lengths being on the device: a table much wider than its longest
+ * sequence costs time; a copy of it cut to the blocks that the longest needs does not.
  */
 PA_API pa_status pa_evict(int32_t* kept, int32_t* seq_lens_out, float* weights_out, const float* weights,
                           long long weight_stride, void* k_cache, void* v_cache, const int32_t* block_tables,

@@ -478,7 +478,9 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kmap, const CUten
                     qf[kk][0] = live ? *reinterpret_cast<const uint32_t*>(qrow + 16 * kk + 2 * t) : 0u;
                     qf[kk][1] = live ? *reinterpret_cast<const uint32_t*>(qrow + 16 * kk + 2 * t + 8) : 0u;
                 } else {
-                    // k-slots (2t, 2t+1) <-> d (16kk+4t, +1); (2t+8, 2t+9) <-> d (16kk+4t+2, +3)
+                    // k-slots (2t, 2t+1) <-> d (16kk+4t, +1); (2t+8, 2t+9) <-> d (16kk+4t+2, +3).
+                    // fp16, as the widened codes: exact for a bf16 query of magnitude 2^-14 to
+                    // 65504, 2^-25 off below, infinite above
                     uint2 raw = live ? *reinterpret_cast<const uint2*>(qrow + 16 * kk + 4 * t) : make_uint2(0, 0);
                     qf[kk][0] = pack2<false>(to_float<QBf16>(raw.x & 0xffff), to_float<QBf16>(raw.x >> 16));
                     qf[kk][1] = pack2<false>(to_float<QBf16>(raw.y & 0xffff), to_float<QBf16>(raw.y >> 16));
@@ -635,7 +637,12 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kmap, const CUten
             o[dt][2] *= al0;
             o[dt][3] *= al1;
         }
-        // P^T as the B operand: keys 2t,2t+1 (and +8) of head g
+        // P^T as the B operand: keys 2t,2t+1 (and +8) of head g.  Each probability is rounded
+        // to the 16 bits that the tensor cores take beside V's (bf16 2^-8 of it at most, fp16,
+        // FP8 caches' type too, 2^-11); their sum l is of the unrounded ones.  Against 64 bits
+        // the outputs of 64 sequences of up to 4096 tokens in bf16 are off by 0.0021 of their
+        // norm, of which their own rounding to bf16 is 0.0017 (40 x 8192 in fp16: 0.00028, of
+        // which 0.00021).  P in two 16-bit parts would double the MMAs of P V.
         const uint32_t pb0 = movmatrix_t(pack2<kMmaBf16>(p0, p1));
         const uint32_t pb1 = movmatrix_t(pack2<kMmaBf16>(p2, p3));
 
@@ -1236,7 +1243,10 @@ __global__ void __maxnreg__(112) combine_cascade_kernel(const DecodeParams p) {
 // Scores stay in 32 bits: a 16-bit score or exponential would cost the weights 2^-9 of
 // themselves.  They stay in L2 too (stored with evict_last behind a K/V stream that leaves
 // first), and a warp drops the lines it has used, so that they are not written back: 16
-// sequences of up to 32768 over FP8 took 131 us with plain stores, 119 so.
+// sequences of up to 32768 over FP8 took 131 us with plain stores, 119 so.  Scores that L2
+// cannot hold go to HBM and back: 16 sequences of 32768, 64/8 heads, FP8 (134 MB of scores)
+// 231 us against pa_decode's 173, 32 of them (268 MB) 463 against 334.  A group of 9 to 15
+// heads keeps 16 scores per token: 40 x 8192 of 96/8 heads in fp16 (168 MB) 500 against 422.
 // Every warp takes one run of consecutive units, all of the same size: it finds its place
 // in the flattened order while it waits for the combine, loads the heads' (M, 1 / L) once
 // per (sequence, KV head), and then only streams, a key per lane with kKeys of them in

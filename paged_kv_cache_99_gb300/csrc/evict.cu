@@ -7,7 +7,7 @@
 // go, in order, to the blocks of a new table; the source blocks are only read, so they
 // may be shared with other sequences.
 //
-// One launch.  A cluster of CTAs (one CTA for rows of up to 8192 tokens, 4096 where there
+// One launch.  A cluster of CTAs (one CTA for tables of up to 8192 tokens, 4096 where there
 // are few rows) takes a row, that is, a sequence and KV head: it finds the k-th largest
 // weight by radix select, writes the kept places in order, and copies their rows.
 #include <cooperative_groups.h>
@@ -370,7 +370,12 @@ __global__ void __launch_bounds__(Threads, Threads == 1024 ? 1 : Threads == 512 
 
 // CTAs per row and threads per CTA: one CTA up to 8192 tokens, a cluster beyond, or for
 // long rows while they leave most of the device idle; 1024 threads where there is an SM for
-// every CTA, else 512, and 256 for short rows.
+// every CTA, else 512, and 256 for short rows.  "Tokens" are the block table's (cap): the
+// host does not know the lengths, and a CTA's shared memory must hold its part of the
+// longest row they allow.  A table wider than its sequences costs: 512 rows of 400 to 800
+// tokens take 33 us with a table of 800, 42 with 8192, 55 with 8208, 69 with 32768 and 156
+// with 131072; 320 rows of 8192 tokens 121 with a table of 8192, 128 with 8208 and 16384,
+// 193 with 131072.  Tables cut to the longest sequence avoid it.
 EvictPlan evict_plan(long long rows, long long cap, int sms) {
     EvictPlan e;
     e.parts = 1;
