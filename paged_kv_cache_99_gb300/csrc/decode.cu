@@ -857,8 +857,10 @@ __global__ void __maxnreg__(decode_max_regs<Kind>())
 // computed from the lengths before waiting for the decode grid), or for large
 // batches from the plan the decode grid published; after the wait one round trip
 // brings up to kBatch slots' fragments together with their (m, l) for the lane's
-// two heads, reduced in registers (online across batches): no shuffles.
-template <bool OutBf16, bool Fp8Layout, bool Cascade, int kBatch>
+// two heads, reduced in registers (online across batches): no shuffles.  Weights: the unit's
+// maximum and 1 / sum go to weights_kernel too (an instantiation of its own: asked at run
+// time, it cost a plain decode of 40 layers at 8k contexts 0.15%).
+template <bool OutBf16, bool Fp8Layout, bool Cascade, int kBatch, bool Weights>
 __device__ __forceinline__ void combine_unit(const DecodeParams& p, int u, const int* pre_sum) {
     const int UH = p.num_kv_heads * p.head_groups;
     const int s = u / UH, uh = u % UH;
@@ -989,7 +991,7 @@ __device__ __forceinline__ void combine_unit(const DecodeParams& p, int u, const
         }
         fold(v, mv, lv, min(kBatch, nseg - base));
     }
-    if (!Cascade && p.unit_ml && threadIdx.x < 4) {      // the unit's maximum and 1 / sum, for weights_kernel
+    if (Weights && threadIdx.x < 4) {
         float* um = p.unit_ml + static_cast<size_t>(u) * 16 + 2 * t;
         *reinterpret_cast<float2*>(um) = make_float2(M0, M1);
         *reinterpret_cast<float2*>(um + 8) = make_float2(1.0f / L0, 1.0f / L1);
@@ -1052,7 +1054,7 @@ __device__ __forceinline__ void combine_block_prefix(const DecodeParams& p, int*
     }
 }
 
-template <bool OutBf16, bool Fp8Layout, bool Cascade, int kBatch>
+template <bool OutBf16, bool Fp8Layout, bool Cascade, int kBatch, bool Weights = false>
 __global__ void __maxnreg__(112) combine_kernel(const DecodeParams p) {
     __shared__ int pre_sum[kCombineScanSeqs + 1];
     __shared__ int warp_sum[8];
@@ -1064,7 +1066,7 @@ __global__ void __maxnreg__(112) combine_kernel(const DecodeParams p) {
     if (B <= kCombineScanSeqs) combine_block_prefix(p, pre_sum, warp_sum);
     const long long units = static_cast<long long>(B) * UH;
     for (long long u = blockIdx.x; u < units; u += gridDim.x)
-        combine_unit<OutBf16, Fp8Layout, Cascade, kBatch>(p, static_cast<int>(u), pre_sum);
+        combine_unit<OutBf16, Fp8Layout, Cascade, kBatch, Weights>(p, static_cast<int>(u), pre_sum);
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         // every claim of this call is made: the next call numbers its pieces from here
         grid_dependency_wait();
@@ -1502,6 +1504,9 @@ cudaError_t launch_combine(bool out_bf16, bool fp8_cache, const DecodeParams& p,
         constexpr bool O = decltype(ob)::value, F = decltype(f8)::value;
         if (warp_units) return reinterpret_cast<const void*>(&combine_cascade_kernel<O, F>);
         if (p.cascade) return reinterpret_cast<const void*>(&combine_kernel<O, F, true, 8>);
+        if (p.scores)
+            return wide ? reinterpret_cast<const void*>(&combine_kernel<O, F, false, 10, true>)
+                        : reinterpret_cast<const void*>(&combine_kernel<O, F, false, 8, true>);
         return wide ? reinterpret_cast<const void*>(&combine_kernel<O, F, false, 10>)
                     : reinterpret_cast<const void*>(&combine_kernel<O, F, false, 8>);
     };
