@@ -218,6 +218,42 @@ PA_API pa_status pa_rope_and_cache(void* q_out, long long q_out_stride, const vo
                                    pa_stream_t stream);
 
 /*
+ * pa_rope_and_cache of heads that are normed first, with positions of several axes: each
+ * query and key head x becomes
+ *   y_i = x_i / sqrt(sum_k x_k^2 / 128 + eps) * (weight_offset + weight_i)
+ * (an RMS norm over the head), then its pairs are turned, pair i by
+ *   cos_sin[positions[axis_of_pair[i]][t]][i] and [rot_dim / 2 + i],
+ * and k and v are stored at slot_mapping[t].  With several axes a token of a picture or a
+ * video has a time, a row and a column, and every pair of a head follows one of them.
+ *
+ * Norm and rotation are in float32, rounded once to the type stored (the FP8 slot-write
+ * rule as in pa_rope_and_cache); v is stored as it is.
+ *
+ *   q_weight, k_weight  device, [128] of src_dtype, 16-byte aligned; NULL: those heads are
+ *                  not normed
+ *   eps            >= 0 and finite (the sum of squares is float32: with eps == 0 a head whose
+ *                  squares vanish there becomes NaN)
+ *   weight_offset  added to the weights (1 for checkpoints that store weight - 1)
+ *   positions      device, int64 [num_axes][num_tokens]; a token any of whose positions is
+ *                  negative is padding (nothing of it is written); one with a position >=
+ *                  max_positions is recorded as PA_ERR_OUT_OF_RANGE and not written
+ *   num_axes       1 .. 4
+ *   axis_of_pair   host, [rot_dim / 2], each in [0, num_axes) (read during the call); NULL:
+ *                  every pair follows axis 0
+ * Other arguments as pa_rope_and_cache.
+ */
+PA_API pa_status pa_norm_rope_and_cache(void* q_out, long long q_out_stride, const void* q, long long q_stride,
+                                        const void* k, long long k_stride, const void* v, long long v_stride,
+                                        const void* q_weight, const void* k_weight, float eps, float weight_offset,
+                                        void* k_cache, void* v_cache, const int64_t* slot_mapping,
+                                        const int64_t* positions, int num_axes, const uint8_t* axis_of_pair,
+                                        const float* cos_sin, int max_positions, int rot_dim, pa_rope_layout layout,
+                                        int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                                        int block_size, int num_blocks, pa_dtype src_dtype, pa_dtype cache_dtype,
+                                        const float* k_scale, const float* v_scale, void* workspace,
+                                        pa_stream_t stream);
+
+/*
  * Bytes of workspace pa_decode / pa_mixed need on the CURRENT device for
  * num_seqs sequences (the default worker count depends on the device's SM
  * count).  The workspace is caller-owned device memory, 256-byte aligned.  Its
@@ -448,6 +484,99 @@ PA_API pa_status pa_mixed(void* out, const void* q, const int32_t* query_start_l
                    float scale, pa_dtype q_dtype, pa_dtype cache_dtype, const float* k_scale,
                    const float* v_scale, void* workspace, size_t workspace_bytes,
                    pa_stream_t stream);
+
+/*
+ * Bytes of workspace pa_mixed_scored and pa_tree need on the CURRENT device (they leave the
+ * partial results of sequences that several SMs share in it; the size does not depend on the
+ * batch's lengths).  Same rules as pa_workspace_size, only the status word must start at zero.
+ * Returns 0 for invalid arguments.
+ */
+PA_API size_t pa_workspace_size_scored(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim);
+
+/*
+ * Mixed batch whose scores are capped, biased by distance, windowed or open over a prefix
+ * (no counterpart on the pages, whose attention is plain and causal): rows, lengths and
+ * positions as pa_mixed.  Row j of sequence s, at position pos = seq_lens[s] - q_len_s + j,
+ * sees token t if
+ *   (t <= pos or t < prefix_lens[s])  and  (window == 0 or pos - t < window)  and  t < seq_lens[s],
+ * with the score, x = scale * q . K_s[t],
+ *   cap tanh(x / cap) (cap > 0) or x (cap == 0),  less slopes[query head] * |pos - t|,
+ * and out is the softmax over the tokens it sees times V.  A row that sees nothing is zeros;
+ * rows of out that no sequence owns are left as they were.
+ *
+ *   prefix_lens    device, int32 [num_seqs]: the sequence's first tokens that all its rows
+ *                  see, those behind them too; NULL: none
+ *   slopes         device, float32 [num_q_heads]; NULL: no bias
+ *   cap            >= 0 and finite
+ *   window         >= 0; 0: none.  Table entries of blocks that no row of a call sees through
+ *                  the window need not name a block (they are not read)
+ *   workspace      pa_workspace_size_scored bytes
+ * A sequence whose lengths do not fit (rows outside q, more rows than tokens, more tokens than
+ * the table) is recorded as PA_ERR_OUT_OF_RANGE and its rows are left as they were.  What a
+ * token that no row of its sequence sees holds does not matter (it may be NaN); one that some
+ * of its rows see must be finite for the others.  Other arguments, and the precision, as
+ * pa_mixed; at most 128 query heads per KV head.
+ */
+PA_API pa_status pa_mixed_scored(void* out, const void* q, const int32_t* query_start_loc, const void* k_cache,
+                                 const void* v_cache, const int32_t* block_tables, int max_blocks_per_seq,
+                                 const int32_t* seq_lens, const int32_t* prefix_lens, const float* slopes, float cap,
+                                 int window, int num_seqs, int total_q, int num_q_heads, int num_kv_heads, int head_dim,
+                                 int block_size, int num_blocks, float scale, pa_dtype q_dtype, pa_dtype cache_dtype,
+                                 const float* k_scale, const float* v_scale, void* workspace, size_t workspace_bytes,
+                                 pa_stream_t stream);
+
+/*
+ * Attention for a tree of drafted tokens over the cache (no counterpart on the pages): the
+ * last q_len_s = query_start_loc[s + 1] - query_start_loc[s] cached tokens of sequence s are
+ * the nodes of a tree, written at places seq_lens[s] - q_len_s + i (i < q_len_s), and row j
+ * of the sequence is node j's query.  It sees every token before the tree and node i if bit
+ * i % 64 of masks[row][i / 64] is set: the nodes on its path from the root, its own among
+ * them (a bit has to be set for the row to see itself; bits from q_len_s on are ignored).
+ *
+ *   masks          device, 64-bit words [total_q][mask_words], 8-byte aligned; q_len_s <=
+ *                  64 * mask_words, else the sequence is recorded as PA_ERR_OUT_OF_RANGE and
+ *                  its rows are left as they were
+ *   cap            as pa_mixed_scored
+ *   window         0: none; else of the tokens before the tree row j sees those with
+ *                  pos - t < window, pos being the place of the first node plus the number of
+ *                  nodes that it sees, less one (its depth)
+ * A row that sees nothing (no token before the tree and an empty mask) is zeros.  Other
+ * arguments, and what tokens that no row sees may hold, as pa_mixed_scored.
+ */
+PA_API pa_status pa_tree(void* out, const void* q, const int32_t* query_start_loc, const void* k_cache,
+                         const void* v_cache, const int32_t* block_tables, int max_blocks_per_seq,
+                         const int32_t* seq_lens, const uint64_t* masks, int mask_words, float cap, int window,
+                         int num_seqs, int total_q, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                         int num_blocks, float scale, pa_dtype q_dtype, pa_dtype cache_dtype, const float* k_scale,
+                         const float* v_scale, void* workspace, size_t workspace_bytes, pa_stream_t stream);
+
+/*
+ * Commit of the accepted paths of verified trees, in the caches of several layers at once:
+ * node paths[s][i] of sequence s (i < path_lens[s]) moves to the place behind the tokens
+ * before the tree and the i nodes accepted before it, i.e. the K and V rows at place
+ * seq_lens[s] - q_len_s + paths[s][i] are copied to place seq_lens[s] - q_len_s + i, and
+ *   seq_lens_out[s] = seq_lens[s] - q_len_s + path_lens[s].
+ * Rows behind the accepted ones keep what they hold.
+ *
+ *   seq_lens_out   device, int32 [num_seqs]; not seq_lens itself
+ *   k_caches, v_caches
+ *                  host, num_layers pointers each to a cache (layout as pa_decode); all
+ *                  distinct.  Read during the call
+ *   paths          device, int32 [num_seqs][max_path]: ascending, each in [0, q_len_s);
+ *                  entries from path_lens[s] on are never read
+ *   path_lens      device, int32 [num_seqs]: 0 .. min(max_path, q_len_s)
+ *   query_start_loc, block_tables, seq_lens   as the pa_tree call had them
+ *   workspace      NULL, or a workspace whose status word records errors
+ * A sequence with a path that is none, with lengths that do not fit or with a block outside
+ * the pool among those that its path needs is recorded as PA_ERR_OUT_OF_RANGE; nothing of it
+ * moves and its seq_lens_out is left as it was.  Blocks of a tree must not be shared between
+ * sequences.
+ */
+PA_API pa_status pa_tree_commit(int32_t* seq_lens_out, void* const* k_caches, void* const* v_caches, int num_layers,
+                                const int32_t* paths, const int32_t* path_lens, int max_path,
+                                const int32_t* query_start_loc, const int32_t* block_tables, int max_blocks_per_seq,
+                                const int32_t* seq_lens, int num_seqs, int num_kv_heads, int head_dim, int block_size,
+                                int num_blocks, pa_dtype cache_dtype, void* workspace, pa_stream_t stream);
 
 /*
  * Decode without a caller-provided workspace (no counterpart on the pages; the

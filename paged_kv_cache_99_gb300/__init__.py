@@ -77,6 +77,17 @@ def _lib():
     lib.pa_workspace_size_weights.restype = Z
     lib.pa_decode_weights.argtypes = [P, P, P, LL, P, P, P, P, I, P, I, I, I, I, I, I, F, I, I, P, P, P, Z, P]
     lib.pa_decode_weights.restype = I
+    lib.pa_norm_rope_and_cache.argtypes = [P, LL, P, LL, P, LL, P, LL, P, P, F, F, P, P, P, P, I, P, P, I, I, I, I, I, I,
+                                           I, I, I, I, I, P, P, P, P]
+    lib.pa_norm_rope_and_cache.restype = I
+    lib.pa_workspace_size_scored.argtypes = [I, I, I, I]
+    lib.pa_workspace_size_scored.restype = Z
+    lib.pa_mixed_scored.argtypes = [P, P, P, P, P, P, I, P, P, P, F, I, I, I, I, I, I, I, I, F, I, I, P, P, P, Z, P]
+    lib.pa_mixed_scored.restype = I
+    lib.pa_tree.argtypes = [P, P, P, P, P, P, I, P, P, I, F, I, I, I, I, I, I, I, I, F, I, I, P, P, P, Z, P]
+    lib.pa_tree.restype = I
+    lib.pa_tree_commit.argtypes = [P, P, P, I, P, P, I, P, P, I, P, I, I, I, I, I, I, P, P]
+    lib.pa_tree_commit.restype = I
     lib.pa_workspace_size.argtypes = [I, I, I, I]
     lib.pa_workspace_size.restype = Z
     lib.pa_workspace_size_shared_prefix.argtypes = [I, I, I, I]
@@ -224,6 +235,20 @@ def new_workspace_weights(num_seqs: int, num_q_heads: int, num_kv_heads: int, ma
     return ws
 
 
+def pa_workspace_size_scored(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int = 128) -> int:
+    return int(_lib().pa_workspace_size_scored(num_seqs, num_q_heads, num_kv_heads, head_dim))
+
+
+def new_workspace_scored(num_seqs: int, num_q_heads: int, num_kv_heads: int, device=None) -> torch.Tensor:
+    """Workspace for pa_mixed_scored and pa_tree; only its head is zeroed."""
+    n = pa_workspace_size_scored(num_seqs, num_q_heads, num_kv_heads)
+    if n == 0:
+        raise ValueError("invalid workspace arguments")
+    ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    ws[:256].zero_()
+    return ws
+
+
 def new_workspace(num_seqs: int, num_q_heads: int, num_kv_heads: int, device=None,
                   shared_prefix: bool = False) -> torch.Tensor:
     """Workspace of pa_workspace_size bytes (zeroed, so the status word starts clear);
@@ -282,6 +307,34 @@ def pa_rope_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions,
     token contiguous, any stride between tokens); cos_sin float32 [max_positions, rot] as pa_rope_table builds it."""
     _check(_calls().rope_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, interleaved,
                                    k_scale, v_scale, workspace, _raw(stream)), "pa_rope_and_cache")
+
+
+def rope_axes(sections, in_turns: bool = False) -> bytes:
+    """Axis of every pair for pa_norm_rope_and_cache, from the pairs that each axis has: one axis after the
+    other, or dealt out in turns (0, 1, 2, 0, 1, 2, ...), each axis until its share is used up."""
+    left = [int(n) for n in sections]
+    if not 1 <= len(left) <= 4 or min(left) < 0:
+        raise ValueError("one to four axes with 0 or more pairs each")
+    if not in_turns:
+        return b"".join(bytes([a]) * n for a, n in enumerate(left))
+    out = bytearray()
+    while any(left):
+        for a, n in enumerate(left):
+            if n:
+                out.append(a)
+                left[a] = n - 1
+    return bytes(out)
+
+
+def pa_norm_rope_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, q_weight=None, k_weight=None,
+                           eps: float = 1e-6, weight_offset: float = 0.0, axes=None, interleaved: bool = False,
+                           k_scale=None, v_scale=None, workspace=None, stream=None):
+    """pa_rope_and_cache of heads that are normed first (RMS over the head, times weight_offset + weight;
+    q_weight, k_weight [128] of q's type, None: not normed), with positions [T] or [axes, T] (int64): pair i
+    turns by the positions of axis axes[i] (bytes, as rope_axes makes them; None: axis 0)."""
+    _check(_calls().norm_rope_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, q_weight,
+                                        k_weight, eps, weight_offset, axes, interleaved, k_scale, v_scale, workspace,
+                                        _raw(stream)), "pa_norm_rope_and_cache")
 
 
 def pa_decode(out, q, k_cache, v_cache, block_tables, seq_lens, scale, workspace, k_scale=None, v_scale=None,
@@ -392,6 +445,30 @@ def pa_mixed(out, q, query_start_loc, k_cache, v_cache, block_tables, seq_lens, 
                          Hkv, d, bs, nb, float(scale), _DTYPE[q.dtype], _cache_code(k_cache, k_scale, k_cache.shape[1]), _ptr(k_scale),
                          _ptr(v_scale), _ptr(workspace), workspace.numel(), _stream(stream))
     _check(st, "pa_mixed")
+
+
+def pa_mixed_scored(out, q, query_start_loc, k_cache, v_cache, block_tables, seq_lens, scale, workspace, cap: float = 0.0,
+                    slopes=None, window: int = 0, prefix_lens=None, k_scale=None, v_scale=None, stream=None):
+    """pa_mixed with scores capped by cap tanh(x / cap), less slopes [H_q] (float32) times the distance, over the
+    last window tokens (0: all) and, whatever their order, the first prefix_lens [B] (int32) tokens."""
+    _check(_calls().mixed_scored(out, q, query_start_loc, k_cache, v_cache, block_tables, seq_lens, scale, workspace, cap,
+                                 slopes, window, prefix_lens, k_scale, v_scale, _raw(stream)), "pa_mixed_scored")
+
+
+def pa_tree(out, q, query_start_loc, k_cache, v_cache, block_tables, seq_lens, masks, scale, workspace, cap: float = 0.0,
+            window: int = 0, k_scale=None, v_scale=None, stream=None):
+    """Attention for trees of drafted tokens, the last rows of each sequence: row j sees every token before the
+    tree and node i if bit i % 64 of masks[row, i // 64] (int64 [total_q, words]) is set."""
+    _check(_calls().tree(out, q, query_start_loc, k_cache, v_cache, block_tables, seq_lens, masks, scale, workspace, cap,
+                         window, k_scale, v_scale, _raw(stream)), "pa_tree")
+
+
+def pa_tree_commit(seq_lens_out, k_caches, v_caches, paths, path_lens, query_start_loc, block_tables, seq_lens,
+                   workspace=None, stream=None):
+    """Moves the K and V rows of accepted nodes paths [B, max_path] (int32, ascending; path_lens [B] of them) to the
+    places behind the tokens before the tree, in the caches of all layers (sequences of tensors)."""
+    _check(_calls().tree_commit(seq_lens_out, k_caches, v_caches, paths, path_lens, query_start_loc, block_tables,
+                                seq_lens, workspace, _raw(stream)), "pa_tree_commit")
 
 
 def pa_decode_noalloc(out, q, k_cache, v_cache, block_tables, seq_lens, scale, k_scale=None, v_scale=None,

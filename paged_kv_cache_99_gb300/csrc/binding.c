@@ -322,11 +322,208 @@ static PyObject* evict(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     return leave(back, st);
 }
 
+/* q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, q_weight, k_weight, eps,
+ * weight_offset, axes (None or a buffer of bytes), interleaved, k_scale, v_scale, workspace, stream */
+static PyObject* norm_rope_and_cache(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    Tensor qo, q, k, v, kc, vc, slots, pos, table, qw, kw, ks, vs, ws;
+    long long dev, back;
+    void* stream;
+    if (want_args(n, 19) || device_of(a[1], "q", &dev) || take(a[1], "q", HALVES, 3, dev, 1, &q) ||
+        take(a[0], "q_out", q.type, 3, dev, 1, &qo) || take(a[2], "k", q.type, 3, dev, 1, &k) ||
+        take(a[3], "v", q.type, 3, dev, 1, &v) || take(a[4], "k_cache", CACHES, 4, dev, 0, &kc) ||
+        take(a[5], "v_cache", kc.type, 4, dev, 0, &vc) || take(a[6], "slot_mapping", I64, 1, dev, 0, &slots) ||
+        take(a[7], "positions", I64, 0, dev, 0, &pos) || take(a[8], "cos_sin", F32, 2, dev, 0, &table) ||
+        take_or_none(a[9], "q_weight", q.type, 1, dev, &qw) || take_or_none(a[10], "k_weight", q.type, 1, dev, &kw) ||
+        take_or_none(a[15], "k_scale", F32, 0, dev, &ks) || take_or_none(a[16], "v_scale", F32, 0, dev, &vs) ||
+        take_or_none(a[17], "workspace", U8, 0, dev, &ws) || check_workspace(&ws))
+        return NULL;
+    const long long T = q.shape[0], H = k.shape[1], d = q.shape[2];
+    if (pos.ndim == 1) {                            /* one axis */
+        pos.shape[1] = pos.shape[0];
+        pos.shape[0] = 1;
+    } else if (pos.ndim != 2) {
+        PyErr_SetString(PyExc_ValueError, "positions must be [tokens] or [axes, tokens]");
+        return NULL;
+    }
+    if (!same_shape(&qo, &q) || !is(&k, T, H, d) || !same_shape(&v, &k) || !same_shape(&vc, &kc) ||
+        kc.shape[1] != H || kc.shape[3] != d || !is(&slots, T, -1, -1) || pos.shape[1] != T ||
+        (a[9] != Py_None && !is(&qw, d, -1, -1)) || (a[10] != Py_None && !is(&kw, d, -1, -1)))
+        return mismatch(), NULL;
+    if (pos.shape[0] > INT_MAX) return PyLong_FromLong(PA_ERR_UNSUPPORTED);
+    const int code = cache_code(&kc, &ks, &vs, H);
+    const int interleaved = PyObject_IsTrue(a[14]);
+    const double eps = PyFloat_AsDouble(a[11]);
+    const double offset = eps == -1.0 && PyErr_Occurred() ? 0.0 : PyFloat_AsDouble(a[12]);
+    if (code < 0 || interleaved < 0 || PyErr_Occurred()) return NULL;
+    Py_buffer axes = {0};
+    if (a[13] != Py_None) {
+        if (PyObject_GetBuffer(a[13], &axes, PyBUF_SIMPLE)) return NULL;
+        if (axes.itemsize != 1 || 2 * (long long)axes.len != table.shape[1]) {
+            PyErr_SetString(PyExc_ValueError, "axes must hold one byte for every pair of cos_sin's columns");
+            PyBuffer_Release(&axes);
+            return NULL;
+        }
+    }
+    PyObject* res = NULL;
+    if (!enter(dev, a[18], &stream, &back)) {
+        pa_status st;
+        Py_BEGIN_ALLOW_THREADS
+        st = pa_norm_rope_and_cache(qo.ptr, qo.step, q.ptr, q.step, k.ptr, k.step, v.ptr, v.step, qw.ptr, kw.ptr, (float)eps,
+                                    (float)offset, kc.ptr, vc.ptr, slots.ptr, pos.ptr, (int)pos.shape[0], axes.buf,
+                                    table.ptr, (int)table.shape[0], (int)table.shape[1],
+                                    interleaved ? PA_ROPE_INTERLEAVED : PA_ROPE_HALF, (int)T, (int)q.shape[1], (int)H,
+                                    (int)d, (int)kc.shape[2], (int)kc.shape[0], (pa_dtype)half_code(&q), (pa_dtype)code,
+                                    ks.ptr, vs.ptr, ws.ptr, (pa_stream_t)stream);
+        Py_END_ALLOW_THREADS
+        res = leave(back, st);
+    }
+    if (a[13] != Py_None) PyBuffer_Release(&axes);
+    return res;
+}
+
+/* What the two calls with scores or masks that are not plain have alike: out, q, query_start_loc,
+ * k_cache, v_cache, block_tables, seq_lens first, workspace, cap, window, k_scale, v_scale. */
+typedef struct {
+    Tensor out, q, qsl, kc, vc, bt, sl, ws, ks, vs;
+    long long dev, window;
+    double scale, cap;
+    int code;
+} Scored;
+
+static int take_scored(PyObject* const* a, PyObject* scale, PyObject* ws, PyObject* cap, PyObject* window, PyObject* ks,
+                       PyObject* vs, Scored* c) {
+    if (device_of(a[1], "q", &c->dev) || take(a[1], "q", HALVES, 3, c->dev, 0, &c->q) ||
+        take(a[0], "out", c->q.type, 3, c->dev, 0, &c->out) || take(a[2], "query_start_loc", I32, 1, c->dev, 0, &c->qsl) ||
+        take(a[3], "k_cache", CACHES, 4, c->dev, 0, &c->kc) || take(a[4], "v_cache", c->kc.type, 4, c->dev, 0, &c->vc) ||
+        take(a[5], "block_tables", I32, 2, c->dev, 0, &c->bt) || take(a[6], "seq_lens", I32, 1, c->dev, 0, &c->sl) ||
+        take(ws, "workspace", U8, 0, c->dev, 0, &c->ws) || take_or_none(ks, "k_scale", F32, 0, c->dev, &c->ks) ||
+        take_or_none(vs, "v_scale", F32, 0, c->dev, &c->vs) || as_int(PyNumber_Index(window), &c->window))
+        return -1;
+    const long long B = c->sl.shape[0];
+    if (!same_shape(&c->out, &c->q) || !same_shape(&c->vc, &c->kc) || c->kc.shape[3] != c->q.shape[2] ||
+        c->bt.shape[0] != B || !is(&c->qsl, B + 1, -1, -1))
+        return mismatch();
+    c->code = cache_code(&c->kc, &c->ks, &c->vs, c->kc.shape[1]);
+    if (c->code < 0) return -1;
+    c->scale = PyFloat_AsDouble(scale);
+    if (c->scale == -1.0 && PyErr_Occurred()) return -1;
+    c->cap = PyFloat_AsDouble(cap);
+    if (c->cap == -1.0 && PyErr_Occurred()) return -1;
+    if (c->window > INT_MAX) c->window = INT_MAX;   /* wider than any sequence */
+    if (c->window < 0) c->window = -1;              /* refused by the library */
+    return 0;
+}
+
+/* out, q, query_start_loc, k_cache, v_cache, block_tables, seq_lens, scale, workspace, cap, slopes, window,
+ * prefix_lens, k_scale, v_scale, stream */
+static PyObject* mixed_scored(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    Scored c;
+    Tensor slopes, prefix;
+    long long back;
+    void* stream;
+    if (want_args(n, 16) || take_scored(a, a[7], a[8], a[9], a[11], a[13], a[14], &c) ||
+        take_or_none(a[10], "slopes", F32, 1, c.dev, &slopes) || take_or_none(a[12], "prefix_lens", I32, 1, c.dev, &prefix))
+        return NULL;
+    if ((a[10] != Py_None && !is(&slopes, c.q.shape[1], -1, -1)) || (a[12] != Py_None && !is(&prefix, c.sl.shape[0], -1, -1)))
+        return mismatch(), NULL;
+    if (enter(c.dev, a[15], &stream, &back)) return NULL;
+    pa_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = pa_mixed_scored(c.out.ptr, c.q.ptr, c.qsl.ptr, c.kc.ptr, c.vc.ptr, c.bt.ptr, (int)c.bt.shape[1], c.sl.ptr, prefix.ptr,
+                         slopes.ptr, (float)c.cap, (int)c.window, (int)c.sl.shape[0], (int)c.q.shape[0], (int)c.q.shape[1],
+                         (int)c.kc.shape[1], (int)c.q.shape[2], (int)c.kc.shape[2], (int)c.kc.shape[0], (float)c.scale,
+                         (pa_dtype)half_code(&c.q), (pa_dtype)c.code, c.ks.ptr, c.vs.ptr, c.ws.ptr, (size_t)c.ws.numel,
+                         (pa_stream_t)stream);
+    Py_END_ALLOW_THREADS
+    return leave(back, st);
+}
+
+/* out, q, query_start_loc, k_cache, v_cache, block_tables, seq_lens, masks, scale, workspace, cap, window, k_scale,
+ * v_scale, stream */
+static PyObject* tree(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    Scored c;
+    Tensor masks;
+    long long back;
+    void* stream;
+    if (want_args(n, 15) || take_scored(a, a[8], a[9], a[10], a[11], a[12], a[13], &c) ||
+        take(a[7], "masks", I64, 2, c.dev, 0, &masks))
+        return NULL;
+    if (masks.shape[0] != c.q.shape[0]) return mismatch(), NULL;
+    if (enter(c.dev, a[14], &stream, &back)) return NULL;
+    pa_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = pa_tree(c.out.ptr, c.q.ptr, c.qsl.ptr, c.kc.ptr, c.vc.ptr, c.bt.ptr, (int)c.bt.shape[1], c.sl.ptr, masks.ptr,
+                 (int)masks.shape[1], (float)c.cap, (int)c.window, (int)c.sl.shape[0], (int)c.q.shape[0], (int)c.q.shape[1],
+                 (int)c.kc.shape[1], (int)c.q.shape[2], (int)c.kc.shape[2], (int)c.kc.shape[0], (float)c.scale,
+                 (pa_dtype)half_code(&c.q), (pa_dtype)c.code, c.ks.ptr, c.vs.ptr, c.ws.ptr, (size_t)c.ws.numel,
+                 (pa_stream_t)stream);
+    Py_END_ALLOW_THREADS
+    return leave(back, st);
+}
+
+#define MAX_LAYERS 1024
+
+/* seq_lens_out, k_caches, v_caches (sequences of tensors), paths, path_lens, query_start_loc, block_tables,
+ * seq_lens, workspace, stream */
+static PyObject* tree_commit(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    Tensor lo, paths, pl, qsl, bt, sl, ws, first = {0}, c;
+    long long dev, back;
+    void *stream, *k[MAX_LAYERS], *v[MAX_LAYERS];
+    if (want_args(n, 10) || device_of(a[7], "seq_lens", &dev) || take(a[7], "seq_lens", I32, 1, dev, 0, &sl) ||
+        take(a[0], "seq_lens_out", I32, 1, dev, 0, &lo) || take(a[3], "paths", I32, 2, dev, 0, &paths) ||
+        take(a[4], "path_lens", I32, 1, dev, 0, &pl) || take(a[5], "query_start_loc", I32, 1, dev, 0, &qsl) ||
+        take(a[6], "block_tables", I32, 2, dev, 0, &bt) || take_or_none(a[8], "workspace", U8, 0, dev, &ws) ||
+        check_workspace(&ws))
+        return NULL;
+    const long long B = sl.shape[0];
+    if (!is(&lo, B, -1, -1) || paths.shape[0] != B || !is(&pl, B, -1, -1) || !is(&qsl, B + 1, -1, -1) || bt.shape[0] != B)
+        return mismatch(), NULL;
+    PyObject* ks = PySequence_Fast(a[1], "k_caches must be a sequence of tensors");
+    PyObject* vs = ks ? PySequence_Fast(a[2], "v_caches must be a sequence of tensors") : NULL;
+    if (!vs) {
+        Py_XDECREF(ks);
+        return NULL;
+    }
+    const Py_ssize_t layers = PySequence_Fast_GET_SIZE(ks);
+    int bad = 0;
+    if (layers < 1 || layers > MAX_LAYERS || PySequence_Fast_GET_SIZE(vs) != layers) {
+        PyErr_Format(PyExc_ValueError, "k_caches and v_caches: 1 to %d layers, K and V alike", MAX_LAYERS);
+        bad = 1;
+    }
+    for (Py_ssize_t i = 0; !bad && i < 2 * layers; ++i) {
+        PyObject* t = PySequence_Fast_GET_ITEM(i & 1 ? vs : ks, i >> 1);
+        bad = take(t, i & 1 ? "v_cache" : "k_cache", i ? first.type : CACHES, 4, dev, 0, &c);
+        if (!bad && i && !same_shape(&c, &first)) bad = mismatch();
+        if (bad) break;
+        if (!i) first = c;
+        (i & 1 ? v : k)[i >> 1] = c.ptr;
+    }
+    Py_DECREF(ks);
+    Py_DECREF(vs);
+    if (bad || enter(dev, a[9], &stream, &back)) return NULL;
+    const int code = first.type & HALVES ? half_code(&first) : PA_FP8_E4M3;
+    pa_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = pa_tree_commit(lo.ptr, k, v, (int)layers, paths.ptr, pl.ptr, (int)paths.shape[1], qsl.ptr, bt.ptr, (int)bt.shape[1],
+                        sl.ptr, (int)B, (int)first.shape[1], (int)first.shape[3], (int)first.shape[2], (int)first.shape[0],
+                        (pa_dtype)code, ws.ptr, (pa_stream_t)stream);
+    Py_END_ALLOW_THREADS
+    return leave(back, st);
+}
+
 static PyMethodDef methods[] = {
     {"rope_table", (PyCFunction)(void (*)(void))rope_table, METH_FASTCALL, NULL},
     {"rope_and_cache", (PyCFunction)(void (*)(void))rope_and_cache, METH_FASTCALL, NULL},
     {"decode_weights", (PyCFunction)(void (*)(void))decode_weights, METH_FASTCALL, NULL},
     {"evict", (PyCFunction)(void (*)(void))evict, METH_FASTCALL, NULL},
+    {"norm_rope_and_cache", (PyCFunction)(void (*)(void))norm_rope_and_cache, METH_FASTCALL, NULL},
+    {"mixed_scored", (PyCFunction)(void (*)(void))mixed_scored, METH_FASTCALL, NULL},
+    {"tree", (PyCFunction)(void (*)(void))tree, METH_FASTCALL, NULL},
+    {"tree_commit", (PyCFunction)(void (*)(void))tree_commit, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL},
 };
 

@@ -320,6 +320,65 @@ pa_status decode_impl(void* out, const void* q, const int32_t* query_start_loc, 
     return launched(launch_weights(p, st->sms, stream), "launch(weights)");
 }
 
+// Checks of the calls that rotate and write slots, and what their kernels take (nothing of it
+// for an empty call, which may have null pointers).
+pa_status rope_params(RopeParams* out, void* q_out, long long q_out_stride, const void* q, long long q_stride, const void* k,
+                      long long k_stride, const void* v, long long v_stride, void* k_cache, void* v_cache,
+                      const int64_t* slot_mapping, const int64_t* positions, const float* cos_sin, int max_positions,
+                      int rot_dim, pa_rope_layout layout, int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                      int block_size, int num_blocks, pa_dtype src_dtype, pa_dtype cache_dtype, const float* k_scale,
+                      const float* v_scale, void* workspace) {
+    if (head_dim != kHeadDim || !block_size_ok(block_size)) return PA_ERR_UNSUPPORTED;
+    if (src_dtype != PA_BF16 && src_dtype != PA_FP16) return PA_ERR_UNSUPPORTED;
+    if (cache_dtype != src_dtype && !is_fp8(cache_dtype)) return PA_ERR_UNSUPPORTED;
+    if (rot_dim < 16 || rot_dim > kHeadDim || rot_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
+    if (layout != PA_ROPE_HALF && layout != PA_ROPE_INTERLEAVED) return PA_ERR_UNSUPPORTED;
+    if (num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_blocks <= 0 || max_positions <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (num_tokens == 0) return PA_OK;
+    if (!q_out || !q || !k || !v || !k_cache || !v_cache || !slot_mapping || !positions || !cos_sin)
+        return PA_ERR_INVALID_ARG;
+    if (is_fp8(cache_dtype) && (!k_scale || !v_scale)) return PA_ERR_INVALID_ARG;
+    if (!aligned(q_out, 16) || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) ||
+        !aligned(v_cache, 16) || !aligned(cos_sin, 16) || !aligned(slot_mapping, 8) || !aligned(positions, 8) ||
+        (workspace && !aligned(workspace, 256)))
+        return PA_ERR_INVALID_ARG;
+    if (q_out_stride % 8 || q_stride % 8 || k_stride % 8 || v_stride % 8 || q_stride < 0 || k_stride < 0 || v_stride < 0 ||
+        (num_tokens > 1 && q_out_stride < static_cast<long long>(num_q_heads) * kHeadDim) ||
+        (q_out == q && num_tokens > 1 && q_out_stride != q_stride))
+        return PA_ERR_INVALID_ARG;
+    // thread groups are numbered in 32 bits
+    if (static_cast<long long>(num_tokens) * (static_cast<long long>(num_q_heads) + 2ll * num_kv_heads) >= (1ll << 31))
+        return PA_ERR_UNSUPPORTED;
+    RopeParams& p = *out;
+    p.q_out = static_cast<uint16_t*>(q_out);
+    p.q = static_cast<const uint16_t*>(q);
+    p.k = static_cast<const uint16_t*>(k);
+    p.v = static_cast<const uint16_t*>(v);
+    p.q_out_stride = q_out_stride;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.slots = slot_mapping;
+    p.positions = positions;
+    p.cos_sin = cos_sin;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.scale_stride = scale_stride_of(cache_dtype);
+    p.status = static_cast<int*>(workspace);
+    p.max_positions = max_positions;
+    p.rot_dim = rot_dim;
+    p.num_tokens = num_tokens;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.num_blocks = num_blocks;
+    p.block_shift = block_shift_of(block_size);
+    p.groups = 0;
+    return PA_OK;
+}
+
 pa_status chunk_impl(void* out, const void* q, const int32_t* query_start_loc, const void* k_cache,
                      const void* v_cache, const CUtensorMap& kmap, const CUtensorMap& vmap,
                      const int32_t* block_tables, int max_blocks_per_seq,
@@ -384,6 +443,54 @@ pa_status chunk_impl(void* out, const void* q, const int32_t* query_start_loc, c
     p.timeout_ns = kDefaultTimeoutNs;
     return launched(launch_chunk(kind, q_bf16, kmap, vmap, p, static_cast<int>(grid_x), smem, stream),
                        "launch(chunk)");
+}
+
+// Checks and launch of the two calls with scores or masks that are not plain; s: the fields
+// that only one of them has.
+pa_status scored_impl(ScoredParams p, void* out, const void* q, const int32_t* query_start_loc, const void* k_cache,
+                      const void* v_cache, const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                      float cap, int window, int num_seqs, int total_q, int num_q_heads, int num_kv_heads, int head_dim,
+                      int block_size, int num_blocks, float scale, pa_dtype q_dtype, pa_dtype cache_dtype,
+                      const float* k_scale, const float* v_scale, void* workspace, size_t workspace_bytes,
+                      cudaStream_t stream) {
+    if (num_seqs < 0 || num_seqs > kMaxSeqs || total_q < 0) return PA_ERR_INVALID_ARG;
+    if (total_q == 0) num_seqs = 0;                 // no rows: the arrays may be null
+    pa_status s = check_attention_args(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, num_seqs,
+                                       num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale, q_dtype,
+                                       cache_dtype, k_scale, v_scale, workspace);
+    if (s != PA_OK) return s;
+    if (!std::isfinite(cap) || !(cap >= 0.f) || window < 0) return PA_ERR_INVALID_ARG;
+    if (num_seqs > 0 && (!query_start_loc || !aligned(query_start_loc, 4))) return PA_ERR_INVALID_ARG;
+    if (num_q_heads / num_kv_heads > chunk_rows()) return PA_ERR_UNSUPPORTED;
+    if (static_cast<long long>(total_q) * num_q_heads >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
+    const size_t need = pa_workspace_size_scored(num_seqs, num_q_heads, num_kv_heads, head_dim);
+    if (need == 0) return PA_ERR_CUDA;
+    if (workspace_bytes < need) return PA_ERR_WORKSPACE;
+    if (num_seqs == 0) return PA_OK;
+    p.out = out;
+    p.q = q;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.query_start_loc = query_start_loc;
+    p.block_tables = block_tables;
+    p.seq_lens = seq_lens;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.scale_stride = scale_stride_of(cache_dtype);
+    p.status = static_cast<int*>(workspace);
+    p.window = window;
+    p.num_seqs = num_seqs;
+    p.total_rows = total_q;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.group = num_q_heads / num_kv_heads;
+    p.max_blocks = max_blocks_per_seq;
+    p.num_blocks = num_blocks;
+    p.block_size = block_size;
+    p.block_shift = block_shift_of(block_size);
+    p.scale = scale;
+    p.cap = cap;
+    return launched(launch_scored(kind_of(cache_dtype), q_dtype == PA_BF16, p, stream), "launch(scored)");
 }
 
 }  // namespace
@@ -494,7 +601,7 @@ const char* pa_status_string(int status) {
     }
 }
 
-int pa_version(void) { return 102; }
+int pa_version(void) { return 103; }
 
 unsigned long long pa_kernel_launches(void) { return g_launches.load(std::memory_order_relaxed); }
 
@@ -562,59 +669,55 @@ pa_status pa_rope_and_cache(void* q_out, long long q_out_stride, const void* q, 
                             int num_kv_heads, int head_dim, int block_size, int num_blocks, pa_dtype src_dtype,
                             pa_dtype cache_dtype, const float* k_scale, const float* v_scale, void* workspace,
                             pa_stream_t stream) {
-    if (head_dim != kHeadDim || !block_size_ok(block_size)) return PA_ERR_UNSUPPORTED;
-    if (src_dtype != PA_BF16 && src_dtype != PA_FP16) return PA_ERR_UNSUPPORTED;
-    if (cache_dtype != src_dtype && !is_fp8(cache_dtype)) return PA_ERR_UNSUPPORTED;
-    if (rot_dim < 16 || rot_dim > kHeadDim || rot_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
-    if (layout != PA_ROPE_HALF && layout != PA_ROPE_INTERLEAVED) return PA_ERR_UNSUPPORTED;
-    if (num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_blocks <= 0 || max_positions <= 0)
-        return PA_ERR_INVALID_ARG;
-    if (num_tokens == 0) return PA_OK;
-    if (!q_out || !q || !k || !v || !k_cache || !v_cache || !slot_mapping || !positions || !cos_sin)
-        return PA_ERR_INVALID_ARG;
-    if (is_fp8(cache_dtype) && (!k_scale || !v_scale)) return PA_ERR_INVALID_ARG;
-    if (!aligned(q_out, 16) || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) ||
-        !aligned(v_cache, 16) || !aligned(cos_sin, 16) || !aligned(slot_mapping, 8) || !aligned(positions, 8) ||
-        (workspace && !aligned(workspace, 256)))
-        return PA_ERR_INVALID_ARG;
-    if (q_out_stride % 8 || q_stride % 8 || k_stride % 8 || v_stride % 8 || q_stride < 0 || k_stride < 0 || v_stride < 0 ||
-        (num_tokens > 1 && q_out_stride < static_cast<long long>(num_q_heads) * kHeadDim) ||
-        (q_out == q && num_tokens > 1 && q_out_stride != q_stride))
-        return PA_ERR_INVALID_ARG;
-    // thread groups are numbered in 32 bits
-    if (static_cast<long long>(num_tokens) * (static_cast<long long>(num_q_heads) + 2ll * num_kv_heads) >= (1ll << 31))
-        return PA_ERR_UNSUPPORTED;
+    RopeParams p;
+    const pa_status s = rope_params(&p, q_out, q_out_stride, q, q_stride, k, k_stride, v, v_stride, k_cache, v_cache,
+                                    slot_mapping, positions, cos_sin, max_positions, rot_dim, layout, num_tokens,
+                                    num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, src_dtype, cache_dtype,
+                                    k_scale, v_scale, workspace);
+    if (s != PA_OK || num_tokens == 0) return s;
     DeviceState* st = device_state(nullptr);
     if (!st) return PA_ERR_CUDA;
-    RopeParams p;
-    p.q_out = static_cast<uint16_t*>(q_out);
-    p.q = static_cast<const uint16_t*>(q);
-    p.k = static_cast<const uint16_t*>(k);
-    p.v = static_cast<const uint16_t*>(v);
-    p.q_out_stride = q_out_stride;
-    p.q_stride = q_stride;
-    p.k_stride = k_stride;
-    p.v_stride = v_stride;
-    p.k_cache = k_cache;
-    p.v_cache = v_cache;
-    p.slots = slot_mapping;
-    p.positions = positions;
-    p.cos_sin = cos_sin;
-    p.k_scale = k_scale;
-    p.v_scale = v_scale;
-    p.scale_stride = scale_stride_of(cache_dtype);
-    p.status = static_cast<int*>(workspace);
-    p.max_positions = max_positions;
-    p.rot_dim = rot_dim;
-    p.num_tokens = num_tokens;
-    p.num_q_heads = num_q_heads;
-    p.num_kv_heads = num_kv_heads;
-    p.num_blocks = num_blocks;
-    p.block_shift = block_shift_of(block_size);
-    p.groups = 0;
     return launched(launch_rope_cache(p, src_dtype == PA_BF16, is_fp8(cache_dtype), layout == PA_ROPE_INTERLEAVED,
                                       st->sms, reinterpret_cast<cudaStream_t>(stream)),
                     "launch(rope_and_cache)");
+}
+
+pa_status pa_norm_rope_and_cache(void* q_out, long long q_out_stride, const void* q, long long q_stride, const void* k,
+                                 long long k_stride, const void* v, long long v_stride, const void* q_weight,
+                                 const void* k_weight, float eps, float weight_offset, void* k_cache, void* v_cache,
+                                 const int64_t* slot_mapping, const int64_t* positions, int num_axes,
+                                 const uint8_t* axis_of_pair, const float* cos_sin, int max_positions, int rot_dim,
+                                 pa_rope_layout layout, int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                                 int block_size, int num_blocks, pa_dtype src_dtype, pa_dtype cache_dtype,
+                                 const float* k_scale, const float* v_scale, void* workspace, pa_stream_t stream) {
+    if (num_axes < 1 || num_axes > kMaxAxes) return PA_ERR_UNSUPPORTED;
+    if (!std::isfinite(eps) || !(eps >= 0.f) || !std::isfinite(weight_offset)) return PA_ERR_INVALID_ARG;
+    if (!aligned(q_weight, 16) || !aligned(k_weight, 16)) return PA_ERR_INVALID_ARG;
+    NormRopeParams p = {};
+    const pa_status s = rope_params(&p.rope, q_out, q_out_stride, q, q_stride, k, k_stride, v, v_stride, k_cache, v_cache,
+                                    slot_mapping, positions, cos_sin, max_positions, rot_dim, layout, num_tokens,
+                                    num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, src_dtype, cache_dtype,
+                                    k_scale, v_scale, workspace);
+    if (s != PA_OK) return s;
+    p.one_axis = 0xffffu;
+    if (axis_of_pair) {
+        for (int i = 0; i < rot_dim / 2; ++i) {
+            if (axis_of_pair[i] >= num_axes) return PA_ERR_INVALID_ARG;
+            p.axis_word[i / 16] |= static_cast<unsigned>(axis_of_pair[i]) << (2 * (i % 16));
+            if (axis_of_pair[i] != axis_of_pair[i & ~7]) p.one_axis &= ~(1u << (i / 8));
+        }
+    }
+    if (num_tokens == 0) return PA_OK;
+    DeviceState* st = device_state(nullptr);
+    if (!st) return PA_ERR_CUDA;
+    p.q_weight = static_cast<const uint16_t*>(q_weight);
+    p.k_weight = static_cast<const uint16_t*>(k_weight);
+    p.eps = eps;
+    p.weight_offset = weight_offset;
+    p.num_axes = num_axes;
+    return launched(launch_norm_rope_cache(p, src_dtype == PA_BF16, is_fp8(cache_dtype), layout == PA_ROPE_INTERLEAVED,
+                                           st->sms, reinterpret_cast<cudaStream_t>(stream)),
+                    "launch(norm_rope_and_cache)");
 }
 
 size_t pa_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim) {
@@ -969,6 +1072,102 @@ pa_status pa_evict(int32_t* kept, int32_t* seq_lens_out, float* weights_out, con
     p.num_blocks = num_blocks;
     p.block_shift = block_shift_of(block_size);
     return launched(launch_evict(p, plan, is_fp8(cache_dtype), reinterpret_cast<cudaStream_t>(stream)), "launch(evict)");
+}
+
+size_t pa_workspace_size_scored(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim) {
+    if (num_seqs < 0 || num_seqs > kMaxSeqs || head_dim != kHeadDim || num_kv_heads <= 0 || num_q_heads <= 0 ||
+        num_q_heads % num_kv_heads != 0)
+        return 0;
+    return 256;
+}
+
+pa_status pa_mixed_scored(void* out, const void* q, const int32_t* query_start_loc, const void* k_cache,
+                          const void* v_cache, const int32_t* block_tables, int max_blocks_per_seq,
+                          const int32_t* seq_lens, const int32_t* prefix_lens, const float* slopes, float cap, int window,
+                          int num_seqs, int total_q, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                          int num_blocks, float scale, pa_dtype q_dtype, pa_dtype cache_dtype, const float* k_scale,
+                          const float* v_scale, void* workspace, size_t workspace_bytes, pa_stream_t stream) {
+    if (!aligned(prefix_lens, 4) || !aligned(slopes, 4)) return PA_ERR_INVALID_ARG;
+    ScoredParams p = {};
+    p.prefix_lens = prefix_lens;
+    p.slopes = slopes;
+    return scored_impl(p, out, q, query_start_loc, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, cap,
+                       window, num_seqs, total_q, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
+                       q_dtype, cache_dtype, k_scale, v_scale, workspace, workspace_bytes,
+                       reinterpret_cast<cudaStream_t>(stream));
+}
+
+pa_status pa_tree(void* out, const void* q, const int32_t* query_start_loc, const void* k_cache, const void* v_cache,
+                  const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens, const uint64_t* masks,
+                  int mask_words, float cap, int window, int num_seqs, int total_q, int num_q_heads, int num_kv_heads,
+                  int head_dim, int block_size, int num_blocks, float scale, pa_dtype q_dtype, pa_dtype cache_dtype,
+                  const float* k_scale, const float* v_scale, void* workspace, size_t workspace_bytes,
+                  pa_stream_t stream) {
+    if (mask_words < 1 || (num_seqs > 0 && total_q > 0 && !masks) || !aligned(masks, 8)) return PA_ERR_INVALID_ARG;
+    ScoredParams p = {};
+    p.masks = reinterpret_cast<const unsigned long long*>(masks);
+    p.mask_words = mask_words;
+    return scored_impl(p, out, q, query_start_loc, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, cap,
+                       window, num_seqs, total_q, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
+                       q_dtype, cache_dtype, k_scale, v_scale, workspace, workspace_bytes,
+                       reinterpret_cast<cudaStream_t>(stream));
+}
+
+pa_status pa_tree_commit(int32_t* seq_lens_out, void* const* k_caches, void* const* v_caches, int num_layers,
+                         const int32_t* paths, const int32_t* path_lens, int max_path, const int32_t* query_start_loc,
+                         const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens, int num_seqs,
+                         int num_kv_heads, int head_dim, int block_size, int num_blocks, pa_dtype cache_dtype,
+                         void* workspace, pa_stream_t stream) {
+    if (head_dim != kHeadDim || !block_size_ok(block_size)) return PA_ERR_UNSUPPORTED;
+    if (cache_dtype != PA_BF16 && cache_dtype != PA_FP16 && !is_fp8(cache_dtype)) return PA_ERR_UNSUPPORTED;
+    if (num_seqs < 0 || num_layers < 0 || max_path < 0 || num_kv_heads <= 0 || num_blocks <= 0 || max_blocks_per_seq <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (num_layers > 0 && (!k_caches || !v_caches)) return PA_ERR_INVALID_ARG;
+    for (int i = 0; i < num_layers; ++i) {
+        if (!k_caches[i] || !v_caches[i] || !aligned(k_caches[i], 16) || !aligned(v_caches[i], 16))
+            return PA_ERR_INVALID_ARG;
+        for (int j = 0; j <= i; ++j)            // the same cache twice would be moved twice at once
+            if (k_caches[i] == v_caches[j] || v_caches[i] == k_caches[j] ||
+                (j < i && (k_caches[i] == k_caches[j] || v_caches[i] == v_caches[j])))
+                return PA_ERR_INVALID_ARG;
+    }
+    if (num_seqs == 0 || num_layers == 0) return PA_OK;
+    if (!seq_lens_out || !path_lens || !query_start_loc || !block_tables || !seq_lens || seq_lens_out == seq_lens ||
+        (max_path > 0 && !paths))
+        return PA_ERR_INVALID_ARG;
+    if (!aligned(seq_lens_out, 4) || !aligned(paths, 4) || !aligned(path_lens, 4) || !aligned(query_start_loc, 4) ||
+        !aligned(block_tables, 4) || !aligned(seq_lens, 4) || (workspace && !aligned(workspace, 256)))
+        return PA_ERR_INVALID_ARG;
+    // places of a sequence in 32 bits, and the warps of a launch
+    const long long group = num_layers < kCommitLayers ? num_layers : kCommitLayers;
+    if (static_cast<long long>(max_blocks_per_seq) * block_size >= (1ll << 31) ||
+        static_cast<long long>(num_seqs) * num_kv_heads * 2 * group >= (1ll << 31))
+        return PA_ERR_UNSUPPORTED;
+    for (int first = 0; first < num_layers; first += kCommitLayers) {
+        CommitParams p = {};
+        p.num_layers = num_layers - first < kCommitLayers ? num_layers - first : kCommitLayers;
+        for (int i = 0; i < p.num_layers; ++i) {
+            p.caches[2 * i] = k_caches[first + i];
+            p.caches[2 * i + 1] = v_caches[first + i];
+        }
+        p.seq_lens_out = first == 0 ? seq_lens_out : nullptr;
+        p.paths = paths;
+        p.path_lens = path_lens;
+        p.query_start_loc = query_start_loc;
+        p.block_tables = block_tables;
+        p.seq_lens = seq_lens;
+        p.status = static_cast<int*>(workspace);
+        p.max_path = max_path;
+        p.max_blocks = max_blocks_per_seq;
+        p.num_seqs = num_seqs;
+        p.num_kv_heads = num_kv_heads;
+        p.num_blocks = num_blocks;
+        p.block_shift = block_shift_of(block_size);
+        const pa_status s = launched(launch_tree_commit(p, is_fp8(cache_dtype), reinterpret_cast<cudaStream_t>(stream)),
+                                     "launch(tree_commit)");
+        if (s != PA_OK) return s;
+    }
+    return PA_OK;
 }
 
 pa_status pa_read_device_status(void* workspace, pa_stream_t stream) {

@@ -342,6 +342,20 @@ __device__ __forceinline__ uint32_t e4m3_pair(uint32_t word, float scale) {
     return c_lo | (c_hi << 8);
 }
 
+// Two e4m3 codes of rotated components by the slot-write rule (a NaN has no source
+// element here and becomes the positive one).
+__device__ __forceinline__ uint32_t e4m3_of(float a, float b, float scale) {
+    const float lo = __fdiv_rn(a, scale), hi = __fdiv_rn(b, scale);
+    uint16_t y;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(y) : "f"(hi), "f"(lo));
+    uint32_t c_lo = y & 0xffu, c_hi = y >> 8;
+    if (isnan(lo)) c_lo = 0x7fu;
+    else if ((c_lo & 0x7fu) == 0) c_lo = signbit(lo) ? 0x80u : 0u;
+    if (isnan(hi)) c_hi = 0x7fu;
+    else if ((c_hi & 0x7fu) == 0) c_hi = signbit(hi) ? 0x80u : 0u;
+    return c_lo | (c_hi << 8);
+}
+
 // Packed pairs of f32 (one 64-bit register pair): the f32x2 arithmetic issues two
 // IEEE single-precision operations per instruction.
 __device__ __forceinline__ uint64_t f2_pack(float a, float b) {

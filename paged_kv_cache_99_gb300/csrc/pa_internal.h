@@ -241,6 +241,23 @@ cudaError_t launch_rope_table(float* cos_sin, int max_positions, int rot_dim, co
                               int sms, cudaStream_t stream);
 cudaError_t launch_rope_cache(RopeParams p, bool src_bf16, bool fp8, bool interleaved, int sms, cudaStream_t stream);
 
+// The same of heads that are normed first, with positions of several axes.
+constexpr int kMaxAxes = 4;
+
+struct NormRopeParams {
+    RopeParams rope;                  // positions: [num_axes][num_tokens]
+    const uint16_t* q_weight;         // [128] of the source type, or null: not normed
+    const uint16_t* k_weight;
+    float eps;
+    float weight_offset;
+    int num_axes;
+    unsigned axis_word[kHeadDim / 32];    // two bits per pair: its axis
+    unsigned one_axis;                // bit c: pairs 8 c .. 8 c + 7 follow one axis
+};
+
+cudaError_t launch_norm_rope_cache(NormRopeParams p, bool src_bf16, bool fp8, bool interleaved, int sms,
+                                   cudaStream_t stream);
+
 // Eviction: selection of the places that stay and the copy of their rows, by a cluster of
 // `parts` CTAs per sequence and KV head.
 struct EvictParams {
@@ -276,6 +293,62 @@ struct EvictPlan {
 EvictPlan evict_plan(long long rows, long long cap, int sms);
 cudaError_t evict_prepare();
 cudaError_t launch_evict(const EvictParams& p, const EvictPlan& plan, bool fp8, cudaStream_t stream);
+
+// Commit of a tree's accepted path: rows of K and V moved inside every layer's caches.
+constexpr int kCommitLayers = 64;     // layers of one launch
+
+struct CommitParams {
+    int32_t* seq_lens_out;            // null in the launches after the first
+    void* caches[2 * kCommitLayers];  // K and V of each layer
+    const int32_t* paths;             // [num_seqs][max_path]
+    const int32_t* path_lens;
+    const int32_t* query_start_loc;
+    const int32_t* block_tables;
+    const int32_t* seq_lens;
+    int* status;                      // device status word, or null
+    int num_layers;
+    int max_path;
+    int max_blocks;
+    int num_seqs;
+    int num_kv_heads;
+    int num_blocks;
+    int block_shift;
+};
+
+cudaError_t launch_tree_commit(const CommitParams& p, bool fp8, cudaStream_t stream);
+
+// Attention with scores or masks that are not plain (pa_mixed_scored, pa_tree).
+struct ScoredParams {
+    void* out;
+    const void* q;
+    const void* k_cache;
+    const void* v_cache;
+    const int32_t* query_start_loc;
+    const int32_t* block_tables;
+    const int32_t* seq_lens;
+    const int32_t* prefix_lens;       // null: none
+    const float* slopes;              // null: no bias
+    const unsigned long long* masks;  // tree: [total_rows][mask_words], else null
+    const float* k_scale;
+    const float* v_scale;
+    int scale_stride;                 // FP8 scales: 0 one per tensor, 1 one per KV head
+    int* status;
+    int mask_words;
+    int window;                       // 0: none
+    int num_seqs;
+    int total_rows;                   // rows of q and out
+    int num_q_heads;
+    int num_kv_heads;
+    int group;                        // query heads per KV head
+    int max_blocks;
+    int num_blocks;
+    int block_size;                   // tokens per physical block: 8, 16 or 32
+    int block_shift;                  // log2(block_size)
+    float scale;
+    float cap;                        // 0: none
+};
+
+cudaError_t launch_scored(CacheKind kind, bool q_bf16, const ScoredParams& p, cudaStream_t stream);
 
 // Prefill chunks.
 size_t chunk_smem_bytes(CacheKind kind, int num_seqs);

@@ -107,20 +107,6 @@ __global__ void __launch_bounds__(256) rope_table_kernel(float* __restrict__ cos
 }
 
 // ---- rotation and slot write ----------------------------------------------------
-// Two e4m3 codes of rotated components by the slot-write rule (a NaN has no source
-// element here and becomes the positive one).
-__device__ __forceinline__ uint32_t e4m3_of(float a, float b, float scale) {
-    const float lo = __fdiv_rn(a, scale), hi = __fdiv_rn(b, scale);
-    uint16_t y;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(y) : "f"(hi), "f"(lo));
-    uint32_t c_lo = y & 0xffu, c_hi = y >> 8;
-    if (isnan(lo)) c_lo = 0x7fu;
-    else if ((c_lo & 0x7fu) == 0) c_lo = signbit(lo) ? 0x80u : 0u;
-    if (isnan(hi)) c_hi = 0x7fu;
-    else if ((c_hi & 0x7fu) == 0) c_hi = signbit(hi) ? 0x80u : 0u;
-    return c_lo | (c_hi << 8);
-}
-
 // HBM-bound: q is read and written once, k and v are read once and written once (16384
 // tokens of 32/8 heads in bf16, 0.41 GB, take 62.3 us: 6.6 TB/s).
 // Eight threads own a row (one head of one token): each holds two 16-byte pieces of it,
