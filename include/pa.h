@@ -539,7 +539,9 @@ PA_API pa_status pa_mixed_scored(void* out, const void* q, const int32_t* query_
  *   cap            as pa_mixed_scored
  *   window         0: none; else of the tokens before the tree row j sees those with
  *                  pos - t < window, pos being the place of the first node plus the number of
- *                  nodes that it sees, less one (its depth)
+ *                  nodes that it sees (one at least), less one: its depth.  Table entries of
+ *                  blocks wholly before place first node - window + 1 are not read; tokens from
+ *                  there on must be finite
  * A row that sees nothing (no token before the tree and an empty mask) is zeros.  Other
  * arguments, and what tokens that no row sees may hold, as pa_mixed_scored.
  */

@@ -66,15 +66,6 @@ constexpr int kRegsFront = 104;              // registers per thread of warps 0-
 constexpr int kRegsSoftmax = 200;            // ... and of the softmax warps 4-11
 static_assert(128 * kRegsFront + 256 * kRegsSoftmax <= 384 * 168, "register split above the launch total");
 
-template <int N>
-__device__ __forceinline__ void setmaxnreg_inc() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void setmaxnreg_dec() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 // barrier indices (8 bytes each from kOffBars)
 enum {
     kBarKFull = 0,                          // [K stage]
@@ -101,50 +92,6 @@ struct TcCfg {
     // warpgroup then hands registers to the two softmax warpgroups.
     static constexpr int kWarps = 12;
 };
-
-// Bounded wait by lane 0 of the warp, then an acquire by every lane.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit) {
-    bool ok = true;
-    if ((threadIdx.x & 31) == 0) ok = mbar_wait_bounded(bar, parity, limit);
-    ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
-    if (ok) mbar_try_wait(bar, parity);
-    return ok;
-}
-
-// Bounded wait that polls with the non-suspending test: for the MMA issuer, which
-// must start the products the moment a softmax releases P.
-__device__ __forceinline__ bool mbar_poll_bounded(uint32_t bar, uint32_t parity, uint64_t limit) {
-    if (mbar_test(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
-    while (true) {
-#pragma unroll 1
-        for (int k = 0; k < 64; ++k)
-            if (mbar_test(bar, parity)) return true;
-        if (global_timer_ns() - t0 > limit) return false;
-    }
-}
-
-// Three-input maximum / minimum (one instruction on sm_100 and later).
-__device__ __forceinline__ float max3f(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-__device__ __forceinline__ float min3f(float a, float b, float c) {
-    float r;
-    asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-
-// 16 consecutive 32-bit columns of this thread's tensor-memory lane.
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-            taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
 
 }  // namespace
 

@@ -27,6 +27,7 @@ struct DeviceState {
     bool decode_prepared[3][2][3][2][2] = {};
     bool chunk_prepared[3][2] = {};
     bool evict_prepared = false;
+    bool scored_prepared[3][2][2] = {};
 };
 
 std::mutex g_mu;
@@ -461,12 +462,35 @@ pa_status scored_impl(ScoredParams p, void* out, const void* q, const int32_t* q
     if (s != PA_OK) return s;
     if (!std::isfinite(cap) || !(cap >= 0.f) || window < 0) return PA_ERR_INVALID_ARG;
     if (num_seqs > 0 && (!query_start_loc || !aligned(query_start_loc, 4))) return PA_ERR_INVALID_ARG;
-    if (num_q_heads / num_kv_heads > chunk_rows()) return PA_ERR_UNSUPPORTED;
-    if (static_cast<long long>(total_q) * num_q_heads >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
-    const size_t need = pa_workspace_size_scored(num_seqs, num_q_heads, num_kv_heads, head_dim);
-    if (need == 0) return PA_ERR_CUDA;
-    if (workspace_bytes < need) return PA_ERR_WORKSPACE;
+    const int group = num_q_heads / num_kv_heads;
+    if (group > scored_rows()) return PA_ERR_UNSUPPORTED;
+    // rows, and steps of 128 keys of all units, in 32 bits
+    const long long pair = 2ll * (scored_rows() / group);
+    const long long units = (num_seqs + (total_q + pair - 1) / pair) * num_kv_heads;
+    const long long steps = static_cast<long long>(max_blocks_per_seq) * block_size / scored_rows() + 1;
+    if (static_cast<long long>(total_q) * num_q_heads >= (1ll << 31) || units * steps >= (1ll << 31))
+        return PA_ERR_UNSUPPORTED;
     if (num_seqs == 0) return PA_OK;
+    DeviceState* st = device_state(nullptr);
+    if (!st) return PA_ERR_CUDA;
+    const ScoredLayout lay = scored_layout(st->sms);
+    if (workspace_bytes < lay.total) return PA_ERR_WORKSPACE;
+    const CacheKind kind = kind_of(cache_dtype);
+    const bool q_bf16 = q_dtype == PA_BF16, fp8 = kind == kKindFp8;
+    const bool mod = cap > 0.f || p.slopes != nullptr;
+    {
+        std::lock_guard<std::mutex> lock(g_mu);
+        if (!st->scored_prepared[kind][q_bf16][mod]) {
+            cudaError_t e = scored_prepare(kind, q_bf16, mod);
+            if (e != cudaSuccess) return fail("cudaFuncSetAttribute(scored)", e);
+            st->scored_prepared[kind][q_bf16][mod] = true;
+        }
+    }
+    CUtensorMap kmap, vmap;
+    s = encode_cache_map(&kmap, k_cache, num_blocks, num_kv_heads, block_size, fp8);
+    if (s != PA_OK) return s;
+    s = encode_cache_map(&vmap, v_cache, num_blocks, num_kv_heads, block_size, fp8);
+    if (s != PA_OK) return s;
     p.out = out;
     p.q = q;
     p.k_cache = k_cache;
@@ -490,7 +514,16 @@ pa_status scored_impl(ScoredParams p, void* out, const void* q, const int32_t* q
     p.block_shift = block_shift_of(block_size);
     p.scale = scale;
     p.cap = cap;
-    return launched(launch_scored(kind_of(cache_dtype), q_dtype == PA_BF16, p, stream), "launch(scored)");
+    p.queries_per_tile = scored_rows() / group;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.records = reinterpret_cast<CombineRecord*>(ws + lay.records_off);
+    p.ml = reinterpret_cast<float2*>(ws + lay.ml_off);
+    p.partial = reinterpret_cast<float*>(ws + lay.partial_off);
+    p.timeout_ns = kDefaultTimeoutNs;
+    s = launched(launch_scored(kind, q_bf16, mod, kmap, vmap, p, st->sms, stream), "launch(scored)");
+    // tables of one step: no unit is ever shared
+    if (s != PA_OK || static_cast<long long>(max_blocks_per_seq) * block_size <= scored_rows()) return s;
+    return launched(launch_scored_combine(q_bf16, fp8, p, st->sms, stream), "launch(scored combine)");
 }
 
 }  // namespace
@@ -1078,7 +1111,8 @@ size_t pa_workspace_size_scored(int num_seqs, int num_q_heads, int num_kv_heads,
     if (num_seqs < 0 || num_seqs > kMaxSeqs || head_dim != kHeadDim || num_kv_heads <= 0 || num_q_heads <= 0 ||
         num_q_heads % num_kv_heads != 0)
         return 0;
-    return 256;
+    DeviceState* st = device_state(nullptr);
+    return st ? scored_layout(st->sms).total : 0;
 }
 
 pa_status pa_mixed_scored(void* out, const void* q, const int32_t* query_start_loc, const void* k_cache,

@@ -318,6 +318,16 @@ struct CommitParams {
 cudaError_t launch_tree_commit(const CommitParams& p, bool fp8, cudaStream_t stream);
 
 // Attention with scores or masks that are not plain (pa_mixed_scored, pa_tree).
+// What a CTA of it tells the combine of the unit that it began and did not finish.
+struct CombineRecord {
+    int rows;                         // rows of the unit; 0: no such unit
+    int row0;                         // its first query
+    int head0;                        // its first query head
+    int solo;                         // one tile of rows
+    int last;                         // the CTA that finished it
+    int pad[3];
+};
+
 struct ScoredParams {
     void* out;
     const void* q;
@@ -344,11 +354,27 @@ struct ScoredParams {
     int num_blocks;
     int block_size;                   // tokens per physical block: 8, 16 or 32
     int block_shift;                  // log2(block_size)
+    int queries_per_tile;             // queries of a 128-row tile
     float scale;
     float cap;                        // 0: none
+    CombineRecord* records;           // [CTAs]
+    float2* ml;                       // [CTAs][2][256]: maximum (log2 units), sum
+    float* partial;                   // [CTAs][2][256][128]: unnormalised outputs
+    unsigned long long timeout_ns;    // bound of every barrier wait
 };
 
-cudaError_t launch_scored(CacheKind kind, bool q_bf16, const ScoredParams& p, cudaStream_t stream);
+// Offsets in the workspace, behind the status word.
+struct ScoredLayout {
+    size_t records_off, ml_off, partial_off, total;
+};
+
+ScoredLayout scored_layout(int sms);
+int scored_rows();                    // rows of one tile
+// mod: the kernel that caps and biases scores
+cudaError_t scored_prepare(CacheKind kind, bool q_bf16, bool mod);
+cudaError_t launch_scored(CacheKind kind, bool q_bf16, bool mod, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                          const ScoredParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_scored_combine(bool out_bf16, bool fp8, const ScoredParams& p, int sms, cudaStream_t stream);
 
 // Prefill chunks.
 size_t chunk_smem_bytes(CacheKind kind, int num_seqs);

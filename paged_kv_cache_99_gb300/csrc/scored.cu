@@ -1,6 +1,37 @@
-// Attention over the paged cache whose scores or masks are not plain (sm_103a): scores capped by
-// a tanh, biased by distance, windowed, open over a prefix, or masked by a tree of drafted tokens.
+// Attention over the paged cache whose scores or masks are not plain, on the 5th-generation
+// tensor cores (sm_103a): scores capped by a tanh, biased by distance, windowed, open over a
+// prefix, or masked by a tree of drafted tokens; decode rows, drafts and prompts in one launch.
+//
+// A row (query, head) at position pos sees the cached tokens [lo, hi) of its sequence, a tree's
+// row also the nodes of its mask behind them; with x = scale q.k its score is cap tanh(x / cap)
+// - slope |pos - t|, and its output the softmax of the scores times V, by a running maximum and
+// sum over steps of 128 keys.
+//
+// Work.  A unit is one KV head and up to 256 rows (queries x the head's group) of one sequence;
+// it takes the steps of 128 keys that any of its rows sees.  All units' steps are laid end to
+// end and cut into one equal range per SM, whatever the lengths: a decode step over a few long
+// sequences, a verification of small trees and a long prompt all fill the GPU.  A CTA takes
+// its range as segments, one per unit it touches; a unit that several CTAs share leaves
+// unnormalised partials (output, maximum, sum) that a second small kernel adds up.
+//
+// A unit of more than 128 rows is a pair: tiles A and B are its first and second 128 rows and
+// share every K and V tile.  A unit of up to 128 rows (decode rows, most trees) is a solo: A
+// takes the even steps and B the odd ones, with a softmax of their own, and the two are added
+// up at the end through tensor memory, where both hold a row in the same lane.  Either way one
+// tile's softmax runs beside the other's products, and K and V stream through a ring that runs
+// ahead across segments.  Rows past the unit's are not computed: a warp whose 32 rows are all
+// past them only passes the barriers.
+//
+// Warps: 0 copies K and V (TMA, 128-byte swizzle, a lane per 8 or 16 rows of a block), 1 issues
+// tcgen05.mma, 2 walks the range and describes the segments to the others, 3 fetches the
+// queries a segment ahead and zeroes V rows that no row sees (0 x NaN is NaN), 4-7 and 8-11 are
+// the softmax of tiles A and B, a thread per row; with an FP8 cache 12-15 widen the copied e4m3
+// rows exactly to fp16, which costs them about as long as the copies take.
+// Every wait is bounded.
+#include <cuda.h>
 #include <cuda_runtime.h>
+
+#include <climits>
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
@@ -9,132 +40,1232 @@ namespace pa {
 
 namespace {
 
+constexpr int kRows = 128;                   // MMA M of one tile
+constexpr int kKeys = 128;                   // keys per step (MMA N of S, K of P.V)
+constexpr uint32_t kHalfBytes = 16384;       // [128 rows][64 elements], 128-byte swizzle
+constexpr uint32_t kTileBytes = 2 * kHalfBytes;
+constexpr int kSegs = 4;                     // segments described ahead
+constexpr int kSegInts = 16;
+constexpr float kRescale = 8.0f;             // lazy rescale threshold (factor 256)
+constexpr float kCapSmall = 0.6f;            // |x / cap| up to which the tanh is a polynomial
+
+template <int Kind>
+struct Cfg {
+    static constexpr bool kFp8 = Kind == kKindFp8;
+    static constexpr bool kMmaBf16 = Kind == kKindBf16;
+    static constexpr int kWarps = kFp8 ? 16 : 12;
+    static constexpr int kStages = kFp8 ? 3 : 5;         // K and V tiles of 16-bit elements
+    static constexpr int kRaw = kFp8 ? 4 : 0;            // e4m3 tiles as copied
+    // launch registers per thread, and the shares after setmaxnreg
+    [[maybe_unused]] static constexpr int kRegsLaunch = kFp8 ? 128 : 168;
+    static constexpr int kRegsFront = kFp8 ? 64 : 104;
+    static constexpr int kRegsSoftmax = kFp8 ? 192 : 200;
+    static constexpr uint32_t kOffStage = 2 * kTileBytes;                    // behind Q_A, Q_B
+    static constexpr uint32_t kOffRaw = kOffStage + kStages * kTileBytes;
+    static constexpr uint32_t kOffBars = kOffRaw + kRaw * kHalfBytes;
+    static constexpr uint32_t kOffSegs = kOffBars + 448;
+    static constexpr uint32_t kOffMl = kOffSegs + kSegs * kSegInts * 4;      // [2][128] (maximum, sum)
+    static constexpr uint32_t kOffScan = kOffMl + 2 * kRows * 8;             // [kWarps]
+    static constexpr uint32_t kSmem = kOffScan + 64;
+};
+static_assert(256 * Cfg<kKindFp8>::kRegsFront + 256 * Cfg<kKindFp8>::kRegsSoftmax <=
+                  Cfg<kKindFp8>::kWarps * 32 * Cfg<kKindFp8>::kRegsLaunch, "register split above the launch total");
+static_assert(128 * Cfg<kKindBf16>::kRegsFront + 256 * Cfg<kKindBf16>::kRegsSoftmax <=
+                  Cfg<kKindBf16>::kWarps * 32 * Cfg<kKindBf16>::kRegsLaunch, "register split above the launch total");
+static_assert(Cfg<kKindBf16>::kSmem <= 232448 && Cfg<kKindFp8>::kSmem <= 232448, "shared memory");
+
+enum {                                       // barriers, 8 bytes each
+    kFull = 0,                               // [stage] a 16-bit tile has landed
+    kEmpty = kFull + 5,                      // [stage]
+    kRawFull = kEmpty + 5,                   // [raw stage]
+    kRawEmpty = kRawFull + 4,                // [raw stage]
+    kSegFull = kRawEmpty + 4,                // [segment slot]
+    kSegEmpty = kSegFull + kSegs,            // [segment slot]
+    kQFull = kSegEmpty + kSegs,              // [Q buffer]
+    kQEmpty = kQFull + 2,                    // [Q buffer]
+    kSFull = kQEmpty + 2,                    // [tile]
+    kPHalf = kSFull + 2,                     // [tile] P of the step's first 64 keys is stored
+    kPFull = kPHalf + 2,                     // [tile]
+    kSegDone = kPFull + 2,                   // every product of the segment is done
+    kMlReady,                                // solo: both tiles' (maximum, sum) are in shared memory
+    kOFree,                                  // the segment's outputs are read
+    kFixed,                                  // [stage] V rows that no row sees are zeroed (edge steps)
+    kIssued = kFixed + 5,                    // [stage] the copy of an edge step's V is under way
+    kNumBars = kIssued + 5
+};
+static_assert(kNumBars * 8 + 4 <= 448, "barriers");
+
 // The cached tokens [lo, hi) that a row sees and its position; a tree's row also sees the nodes
 // of its mask, which lie behind hi.
 struct RowView {
     int pos, lo, hi;
 };
 
-// Lengths of a sequence that fit q, the table and the masks.
-__device__ __forceinline__ bool scored_lengths_ok(const ScoredParams& p, int q0, int q_len, int n) {
-    return q0 >= 0 && q_len >= 0 && q0 <= p.total_rows && q_len <= p.total_rows - q0 && n >= q_len &&
-           n <= (p.max_blocks << p.block_shift) && (!p.masks || q_len <= 64ll * p.mask_words);
+// A sequence's rows and lengths; q_len is 0 where there is nothing to do.
+struct SeqView {
+    int q0, q_len, n, prefix;
+};
+
+__device__ __forceinline__ SeqView seq_view(const ScoredParams& p, int s, bool report) {
+    SeqView v;
+    v.q0 = p.query_start_loc[s];
+    const int q1 = p.query_start_loc[s + 1];
+    v.n = p.seq_lens[s];
+    v.prefix = p.prefix_lens ? min(p.prefix_lens[s], v.n) : 0;
+    v.q_len = q1 - v.q0;
+    if (v.q_len == 0) return v;
+    // lengths that fit q, the table and the masks
+    if (v.q0 < 0 || q1 < v.q0 || q1 > p.total_rows || v.n < v.q_len || v.n > (p.max_blocks << p.block_shift) ||
+        (p.masks && v.q_len > 64ll * p.mask_words)) {
+        if (report) atomicOr(p.status, kDevErrRange);
+        v.q_len = 0;
+    }
+    return v;
 }
 
-// Row j of a sequence of n tokens whose last q_len are the rows'.
-__device__ __forceinline__ RowView row_view(const ScoredParams& p, int s, int q0, int q_len, int n, int j) {
+// 32 bits of a row's mask from node `at` on (negative: the nodes start inside the word).
+__device__ __forceinline__ uint32_t tree_bits(const unsigned long long* words, int q_len, int at) {
+    if (at >= q_len || at <= -32) return 0;
+    uint32_t w;
+    if (at < 0) {
+        w = static_cast<uint32_t>(__ldg(words)) << -at;
+        const int left = q_len - at;             // bits of the word before the tree's end
+        return left < 32 ? w & ((1u << left) - 1) : w;
+    }
+    const int i = at >> 6, sh = at & 63;
+    w = static_cast<uint32_t>(__ldg(words + i) >> sh);
+    if (sh > 32 && 64 * (i + 1) < q_len) w |= static_cast<uint32_t>(__ldg(words + i + 1) << (64 - sh));
+    const int left = q_len - at;
+    return left < 32 ? w & ((1u << left) - 1) : w;
+}
+
+// Row j of a sequence.
+__device__ __forceinline__ RowView row_view(const ScoredParams& p, const SeqView& s, int j) {
     RowView v;
-    v.pos = n - q_len + j;
+    v.pos = s.n - s.q_len + j;
     v.hi = v.pos + 1;
     if (p.masks) {
         // a node's position: behind the context, as deep as its path is long
         int bits = 0;
-        const unsigned long long* words = p.masks + static_cast<size_t>(q0 + j) * p.mask_words;
-        for (int i = 0; 64 * i < q_len; ++i) {
-            unsigned long long w = words[i];
-            if (q_len - 64 * i < 64) w &= (1ull << (q_len - 64 * i)) - 1;
-            bits += __popcll(w);
-        }
-        v.pos = n - q_len + bits - 1;
-        v.hi = n - q_len;
-    } else if (p.prefix_lens) {
-        v.hi = max(v.hi, min(p.prefix_lens[s], n));
+        const unsigned long long* words = p.masks + static_cast<size_t>(s.q0 + j) * p.mask_words;
+        for (int i = 0; i < s.q_len; i += 32) bits += __popc(tree_bits(words, s.q_len, i));
+        v.hi = s.n - s.q_len;
+        v.pos = v.hi + max(bits - 1, 0);
+    } else {
+        v.hi = max(v.hi, s.prefix);
     }
     v.lo = p.window > 0 ? max(0, v.pos - p.window + 1) : 0;
     return v;
 }
 
-// One warp per (query row, query head): a lane holds four of the head's 128 components, every
-// visible key costs one shuffled sum.  Online softmax in 32 bits.
-template <int Kind, bool QBf16>
-__global__ void __launch_bounds__(256) scored_kernel(const ScoredParams p) {
-    grid_dependency_wait();
-    grid_launch_dependents();
-    constexpr bool kFp8 = Kind == kKindFp8;
-    const int lane = threadIdx.x & 31;
-    const long long item = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int row = static_cast<int>(item / p.num_q_heads), head = static_cast<int>(item % p.num_q_heads);
-    if (row >= p.total_rows) return;
-    // the sequence whose rows hold `row`
-    int lo = 0, hi = p.num_seqs;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.query_start_loc[mid] <= row) lo = mid; else hi = mid;
-    }
-    const int s = lo;
-    const int q0 = p.query_start_loc[s], q_len = p.query_start_loc[s + 1] - q0, n = p.seq_lens[s];
-    const int j = row - q0;
-    if (j < 0 || j >= q_len) return;                        // a row behind the last sequence
-    if (!scored_lengths_ok(p, q0, q_len, n)) {
-        if (lane == 0) atomicOr(p.status, kDevErrRange);
-        return;
-    }
-    const RowView v = row_view(p, s, q0, q_len, n, j);
-    const int h = head / p.group;
-    float ks = 1.f, vs = 1.f;
-    if constexpr (kFp8) {
-        ks = __ldg(p.k_scale + h * p.scale_stride);
-        vs = __ldg(p.v_scale + h * p.scale_stride);
-    }
-    const uint2 qw = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) +
-                                                     (static_cast<size_t>(row) * p.num_q_heads + head) * kHeadDim + 4 * lane);
-    const float q[4] = {to_float<QBf16>(qw.x & 0xffffu), to_float<QBf16>(qw.x >> 16), to_float<QBf16>(qw.y & 0xffffu),
-                        to_float<QBf16>(qw.y >> 16)};
-    const float slope = p.slopes ? __ldg(p.slopes + head) : 0.f;
-    const int32_t* bt = p.block_tables + static_cast<size_t>(s) * p.max_blocks;
-    auto load4 = [&](const void* cache, size_t at, float (&x)[4]) {
-        if constexpr (kFp8) {
-            const uint32_t w = __ldg(reinterpret_cast<const unsigned*>(static_cast<const uint8_t*>(cache) + at));
-            const uint32_t a = e4m3x2_to_f16x2(w & 0xffffu), b = e4m3x2_to_f16x2(w >> 16);
-            x[0] = to_float<false>(a & 0xffffu); x[1] = to_float<false>(a >> 16);
-            x[2] = to_float<false>(b & 0xffffu); x[3] = to_float<false>(b >> 16);
-        } else {
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(cache) + at));
-            x[0] = to_float<Kind == kKindBf16>(w.x & 0xffffu); x[1] = to_float<Kind == kKindBf16>(w.x >> 16);
-            x[2] = to_float<Kind == kKindBf16>(w.y & 0xffffu); x[3] = to_float<Kind == kKindBf16>(w.y >> 16);
-        }
-    };
-    float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    auto take = [&](int t) {
-        int phys = __ldg(bt + (t >> p.block_shift));
-        if (static_cast<unsigned>(phys) >= static_cast<unsigned>(p.num_blocks)) {
-            if (lane == 0) atomicOr(p.status, kDevErrRange);
-            phys = 0;
-        }
-        const size_t at = ((((static_cast<size_t>(phys) * p.num_kv_heads + h) << p.block_shift) +
-                            (t & (p.block_size - 1))) * kHeadDim) + 4 * lane;
-        float k[4], x[4];
-        load4(p.k_cache, at, k);
-        load4(p.v_cache, at, x);
-        float dot = q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3];
-#pragma unroll
-        for (int e = 16; e; e >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, e);
-        float sc = dot * (p.scale * ks);
-        if (p.cap > 0.f) sc = p.cap * tanhf(sc / p.cap);
-        sc -= slope * fabsf(static_cast<float>(v.pos - t));
-        const float mn = fmaxf(m, sc), a = expf(m - mn), w = expf(sc - mn);
-        m = mn;
-        l = l * a + w;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = o[e] * a + w * x[e];
-    };
-    for (int t = v.lo; t < v.hi; ++t) take(t);
-    if (p.masks) {
-        const unsigned long long* words = p.masks + static_cast<size_t>(row) * p.mask_words;
-        for (int i = 0; i < q_len; ++i)
-            if (words[i >> 6] >> (i & 63) & 1) take(n - q_len + i);
-    }
-    const float inv = l > 0.f ? vs / l : 0.f;
-    uint16_t* dst = static_cast<uint16_t*>(p.out) + (static_cast<size_t>(row) * p.num_q_heads + head) * kHeadDim + 4 * lane;
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<QBf16>(o[0] * inv, o[1] * inv), pack2<QBf16>(o[2] * inv, o[3] * inv));
+// Unit t of a sequence: its queries [ja, ja + nq), the keys [klo, khi) that they see in all,
+// and the steps of 128 keys that hold these.
+struct Unit {
+    int ja, nq, klo, khi, step0, steps;
+};
+
+__device__ __forceinline__ Unit unit_of(const ScoredParams& p, const SeqView& s, int t) {
+    Unit u;
+    u.ja = t * 2 * p.queries_per_tile;
+    u.nq = min(s.q_len - u.ja, 2 * p.queries_per_tile);
+    const int ctx = s.n - s.q_len;
+    // position of the first row (of any node: not before the first)
+    const int first = p.masks ? ctx : ctx + u.ja;
+    u.khi = p.masks ? s.n : max(ctx + u.ja + u.nq, s.prefix);
+    u.klo = p.window > 0 ? max(0, first - p.window + 1) : 0;
+    u.step0 = u.klo / kKeys;
+    u.steps = (u.khi + kKeys - 1) / kKeys - u.step0;
+    return u;
 }
+
+__device__ __forceinline__ int units_per_head(const ScoredParams& p, const SeqView& s) {
+    return (s.q_len + 2 * p.queries_per_tile - 1) / (2 * p.queries_per_tile);
+}
+
+// Steps of a sequence, all heads.
+__device__ __forceinline__ int seq_steps(const ScoredParams& p, int s, bool report) {
+    const SeqView v = seq_view(p, s, report);
+    const int np = units_per_head(p, v);
+    int sum = 0;
+    for (int t = 0; t < np; ++t) sum += unit_of(p, v, t).steps;
+    return sum * p.num_kv_heads;
+}
+
+// A segment as its CTA's warps see it: steps [step, step + steps) of a unit.
+struct Seg {
+    int h, row0, nq, step, steps, klo, khi;
+    int ctx;                                 // tree: tokens before it, else INT_MAX
+    int j0, q0, q_len, n, prefix;            // the unit's first query, and its sequence
+    int seq;
+    int flags;                               // 1: solo, 2: the whole unit
+    int slot;                                // where its partial goes
+};
+
+__device__ __forceinline__ Seg read_seg(const int* d) {
+    Seg g;
+    const int4* v = reinterpret_cast<const int4*>(d);
+    const int4 a = v[0], b = v[1], c = v[2], e = v[3];
+    g.h = a.x; g.row0 = a.y; g.nq = a.z; g.step = a.w;
+    g.steps = b.x; g.klo = b.y; g.khi = b.z; g.ctx = b.w;
+    g.j0 = c.x; g.q0 = c.y; g.q_len = c.z; g.n = c.w;
+    g.prefix = e.x; g.seq = e.y; g.flags = e.z; g.slot = e.w;
+    return g;
+}
+
+// A step some of whose V rows no row may see.
+__device__ __forceinline__ bool edge_step(const Seg& g, int key0) {
+    return key0 < g.klo || key0 + kKeys > g.khi || key0 + kKeys > g.ctx;
+}
+
+// Tile order in the ring: K0, K1, V0, K2, V1, K3, ...: each K two steps ahead of its use, V as
+// its step begins.
+__device__ __forceinline__ int item_v(int steps, int i) { return min(2, steps) + i + min(i, max(steps - 2, 0)); }
+__device__ __forceinline__ int item_k(int steps, int i) { return i < 2 ? i : item_v(steps, i - 2) + 1; }
+
+// tanh(x) / x on |x| <= kCapSmall as a polynomial in x^2 (interpolated at Chebyshev nodes):
+// within 2^-23.7 of it.
+constexpr float kTanh0 = 0.999999926f, kTanh1 = -0.33332302f, kTanh2 = 0.133100644f, kTanh3 = -0.0520966534f,
+                kTanh4 = 0.0154687513f;
 
 }  // namespace
 
-cudaError_t launch_scored(CacheKind kind, bool q_bf16, const ScoredParams& p, cudaStream_t stream) {
-    const long long items = static_cast<long long>(p.total_rows) * p.num_q_heads;
+template <int Kind, bool QBf16, bool Mod>
+__global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
+    scored_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const ScoredParams p) {
+    using C = Cfg<Kind>;
+    constexpr bool kFp8 = C::kFp8;
+    constexpr bool kMmaBf16 = C::kMmaBf16;
+    constexpr int NS = C::kStages;
+    constexpr int kThreads = C::kWarps * 32;
+    constexpr int kSegReaders = kFp8 ? 15 : 11;
+
+    extern __shared__ __align__(1024) uint8_t sm[];             // as the 128-byte swizzle wants it
+    const uint32_t sbase = smem_addr(sm);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kOffBars + kNumBars * 8);
+    int* segs = reinterpret_cast<int*>(sm + C::kOffSegs);
+    float2* ml_smem = reinterpret_cast<float2*>(sm + C::kOffMl);
+    int* scan = reinterpret_cast<int*>(sm + C::kOffScan);
+    int* cum = reinterpret_cast<int*>(sm + C::kOffStage);        // only before the first copy
+    auto bar = [&](int i) -> uint32_t { return sbase + C::kOffBars + 8u * i; };
+    auto stage = [&](int r) -> uint32_t { return sbase + C::kOffStage + static_cast<uint32_t>(r % NS) * kTileBytes; };
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(bar(kFull + i), kFp8 ? 4 : 1);
+            mbar_init(bar(kEmpty + i), 1);
+            mbar_init(bar(kFixed + i), 1);
+            mbar_init(bar(kIssued + i), 1);
+        }
+        for (int i = 0; i < C::kRaw; ++i) {
+            mbar_init(bar(kRawFull + i), 1);
+            mbar_init(bar(kRawEmpty + i), 4);
+        }
+        for (int i = 0; i < kSegs; ++i) {
+            mbar_init(bar(kSegFull + i), 1);
+            mbar_init(bar(kSegEmpty + i), kSegReaders);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(kQFull + i), 1);
+            mbar_init(bar(kQEmpty + i), 1);
+            mbar_init(bar(kSFull + i), 1);
+            mbar_init(bar(kPHalf + i), 4);
+            mbar_init(bar(kPFull + i), 4);
+        }
+        mbar_init(bar(kSegDone), 1);
+        mbar_init(bar(kMlReady), 8);
+        mbar_init(bar(kOFree), 8);
+        fence_barrier_init();
+        tmap_prefetch(&kmap);
+        tmap_prefetch(&vmap);
+    }
+
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    // ---- steps per sequence: exclusive scan into cum ----
+    const int B = p.num_seqs;
+    {
+        const int per = (B + kThreads - 1) / kThreads;
+        const int beg = min(B, static_cast<int>(threadIdx.x) * per), end = min(B, beg + per);
+        int local = 0;
+        for (int s = beg; s < end; ++s) {
+            const int w = seq_steps(p, s, blockIdx.x == 0);
+            cum[s] = w;
+            local += w;
+        }
+        int incl = local;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) scan[warp] = incl;
+        __syncthreads();
+        int run = incl - local;
+        for (int w = 0; w < warp; ++w) run += scan[w];
+        for (int s = beg; s < end; ++s) {
+            const int w = cum[s];
+            cum[s] = run;
+            run += w;
+        }
+        if (threadIdx.x == kThreads - 1) cum[B] = run;
+        __syncthreads();
+    }
+    const int T = cum[B];
+    const int W = min(static_cast<int>(gridDim.x), T);
+    const int cta = blockIdx.x;
+    if (cta >= W) {
+        if (threadIdx.x == 0) p.records[cta].rows = 0;
+        return;
+    }
+    // ---- this CTA's range, found by warp 2 ----
+    int f = static_cast<int>(static_cast<long long>(T) * cta / W);
+    int left = static_cast<int>(static_cast<long long>(T) * (cta + 1) / W) - f;
+    int cs = 0, ct = 0, ch = 0, coff = 0;    // sequence, unit, head, step within the unit
+    SeqView sv_cur = {};
+    if (warp == 2) {
+        int lo = 0, hi = B;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (cum[mid] <= f) lo = mid; else hi = mid;
+        }
+        cs = lo;
+        int rem = f - cum[lo];
+        sv_cur = seq_view(p, cs, false);
+        const int np = units_per_head(p, sv_cur);
+        // a lane per unit: the unit whose steps (all heads) hold the rest
+        for (int t0 = 0; t0 < np; t0 += 32) {
+            const int w = t0 + lane < np ? unit_of(p, sv_cur, t0 + lane).steps * p.num_kv_heads : 0;
+            int incl = w;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, incl > rem);
+            if (past) {
+                const int k = __ffs(past) - 1;
+                ct = t0 + k;
+                rem -= __shfl_sync(0xffffffffu, incl - w, k);
+                break;
+            }
+            rem -= __shfl_sync(0xffffffffu, incl, 31);
+        }
+        const int steps = unit_of(p, sv_cur, ct).steps;
+        ch = rem / steps;
+        coff = rem % steps;
+    }
+    fence_proxy_async_smem();                // cum was written where the first copies go
+    if (warp == 1) tmem_alloc(smem_addr(tmem_slot), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    auto tS = [&](int x) -> uint32_t { return tmem + 128u * x; };          // S, then P over its first 64 columns
+    auto tO = [&](int x) -> uint32_t { return tmem + 256u + 128u * x; };
+    const int G = p.group;
+    const int QT = p.queries_per_tile;
+    bool ok = true;
+
+    // every role follows the segments in order
+    int k = 0;                               // segments taken so far
+    auto next_seg = [&](Seg& g) -> bool {
+        if (!warp_wait(bar(kSegFull + k % kSegs), (k / kSegs) & 1, p.timeout_ns)) {
+            ok = false;
+            return false;
+        }
+        g = read_seg(segs + (k % kSegs) * kSegInts);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kSegEmpty + k % kSegs));
+        ++k;
+        return g.steps > 0;
+    };
+
+    if (warp < 4) {
+        setmaxnreg_dec<C::kRegsFront>();
+        if (warp == 0) {
+            // ================= K and V copies =================
+            const int bsh = p.block_shift;
+            const int rsh = min(bsh, 4);                          // log2 of a piece's rows
+            const int per_step = kKeys >> rsh;                    // pieces per step: 8 or 16
+            int r = 0;                                            // tiles copied so far
+            Seg g;
+            while (ok && next_seg(g)) {
+                const int32_t* bt = p.block_tables + static_cast<size_t>(g.seq) * p.max_blocks;
+                const int c_lo = g.klo >> rsh, c_hi = (g.khi - 1) >> rsh;     // pieces that hold keys
+                // the lane's piece of a step: its row in the cache, -1 for none
+                auto entry = [&](int i) -> int {
+                    const int c = (g.step + i) * per_step + lane;
+                    if (i >= g.steps || lane >= per_step || c < c_lo || c > c_hi) return -1;
+                    const int key = c << rsh;
+                    int phys = __ldg(bt + (key >> bsh));
+                    if (static_cast<unsigned>(phys) >= static_cast<unsigned>(p.num_blocks)) {
+                        atomicOr(p.status, kDevErrRange);
+                        phys = 0;
+                    }
+                    return ((phys * p.num_kv_heads + g.h) << bsh) + (key & (p.block_size - 1));
+                };
+                auto copy = [&](const CUtensorMap* map, int y) {
+                    constexpr int kRing = kFp8 ? C::kRaw : NS;
+                    constexpr int kF = kFp8 ? static_cast<int>(kRawFull) : static_cast<int>(kFull);
+                    constexpr int kE = kFp8 ? static_cast<int>(kRawEmpty) : static_cast<int>(kEmpty);
+                    const int st = r % kRing;
+                    if (r >= kRing && !warp_wait(bar(kE + st), ((r / kRing) - 1) & 1, p.timeout_ns)) {
+                        ok = false;
+                        return;
+                    }
+                    const unsigned live = __ballot_sync(0xffffffffu, y >= 0);
+                    const uint32_t full = bar(kF + st);
+                    if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(__popc(live)) * ((kFp8 ? 128u : 256u) << rsh));
+                    __syncwarp();
+                    if (y >= 0) {
+                        if constexpr (kFp8) {
+                            tma_load_2d(sbase + C::kOffRaw + st * kHalfBytes + (lane << rsh) * 128, map, 0, y, full);
+                        } else {
+                            const uint32_t dst = sbase + C::kOffStage + st * kTileBytes + (lane << rsh) * 128;
+                            tma_load_2d(dst, map, 0, y, full);
+                            tma_load_2d(dst + kHalfBytes, map, 64, y, full);
+                        }
+                    }
+                    ++r;
+                };
+                // K0, K1, then V(i), K(i + 2); the table's entries a step ahead of their use
+                int y0 = entry(0), y1 = entry(1);
+                copy(&kmap, y0);
+                if (ok && g.steps > 1) copy(&kmap, y1);
+                for (int i = 0; i < g.steps && ok; ++i) {
+                    const int y2 = entry(i + 2);
+                    copy(&vmap, y0);
+                    // (the tile's barrier is in its phase from here until the zeroing is done)
+                    if (!kFp8 && ok && lane == 0 && edge_step(g, (g.step + i) * kKeys)) mbar_arrive(bar(kIssued + (r - 1) % NS));
+                    if (ok && i + 2 < g.steps) copy(&kmap, y2);
+                    y0 = y1;
+                    y1 = y2;
+                }
+            }
+            if (!ok) {
+                if (lane == 0) atomicOr(p.status, kDevErrTimeout);
+                // let the copies still in flight land before the CTA leaves
+                constexpr int kRing = kFp8 ? C::kRaw : NS;
+                constexpr int kF = kFp8 ? static_cast<int>(kRawFull) : static_cast<int>(kFull);
+                for (int i = max(0, r - kRing); i < r; ++i) warp_wait(bar(kF + i % kRing), (i / kRing) & 1, p.timeout_ns);
+            }
+        } else if (warp == 1) {
+            // ================= MMA issuer =================
+            if (lane == 0) {
+                constexpr uint32_t idS = umma_idesc_f16<kMmaBf16>(kRows, kKeys, false);
+                constexpr uint32_t idPV = umma_idesc_f16<kMmaBf16>(kRows, kHeadDim, true);
+                auto wait = [&](uint32_t b, uint32_t par) -> bool {
+                    if (ok && !mbar_wait_bounded(b, par, p.timeout_ns)) ok = false;
+                    return ok;
+                };
+                auto poll = [&](uint32_t b, uint32_t par) -> bool {
+                    if (ok && !mbar_poll_bounded(b, par, p.timeout_ns)) ok = false;
+                    return ok;
+                };
+                auto tile_ready = [&](int r) -> bool { return wait(bar(kFull + r % NS), (r / NS) & 1); };
+                auto issue_s = [&](int x, uint32_t qbase, int r) {
+                    const uint32_t kbase = stage(r);
+#pragma unroll
+                    for (int kk = 0; kk < kHeadDim / 16; ++kk) {
+                        const uint64_t a = umma_desc_sw128(qbase + (kk >> 2) * kHalfBytes + (kk & 3) * 32, 16, 1024);
+                        const uint64_t b = umma_desc_sw128(kbase + (kk >> 2) * kHalfBytes + (kk & 3) * 32, 16, 1024);
+                        umma_f16(tS(x), a, b, idS, kk > 0 ? 1u : 0u);
+                    }
+                    umma_commit(bar(kSFull + x));
+                };
+                // P.V over the step's keys 64 half .. 64 half + 63
+                auto issue_pv = [&](int x, int r, int half, bool first) {
+                    const uint32_t vbase = stage(r);
+#pragma unroll
+                    for (int e = 0; e < kKeys / 32; ++e) {
+                        const int kk = half * (kKeys / 32) + e;
+                        // V is MN-major: d-halves kHalfBytes apart, 16 keys = 2 KiB
+                        const uint64_t b = umma_desc_sw128(vbase + kk * 2048, kHalfBytes, 1024);
+                        umma_f16_ts(tO(x), tS(x) + 8 * kk, b, idPV, (!first || kk > 0) ? 1u : 0u);
+                    }
+                };
+                int r0 = 0, seg = 0;
+                unsigned fixes = 0;                  // bit st: parity of the stage's zeroings
+                int q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
+                while (ok) {
+                    if (!wait(bar(kSegFull + seg % kSegs), (seg / kSegs) & 1)) break;
+                    const Seg g = read_seg(segs + (seg % kSegs) * kSegInts);
+                    mbar_arrive(bar(kSegEmpty + seg % kSegs));
+                    if (g.steps == 0) break;
+                    const bool solo = g.flags & 1;
+                    const int n = g.steps;
+                    const int qb = solo ? seg & 1 : 0;
+                    const uint32_t q_a = sbase + qb * kTileBytes, q_b = solo ? q_a : sbase + kTileBytes;
+                    if (!wait(bar(kQFull + qb), q_uses[qb] & 1)) break;
+                    ++q_uses[qb];
+                    if (!solo) {
+                        if (!wait(bar(kQFull + 1), q_uses[1] & 1)) break;
+                        ++q_uses[1];
+                    }
+                    auto q_free = [&]() {            // behind the segment's last S
+                        umma_commit(bar(kQEmpty + qb));
+                        if (!solo) umma_commit(bar(kQEmpty + 1));
+                    };
+                    // P(i) of tile x, in two halves, into O_x
+                    auto pv = [&](int x, int i, bool first) -> bool {
+                        const int r = r0 + item_v(n, i);
+                        if (!poll(bar(kPHalf + x), p_uses[x] & 1)) return false;
+                        tc_fence_after();
+                        issue_pv(x, r, 0, first);
+                        if (!poll(bar(kPFull + x), p_uses[x] & 1)) return false;
+                        tc_fence_after();
+                        issue_pv(x, r, 1, first);
+                        ++p_uses[x];
+                        return true;
+                    };
+                    auto v_ready = [&](int i) -> bool {
+                        const int st = (r0 + item_v(n, i)) % NS;
+                        if (!tile_ready(r0 + item_v(n, i))) return false;
+                        if (!kFp8 && edge_step(g, (g.step + i) * kKeys)) {
+                            if (!wait(bar(kFixed + st), fixes >> st & 1)) return false;
+                            fixes ^= 1u << st;
+                        }
+                        return true;
+                    };
+                    if (!tile_ready(r0)) break;
+                    tc_fence_after();
+                    issue_s(0, q_a, r0);
+                    if (!solo) issue_s(1, q_b, r0);
+                    umma_commit(bar(kEmpty + r0 % NS));
+                    if (n == 1) q_free();
+                    if (solo && n > 1) {
+                        if (!tile_ready(r0 + 1)) break;
+                        tc_fence_after();
+                        issue_s(1, q_b, r0 + 1);
+                        umma_commit(bar(kEmpty + (r0 + 1) % NS));
+                        if (n == 2) q_free();
+                    }
+                    for (int i = 0; i < n && ok; ++i) {
+                        if (!v_ready(i)) break;
+                        if (solo) {
+                            if (!pv(i & 1, i, i < 2)) break;
+                            umma_commit(bar(kEmpty + (r0 + item_v(n, i)) % NS));
+                            if (i + 2 < n) {
+                                const int rk = r0 + item_k(n, i + 2);
+                                if (!tile_ready(rk)) break;
+                                tc_fence_after();
+                                issue_s(i & 1, q_a, rk);
+                                umma_commit(bar(kEmpty + rk % NS));
+                                if (i + 3 == n) q_free();
+                            }
+                        } else {
+                            const int rk = r0 + item_k(n, i + 1);
+                            if (i + 1 < n && !tile_ready(rk)) break;
+                            for (int x = 0; x < 2; ++x) {
+                                if (!pv(x, i, i == 0)) break;
+                                if (i + 1 < n) issue_s(x, x ? q_b : q_a, rk);
+                            }
+                            if (!ok) break;
+                            umma_commit(bar(kEmpty + (r0 + item_v(n, i)) % NS));
+                            if (i + 1 < n) umma_commit(bar(kEmpty + rk % NS));
+                            if (i + 2 == n) q_free();
+                        }
+                    }
+                    if (!ok) break;
+                    umma_commit(bar(kSegDone));
+                    r0 += 2 * n;
+                    ++seg;
+                }
+                if (!ok) atomicOr(p.status, kDevErrTimeout);
+            }
+            __syncwarp();
+        } else if (warp == 2) {
+            // ================= the walk over the range =================
+            CombineRecord rec = {};
+            int seg = 0;
+            while (true) {
+                const int sl = seg % kSegs;
+                if (seg >= kSegs && !warp_wait(bar(kSegEmpty + sl), ((seg / kSegs) - 1) & 1, p.timeout_ns)) {
+                    if (lane == 0) atomicOr(p.status, kDevErrTimeout);
+                    break;
+                }
+                int* d = segs + sl * kSegInts;
+                if (left == 0) {
+                    if (lane == 0) {
+                        d[4] = 0;
+                        mbar_arrive(bar(kSegFull + sl));
+                    }
+                    break;
+                }
+                const Unit u = unit_of(p, sv_cur, ct);
+                const int take = min(left, u.steps - coff);
+                const bool starts = coff == 0, ends = coff + take == u.steps;
+                const bool solo = u.nq <= QT;
+                if (lane == 0) {
+                    // a partial that continues another CTA's unit goes to the CTA's first slot,
+                    // one that starts a unit to its second: the range has one of each at most
+                    d[0] = ch;
+                    d[1] = sv_cur.q0 + u.ja;
+                    d[2] = u.nq;
+                    d[3] = u.step0 + coff;
+                    d[4] = take;
+                    d[5] = u.klo;
+                    d[6] = u.khi;
+                    d[7] = p.masks ? sv_cur.n - sv_cur.q_len : INT_MAX;
+                    d[8] = u.ja;
+                    d[9] = sv_cur.q0;
+                    d[10] = sv_cur.q_len;
+                    d[11] = sv_cur.n;
+                    d[12] = sv_cur.prefix;
+                    d[13] = cs;
+                    d[14] = (solo ? 1 : 0) | (starts && ends ? 2 : 0);
+                    d[15] = 2 * cta + (starts ? 1 : 0);
+                    mbar_arrive(bar(kSegFull + sl));
+                }
+                if (starts && !ends) {
+                    rec.rows = u.nq * G;
+                    rec.row0 = sv_cur.q0 + u.ja;
+                    rec.head0 = ch * G;
+                    rec.solo = solo ? 1 : 0;
+                    // the CTA whose range holds the unit's last step
+                    rec.last = static_cast<int>(((static_cast<long long>(f) + u.steps) * W - 1) / T);
+                }
+                f += take;
+                left -= take;
+                coff = 0;
+                if (left > 0 && ++ch == p.num_kv_heads) {
+                    ch = 0;
+                    if (++ct == units_per_head(p, sv_cur)) {
+                        ct = 0;
+                        do {
+                            sv_cur = seq_view(p, ++cs, false);
+                        } while (sv_cur.q_len == 0);
+                    }
+                }
+                ++seg;
+            }
+            if (lane == 0) p.records[cta] = rec;
+        } else {
+            // ================= queries, and V rows that no row sees =================
+            int q_uses[2] = {0, 0}, r0 = 0;
+            unsigned issued = 0;                     // bit st: parity of the stage's edge copies
+            Seg g;
+            while (ok && next_seg(g)) {
+                const bool solo = g.flags & 1;
+                const int qb = solo ? (k - 1) & 1 : 0;
+                for (int x = 0; x < (solo ? 1 : 2) && ok; ++x) {
+                    const int b = solo ? qb : x;
+                    if (q_uses[b] >= 1 && !warp_wait(bar(kQEmpty + b), (q_uses[b] - 1) & 1, p.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    ++q_uses[b];
+                    // rows of the tile, half a warp each; up to a whole warp of the softmax they are
+                    // zeros behind the last (their scores then stay small)
+                    const int rows = min(QT, g.nq - x * QT) * G;
+                    const int zero_to = (rows + 31) & ~31;
+                    const int c = lane & 15;
+                    uint8_t* qdst = sm + b * kTileBytes + (c >> 3) * kHalfBytes;
+                    for (int i0 = lane >> 4; i0 < zero_to; i0 += 16) {
+                        uint4 v[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const int i = i0 + 2 * e;
+                            v[e] = make_uint4(0, 0, 0, 0);
+                            if (i < rows) {
+                                const size_t at = (static_cast<size_t>(g.row0 + x * QT + i / G) * p.num_q_heads + g.h * G + i % G) *
+                                                  kHeadDim + 8 * c;
+                                v[e] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + at));
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const int i = i0 + 2 * e;
+                            if (i >= zero_to) continue;
+                            if constexpr (kFp8 && QBf16) {
+                                // fp16, as the widened codes: exact for a bf16 query of magnitude 2^-14
+                                // to 65504, 2^-25 off below, infinite above
+                                uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
+#pragma unroll
+                                for (int a = 0; a < 4; ++a)
+                                    w[a] = pack2<false>(to_float<true>(w[a] & 0xffffu), to_float<true>(w[a] >> 16));
+                                v[e] = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                            *reinterpret_cast<uint4*>(qdst + sw128_offset(i, (c & 7) * 8)) = v[e];
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kQFull + b));
+                }
+                if constexpr (!kFp8) {
+                    for (int i = 0; i < g.steps && ok; ++i) {
+                        const int key0 = (g.step + i) * kKeys;
+                        if (!edge_step(g, key0)) continue;
+                        const int r = r0 + item_v(g.steps, i);
+                        // nodes that some row of the unit sees (lane w: keys 32 w .. of the step)
+                        uint32_t seen[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+                        if (key0 + kKeys > g.ctx) {
+#pragma unroll
+                            for (int w = 0; w < 4; ++w) {
+                                const int at = key0 + 32 * w - g.ctx;
+                                uint32_t any = 0;
+                                if (at > -32 && at < g.q_len)
+                                    for (int j = lane; j < g.nq; j += 32)
+                                        any |= tree_bits(p.masks + static_cast<size_t>(g.row0 + j) * p.mask_words, g.q_len, at);
+                                any = __reduce_or_sync(0xffffffffu, any);
+                                // tokens before the tree
+                                seen[w] = at >= 0 ? any : at <= -32 ? 0xffffffffu : any | ((1u << -at) - 1);
+                            }
+                        }
+                        // not before its copy is issued: the stage may still be a phase or two behind
+                        if (!warp_wait(bar(kIssued + r % NS), issued >> (r % NS) & 1, p.timeout_ns) ||
+                            !warp_wait(bar(kFull + r % NS), (r / NS) & 1, p.timeout_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        issued ^= 1u << (r % NS);
+                        uint8_t* vst = sm + C::kOffStage + (r % NS) * kTileBytes;
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            const int row = 32 * w + lane;
+                            if (key0 + row >= g.klo && key0 + row < g.khi && (seen[w] >> lane & 1)) continue;
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                *reinterpret_cast<uint4*>(vst + row * 128 + 16 * c) = make_uint4(0, 0, 0, 0);
+                                *reinterpret_cast<uint4*>(vst + kHalfBytes + row * 128 + 16 * c) = make_uint4(0, 0, 0, 0);
+                            }
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(kFixed + r % NS));
+                    }
+                }
+                r0 += 2 * g.steps;
+            }
+            if (!ok && lane == 0) atomicOr(p.status, kDevErrTimeout);
+        }
+    } else if (warp < 12) {
+        setmaxnreg_inc<C::kRegsSoftmax>();
+        // ================= softmax: warps 4-7 tile A, 8-11 tile B; thread = one row =================
+        const int x = warp < 8 ? 0 : 1;
+        const int quarter = warp & 3;                  // tensor-memory lanes 32 quarter .. + 31
+        const int r = quarter * 32 + lane;
+        const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+        const uint32_t s_addr = tS(x) + lane_off;
+        int uses = 0, solos = 0;
+        Seg g;
+        while (ok && next_seg(g)) {
+            const bool solo = g.flags & 1;
+            const int jq = (solo ? 0 : x * QT) + r / G;
+            const bool live = r < QT * G && jq < g.nq;
+            const bool warp_live = __any_sync(0xffffffffu, live);
+            const int head = g.h * G + r % G;
+            SeqView sq = {g.q0, g.q_len, g.n, g.prefix};
+            RowView view = {0, 0, INT_MAX};
+            if (live) view = row_view(p, sq, g.j0 + jq);
+            const int lo_max = __reduce_max_sync(0xffffffffu, view.lo);
+            const int hi_min = __reduce_min_sync(0xffffffffu, view.hi);
+            const unsigned long long* words = p.masks && live ? p.masks + static_cast<size_t>(g.row0 + jq) * p.mask_words : nullptr;
+            const float kscale = kFp8 ? __ldg(p.k_scale + g.h * p.scale_stride) : 1.0f;
+            const float vscale = kFp8 ? __ldg(p.v_scale + g.h * p.scale_stride) : 1.0f;
+            const float s_log2 = p.scale * 1.4426950408889634f * kscale;
+            const float slope2 = Mod && p.slopes && live ? __ldg(p.slopes + head) * 1.4426950408889634f : 0.f;
+            const bool pos_scale = s_log2 >= 0.f;
+            float m_used = -INFINITY, l = 0.f;
+            for (int i = solo ? x : 0; i < g.steps; i += solo ? 2 : 1) {
+                const bool first = i < (solo ? 2 : 1);
+                if (!warp_wait(bar(kSFull + x), uses & 1, p.timeout_ns)) {
+                    ok = false;
+                    break;
+                }
+                ++uses;
+                if (!warp_live) {                       // rows past the unit's: nothing reads their P
+                    if (lane == 0) {
+                        mbar_arrive(bar(kPHalf + x));
+                        mbar_arrive(bar(kPFull + x));
+                    }
+                    continue;
+                }
+                tc_fence_after();
+                const int key0 = (g.step + i) * kKeys;
+                const bool need_mask = key0 < lo_max || key0 + kKeys > hi_min;
+                // what the row sees of the step's keys
+                uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+                if (need_mask) {
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const int base = key0 + 32 * w;
+                        const int a = max(view.lo - base, 0), b = min(view.hi - base, 32);
+                        vis[w] = b <= a ? 0u : (0xffffffffu << a) & (0xffffffffu >> (32 - b));
+                        if (words) vis[w] |= tree_bits(words, g.q_len, base - g.ctx);
+                    }
+                }
+                __syncwarp();
+                // the whole row of S in registers: one tensor-memory round trip per step
+                uint32_t sv[kKeys];
+#pragma unroll
+                for (int c = 0; c < kKeys / 32; ++c)
+                    tmem_ld32(s_addr + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * c));
+                tmem_wait_ld();
+                if constexpr (Mod) {
+                    // scores in log2 units, capped and biased (what stands in hidden places, keys that
+                    // were never copied, must not choose the form of the tanh)
+                    if (need_mask) {
+#pragma unroll
+                        for (int e = 0; e < kKeys; ++e) sv[e] = vis[e >> 5] >> (e & 31) & 1 ? sv[e] : 0u;
+                    }
+                    if (p.cap > 0.f) {
+                        // |x / cap| small in the whole warp (nearly always: caps lie far above most
+                        // scores): the polynomial, 3.5 packed instructions a score; else 1 - 2 / (1 +
+                        // e^2x), two steps of the exponential unit, which the softmax waits for too.
+                        // tanh.approx is 2^-11 off, 0.02 of a score at a cap of 50.
+                        const float k1 = p.scale * kscale / p.cap;
+                        float a4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int e = 0; e < kKeys; e += 2)
+                            a4[(e >> 1) & 3] = max3f(a4[(e >> 1) & 3], fabsf(__uint_as_float(sv[e])), fabsf(__uint_as_float(sv[e + 1])));
+                        const float am = fmaxf(fmaxf(a4[0], a4[1]), fmaxf(a4[2], a4[3]));
+                        if (!__any_sync(0xffffffffu, am * fabsf(k1) > kCapSmall)) {
+                            const uint64_t k12 = f2_pack(k1, k1), sc2 = f2_pack(s_log2, s_log2);
+                            const uint64_t c0 = f2_pack(kTanh0, kTanh0), c1 = f2_pack(kTanh1, kTanh1),
+                                           c2 = f2_pack(kTanh2, kTanh2), c3 = f2_pack(kTanh3, kTanh3),
+                                           c4 = f2_pack(kTanh4, kTanh4);
+#pragma unroll
+                            for (int e = 0; e < kKeys; e += 2) {
+                                const uint64_t v = f2_pack(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
+                                const uint64_t y = f2_mul(v, k12), u = f2_mul(y, y);
+                                uint64_t q = f2_fma(u, c4, c3);
+                                q = f2_fma(u, q, c2);
+                                q = f2_fma(u, q, c1);
+                                q = f2_fma(u, q, c0);
+                                float a0, a1;
+                                f2_unpack(f2_mul(f2_mul(v, sc2), q), a0, a1);
+                                sv[e] = __float_as_uint(a0);
+                                sv[e + 1] = __float_as_uint(a1);
+                            }
+                        } else {
+                            const float c2 = p.cap * 1.4426950408889634f, k2 = k1 * 2.8853900817779268f;
+#pragma unroll
+                            for (int e = 0; e < kKeys; ++e)
+                                sv[e] = __float_as_uint(fmaf(-2.f * c2, rcp_approx(1.f + ex2_approx(__uint_as_float(sv[e]) * k2)), c2));
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < kKeys; ++e) sv[e] = __float_as_uint(__uint_as_float(sv[e]) * s_log2);
+                    }
+                    if (p.slopes) {
+                        const float base = static_cast<float>(key0 - view.pos);
+#pragma unroll
+                        for (int e = 0; e < kKeys; ++e)
+                            sv[e] = __float_as_uint(fmaf(-slope2, fabsf(base + static_cast<float>(e)), __uint_as_float(sv[e])));
+                    }
+                }
+                // row maximum of s * scale = max(s) * scale for scale >= 0, min(s) * scale
+                // otherwise; four independent chains, hidden columns only where a row has some
+                const float mul = Mod ? 1.0f : s_log2;
+                float mx;
+                if (need_mask) {
+                    const float hidden = Mod || pos_scale ? -INFINITY : INFINITY;
+#pragma unroll
+                    for (int e = 0; e < kKeys; ++e)
+                        sv[e] = vis[e >> 5] >> (e & 31) & 1 ? sv[e] : __float_as_uint(hidden);
+                }
+                {
+                    float e4[4];
+                    if (Mod || pos_scale) {
+                        e4[0] = e4[1] = e4[2] = e4[3] = -INFINITY;
+#pragma unroll
+                        for (int e = 0; e < kKeys; e += 2)
+                            e4[(e >> 1) & 3] = max3f(e4[(e >> 1) & 3], __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
+                        mx = fmaxf(fmaxf(e4[0], e4[1]), fmaxf(e4[2], e4[3]));
+                    } else {
+                        e4[0] = e4[1] = e4[2] = e4[3] = INFINITY;
+#pragma unroll
+                        for (int e = 0; e < kKeys; e += 2)
+                            e4[(e >> 1) & 3] = min3f(e4[(e >> 1) & 3], __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
+                        mx = fminf(fminf(e4[0], e4[1]), fminf(e4[2], e4[3]));
+                    }
+                    // (a scale of 0 would turn a hidden row's infinity into NaN)
+                    if (!Mod) mx = isinf(mx) && mul == 0.f ? -INFINITY : mx * mul;
+                }
+                const bool need = mx > m_used + kRescale;
+                const bool resc = __any_sync(0xffffffffu, need);
+                const float m_new = need ? mx : m_used;
+                // a row that has seen nothing yet: exponents against 0, all of hidden scores
+                const float m_at = m_new == -INFINITY ? 0.f : m_new;
+                const float alpha = ex2_approx(m_used - m_at);    // 0 before the row's first key, 1 when kept
+                m_used = m_new;
+                // O is final for the products before: S(i) was issued behind them.  Rescaled
+                // before any of P(i) is released, since P.V(i) accumulates into it.
+                if (!first && resc) {
+#pragma unroll 1
+                    for (int c = 0; c < kHeadDim / 32; ++c) {
+                        uint32_t ov[32];
+                        tmem_ld32(tO(x) + lane_off + 32 * c, ov);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                        tmem_st32(tO(x) + lane_off + 32 * c, ov);
+                    }
+                }
+                // p = 2^(s * scale - m), rounded to the 16 bits that the tensor cores take beside V's
+                // (bf16 2^-8 of it at most, fp16, FP8 caches' type too, 2^-11; their sum is of the
+                // unrounded ones), written over the columns of S (keys 32 c .. +31 -> columns 16 c
+                // .. +15).  P in two 16-bit parts would double the products of P.V.
+                uint64_t sum2[2] = {0ull, 0ull};
+                const uint64_t scale2 = f2_pack(mul, mul);
+                const uint64_t negm2 = f2_pack(-m_at, -m_at);
+#pragma unroll
+                for (int c = 0; c < kKeys / 32; ++c) {
+                    uint32_t pw[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const int kk = 32 * c + e;
+                        const uint64_t v = f2_pack(__uint_as_float(sv[kk]), __uint_as_float(sv[kk + 1]));
+                        float a0, a1;
+                        if constexpr (Mod) f2_unpack(f2_add(v, negm2), a0, a1);
+                        else f2_unpack(f2_fma(v, scale2, negm2), a0, a1);
+                        float p0 = ex2_approx(a0);
+                        float p1 = ex2_approx(a1);
+                        if (need_mask) {
+                            p0 = vis[c] >> e & 1 ? p0 : 0.f;
+                            p1 = vis[c] >> (e + 1) & 1 ? p1 : 0.f;
+                        }
+                        sum2[(e >> 1) & 1] = f2_add(sum2[(e >> 1) & 1], f2_pack(p0, p1));
+                        pw[e >> 1] = pack2<kMmaBf16>(p0, p1);
+                    }
+                    tmem_st16(s_addr + 16 * c, pw);
+                    if (c == kKeys / 64 - 1) {
+                        // the first 64 keys' P (and any rescale of O) is in tensor memory
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(kPHalf + x));
+                    }
+                }
+                tmem_wait_st();
+                float s0, s1, s2, s3;
+                f2_unpack(sum2[0], s0, s1);
+                f2_unpack(sum2[1], s2, s3);
+                l = l * alpha + ((s0 + s1) + (s2 + s3));
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kPFull + x));
+            }
+            // ---- the segment's outputs ----
+            if (!ok || !warp_wait(bar(kSegDone), (k - 1) & 1, p.timeout_ns)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const bool whole = g.flags & 2;
+            const size_t orow = (static_cast<size_t>(g.row0 + jq) * p.num_q_heads + head) * kHeadDim;
+            const size_t prow = static_cast<size_t>(g.slot) * (2 * kRows) + (solo ? r : x * kRows + r);
+            // 32 components from 32 c on: the row itself, or its partial
+            auto put = [&](int c, const uint32_t (&ov)[32], float inv) {
+                if (!live) return;
+                if (whole) {
+                    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + orow) + 4 * c;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int a = 0; a < 4; ++a)
+                            w[a] = pack2<QBf16>(__uint_as_float(ov[8 * e + 2 * a]) * inv, __uint_as_float(ov[8 * e + 2 * a + 1]) * inv);
+                        dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                } else {
+                    float4* dst = reinterpret_cast<float4*>(p.partial + prow * kHeadDim) + 8 * c;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        dst[e] = make_float4(__uint_as_float(ov[4 * e]), __uint_as_float(ov[4 * e + 1]),
+                                             __uint_as_float(ov[4 * e + 2]), __uint_as_float(ov[4 * e + 3]));
+                }
+            };
+            // A warp goes on to the next segment once all have seen this one's end: its products
+            // (solo: also read by the other tile's warps) are overwritten, and no barrier can get
+            // two phases ahead of a warp.
+            if (!solo) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kOFree));
+                if (warp_live) {
+                    const float inv = l == 0.f ? 0.f : vscale / l;
+#pragma unroll 1
+                    for (int c = 0; c < kHeadDim / 32; ++c) {
+                        uint32_t ov[32];
+                        tmem_ld32(tO(x) + lane_off + 32 * c, ov);
+                        tmem_wait_ld();
+                        put(c, ov, inv);
+                        __syncwarp();
+                    }
+                    if (!whole && live) p.ml[prow] = make_float2(m_used, l);
+                }
+            } else {
+                // A's steps and B's: both tiles hold the row in this lane; A's warps write its first
+                // 64 components, B's the others
+                ml_smem[x * kRows + r] = make_float2(m_used, l);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kMlReady));
+                if (!warp_wait(bar(kMlReady), solos & 1, p.timeout_ns)) {
+                    ok = false;
+                    break;
+                }
+                if (warp_live) {
+                    const float2 other = ml_smem[(1 - x) * kRows + r];
+                    const float m = fmaxf(m_used, other.x), m_at = m == -INFINITY ? 0.f : m;
+                    const float own_w = ex2_approx(m_used - m_at), other_w = ex2_approx(other.x - m_at);
+                    const float sum = l * own_w + other.y * other_w;
+                    const float inv = sum == 0.f ? 0.f : vscale / sum;
+                    const float wa = x == 0 ? own_w : other_w, wb = x == 0 ? other_w : own_w;
+                    const bool two = g.steps > 1;       // else B has no products
+#pragma unroll 1
+                    for (int c = 2 * x; c < 2 * x + 2; ++c) {
+                        uint32_t ov[32];
+                        tmem_ld32(tO(0) + lane_off + 32 * c, ov);
+                        tmem_wait_ld();
+                        if (two) {
+                            uint32_t ob[32];
+                            tmem_ld32(tO(1) + lane_off + 32 * c, ob);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                ov[e] = __float_as_uint(fmaf(__uint_as_float(ov[e]), wa, __uint_as_float(ob[e]) * wb));
+                        }
+                        put(c, ov, inv);
+                        __syncwarp();
+                    }
+                    if (!whole && live && x == 0) p.ml[prow] = make_float2(m, sum);
+                }
+                ++solos;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kOFree));
+            }
+            if (!warp_wait(bar(kOFree), (k - 1) & 1, p.timeout_ns)) {
+                ok = false;
+                break;
+            }
+        }
+        if (!ok && lane == 0) atomicOr(p.status, kDevErrTimeout);
+    } else {
+        setmaxnreg_dec<C::kRegsFront>();
+        // ================= FP8: e4m3 rows to fp16 tiles; thread = one key's row =================
+        if constexpr (kFp8) {
+            const int row = (warp - 12) * 32 + lane;
+            int r = 0;
+            Seg g;
+            while (ok && next_seg(g)) {
+                for (int it = 0; it < 2 * g.steps && ok; ++it, ++r) {
+                    // the item's step, and whether it is V
+                    const int two = min(2, g.steps);
+                    int i = it;
+                    bool is_v = false;
+                    if (it >= two) {
+                        const int e = it - two, both = 2 * max(g.steps - 2, 0);
+                        i = e < both ? e >> 1 : e - both / 2;
+                        is_v = e >= both || !(e & 1);
+                        if (!is_v) i += 2;
+                    }
+                    const int key0 = (g.step + i) * kKeys;
+                    bool zero = false;
+                    if (is_v && edge_step(g, key0)) {
+                        zero = key0 + row < g.klo || key0 + row >= g.khi;
+                        const int at = key0 + row - lane - g.ctx;        // of the warp's first key
+                        if (at > -32 && key0 + kKeys > g.ctx) {
+                            uint32_t any = 0;
+                            for (int j = lane; j < g.nq; j += 32)
+                                any |= tree_bits(p.masks + static_cast<size_t>(g.row0 + j) * p.mask_words, g.q_len, at);
+                            any = __reduce_or_sync(0xffffffffu, any);
+                            if (at + lane >= 0 && !(any >> lane & 1)) zero = true;
+                        }
+                    }
+                    const int rs = r % C::kRaw, st = r % NS;
+                    if (!warp_wait(bar(kRawFull + rs), (r / C::kRaw) & 1, p.timeout_ns) ||
+                        (r >= NS && !warp_wait(bar(kEmpty + st), ((r / NS) - 1) & 1, p.timeout_ns))) {
+                        ok = false;
+                        break;
+                    }
+                    const uint8_t* src = sm + C::kOffRaw + rs * kHalfBytes + row * 128;
+                    uint8_t* dst = sm + C::kOffStage + st * kTileBytes;
+                    uint4 x8[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        x8[e] = zero ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(src + ((e ^ (row & 7)) << 4));
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t w[4] = {x8[e].x, x8[e].y, x8[e].z, x8[e].w};
+                        uint32_t h[8];
+#pragma unroll
+                        for (int a = 0; a < 4; ++a) {
+                            h[2 * a] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[a] & 0xffffu));
+                            h[2 * a + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[a] >> 16));
+                        }
+                        uint8_t* d = dst + (e >> 2) * kHalfBytes;
+                        *reinterpret_cast<uint4*>(d + sw128_offset(row, 16 * (e & 3))) = make_uint4(h[0], h[1], h[2], h[3]);
+                        *reinterpret_cast<uint4*>(d + sw128_offset(row, 16 * (e & 3) + 8)) = make_uint4(h[4], h[5], h[6], h[7]);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bar(kFull + st));
+                        mbar_arrive(bar(kRawEmpty + rs));
+                    }
+                }
+            }
+            if (!ok && lane == 0) atomicOr(p.status, kDevErrTimeout);
+        }
+    }
+
+    // ---- teardown ----
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Units that several CTAs share:
+//   out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,   M = max_i m_i,
+// over the partials (o_i, m_i in log2 units, l_i).  CTA (w, z) takes rows of the unit that main
+// CTA w began and did not finish; its partials lie in w's second slot and in the first slots of
+// the CTAs behind it up to `last`.  A row has a warp, or with many partials several, whose
+// sums meet in shared memory.
+template <bool OutBf16, bool Fp8>
+__global__ void __launch_bounds__(256) scored_combine_kernel(const ScoredParams p) {
+    __shared__ float4 acc_smem[8][32];
+    __shared__ float2 ml_smem[8];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int w = blockIdx.x;
+    const CombineRecord rec = p.records[w];
+    if (rec.rows == 0) return;
+    const int parts = rec.last - w + 1;
+    const int per_row = parts > 16 ? 8 : parts > 8 ? 4 : parts > 4 ? 2 : 1;       // warps of a row
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int sub = warp % per_row, rows_at_once = 8 / per_row;
+    const int QT = p.queries_per_tile, G = p.group;
+    for (int i0 = blockIdx.y * rows_at_once; i0 < rec.rows; i0 += gridDim.y * rows_at_once) {
+        const int i = i0 + warp / per_row;
+        const bool live = i < rec.rows;
+        const int query = i / G;
+        const int at = rec.solo ? i : (query / QT) * kRows + (query % QT) * G + i % G;
+        float m = -INFINITY, l = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (live) {
+            for (int k0 = sub; k0 < parts; k0 += 4 * per_row) {
+                float4 o[4];
+                float2 ml[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int kk = k0 + e * per_row;
+                    ml[e] = make_float2(-INFINITY, 0.f);
+                    o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (kk < parts) {
+                        const size_t row = static_cast<size_t>(kk == 0 ? 2 * w + 1 : 2 * (w + kk)) * (2 * kRows) + at;
+                        ml[e] = __ldcg(p.ml + row);
+                        o[e] = __ldcg(reinterpret_cast<const float4*>(p.partial + row * kHeadDim) + lane);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float mn = fmaxf(m, ml[e].x), m_at = mn == -INFINITY ? 0.f : mn;
+                    const float a = ex2_approx(m - m_at), b = ex2_approx(ml[e].x - m_at);
+                    acc = make_float4(acc.x * a + o[e].x * b, acc.y * a + o[e].y * b, acc.z * a + o[e].z * b,
+                                      acc.w * a + o[e].w * b);
+                    l = l * a + ml[e].y * b;
+                    m = mn;
+                }
+            }
+        }
+        if (per_row > 1) {
+            acc_smem[warp][lane] = acc;
+            if (lane == 0) ml_smem[warp] = make_float2(m, l);
+            __syncthreads();
+            if (sub == 0) {
+                for (int e = 1; e < per_row; ++e) {
+                    const float2 ml = ml_smem[warp + e];
+                    const float4 o = acc_smem[warp + e][lane];
+                    const float mn = fmaxf(m, ml.x), m_at = mn == -INFINITY ? 0.f : mn;
+                    const float a = ex2_approx(m - m_at), b = ex2_approx(ml.x - m_at);
+                    acc = make_float4(acc.x * a + o.x * b, acc.y * a + o.y * b, acc.z * a + o.z * b, acc.w * a + o.w * b);
+                    l = l * a + ml.y * b;
+                    m = mn;
+                }
+            }
+            __syncthreads();
+        }
+        if (live && sub == 0) {
+            const int head = rec.head0 + i % G;
+            const float vscale = Fp8 ? __ldg(p.v_scale + rec.head0 / G * p.scale_stride) : 1.0f;
+            const float inv = l == 0.f ? 0.f : vscale / l;
+            uint16_t* dst = static_cast<uint16_t*>(p.out) +
+                            (static_cast<size_t>(rec.row0 + query) * p.num_q_heads + head) * kHeadDim + 4 * lane;
+            *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<OutBf16>(acc.x * inv, acc.y * inv), pack2<OutBf16>(acc.z * inv, acc.w * inv));
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+namespace {
+
+template <int Kind, bool QBf16>
+const void* scored_fn(bool mod) {
+    return mod ? reinterpret_cast<const void*>(&scored_kernel<Kind, QBf16, true>)
+               : reinterpret_cast<const void*>(&scored_kernel<Kind, QBf16, false>);
+}
+
+const void* scored_fn(CacheKind kind, bool q_bf16, bool mod) {
+    switch (kind) {
+        case kKindBf16: return scored_fn<kKindBf16, true>(mod);
+        case kKindFp16: return scored_fn<kKindFp16, false>(mod);
+        case kKindFp8: return q_bf16 ? scored_fn<kKindFp8, true>(mod) : scored_fn<kKindFp8, false>(mod);
+    }
+    return nullptr;
+}
+
+size_t scored_smem(CacheKind kind) { return kind == kKindFp8 ? Cfg<kKindFp8>::kSmem : Cfg<kKindBf16>::kSmem; }
+
+}  // namespace
+
+ScoredLayout scored_layout(int sms) {
+    ScoredLayout l;
+    const size_t rows = static_cast<size_t>(sms) * 2 * 2 * kRows;        // two slots per CTA
+    l.records_off = 256;
+    l.ml_off = l.records_off + (static_cast<size_t>(sms) * sizeof(CombineRecord) + 255) / 256 * 256;
+    l.partial_off = l.ml_off + rows * sizeof(float2);
+    l.total = l.partial_off + rows * kHeadDim * sizeof(float);
+    return l;
+}
+
+int scored_rows() { return kRows; }
+
+cudaError_t scored_prepare(CacheKind kind, bool q_bf16, bool mod) {
+    return cudaFuncSetAttribute(scored_fn(kind, q_bf16, mod), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(scored_smem(kind)));
+}
+
+cudaError_t launch_scored(CacheKind kind, bool q_bf16, bool mod, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                          const ScoredParams& p, int sms, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((items + 7) / 8));
+    cfg.gridDim = dim3(static_cast<unsigned>(sms));
+    cfg.blockDim = dim3(static_cast<unsigned>(32 * (kind == kKindFp8 ? Cfg<kKindFp8>::kWarps : Cfg<kKindBf16>::kWarps)));
+    cfg.dynamicSmemBytes = scored_smem(kind);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    void* args[] = {const_cast<CUtensorMap*>(&kmap), const_cast<CUtensorMap*>(&vmap), const_cast<ScoredParams*>(&p)};
+    return cudaLaunchKernelExC(&cfg, scored_fn(kind, q_bf16, mod), args);
+}
+
+cudaError_t launch_scored_combine(bool out_bf16, bool fp8, const ScoredParams& p, int sms, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(sms), 8);
     cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -142,14 +1273,11 @@ cudaError_t launch_scored(CacheKind kind, bool q_bf16, const ScoredParams& p, cu
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    switch (kind) {
-        case kKindBf16: return cudaLaunchKernelEx(&cfg, scored_kernel<kKindBf16, true>, p);
-        case kKindFp16: return cudaLaunchKernelEx(&cfg, scored_kernel<kKindFp16, false>, p);
-        case kKindFp8:
-            return q_bf16 ? cudaLaunchKernelEx(&cfg, scored_kernel<kKindFp8, true>, p)
-                          : cudaLaunchKernelEx(&cfg, scored_kernel<kKindFp8, false>, p);
-    }
-    return cudaErrorInvalidValue;
+    if (out_bf16)
+        return fp8 ? cudaLaunchKernelEx(&cfg, scored_combine_kernel<true, true>, p)
+                   : cudaLaunchKernelEx(&cfg, scored_combine_kernel<true, false>, p);
+    return fp8 ? cudaLaunchKernelEx(&cfg, scored_combine_kernel<false, true>, p)
+               : cudaLaunchKernelEx(&cfg, scored_combine_kernel<false, false>, p);
 }
 
 }  // namespace pa
