@@ -119,6 +119,24 @@ pa_status encode_cache_map(CUtensorMap* map, const void* base, int num_blocks, i
     return PA_OK;
 }
 
+// Tensor map over the queries [rows][heads][128] of a 16-bit type: boxes of 64 components of
+// `group` heads of `queries` rows, 128-byte swizzle.
+pa_status encode_query_map(CUtensorMap* map, const void* base, int rows, int heads, int group, int queries) {
+    if (!encode_fn()) return PA_ERR_CUDA;
+    const cuuint64_t dims[3] = {kHeadDim, static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[2] = {2 * kHeadDim, 2 * kHeadDim * static_cast<cuuint64_t>(heads)};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(queries)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        snprintf(g_last_error, sizeof g_last_error, "cuTensorMapEncodeTiled failed (CUresult %d)", static_cast<int>(r));
+        return PA_ERR_CUDA;
+    }
+    return PA_OK;
+}
+
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Tokens per physical block: 8, 16 or 32 (the kernels work in 16-key units).
@@ -518,9 +536,13 @@ pa_status scored_impl(ScoredParams p, void* out, const void* q, const int32_t* q
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.records = reinterpret_cast<CombineRecord*>(ws + lay.records_off);
     p.ml = reinterpret_cast<float2*>(ws + lay.ml_off);
-    p.partial = reinterpret_cast<float*>(ws + lay.partial_off);
+    p.partial = reinterpret_cast<float4*>(ws + lay.partial_off);
+    p.out_sectors = aligned(out, 32) ? 1 : 0;
     p.timeout_ns = kDefaultTimeoutNs;
-    s = launched(launch_scored(kind, q_bf16, mod, kmap, vmap, p, st->sms, stream), "launch(scored)");
+    CUtensorMap qmap;
+    s = encode_query_map(&qmap, q, total_q, num_q_heads, group, p.queries_per_tile);
+    if (s != PA_OK) return s;
+    s = launched(launch_scored(kind, q_bf16, mod, kmap, vmap, qmap, p, st->sms, stream), "launch(scored)");
     // tables of one step: no unit is ever shared
     if (s != PA_OK || static_cast<long long>(max_blocks_per_seq) * block_size <= scored_rows()) return s;
     return launched(launch_scored_combine(q_bf16, fp8, p, st->sms, stream), "launch(scored combine)");

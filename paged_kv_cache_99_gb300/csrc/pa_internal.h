@@ -359,7 +359,8 @@ struct ScoredParams {
     float cap;                        // 0: none
     CombineRecord* records;           // [CTAs]
     float2* ml;                       // [CTAs][2][256]: maximum (log2 units), sum
-    float* partial;                   // [CTAs][2][256][128]: unnormalised outputs
+    float4* partial;                  // [CTAs][2][32 quads][256]: unnormalised outputs
+    int out_sectors;                  // out is 32-byte aligned
     unsigned long long timeout_ns;    // bound of every barrier wait
 };
 
@@ -373,7 +374,7 @@ int scored_rows();                    // rows of one tile
 // mod: the kernel that caps and biases scores
 cudaError_t scored_prepare(CacheKind kind, bool q_bf16, bool mod);
 cudaError_t launch_scored(CacheKind kind, bool q_bf16, bool mod, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                          const ScoredParams& p, int sms, cudaStream_t stream);
+                          const CUtensorMap& qmap, const ScoredParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_scored_combine(bool out_bf16, bool fp8, const ScoredParams& p, int sms, cudaStream_t stream);
 
 // Prefill chunks.

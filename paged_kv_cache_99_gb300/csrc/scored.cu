@@ -23,8 +23,8 @@
 // past them only passes the barriers.
 //
 // Warps: 0 copies K and V (TMA, 128-byte swizzle, a lane per 8 or 16 rows of a block), 1 issues
-// tcgen05.mma, 2 walks the range and describes the segments to the others, 3 fetches the
-// queries a segment ahead and zeroes V rows that no row sees (0 x NaN is NaN), 4-7 and 8-11 are
+// tcgen05.mma, 2 walks the range and describes the segments to the others, 3 copies
+// the queries (TMA) and zeroes V rows that no row sees (0 x NaN is NaN), 4-7 and 8-11 are
 // the softmax of tiles A and B, a thread per row; with an FP8 cache 12-15 widen the copied e4m3
 // rows exactly to fp16, which costs them about as long as the copies take.
 // Every wait is bounded.
@@ -54,8 +54,8 @@ struct Cfg {
     static constexpr bool kFp8 = Kind == kKindFp8;
     static constexpr bool kMmaBf16 = Kind == kKindBf16;
     static constexpr int kWarps = kFp8 ? 16 : 12;
-    static constexpr int kStages = kFp8 ? 3 : 5;         // K and V tiles of 16-bit elements
-    static constexpr int kRaw = kFp8 ? 4 : 0;            // e4m3 tiles as copied
+    static constexpr int kStages = kFp8 ? 4 : 5;         // K and V tiles of 16-bit elements
+    static constexpr int kRaw = kFp8 ? 2 : 0;            // e4m3 tiles as copied
     // launch registers per thread, and the shares after setmaxnreg
     [[maybe_unused]] static constexpr int kRegsLaunch = kFp8 ? 128 : 168;
     static constexpr int kRegsFront = kFp8 ? 64 : 104;
@@ -91,7 +91,8 @@ enum {                                       // barriers, 8 bytes each
     kOFree,                                  // the segment's outputs are read
     kFixed,                                  // [stage] V rows that no row sees are zeroed (edge steps)
     kIssued = kFixed + 5,                    // [stage] the copy of an edge step's V is under way
-    kNumBars = kIssued + 5
+    kQLand = kIssued + 5,                    // [Q buffer] a bf16 query of an FP8 cache has landed
+    kNumBars = kQLand + 2
 };
 static_assert(kNumBars * 8 + 4 <= 448, "barriers");
 
@@ -231,7 +232,8 @@ constexpr float kTanh0 = 0.999999926f, kTanh1 = -0.33332302f, kTanh2 = 0.1331006
 
 template <int Kind, bool QBf16, bool Mod>
 __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
-    scored_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const ScoredParams p) {
+    scored_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                  const __grid_constant__ CUtensorMap qmap, const ScoredParams p) {
     using C = Cfg<Kind>;
     constexpr bool kFp8 = C::kFp8;
     constexpr bool kMmaBf16 = C::kMmaBf16;
@@ -269,6 +271,7 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(kQFull + i), 1);
             mbar_init(bar(kQEmpty + i), 1);
+            mbar_init(bar(kQLand + i), 1);
             mbar_init(bar(kSFull + i), 1);
             mbar_init(bar(kPHalf + i), 4);
             mbar_init(bar(kPFull + i), 4);
@@ -279,6 +282,7 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
         fence_barrier_init();
         tmap_prefetch(&kmap);
         tmap_prefetch(&vmap);
+        tmap_prefetch(&qmap);
     }
 
     grid_dependency_wait();
@@ -488,8 +492,10 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                     }
                 };
                 int r0 = 0, seg = 0;
-                unsigned fixes = 0;                  // bit st: parity of the stage's zeroings
-                int q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
+                // parities as bits: an array indexed at run time would live in local memory, whose
+                // loads miss the little L1 that is left (prompt 8k: 5 times the time)
+                unsigned fixes = 0;                  // bit st: of the stage's zeroings
+                unsigned q_par = 0, p_par = 0;       // bit x: of the buffer's fills, of the tile's P
                 while (ok) {
                     if (!wait(bar(kSegFull + seg % kSegs), (seg / kSegs) & 1)) break;
                     const Seg g = read_seg(segs + (seg % kSegs) * kSegInts);
@@ -499,11 +505,11 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                     const int n = g.steps;
                     const int qb = solo ? seg & 1 : 0;
                     const uint32_t q_a = sbase + qb * kTileBytes, q_b = solo ? q_a : sbase + kTileBytes;
-                    if (!wait(bar(kQFull + qb), q_uses[qb] & 1)) break;
-                    ++q_uses[qb];
+                    if (!wait(bar(kQFull + qb), q_par >> qb & 1)) break;
+                    q_par ^= 1u << qb;
                     if (!solo) {
-                        if (!wait(bar(kQFull + 1), q_uses[1] & 1)) break;
-                        ++q_uses[1];
+                        if (!wait(bar(kQFull + 1), q_par >> 1 & 1)) break;
+                        q_par ^= 2u;
                     }
                     auto q_free = [&]() {            // behind the segment's last S
                         umma_commit(bar(kQEmpty + qb));
@@ -512,13 +518,13 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                     // P(i) of tile x, in two halves, into O_x
                     auto pv = [&](int x, int i, bool first) -> bool {
                         const int r = r0 + item_v(n, i);
-                        if (!poll(bar(kPHalf + x), p_uses[x] & 1)) return false;
+                        if (!poll(bar(kPHalf + x), p_par >> x & 1)) return false;
                         tc_fence_after();
                         issue_pv(x, r, 0, first);
-                        if (!poll(bar(kPFull + x), p_uses[x] & 1)) return false;
+                        if (!poll(bar(kPFull + x), p_par >> x & 1)) return false;
                         tc_fence_after();
                         issue_pv(x, r, 1, first);
-                        ++p_uses[x];
+                        p_par ^= 1u << x;
                         return true;
                     };
                     auto v_ready = [&](int i) -> bool {
@@ -645,7 +651,9 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
             if (lane == 0) p.records[cta] = rec;
         } else {
             // ================= queries, and V rows that no row sees =================
-            int q_uses[2] = {0, 0}, r0 = 0;
+            int r0 = 0;
+            unsigned q_used = 0, q_par = 0;          // bit b: the buffer was filled, parity of its releases
+            [[maybe_unused]] unsigned q_fills = 0;   // bit b: parity of its copies
             unsigned issued = 0;                     // bit st: parity of the stage's edge copies
             Seg g;
             while (ok && next_seg(g)) {
@@ -653,48 +661,49 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                 const int qb = solo ? (k - 1) & 1 : 0;
                 for (int x = 0; x < (solo ? 1 : 2) && ok; ++x) {
                     const int b = solo ? qb : x;
-                    if (q_uses[b] >= 1 && !warp_wait(bar(kQEmpty + b), (q_uses[b] - 1) & 1, p.timeout_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    ++q_uses[b];
-                    // rows of the tile, half a warp each; up to a whole warp of the softmax they are
-                    // zeros behind the last (their scores then stay small)
-                    const int rows = min(QT, g.nq - x * QT) * G;
-                    const int zero_to = (rows + 31) & ~31;
-                    const int c = lane & 15;
-                    uint8_t* qdst = sm + b * kTileBytes + (c >> 3) * kHalfBytes;
-                    for (int i0 = lane >> 4; i0 < zero_to; i0 += 16) {
-                        uint4 v[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const int i = i0 + 2 * e;
-                            v[e] = make_uint4(0, 0, 0, 0);
-                            if (i < rows) {
-                                const size_t at = (static_cast<size_t>(g.row0 + x * QT + i / G) * p.num_q_heads + g.h * G + i % G) *
-                                                  kHeadDim + 8 * c;
-                                v[e] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + at));
-                            }
+                    if (q_used >> b & 1) {
+                        if (!warp_wait(bar(kQEmpty + b), q_par >> b & 1, p.timeout_ns)) {
+                            ok = false;
+                            break;
                         }
+                        q_par ^= 1u << b;
+                    }
+                    q_used |= 1u << b;
+                    // one copy of QT queries x G heads; those past the unit's are other rows or zeros
+                    // and end in rows of S that nothing reads
+                    constexpr bool kWiden = kFp8 && QBf16;
+                    const uint32_t landed = bar((kWiden ? kQLand : kQFull) + b), dst = sbase + b * kTileBytes;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(landed, static_cast<uint32_t>(QT * G) * 256);
+                        tma_load_3d(dst, &qmap, 0, g.h * G, g.row0 + x * QT, landed);
+                        tma_load_3d(dst + kHalfBytes, &qmap, 64, g.h * G, g.row0 + x * QT, landed);
+                    }
+                    __syncwarp();
+                    if constexpr (kWiden) {
+                        // bf16 to fp16, as the widened codes: exact for magnitudes 2^-14 to 65504, 2^-25
+                        // off below, infinite above
+                        if (!warp_wait(landed, q_fills >> b & 1, p.timeout_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        q_fills ^= 1u << b;
+                        uint4* q = reinterpret_cast<uint4*>(sm + b * kTileBytes);
+                        const int chunks = min(QT, g.nq - x * QT) * G * 8;      // of 16 bytes, in each half
+                        for (int i = lane; i < chunks; i += 32) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const int i = i0 + 2 * e;
-                            if (i >= zero_to) continue;
-                            if constexpr (kFp8 && QBf16) {
-                                // fp16, as the widened codes: exact for a bf16 query of magnitude 2^-14
-                                // to 65504, 2^-25 off below, infinite above
-                                uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
+                            for (int e = 0; e < 2; ++e) {
+                                uint4& v = q[e * (kHalfBytes / 16) + i];
+                                uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                                 for (int a = 0; a < 4; ++a)
                                     w[a] = pack2<false>(to_float<true>(w[a] & 0xffffu), to_float<true>(w[a] >> 16));
-                                v[e] = make_uint4(w[0], w[1], w[2], w[3]);
+                                v = make_uint4(w[0], w[1], w[2], w[3]);
                             }
-                            *reinterpret_cast<uint4*>(qdst + sw128_offset(i, (c & 7) * 8)) = v[e];
                         }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(kQFull + b));
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(kQFull + b));
                 }
                 if constexpr (!kFp8) {
                     for (int i = 0; i < g.steps && ok; ++i) {
@@ -824,7 +833,7 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                         for (int e = 0; e < kKeys; e += 2)
                             a4[(e >> 1) & 3] = max3f(a4[(e >> 1) & 3], fabsf(__uint_as_float(sv[e])), fabsf(__uint_as_float(sv[e + 1])));
                         const float am = fmaxf(fmaxf(a4[0], a4[1]), fmaxf(a4[2], a4[3]));
-                        if (!__any_sync(0xffffffffu, am * fabsf(k1) > kCapSmall)) {
+                        if (!__any_sync(0xffffffffu, live && am * fabsf(k1) > kCapSmall)) {
                             const uint64_t k12 = f2_pack(k1, k1), sc2 = f2_pack(s_log2, s_log2);
                             const uint64_t c0 = f2_pack(kTanh0, kTanh0), c1 = f2_pack(kTanh1, kTanh1),
                                            c2 = f2_pack(kTanh2, kTanh2), c3 = f2_pack(kTanh3, kTanh3),
@@ -887,7 +896,7 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                     // (a scale of 0 would turn a hidden row's infinity into NaN)
                     if (!Mod) mx = isinf(mx) && mul == 0.f ? -INFINITY : mx * mul;
                 }
-                const bool need = mx > m_used + kRescale;
+                const bool need = live && mx > m_used + kRescale;
                 const bool resc = __any_sync(0xffffffffu, need);
                 const float m_new = need ? mx : m_used;
                 // a row that has seen nothing yet: exponents against 0, all of hidden scores
@@ -959,27 +968,33 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
             tc_fence_after();
             const bool whole = g.flags & 2;
             const size_t orow = (static_cast<size_t>(g.row0 + jq) * p.num_q_heads + head) * kHeadDim;
-            const size_t prow = static_cast<size_t>(g.slot) * (2 * kRows) + (solo ? r : x * kRows + r);
-            // 32 components from 32 c on: the row itself, or its partial
+            const size_t at_row = static_cast<size_t>(g.slot) * (2 * kRows) + (solo ? r : x * kRows + r);
+            // 32 components from 32 c on: of the row itself, in whole sectors, or of its partial, in an
+            // order in which a warp's rows lie side by side ([quad of components][row][4])
             auto put = [&](int c, const uint32_t (&ov)[32], float inv) {
-                if (!live) return;
-                if (whole) {
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + orow) + 4 * c;
+                if (live && whole) {
+                    uint16_t* dst = static_cast<uint16_t*>(p.out) + orow + 32 * c;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t w[4];
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t w[8];
 #pragma unroll
-                        for (int a = 0; a < 4; ++a)
-                            w[a] = pack2<QBf16>(__uint_as_float(ov[8 * e + 2 * a]) * inv, __uint_as_float(ov[8 * e + 2 * a + 1]) * inv);
-                        dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int a = 0; a < 8; ++a)
+                            w[a] = pack2<QBf16>(__uint_as_float(ov[16 * e + 2 * a]) * inv, __uint_as_float(ov[16 * e + 2 * a + 1]) * inv);
+                        if (p.out_sectors) {
+                            st_global_32(dst + 16 * e, w);
+                        } else {
+                            reinterpret_cast<uint4*>(dst)[2 * e] = make_uint4(w[0], w[1], w[2], w[3]);
+                            reinterpret_cast<uint4*>(dst)[2 * e + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+                        }
                     }
-                } else {
-                    float4* dst = reinterpret_cast<float4*>(p.partial + prow * kHeadDim) + 8 * c;
+                } else if (live) {
+                    float4* dst = p.partial + (static_cast<size_t>(g.slot) * 32 + 8 * c) * (2 * kRows) + (solo ? r : x * kRows + r);
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        dst[e] = make_float4(__uint_as_float(ov[4 * e]), __uint_as_float(ov[4 * e + 1]),
-                                             __uint_as_float(ov[4 * e + 2]), __uint_as_float(ov[4 * e + 3]));
+                        dst[e * 2 * kRows] = make_float4(__uint_as_float(ov[4 * e]), __uint_as_float(ov[4 * e + 1]),
+                                                         __uint_as_float(ov[4 * e + 2]), __uint_as_float(ov[4 * e + 3]));
                 }
+                __syncwarp();
             };
             // A warp goes on to the next segment once all have seen this one's end: its products
             // (solo: also read by the other tile's warps) are overwritten, and no barrier can get
@@ -995,9 +1010,8 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                         tmem_ld32(tO(x) + lane_off + 32 * c, ov);
                         tmem_wait_ld();
                         put(c, ov, inv);
-                        __syncwarp();
                     }
-                    if (!whole && live) p.ml[prow] = make_float2(m_used, l);
+                    if (!whole && live) p.ml[at_row] = make_float2(m_used, l);
                 }
             } else {
                 // A's steps and B's: both tiles hold the row in this lane; A's warps write its first
@@ -1031,9 +1045,8 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                                 ov[e] = __float_as_uint(fmaf(__uint_as_float(ov[e]), wa, __uint_as_float(ob[e]) * wb));
                         }
                         put(c, ov, inv);
-                        __syncwarp();
                     }
-                    if (!whole && live && x == 0) p.ml[prow] = make_float2(m, sum);
+                    if (!whole && live && x == 0) p.ml[at_row] = make_float2(m, sum);
                 }
                 ++solos;
                 tc_fence_before();
@@ -1126,80 +1139,77 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
 
 // Units that several CTAs share:
 //   out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,   M = max_i m_i,
-// over the partials (o_i, m_i in log2 units, l_i).  CTA (w, z) takes rows of the unit that main
+// over the partials (o_i, m_i in log2 units, l_i).  CTA (w, y) takes parts of the unit that main
 // CTA w began and did not finish; its partials lie in w's second slot and in the first slots of
-// the CTAs behind it up to `last`.  A row has a warp, or with many partials several, whose
-// sums meet in shared memory.
+// the CTAs behind it up to `last`.  A part is up to 32 rows and four quads of their components;
+// the threads that are left when the rows are few share out the partials, and their sums meet
+// in shared memory.
 template <bool OutBf16, bool Fp8>
 __global__ void __launch_bounds__(256) scored_combine_kernel(const ScoredParams p) {
-    __shared__ float4 acc_smem[8][32];
-    __shared__ float2 ml_smem[8];
+    __shared__ float4 acc_smem[256];
+    __shared__ float2 ml_smem[256];
     grid_dependency_wait();
     grid_launch_dependents();
     const int w = blockIdx.x;
     const CombineRecord rec = p.records[w];
     if (rec.rows == 0) return;
     const int parts = rec.last - w + 1;
-    const int per_row = parts > 16 ? 8 : parts > 8 ? 4 : parts > 4 ? 2 : 1;       // warps of a row
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int sub = warp % per_row, rows_at_once = 8 / per_row;
     const int QT = p.queries_per_tile, G = p.group;
-    for (int i0 = blockIdx.y * rows_at_once; i0 < rec.rows; i0 += gridDim.y * rows_at_once) {
-        const int i = i0 + warp / per_row;
+    // threads: row (a power of two of them up to 32) x 4 quads x share of the partials
+    int shift = 0;
+    while (shift < 5 && (1 << shift) < rec.rows) ++shift;
+    const int row = threadIdx.x & ((1 << shift) - 1), quad = threadIdx.x >> shift & 3, share = threadIdx.x >> (shift + 2);
+    const int shares = 64 >> shift;
+    const int tasks = ((rec.rows + (1 << shift) - 1) >> shift) * 8;
+    for (int task = blockIdx.y; task < tasks; task += gridDim.y) {
+        const int i = ((task >> 3) << shift) + row;
+        const int q4 = (task & 7) * 4 + quad;
         const bool live = i < rec.rows;
         const int query = i / G;
         const int at = rec.solo ? i : (query / QT) * kRows + (query % QT) * G + i % G;
         float m = -INFINITY, l = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto fold = [&](float2 ml, float4 o) {
+            const float mn = fmaxf(m, ml.x), m_at = mn == -INFINITY ? 0.f : mn;
+            const float a = ex2_approx(m - m_at), b = ex2_approx(ml.x - m_at);
+            acc = make_float4(acc.x * a + o.x * b, acc.y * a + o.y * b, acc.z * a + o.z * b, acc.w * a + o.w * b);
+            l = l * a + ml.y * b;
+            m = mn;
+        };
         if (live) {
-            for (int k0 = sub; k0 < parts; k0 += 4 * per_row) {
+            for (int k0 = share; k0 < parts; k0 += 4 * shares) {
                 float4 o[4];
                 float2 ml[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int kk = k0 + e * per_row;
+                    const int kk = k0 + e * shares;
                     ml[e] = make_float2(-INFINITY, 0.f);
                     o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (kk < parts) {
-                        const size_t row = static_cast<size_t>(kk == 0 ? 2 * w + 1 : 2 * (w + kk)) * (2 * kRows) + at;
-                        ml[e] = __ldcg(p.ml + row);
-                        o[e] = __ldcg(reinterpret_cast<const float4*>(p.partial + row * kHeadDim) + lane);
+                        const size_t slot = kk == 0 ? 2 * w + 1 : 2 * (w + kk);
+                        ml[e] = __ldcg(p.ml + slot * (2 * kRows) + at);
+                        o[e] = __ldcg(p.partial + (slot * 32 + q4) * (2 * kRows) + at);
                     }
                 }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float mn = fmaxf(m, ml[e].x), m_at = mn == -INFINITY ? 0.f : mn;
-                    const float a = ex2_approx(m - m_at), b = ex2_approx(ml[e].x - m_at);
-                    acc = make_float4(acc.x * a + o[e].x * b, acc.y * a + o[e].y * b, acc.z * a + o[e].z * b,
-                                      acc.w * a + o[e].w * b);
-                    l = l * a + ml[e].y * b;
-                    m = mn;
-                }
+                for (int e = 0; e < 4; ++e) fold(ml[e], o[e]);
             }
         }
-        if (per_row > 1) {
-            acc_smem[warp][lane] = acc;
-            if (lane == 0) ml_smem[warp] = make_float2(m, l);
+        if (shares > 1 && parts > 1) {
             __syncthreads();
-            if (sub == 0) {
-                for (int e = 1; e < per_row; ++e) {
-                    const float2 ml = ml_smem[warp + e];
-                    const float4 o = acc_smem[warp + e][lane];
-                    const float mn = fmaxf(m, ml.x), m_at = mn == -INFINITY ? 0.f : mn;
-                    const float a = ex2_approx(m - m_at), b = ex2_approx(ml.x - m_at);
-                    acc = make_float4(acc.x * a + o.x * b, acc.y * a + o.y * b, acc.z * a + o.z * b, acc.w * a + o.w * b);
-                    l = l * a + ml.y * b;
-                    m = mn;
-                }
-            }
+            acc_smem[threadIdx.x] = acc;
+            ml_smem[threadIdx.x] = make_float2(m, l);
             __syncthreads();
+            if (share == 0)
+                for (int e = 1; e < min(shares, parts); ++e)
+                    fold(ml_smem[threadIdx.x + (e << (shift + 2))], acc_smem[threadIdx.x + (e << (shift + 2))]);
         }
-        if (live && sub == 0) {
+        if (live && share == 0) {
             const int head = rec.head0 + i % G;
             const float vscale = Fp8 ? __ldg(p.v_scale + rec.head0 / G * p.scale_stride) : 1.0f;
             const float inv = l == 0.f ? 0.f : vscale / l;
             uint16_t* dst = static_cast<uint16_t*>(p.out) +
-                            (static_cast<size_t>(rec.row0 + query) * p.num_q_heads + head) * kHeadDim + 4 * lane;
+                            (static_cast<size_t>(rec.row0 + query) * p.num_q_heads + head) * kHeadDim + 4 * q4;
             *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<OutBf16>(acc.x * inv, acc.y * inv), pack2<OutBf16>(acc.z * inv, acc.w * inv));
         }
     }
@@ -1248,7 +1258,7 @@ cudaError_t scored_prepare(CacheKind kind, bool q_bf16, bool mod) {
 }
 
 cudaError_t launch_scored(CacheKind kind, bool q_bf16, bool mod, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                          const ScoredParams& p, int sms, cudaStream_t stream) {
+                          const CUtensorMap& qmap, const ScoredParams& p, int sms, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(sms));
     cfg.blockDim = dim3(static_cast<unsigned>(32 * (kind == kKindFp8 ? Cfg<kKindFp8>::kWarps : Cfg<kKindBf16>::kWarps)));
@@ -1259,7 +1269,8 @@ cudaError_t launch_scored(CacheKind kind, bool q_bf16, bool mod, const CUtensorM
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    void* args[] = {const_cast<CUtensorMap*>(&kmap), const_cast<CUtensorMap*>(&vmap), const_cast<ScoredParams*>(&p)};
+    void* args[] = {const_cast<CUtensorMap*>(&kmap), const_cast<CUtensorMap*>(&vmap), const_cast<CUtensorMap*>(&qmap),
+                    const_cast<ScoredParams*>(&p)};
     return cudaLaunchKernelExC(&cfg, scored_fn(kind, q_bf16, mod), args);
 }
 
