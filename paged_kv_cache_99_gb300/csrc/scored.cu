@@ -53,25 +53,32 @@ template <int Kind>
 struct Cfg {
     static constexpr bool kFp8 = Kind == kKindFp8;
     static constexpr bool kMmaBf16 = Kind == kKindBf16;
-    static constexpr int kWarps = kFp8 ? 16 : 12;
+    static constexpr int kHalves = kFp8 ? 1 : 2;         // threads of a row
+    static constexpr int kCols = kKeys / kHalves;        // a thread's keys of a step
+    static constexpr int kSoftmaxWarps = 8 * kHalves;    // 4 ..
+    static constexpr int kWarps = 4 + kSoftmaxWarps + (kFp8 ? 4 : 0);
     static constexpr int kStages = kFp8 ? 4 : 5;         // K and V tiles of 16-bit elements
     static constexpr int kRaw = kFp8 ? 2 : 0;            // e4m3 tiles as copied
     // launch registers per thread, and the shares after setmaxnreg
-    [[maybe_unused]] static constexpr int kRegsLaunch = kFp8 ? 128 : 168;
-    static constexpr int kRegsFront = kFp8 ? 64 : 104;
-    static constexpr int kRegsSoftmax = kFp8 ? 192 : 200;
+    [[maybe_unused]] static constexpr int kRegsLaunch = kFp8 ? 128 : 96;
+    static constexpr int kRegsFront = 64;
+    static constexpr int kRegsSoftmax = kFp8 ? 192 : 104;
     static constexpr uint32_t kOffStage = 2 * kTileBytes;                    // behind Q_A, Q_B
     static constexpr uint32_t kOffRaw = kOffStage + kStages * kTileBytes;
     static constexpr uint32_t kOffBars = kOffRaw + kRaw * kHalfBytes;
-    static constexpr uint32_t kOffSegs = kOffBars + 448;
-    static constexpr uint32_t kOffMl = kOffSegs + kSegs * kSegInts * 4;      // [2][128] (maximum, sum)
-    static constexpr uint32_t kOffScan = kOffMl + 2 * kRows * 8;             // [kWarps]
-    static constexpr uint32_t kSmem = kOffScan + 64;
+    static constexpr uint32_t kOffSegs = kOffBars + 480;
+    static constexpr uint32_t kOffRow = kOffSegs + kSegs * kSegInts * 4;     // [tile][2][128] values of rows
+    static constexpr uint32_t kOffScan = kOffRow + 4 * kRows * 4;            // [kWarps]
+    static constexpr uint32_t kSmem = kOffScan + 96;
 };
-static_assert(256 * Cfg<kKindFp8>::kRegsFront + 256 * Cfg<kKindFp8>::kRegsSoftmax <=
-                  Cfg<kKindFp8>::kWarps * 32 * Cfg<kKindFp8>::kRegsLaunch, "register split above the launch total");
-static_assert(128 * Cfg<kKindBf16>::kRegsFront + 256 * Cfg<kKindBf16>::kRegsSoftmax <=
-                  Cfg<kKindBf16>::kWarps * 32 * Cfg<kKindBf16>::kRegsLaunch, "register split above the launch total");
+static_assert(kSegs * kSegInts * 4 % 16 == 0 && 480 % 16 == 0, "alignment");
+template <int Kind>
+constexpr bool regs_fit() {
+    using C = Cfg<Kind>;
+    return 32 * ((C::kWarps - C::kSoftmaxWarps) * C::kRegsFront + C::kSoftmaxWarps * C::kRegsSoftmax) <= 32 * C::kWarps * C::kRegsLaunch &&
+           32 * C::kWarps * C::kRegsLaunch <= 65536;
+}
+static_assert(regs_fit<kKindFp8>() && regs_fit<kKindBf16>(), "register split above the launch total");
 static_assert(Cfg<kKindBf16>::kSmem <= 232448 && Cfg<kKindFp8>::kSmem <= 232448, "shared memory");
 
 enum {                                       // barriers, 8 bytes each
@@ -92,9 +99,10 @@ enum {                                       // barriers, 8 bytes each
     kFixed,                                  // [stage] V rows that no row sees are zeroed (edge steps)
     kIssued = kFixed + 5,                    // [stage] the copy of an edge step's V is under way
     kQLand = kIssued + 5,                    // [Q buffer] a bf16 query of an FP8 cache has landed
-    kNumBars = kQLand + 2
+    kPair = kQLand + 2,                      // [tile][warp's rows] the two threads of a row have met
+    kNumBars = kPair + 8
 };
-static_assert(kNumBars * 8 + 4 <= 448, "barriers");
+static_assert(kNumBars * 8 + 4 <= 480, "barriers");
 
 // The cached tokens [lo, hi) that a row sees and its position; a tree's row also sees the nodes
 // of its mask, which lie behind hi.
@@ -179,44 +187,50 @@ __device__ __forceinline__ Unit unit_of(const ScoredParams& p, const SeqView& s,
     return u;
 }
 
+// A unit's share of the ranges: its steps, and what beginning a unit costs in steps (the
+// queries, the first scores and the last products run alone): about 4.8 us of a pair, whose step
+// takes 2.5, and 1 to 2 us of a solo, whose step takes 2.
+__device__ __forceinline__ int unit_lead(const ScoredParams& p, const Unit& u) { return u.nq <= p.queries_per_tile ? 1 : 2; }
+__device__ __forceinline__ int unit_cost(const ScoredParams& p, const Unit& u) { return u.steps + unit_lead(p, u); }
+
 __device__ __forceinline__ int units_per_head(const ScoredParams& p, const SeqView& s) {
     return (s.q_len + 2 * p.queries_per_tile - 1) / (2 * p.queries_per_tile);
 }
 
-// Steps of a sequence, all heads.
-__device__ __forceinline__ int seq_steps(const ScoredParams& p, int s, bool report) {
+// Cost of a sequence, all heads.
+__device__ __forceinline__ int seq_cost(const ScoredParams& p, int s, bool report) {
     const SeqView v = seq_view(p, s, report);
     const int np = units_per_head(p, v);
     int sum = 0;
-    for (int t = 0; t < np; ++t) sum += unit_of(p, v, t).steps;
+    for (int t = 0; t < np; ++t) sum += unit_cost(p, unit_of(p, v, t));
     return sum * p.num_kv_heads;
 }
 
 // A segment as its CTA's warps see it: steps [step, step + steps) of a unit.
+enum {
+    kSegHead, kSegRow0, kSegNq, kSegStep, kSegSteps, kSegKlo, kSegKhi,
+    kSegCtx,                                 // tree: tokens before it, else INT_MAX
+    kSegJ0, kSegTail, kSegQLen, kSegN, kSegPrefix,   // the unit's first query, see edge_step, the sequence
+    kSegSeq,
+    kSegFlags,                               // 1: solo, 2: the whole unit, 4: the first step is an edge
+    kSegSlot                                 // where its partial goes
+};
+
 struct Seg {
-    int h, row0, nq, step, steps, klo, khi;
-    int ctx;                                 // tree: tokens before it, else INT_MAX
-    int j0, q0, q_len, n, prefix;            // the unit's first query, and its sequence
-    int seq;
-    int flags;                               // 1: solo, 2: the whole unit
-    int slot;                                // where its partial goes
+    int h, row0, nq, step, steps, klo, khi, ctx, q_len, seq, tail, flags;
 };
 
 __device__ __forceinline__ Seg read_seg(const int* d) {
     Seg g;
-    const int4* v = reinterpret_cast<const int4*>(d);
-    const int4 a = v[0], b = v[1], c = v[2], e = v[3];
-    g.h = a.x; g.row0 = a.y; g.nq = a.z; g.step = a.w;
-    g.steps = b.x; g.klo = b.y; g.khi = b.z; g.ctx = b.w;
-    g.j0 = c.x; g.q0 = c.y; g.q_len = c.z; g.n = c.w;
-    g.prefix = e.x; g.seq = e.y; g.flags = e.z; g.slot = e.w;
+    g.h = d[kSegHead]; g.row0 = d[kSegRow0]; g.nq = d[kSegNq]; g.step = d[kSegStep]; g.steps = d[kSegSteps];
+    g.klo = d[kSegKlo]; g.khi = d[kSegKhi]; g.ctx = d[kSegCtx]; g.q_len = d[kSegQLen]; g.seq = d[kSegSeq];
+    g.tail = d[kSegTail]; g.flags = d[kSegFlags];
     return g;
 }
 
-// A step some of whose V rows no row may see.
-__device__ __forceinline__ bool edge_step(const Seg& g, int key0) {
-    return key0 < g.klo || key0 + kKeys > g.khi || key0 + kKeys > g.ctx;
-}
+// Whether some of a segment's i-th step's V rows may be seen by no row: keys before the
+// unit's first, from step `tail` on keys behind its last or nodes of a tree.
+__device__ __forceinline__ bool edge_step(int flags, int tail, int i) { return (i == 0 && (flags & 4)) || i >= tail; }
 
 // Tile order in the ring: K0, K1, V0, K2, V1, K3, ...: each K two steps ahead of its use, V as
 // its step begins.
@@ -239,13 +253,14 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
     constexpr bool kMmaBf16 = C::kMmaBf16;
     constexpr int NS = C::kStages;
     constexpr int kThreads = C::kWarps * 32;
-    constexpr int kSegReaders = kFp8 ? 15 : 11;
+    constexpr int H = C::kHalves;
+    constexpr int kSegReaders = C::kWarps - 1;
 
     extern __shared__ __align__(1024) uint8_t sm[];             // as the 128-byte swizzle wants it
     const uint32_t sbase = smem_addr(sm);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kOffBars + kNumBars * 8);
     int* segs = reinterpret_cast<int*>(sm + C::kOffSegs);
-    float2* ml_smem = reinterpret_cast<float2*>(sm + C::kOffMl);
+    float* row_smem = reinterpret_cast<float*>(sm + C::kOffRow);
     int* scan = reinterpret_cast<int*>(sm + C::kOffScan);
     int* cum = reinterpret_cast<int*>(sm + C::kOffStage);        // only before the first copy
     auto bar = [&](int i) -> uint32_t { return sbase + C::kOffBars + 8u * i; };
@@ -273,12 +288,13 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
             mbar_init(bar(kQEmpty + i), 1);
             mbar_init(bar(kQLand + i), 1);
             mbar_init(bar(kSFull + i), 1);
-            mbar_init(bar(kPHalf + i), 4);
+            mbar_init(bar(kPHalf + i), 4 * H);
             mbar_init(bar(kPFull + i), 4);
         }
         mbar_init(bar(kSegDone), 1);
-        mbar_init(bar(kMlReady), 8);
-        mbar_init(bar(kOFree), 8);
+        mbar_init(bar(kMlReady), C::kSoftmaxWarps);
+        mbar_init(bar(kOFree), C::kSoftmaxWarps);
+        for (int i = 0; i < 8; ++i) mbar_init(bar(kPair + i), 2);
         fence_barrier_init();
         tmap_prefetch(&kmap);
         tmap_prefetch(&vmap);
@@ -288,14 +304,14 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
     grid_dependency_wait();
     grid_launch_dependents();
 
-    // ---- steps per sequence: exclusive scan into cum ----
+    // ---- cost per sequence: exclusive scan into cum ----
     const int B = p.num_seqs;
     {
         const int per = (B + kThreads - 1) / kThreads;
         const int beg = min(B, static_cast<int>(threadIdx.x) * per), end = min(B, beg + per);
         int local = 0;
         for (int s = beg; s < end; ++s) {
-            const int w = seq_steps(p, s, blockIdx.x == 0);
+            const int w = seq_cost(p, s, blockIdx.x == 0);
             cum[s] = w;
             local += w;
         }
@@ -327,7 +343,7 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
     // ---- this CTA's range, found by warp 2 ----
     int f = static_cast<int>(static_cast<long long>(T) * cta / W);
     int left = static_cast<int>(static_cast<long long>(T) * (cta + 1) / W) - f;
-    int cs = 0, ct = 0, ch = 0, coff = 0;    // sequence, unit, head, step within the unit
+    int cs = 0, ct = 0, ch = 0, coff = 0;    // sequence, unit, head, place within the unit's cost
     SeqView sv_cur = {};
     if (warp == 2) {
         int lo = 0, hi = B;
@@ -339,9 +355,9 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
         int rem = f - cum[lo];
         sv_cur = seq_view(p, cs, false);
         const int np = units_per_head(p, sv_cur);
-        // a lane per unit: the unit whose steps (all heads) hold the rest
+        // a lane per unit: the unit whose cost (all heads) holds the rest
         for (int t0 = 0; t0 < np; t0 += 32) {
-            const int w = t0 + lane < np ? unit_of(p, sv_cur, t0 + lane).steps * p.num_kv_heads : 0;
+            const int w = t0 + lane < np ? unit_cost(p, unit_of(p, sv_cur, t0 + lane)) * p.num_kv_heads : 0;
             int incl = w;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -357,9 +373,9 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
             }
             rem -= __shfl_sync(0xffffffffu, incl, 31);
         }
-        const int steps = unit_of(p, sv_cur, ct).steps;
-        ch = rem / steps;
-        coff = rem % steps;
+        const int cost = unit_cost(p, unit_of(p, sv_cur, ct));
+        ch = rem / cost;
+        coff = rem % cost;
     }
     fence_proxy_async_smem();                // cum was written where the first copies go
     if (warp == 1) tmem_alloc(smem_addr(tmem_slot), 512);
@@ -443,7 +459,7 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                     const int y2 = entry(i + 2);
                     copy(&vmap, y0);
                     // (the tile's barrier is in its phase from here until the zeroing is done)
-                    if (!kFp8 && ok && lane == 0 && edge_step(g, (g.step + i) * kKeys)) mbar_arrive(bar(kIssued + (r - 1) % NS));
+                    if (!kFp8 && ok && lane == 0 && edge_step(g.flags, g.tail, i)) mbar_arrive(bar(kIssued + (r - 1) % NS));
                     if (ok && i + 2 < g.steps) copy(&kmap, y2);
                     y0 = y1;
                     y1 = y2;
@@ -498,11 +514,11 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                 unsigned q_par = 0, p_par = 0;       // bit x: of the buffer's fills, of the tile's P
                 while (ok) {
                     if (!wait(bar(kSegFull + seg % kSegs), (seg / kSegs) & 1)) break;
-                    const Seg g = read_seg(segs + (seg % kSegs) * kSegInts);
+                    const int* d = segs + (seg % kSegs) * kSegInts;
+                    const int n = d[kSegSteps], flags = d[kSegFlags], tail = d[kSegTail];
                     mbar_arrive(bar(kSegEmpty + seg % kSegs));
-                    if (g.steps == 0) break;
-                    const bool solo = g.flags & 1;
-                    const int n = g.steps;
+                    if (n == 0) break;
+                    const bool solo = flags & 1;
                     const int qb = solo ? seg & 1 : 0;
                     const uint32_t q_a = sbase + qb * kTileBytes, q_b = solo ? q_a : sbase + kTileBytes;
                     if (!wait(bar(kQFull + qb), q_par >> qb & 1)) break;
@@ -530,7 +546,7 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                     auto v_ready = [&](int i) -> bool {
                         const int st = (r0 + item_v(n, i)) % NS;
                         if (!tile_ready(r0 + item_v(n, i))) return false;
-                        if (!kFp8 && edge_step(g, (g.step + i) * kKeys)) {
+                        if (!kFp8 && edge_step(flags, tail, i)) {
                             if (!wait(bar(kFixed + st), fixes >> st & 1)) return false;
                             fixes ^= 1u << st;
                         }
@@ -596,47 +612,25 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                 int* d = segs + sl * kSegInts;
                 if (left == 0) {
                     if (lane == 0) {
-                        d[4] = 0;
+                        d[kSegSteps] = 0;
                         mbar_arrive(bar(kSegFull + sl));
                     }
                     break;
                 }
+                // the range's part of the unit, places [coff, coff + take) of its cost, of which the
+                // first `lead` stand for its start: steps [a, b)
                 const Unit u = unit_of(p, sv_cur, ct);
-                const int take = min(left, u.steps - coff);
-                const bool starts = coff == 0, ends = coff + take == u.steps;
+                const int lead = unit_lead(p, u), cost = u.steps + lead;
+                const int take = min(left, cost - coff);
+                const int a = max(coff - lead, 0), b = coff + take - lead;
+                const bool starts = a == 0, ends = b == u.steps;
                 const bool solo = u.nq <= QT;
-                if (lane == 0) {
-                    // a partial that continues another CTA's unit goes to the CTA's first slot,
-                    // one that starts a unit to its second: the range has one of each at most
-                    d[0] = ch;
-                    d[1] = sv_cur.q0 + u.ja;
-                    d[2] = u.nq;
-                    d[3] = u.step0 + coff;
-                    d[4] = take;
-                    d[5] = u.klo;
-                    d[6] = u.khi;
-                    d[7] = p.masks ? sv_cur.n - sv_cur.q_len : INT_MAX;
-                    d[8] = u.ja;
-                    d[9] = sv_cur.q0;
-                    d[10] = sv_cur.q_len;
-                    d[11] = sv_cur.n;
-                    d[12] = sv_cur.prefix;
-                    d[13] = cs;
-                    d[14] = (solo ? 1 : 0) | (starts && ends ? 2 : 0);
-                    d[15] = 2 * cta + (starts ? 1 : 0);
-                    mbar_arrive(bar(kSegFull + sl));
-                }
-                if (starts && !ends) {
-                    rec.rows = u.nq * G;
-                    rec.row0 = sv_cur.q0 + u.ja;
-                    rec.head0 = ch * G;
-                    rec.solo = solo ? 1 : 0;
-                    // the CTA whose range holds the unit's last step
-                    rec.last = static_cast<int>(((static_cast<long long>(f) + u.steps) * W - 1) / T);
-                }
+                const int unit_f = f - coff;
                 f += take;
                 left -= take;
                 coff = 0;
+                const int at_s = cs, at_h = ch;
+                const SeqView at_v = sv_cur;
                 if (left > 0 && ++ch == p.num_kv_heads) {
                     ch = 0;
                     if (++ct == units_per_head(p, sv_cur)) {
@@ -645,6 +639,40 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                             sv_cur = seq_view(p, ++cs, false);
                         } while (sv_cur.q_len == 0);
                     }
+                }
+                if (b <= 0) continue;            // nothing but the start: the next CTA has the steps
+                if (lane == 0) {
+                    // a partial that continues another CTA's unit goes to the CTA's first slot,
+                    // one that starts a unit to its second: the range has one of each at most
+                    d[kSegHead] = at_h;
+                    d[kSegRow0] = at_v.q0 + u.ja;
+                    d[kSegNq] = u.nq;
+                    d[kSegStep] = u.step0 + a;
+                    d[kSegSteps] = b - a;
+                    d[kSegKlo] = u.klo;
+                    d[kSegKhi] = u.khi;
+                    d[kSegCtx] = p.masks ? at_v.n - at_v.q_len : INT_MAX;
+                    d[kSegJ0] = u.ja;
+                    {
+                        // the first step that reaches behind the last key, or the first node
+                        const int end = p.masks ? at_v.n - at_v.q_len : u.khi;
+                        d[kSegTail] = max(end / kKeys - u.step0 - a, 0);
+                    }
+                    d[kSegQLen] = at_v.q_len;
+                    d[kSegN] = at_v.n;
+                    d[kSegPrefix] = at_v.prefix;
+                    d[kSegSeq] = at_s;
+                    d[kSegFlags] = (solo ? 1 : 0) | (starts && ends ? 2 : 0) | ((u.step0 + a) * kKeys < u.klo ? 4 : 0);
+                    d[kSegSlot] = 2 * cta + (starts ? 1 : 0);
+                    mbar_arrive(bar(kSegFull + sl));
+                }
+                if (starts && !ends) {
+                    rec.rows = u.nq * G;
+                    rec.row0 = at_v.q0 + u.ja;
+                    rec.head0 = at_h * G;
+                    rec.solo = solo ? 1 : 0;
+                    // the CTA whose range holds the unit's last step
+                    rec.last = static_cast<int>(((static_cast<long long>(unit_f) + cost) * W - 1) / T);
                 }
                 ++seg;
             }
@@ -708,7 +736,7 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                 if constexpr (!kFp8) {
                     for (int i = 0; i < g.steps && ok; ++i) {
                         const int key0 = (g.step + i) * kKeys;
-                        if (!edge_step(g, key0)) continue;
+                        if (!edge_step(g.flags, g.tail, i)) continue;
                         const int r = r0 + item_v(g.steps, i);
                         // nodes that some row of the unit sees (lane w: keys 32 w .. of the step)
                         uint32_t seen[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
@@ -752,67 +780,96 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
             }
             if (!ok && lane == 0) atomicOr(p.status, kDevErrTimeout);
         }
-    } else if (warp < 12) {
+    } else if (warp < 4 + C::kSoftmaxWarps) {
         setmaxnreg_inc<C::kRegsSoftmax>();
-        // ================= softmax: warps 4-7 tile A, 8-11 tile B; thread = one row =================
-        const int x = warp < 8 ? 0 : 1;
+        // ================= softmax: tile A's warps, then tile B's; H threads for a row =================
+        constexpr int NC = C::kCols;
+        const int x = (warp - 4) / (4 * H);
+        const int half = (warp - 4) / 4 % H;           // the thread's keys of a step: NC half ..
         const int quarter = warp & 3;                  // tensor-memory lanes 32 quarter .. + 31
         const int r = quarter * 32 + lane;
         const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-        const uint32_t s_addr = tS(x) + lane_off;
-        int uses = 0, solos = 0;
-        Seg g;
-        while (ok && next_seg(g)) {
-            const bool solo = g.flags & 1;
-            const int jq = (solo ? 0 : x * QT) + r / G;
-            const bool live = r < QT * G && jq < g.nq;
-            const bool warp_live = __any_sync(0xffffffffu, live);
-            const int head = g.h * G + r % G;
-            SeqView sq = {g.q0, g.q_len, g.n, g.prefix};
+        const uint32_t s_addr = tS(x) + lane_off + NC * half;               // its scores
+        const uint32_t p_addr = s_addr - NC / 2 * half;                     // its P, 16 bits each
+        const int exch = (2 * x + half) * kRows + r;   // in row_smem; the row's other thread: exch ^ kRows
+        unsigned par = 0;                              // parities: 1 of S, 2 of the solos, 4 of the meetings
+        auto meet = [&]() -> bool {                    // both threads of the row
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kPair + 4 * x + quarter));
+            if (!warp_wait(bar(kPair + 4 * x + quarter), par >> 2 & 1, p.timeout_ns)) ok = false;
+            par ^= 4u;
+            return ok;
+        };
+        // Registers are short (a thread's scores take most of them, and a spill misses the little
+        // L1 that is left): a segment's fields are read from shared memory where they are used,
+        // and its slot is given back when its outputs are written.
+        while (ok) {
+            if (!warp_wait(bar(kSegFull + k % kSegs), (k / kSegs) & 1, p.timeout_ns)) {
+                ok = false;
+                break;
+            }
+            const int* d = segs + (k % kSegs) * kSegInts;
+            ++k;
+            if (d[kSegSteps] == 0) break;
+            const bool solo = d[kSegFlags] & 1;
             RowView view = {0, 0, INT_MAX};
-            if (live) view = row_view(p, sq, g.j0 + jq);
+            float kscale = 1.0f, slope2 = 0.f;
+            bool live;
+            {
+                const int jq = (solo ? 0 : x * QT) + r / G;
+                live = r < QT * G && jq < d[kSegNq];
+                if (live) view = row_view(p, SeqView{d[kSegRow0] - d[kSegJ0], d[kSegQLen], d[kSegN], d[kSegPrefix]}, d[kSegJ0] + jq);
+                if (kFp8) kscale = __ldg(p.k_scale + d[kSegHead] * p.scale_stride);
+                if (Mod && p.slopes && live) slope2 = __ldg(p.slopes + d[kSegHead] * G + r % G) * 1.4426950408889634f;
+            }
+            const bool warp_live = __any_sync(0xffffffffu, live);
             const int lo_max = __reduce_max_sync(0xffffffffu, view.lo);
             const int hi_min = __reduce_min_sync(0xffffffffu, view.hi);
-            const unsigned long long* words = p.masks && live ? p.masks + static_cast<size_t>(g.row0 + jq) * p.mask_words : nullptr;
-            const float kscale = kFp8 ? __ldg(p.k_scale + g.h * p.scale_stride) : 1.0f;
-            const float vscale = kFp8 ? __ldg(p.v_scale + g.h * p.scale_stride) : 1.0f;
-            const float s_log2 = p.scale * 1.4426950408889634f * kscale;
-            const float slope2 = Mod && p.slopes && live ? __ldg(p.slopes + head) * 1.4426950408889634f : 0.f;
+            // never 0: hidden scores are infinite, and stay so under it
+            const float s_raw = p.scale * 1.4426950408889634f * kscale;
+            const float s_log2 = s_raw == 0.f ? 1e-30f : s_raw;
             const bool pos_scale = s_log2 >= 0.f;
             float m_used = -INFINITY, l = 0.f;
-            for (int i = solo ? x : 0; i < g.steps; i += solo ? 2 : 1) {
-                const bool first = i < (solo ? 2 : 1);
-                if (!warp_wait(bar(kSFull + x), uses & 1, p.timeout_ns)) {
+            const int stride = solo ? 2 : 1;
+            int key0 = (d[kSegStep] + (solo ? x : 0)) * kKeys + NC * half;
+            bool first = true;
+            for (int left_steps = solo ? (d[kSegSteps] + 1 - x) >> 1 : d[kSegSteps]; left_steps > 0;
+                 --left_steps, key0 += stride * kKeys, first = false) {
+                if (!warp_wait(bar(kSFull + x), par & 1, p.timeout_ns)) {
                     ok = false;
                     break;
                 }
-                ++uses;
+                par ^= 1u;
                 if (!warp_live) {                       // rows past the unit's: nothing reads their P
                     if (lane == 0) {
                         mbar_arrive(bar(kPHalf + x));
-                        mbar_arrive(bar(kPFull + x));
+                        if (half == H - 1) mbar_arrive(bar(kPFull + x));
                     }
                     continue;
                 }
                 tc_fence_after();
-                const int key0 = (g.step + i) * kKeys;
-                const bool need_mask = key0 < lo_max || key0 + kKeys > hi_min;
-                // what the row sees of the step's keys
-                uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+                const bool need_mask = key0 < lo_max || key0 + NC > hi_min;
+                // what the row sees of the thread's keys
+                uint32_t vis[NC / 32];
+#pragma unroll
+                for (int w = 0; w < NC / 32; ++w) vis[w] = 0xffffffffu;
                 if (need_mask) {
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
+                    for (int w = 0; w < NC / 32; ++w) {
                         const int base = key0 + 32 * w;
                         const int a = max(view.lo - base, 0), b = min(view.hi - base, 32);
                         vis[w] = b <= a ? 0u : (0xffffffffu << a) & (0xffffffffu >> (32 - b));
-                        if (words) vis[w] |= tree_bits(words, g.q_len, base - g.ctx);
+                        if (p.masks && live) {
+                            const size_t row = static_cast<size_t>(d[kSegRow0] + (solo ? 0 : x * QT) + r / G);
+                            vis[w] |= tree_bits(p.masks + row * p.mask_words, d[kSegQLen], base - d[kSegCtx]);
+                        }
                     }
                 }
                 __syncwarp();
-                // the whole row of S in registers: one tensor-memory round trip per step
-                uint32_t sv[kKeys];
+                // the scores in registers: one tensor-memory round trip per step
+                uint32_t sv[NC];
 #pragma unroll
-                for (int c = 0; c < kKeys / 32; ++c)
+                for (int c = 0; c < NC / 32; ++c)
                     tmem_ld32(s_addr + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * c));
                 tmem_wait_ld();
                 if constexpr (Mod) {
@@ -820,7 +877,7 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                     // were never copied, must not choose the form of the tanh)
                     if (need_mask) {
 #pragma unroll
-                        for (int e = 0; e < kKeys; ++e) sv[e] = vis[e >> 5] >> (e & 31) & 1 ? sv[e] : 0u;
+                        for (int e = 0; e < NC; ++e) sv[e] = vis[e >> 5] >> (e & 31) & 1 ? sv[e] : 0u;
                     }
                     if (p.cap > 0.f) {
                         // |x / cap| small in the whole warp (nearly always: caps lie far above most
@@ -830,7 +887,7 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                         const float k1 = p.scale * kscale / p.cap;
                         float a4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int e = 0; e < kKeys; e += 2)
+                        for (int e = 0; e < NC; e += 2)
                             a4[(e >> 1) & 3] = max3f(a4[(e >> 1) & 3], fabsf(__uint_as_float(sv[e])), fabsf(__uint_as_float(sv[e + 1])));
                         const float am = fmaxf(fmaxf(a4[0], a4[1]), fmaxf(a4[2], a4[3]));
                         if (!__any_sync(0xffffffffu, live && am * fabsf(k1) > kCapSmall)) {
@@ -839,7 +896,7 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                                            c2 = f2_pack(kTanh2, kTanh2), c3 = f2_pack(kTanh3, kTanh3),
                                            c4 = f2_pack(kTanh4, kTanh4);
 #pragma unroll
-                            for (int e = 0; e < kKeys; e += 2) {
+                            for (int e = 0; e < NC; e += 2) {
                                 const uint64_t v = f2_pack(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
                                 const uint64_t y = f2_mul(v, k12), u = f2_mul(y, y);
                                 uint64_t q = f2_fma(u, c4, c3);
@@ -854,28 +911,28 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                         } else {
                             const float c2 = p.cap * 1.4426950408889634f, k2 = k1 * 2.8853900817779268f;
 #pragma unroll
-                            for (int e = 0; e < kKeys; ++e)
+                            for (int e = 0; e < NC; ++e)
                                 sv[e] = __float_as_uint(fmaf(-2.f * c2, rcp_approx(1.f + ex2_approx(__uint_as_float(sv[e]) * k2)), c2));
                         }
                     } else {
 #pragma unroll
-                        for (int e = 0; e < kKeys; ++e) sv[e] = __float_as_uint(__uint_as_float(sv[e]) * s_log2);
+                        for (int e = 0; e < NC; ++e) sv[e] = __float_as_uint(__uint_as_float(sv[e]) * s_log2);
                     }
                     if (p.slopes) {
                         const float base = static_cast<float>(key0 - view.pos);
 #pragma unroll
-                        for (int e = 0; e < kKeys; ++e)
+                        for (int e = 0; e < NC; ++e)
                             sv[e] = __float_as_uint(fmaf(-slope2, fabsf(base + static_cast<float>(e)), __uint_as_float(sv[e])));
                     }
                 }
                 // row maximum of s * scale = max(s) * scale for scale >= 0, min(s) * scale
-                // otherwise; four independent chains, hidden columns only where a row has some
+                // otherwise; four independent chains
                 const float mul = Mod ? 1.0f : s_log2;
                 float mx;
                 if (need_mask) {
                     const float hidden = Mod || pos_scale ? -INFINITY : INFINITY;
 #pragma unroll
-                    for (int e = 0; e < kKeys; ++e)
+                    for (int e = 0; e < NC; ++e)
                         sv[e] = vis[e >> 5] >> (e & 31) & 1 ? sv[e] : __float_as_uint(hidden);
                 }
                 {
@@ -883,18 +940,23 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                     if (Mod || pos_scale) {
                         e4[0] = e4[1] = e4[2] = e4[3] = -INFINITY;
 #pragma unroll
-                        for (int e = 0; e < kKeys; e += 2)
+                        for (int e = 0; e < NC; e += 2)
                             e4[(e >> 1) & 3] = max3f(e4[(e >> 1) & 3], __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
                         mx = fmaxf(fmaxf(e4[0], e4[1]), fmaxf(e4[2], e4[3]));
                     } else {
                         e4[0] = e4[1] = e4[2] = e4[3] = INFINITY;
 #pragma unroll
-                        for (int e = 0; e < kKeys; e += 2)
+                        for (int e = 0; e < NC; e += 2)
                             e4[(e >> 1) & 3] = min3f(e4[(e >> 1) & 3], __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
                         mx = fminf(fminf(e4[0], e4[1]), fminf(e4[2], e4[3]));
                     }
-                    // (a scale of 0 would turn a hidden row's infinity into NaN)
-                    if (!Mod) mx = isinf(mx) && mul == 0.f ? -INFINITY : mx * mul;
+                    mx *= mul;
+                }
+                if constexpr (H == 2) {
+                    // with the row's other thread, which has read its scores too: P may go over them
+                    row_smem[exch] = mx;
+                    if (!meet()) break;
+                    mx = fmaxf(mx, row_smem[exch ^ kRows]);
                 }
                 const bool need = live && mx > m_used + kRescale;
                 const bool resc = __any_sync(0xffffffffu, need);
@@ -907,14 +969,22 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                 // before any of P(i) is released, since P.V(i) accumulates into it.
                 if (!first && resc) {
 #pragma unroll 1
-                    for (int c = 0; c < kHeadDim / 32; ++c) {
-                        uint32_t ov[32];
-                        tmem_ld32(tO(x) + lane_off + 32 * c, ov);
+                    for (int c = 0; c < kHeadDim / 16 / H; ++c) {       // few registers beside the scores
+                        const uint32_t o_addr = tO(x) + lane_off + kHeadDim / H * half + 16 * c;
+                        uint32_t ov[16];
+                        tmem_ld16(o_addr, ov);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-                        tmem_st32(tO(x) + lane_off + 32 * c, ov);
+                        for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                        tmem_st16(o_addr, ov);
                     }
+                    if (H == 2 && half == 1) tmem_wait_st();
+                }
+                // the products of the first 64 keys wait for this half of O as well
+                if (H == 2 && half == 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kPHalf + x));
                 }
                 // p = 2^(s * scale - m), rounded to the 16 bits that the tensor cores take beside V's
                 // (bf16 2^-8 of it at most, fp16, FP8 caches' type too, 2^-11; their sum is of the
@@ -924,26 +994,21 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                 const uint64_t scale2 = f2_pack(mul, mul);
                 const uint64_t negm2 = f2_pack(-m_at, -m_at);
 #pragma unroll
-                for (int c = 0; c < kKeys / 32; ++c) {
-                    uint32_t pw[16];
+                for (int c = 0; c < NC / 16; ++c) {
+                    uint32_t pw[8];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const int kk = 32 * c + e;
+                    for (int e = 0; e < 16; e += 2) {
+                        const int kk = 16 * c + e;
                         const uint64_t v = f2_pack(__uint_as_float(sv[kk]), __uint_as_float(sv[kk + 1]));
                         float a0, a1;
                         if constexpr (Mod) f2_unpack(f2_add(v, negm2), a0, a1);
                         else f2_unpack(f2_fma(v, scale2, negm2), a0, a1);
-                        float p0 = ex2_approx(a0);
-                        float p1 = ex2_approx(a1);
-                        if (need_mask) {
-                            p0 = vis[c] >> e & 1 ? p0 : 0.f;
-                            p1 = vis[c] >> (e + 1) & 1 ? p1 : 0.f;
-                        }
+                        const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);     // hidden: 0
                         sum2[(e >> 1) & 1] = f2_add(sum2[(e >> 1) & 1], f2_pack(p0, p1));
                         pw[e >> 1] = pack2<kMmaBf16>(p0, p1);
                     }
-                    tmem_st16(s_addr + 16 * c, pw);
-                    if (c == kKeys / 64 - 1) {
+                    tmem_st8(p_addr + 8 * c, pw);
+                    if (H == 1 && c == kKeys / 32 - 1) {
                         // the first 64 keys' P (and any rescale of O) is in tensor memory
                         tmem_wait_st();
                         tc_fence_before();
@@ -958,17 +1023,29 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                 l = l * alpha + ((s0 + s1) + (s2 + s3));
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(kPFull + x));
+                if (lane == 0) mbar_arrive(bar((half == H - 1 ? kPFull : kPHalf) + x));
             }
             // ---- the segment's outputs ----
-            if (!ok || !warp_wait(bar(kSegDone), (k - 1) & 1, p.timeout_ns)) {
+            if (!ok) break;
+            if constexpr (H == 2) {
+                if (warp_live) {                       // the row's sum
+                    row_smem[exch] = l;
+                    if (!meet()) break;
+                    const float l2 = row_smem[exch ^ kRows];
+                    l = half ? l2 + l : l + l2;
+                    if (solo && !meet()) break;        // both have read: the places are free
+                }
+            }
+            if (!warp_wait(bar(kSegDone), (k - 1) & 1, p.timeout_ns)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            const bool whole = g.flags & 2;
-            const size_t orow = (static_cast<size_t>(g.row0 + jq) * p.num_q_heads + head) * kHeadDim;
-            const size_t at_row = static_cast<size_t>(g.slot) * (2 * kRows) + (solo ? r : x * kRows + r);
+            const float vscale = kFp8 ? __ldg(p.v_scale + d[kSegHead] * p.scale_stride) : 1.0f;
+            const bool whole = d[kSegFlags] & 2;
+            const size_t slot = static_cast<size_t>(d[kSegSlot]);
+            const size_t orow = (static_cast<size_t>(d[kSegRow0] + (solo ? 0 : x * QT) + r / G) * p.num_q_heads + d[kSegHead] * G + r % G) * kHeadDim;
+            const int at_row = solo ? r : x * kRows + r;
             // 32 components from 32 c on: of the row itself, in whole sectors, or of its partial, in an
             // order in which a warp's rows lie side by side ([quad of components][row][4])
             auto put = [&](int c, const uint32_t (&ov)[32], float inv) {
@@ -988,7 +1065,7 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                         }
                     }
                 } else if (live) {
-                    float4* dst = p.partial + (static_cast<size_t>(g.slot) * 32 + 8 * c) * (2 * kRows) + (solo ? r : x * kRows + r);
+                    float4* dst = p.partial + (slot * 32 + 8 * c) * (2 * kRows) + at_row;
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         dst[e * 2 * kRows] = make_float4(__uint_as_float(ov[4 * e]), __uint_as_float(ov[4 * e + 1]),
@@ -996,6 +1073,7 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                 }
                 __syncwarp();
             };
+            float2* ml = p.ml + slot * (2 * kRows) + at_row;
             // A warp goes on to the next segment once all have seen this one's end: its products
             // (solo: also read by the other tile's warps) are overwritten, and no barrier can get
             // two phases ahead of a warp.
@@ -1005,34 +1083,38 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                 if (warp_live) {
                     const float inv = l == 0.f ? 0.f : vscale / l;
 #pragma unroll 1
-                    for (int c = 0; c < kHeadDim / 32; ++c) {
+                    for (int c = 4 / H * half; c < 4 / H * (half + 1); ++c) {
                         uint32_t ov[32];
                         tmem_ld32(tO(x) + lane_off + 32 * c, ov);
                         tmem_wait_ld();
                         put(c, ov, inv);
                     }
-                    if (!whole && live) p.ml[at_row] = make_float2(m_used, l);
+                    if (!whole && live && half == 0) *ml = make_float2(m_used, l);
                 }
             } else {
-                // A's steps and B's: both tiles hold the row in this lane; A's warps write its first
-                // 64 components, B's the others
-                ml_smem[x * kRows + r] = make_float2(m_used, l);
+                // A's steps and B's: both tiles hold the row in this lane; each of the row's 2 H threads
+                // writes its share of the components
+                if (half == 0) {
+                    row_smem[2 * x * kRows + r] = m_used;
+                    row_smem[(2 * x + 1) * kRows + r] = l;
+                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kMlReady));
-                if (!warp_wait(bar(kMlReady), solos & 1, p.timeout_ns)) {
+                if (!warp_wait(bar(kMlReady), par >> 1 & 1, p.timeout_ns)) {
                     ok = false;
                     break;
                 }
                 if (warp_live) {
-                    const float2 other = ml_smem[(1 - x) * kRows + r];
-                    const float m = fmaxf(m_used, other.x), m_at = m == -INFINITY ? 0.f : m;
-                    const float own_w = ex2_approx(m_used - m_at), other_w = ex2_approx(other.x - m_at);
-                    const float sum = l * own_w + other.y * other_w;
+                    const float ma = row_smem[r], la = row_smem[kRows + r];
+                    const float mb = row_smem[2 * kRows + r], lb = row_smem[3 * kRows + r];
+                    const float m = fmaxf(ma, mb), m_at = m == -INFINITY ? 0.f : m;
+                    const float wa = ex2_approx(ma - m_at), wb = ex2_approx(mb - m_at);
+                    const float sum = la * wa + lb * wb;
                     const float inv = sum == 0.f ? 0.f : vscale / sum;
-                    const float wa = x == 0 ? own_w : other_w, wb = x == 0 ? other_w : own_w;
-                    const bool two = g.steps > 1;       // else B has no products
+                    const bool two = d[kSegSteps] > 1;  // else B has no products
+                    const int share = x * H + half;
 #pragma unroll 1
-                    for (int c = 2 * x; c < 2 * x + 2; ++c) {
+                    for (int c = 2 / H * share; c < 2 / H * (share + 1); ++c) {
                         uint32_t ov[32];
                         tmem_ld32(tO(0) + lane_off + 32 * c, ov);
                         tmem_wait_ld();
@@ -1046,9 +1128,9 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                         }
                         put(c, ov, inv);
                     }
-                    if (!whole && live && x == 0) p.ml[at_row] = make_float2(m, sum);
+                    if (!whole && live && share == 0) *ml = make_float2(m, sum);
                 }
-                ++solos;
+                par ^= 2u;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kOFree));
@@ -1057,13 +1139,14 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                 ok = false;
                 break;
             }
+            if (lane == 0) mbar_arrive(bar(kSegEmpty + (k - 1) % kSegs));
         }
         if (!ok && lane == 0) atomicOr(p.status, kDevErrTimeout);
     } else {
         setmaxnreg_dec<C::kRegsFront>();
         // ================= FP8: e4m3 rows to fp16 tiles; thread = one key's row =================
         if constexpr (kFp8) {
-            const int row = (warp - 12) * 32 + lane;
+            const int row = (warp - 4 - C::kSoftmaxWarps) * 32 + lane;
             int r = 0;
             Seg g;
             while (ok && next_seg(g)) {
@@ -1080,7 +1163,7 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                     }
                     const int key0 = (g.step + i) * kKeys;
                     bool zero = false;
-                    if (is_v && edge_step(g, key0)) {
+                    if (is_v && edge_step(g.flags, g.tail, i)) {
                         zero = key0 + row < g.klo || key0 + row >= g.khi;
                         const int at = key0 + row - lane - g.ctx;        // of the warp's first key
                         if (at > -32 && key0 + kKeys > g.ctx) {
