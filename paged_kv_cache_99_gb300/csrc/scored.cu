@@ -46,6 +46,12 @@ constexpr uint32_t kHalfBytes = 16384;       // [128 rows][64 elements], 128-byt
 constexpr uint32_t kTileBytes = 2 * kHalfBytes;
 constexpr int kSegs = 4;                     // segments described ahead
 constexpr int kSegInts = 16;
+constexpr int kSoftmaxWarps = 16;            // 4 ..: two threads to a row of a tile
+constexpr int kWarps = 4 + kSoftmaxWarps;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kCols = kKeys / 2;             // a softmax thread's keys of a step
+// registers per thread at launch, and the shares of warps 0-3 and the softmax after setmaxnreg
+constexpr int kRegsLaunch = 96, kRegsFront = 64, kRegsSoftmax = 104;
 constexpr float kRescale = 8.0f;             // lazy rescale threshold (factor 256)
 constexpr float kCapSmall = 0.6f;            // |x / cap| up to which the tanh is a polynomial
 
@@ -53,32 +59,19 @@ template <int Kind>
 struct Cfg {
     static constexpr bool kFp8 = Kind == kKindFp8;
     static constexpr bool kMmaBf16 = Kind == kKindBf16;
-    static constexpr int kHalves = kFp8 ? 1 : 2;         // threads of a row
-    static constexpr int kCols = kKeys / kHalves;        // a thread's keys of a step
-    static constexpr int kSoftmaxWarps = 8 * kHalves;    // 4 ..
-    static constexpr int kWarps = 4 + kSoftmaxWarps + (kFp8 ? 4 : 0);
-    static constexpr int kStages = kFp8 ? 4 : 5;         // K and V tiles of 16-bit elements
-    static constexpr int kRaw = kFp8 ? 2 : 0;            // e4m3 tiles as copied
-    // launch registers per thread, and the shares after setmaxnreg
-    [[maybe_unused]] static constexpr int kRegsLaunch = kFp8 ? 128 : 96;
-    static constexpr int kRegsFront = 64;
-    static constexpr int kRegsSoftmax = kFp8 ? 192 : 104;
+    static constexpr int kStages = kFp8 ? 3 : 5;         // K and V tiles of 16-bit elements
+    static constexpr int kRaw = kFp8 ? 4 : 1;            // FP8: e4m3 tiles as copied
     static constexpr uint32_t kOffStage = 2 * kTileBytes;                    // behind Q_A, Q_B
     static constexpr uint32_t kOffRaw = kOffStage + kStages * kTileBytes;
-    static constexpr uint32_t kOffBars = kOffRaw + kRaw * kHalfBytes;
+    static constexpr uint32_t kOffBars = kOffRaw + (kFp8 ? kRaw * kHalfBytes : 0);
     static constexpr uint32_t kOffSegs = kOffBars + 480;
     static constexpr uint32_t kOffRow = kOffSegs + kSegs * kSegInts * 4;     // [tile][2][128] values of rows
     static constexpr uint32_t kOffScan = kOffRow + 4 * kRows * 4;            // [kWarps]
     static constexpr uint32_t kSmem = kOffScan + 96;
 };
 static_assert(kSegs * kSegInts * 4 % 16 == 0 && 480 % 16 == 0, "alignment");
-template <int Kind>
-constexpr bool regs_fit() {
-    using C = Cfg<Kind>;
-    return 32 * ((C::kWarps - C::kSoftmaxWarps) * C::kRegsFront + C::kSoftmaxWarps * C::kRegsSoftmax) <= 32 * C::kWarps * C::kRegsLaunch &&
-           32 * C::kWarps * C::kRegsLaunch <= 65536;
-}
-static_assert(regs_fit<kKindFp8>() && regs_fit<kKindBf16>(), "register split above the launch total");
+static_assert(32 * (4 * kRegsFront + kSoftmaxWarps * kRegsSoftmax) <= 32 * kWarps * kRegsLaunch &&
+                  32 * kWarps * kRegsLaunch <= 65536, "register split above the launch total");
 static_assert(Cfg<kKindBf16>::kSmem <= 232448 && Cfg<kKindFp8>::kSmem <= 232448, "shared memory");
 
 enum {                                       // barriers, 8 bytes each
@@ -211,19 +204,18 @@ enum {
     kSegHead, kSegRow0, kSegNq, kSegStep, kSegSteps, kSegKlo, kSegKhi,
     kSegCtx,                                 // tree: tokens before it, else INT_MAX
     kSegJ0, kSegTail, kSegQLen, kSegN, kSegPrefix,   // the unit's first query, see edge_step, the sequence
-    kSegSeq,
     kSegFlags,                               // 1: solo, 2: the whole unit, 4: the first step is an edge
     kSegSlot                                 // where its partial goes
 };
 
 struct Seg {
-    int h, row0, nq, step, steps, klo, khi, ctx, q_len, seq, tail, flags;
+    int h, row0, nq, step, steps, klo, khi, ctx, q_len, tail, flags;
 };
 
 __device__ __forceinline__ Seg read_seg(const int* d) {
     Seg g;
     g.h = d[kSegHead]; g.row0 = d[kSegRow0]; g.nq = d[kSegNq]; g.step = d[kSegStep]; g.steps = d[kSegSteps];
-    g.klo = d[kSegKlo]; g.khi = d[kSegKhi]; g.ctx = d[kSegCtx]; g.q_len = d[kSegQLen]; g.seq = d[kSegSeq];
+    g.klo = d[kSegKlo]; g.khi = d[kSegKhi]; g.ctx = d[kSegCtx]; g.q_len = d[kSegQLen];
     g.tail = d[kSegTail]; g.flags = d[kSegFlags];
     return g;
 }
@@ -231,6 +223,21 @@ __device__ __forceinline__ Seg read_seg(const int* d) {
 // Whether some of a segment's i-th step's V rows may be seen by no row: keys before the
 // unit's first, from step `tail` on keys behind its last or nodes of a tree.
 __device__ __forceinline__ bool edge_step(int flags, int tail, int i) { return (i == 0 && (flags & 4)) || i >= tail; }
+
+// The keys `at` .. at + 31 that some row of the segment's unit may see (by a whole warp).
+__device__ __forceinline__ uint32_t seen_keys(const ScoredParams& p, const Seg& g, int at, int lane) {
+    const int a = max(g.klo - at, 0), b = min(g.khi - at, 32);
+    uint32_t seen = b <= a ? 0u : (0xffffffffu << a) & (0xffffffffu >> (32 - b));
+    if (at + 32 > g.ctx) {
+        // nodes: those in some row's mask
+        uint32_t any = 0;
+        for (int j = lane; j < g.nq; j += 32)
+            any |= tree_bits(p.masks + static_cast<size_t>(g.row0 + j) * p.mask_words, g.q_len, at - g.ctx);
+        any = __reduce_or_sync(0xffffffffu, any);
+        seen &= any | (at < g.ctx ? (1u << (g.ctx - at)) - 1 : 0u);
+    }
+    return seen;
+}
 
 // Tile order in the ring: K0, K1, V0, K2, V1, K3, ...: each K two steps ahead of its use, V as
 // its step begins.
@@ -245,16 +252,14 @@ constexpr float kTanh0 = 0.999999926f, kTanh1 = -0.33332302f, kTanh2 = 0.1331006
 }  // namespace
 
 template <int Kind, bool QBf16, bool Mod>
-__global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     scored_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                   const __grid_constant__ CUtensorMap qmap, const ScoredParams p) {
     using C = Cfg<Kind>;
     constexpr bool kFp8 = C::kFp8;
     constexpr bool kMmaBf16 = C::kMmaBf16;
     constexpr int NS = C::kStages;
-    constexpr int kThreads = C::kWarps * 32;
-    constexpr int H = C::kHalves;
-    constexpr int kSegReaders = C::kWarps - 1;
+    constexpr int kSegReaders = kSoftmaxWarps + (kFp8 ? 3 : 2);      // and warps 1, 3, with FP8 caches 2
 
     extern __shared__ __align__(1024) uint8_t sm[];             // as the 128-byte swizzle wants it
     const uint32_t sbase = smem_addr(sm);
@@ -270,30 +275,30 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
     const int lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(bar(kFull + i), kFp8 ? 4 : 1);
+            mbar_init(bar(kFull + i), kFp8 ? 2 : 1);
             mbar_init(bar(kEmpty + i), 1);
             mbar_init(bar(kFixed + i), 1);
             mbar_init(bar(kIssued + i), 1);
         }
         for (int i = 0; i < C::kRaw; ++i) {
             mbar_init(bar(kRawFull + i), 1);
-            mbar_init(bar(kRawEmpty + i), 4);
+            mbar_init(bar(kRawEmpty + i), 2);
         }
         for (int i = 0; i < kSegs; ++i) {
             mbar_init(bar(kSegFull + i), 1);
             mbar_init(bar(kSegEmpty + i), kSegReaders);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(kQFull + i), 1);
+            mbar_init(bar(kQFull + i), kFp8 && QBf16 ? 2 : 1);
             mbar_init(bar(kQEmpty + i), 1);
             mbar_init(bar(kQLand + i), 1);
             mbar_init(bar(kSFull + i), 1);
-            mbar_init(bar(kPHalf + i), 4 * H);
+            mbar_init(bar(kPHalf + i), 8);
             mbar_init(bar(kPFull + i), 4);
         }
         mbar_init(bar(kSegDone), 1);
-        mbar_init(bar(kMlReady), C::kSoftmaxWarps);
-        mbar_init(bar(kOFree), C::kSoftmaxWarps);
+        mbar_init(bar(kMlReady), kSoftmaxWarps);
+        mbar_init(bar(kOFree), kSoftmaxWarps);
         for (int i = 0; i < 8; ++i) mbar_init(bar(kPair + i), 2);
         fence_barrier_init();
         tmap_prefetch(&kmap);
@@ -340,12 +345,12 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
         if (threadIdx.x == 0) p.records[cta].rows = 0;
         return;
     }
-    // ---- this CTA's range, found by warp 2 ----
+    // ---- this CTA's range, found by warp 0 ----
     int f = static_cast<int>(static_cast<long long>(T) * cta / W);
     int left = static_cast<int>(static_cast<long long>(T) * (cta + 1) / W) - f;
     int cs = 0, ct = 0, ch = 0, coff = 0;    // sequence, unit, head, place within the unit's cost
     SeqView sv_cur = {};
-    if (warp == 2) {
+    if (warp == 0) {
         int lo = 0, hi = B;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -404,35 +409,110 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
     };
 
     if (warp < 4) {
-        setmaxnreg_dec<C::kRegsFront>();
+        setmaxnreg_dec<kRegsFront>();
         if (warp == 0) {
-            // ================= K and V copies =================
+            // ================= the walk over the range, and its copies =================
             const int bsh = p.block_shift;
             const int rsh = min(bsh, 4);                          // log2 of a piece's rows
             const int per_step = kKeys >> rsh;                    // pieces per step: 8 or 16
+            if (lane == 0) p.records[cta].rows = 0;
             int r = 0;                                            // tiles copied so far
-            Seg g;
-            while (ok && next_seg(g)) {
-                const int32_t* bt = p.block_tables + static_cast<size_t>(g.seq) * p.max_blocks;
-                const int c_lo = g.klo >> rsh, c_hi = (g.khi - 1) >> rsh;     // pieces that hold keys
+            unsigned q_used = 0, q_par = 0;                       // bit b: the Q buffer was filled, parity of its releases
+            while (ok) {
+                // the range's part of the next unit, places [coff, coff + take) of its cost, of which
+                // the first `lead` stand for its start: steps [a, b)
+                Unit u = {};
+                SeqView sv = sv_cur;
+                int a = 0, steps = 0, seq = cs, head = ch, cost = 0, unit_f = f;
+                while (left > 0 && steps == 0) {
+                    u = unit_of(p, sv_cur, ct);
+                    const int lead = unit_lead(p, u);
+                    cost = u.steps + lead;
+                    const int take = min(left, cost - coff);
+                    a = max(coff - lead, 0);
+                    steps = max(coff + take - lead, 0) - a;       // 0: nothing but the start, the next CTA has the steps
+                    sv = sv_cur;
+                    seq = cs;
+                    head = ch;
+                    unit_f = f - coff;
+                    f += take;
+                    left -= take;
+                    coff = 0;
+                    if (left > 0 && ++ch == p.num_kv_heads) {
+                        ch = 0;
+                        if (++ct == units_per_head(p, sv_cur)) {
+                            ct = 0;
+                            do {
+                                sv_cur = seq_view(p, ++cs, false);
+                            } while (sv_cur.q_len == 0);
+                        }
+                    }
+                }
+                const bool solo = u.nq <= QT;
+                const int row0 = sv.q0 + u.ja, step0 = u.step0 + a;
+                int flags = solo ? 1 : 0, tail = 0;
+                // ---- its description ----
+                {
+                    const int sl = k % kSegs;
+                    if (k >= kSegs && !warp_wait(bar(kSegEmpty + sl), ((k / kSegs) - 1) & 1, p.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    ++k;
+                    const bool starts = a == 0, ends = a + steps == u.steps;
+                    const int ctx = p.masks ? sv.n - sv.q_len : INT_MAX;
+                    flags |= (starts && ends ? 2 : 0) | (step0 * kKeys < u.klo ? 4 : 0);
+                    // the first step that reaches behind the last key, or the first node
+                    tail = max(min(u.khi, ctx) / kKeys - step0, 0);
+                    if (lane == 0) {
+                        int* d = segs + sl * kSegInts;
+                        d[kSegHead] = head;
+                        d[kSegRow0] = row0;
+                        d[kSegNq] = u.nq;
+                        d[kSegStep] = step0;
+                        d[kSegSteps] = steps;
+                        d[kSegKlo] = u.klo;
+                        d[kSegKhi] = u.khi;
+                        d[kSegCtx] = ctx;
+                        d[kSegJ0] = u.ja;
+                        d[kSegTail] = tail;
+                        d[kSegQLen] = sv.q_len;
+                        d[kSegN] = sv.n;
+                        d[kSegPrefix] = sv.prefix;
+                        d[kSegFlags] = flags;
+                        // a partial that continues another CTA's unit goes to the CTA's first slot, one
+                        // that starts a unit to its second: the range has one of each at most
+                        d[kSegSlot] = 2 * cta + (starts ? 1 : 0);
+                        mbar_arrive(bar(kSegFull + sl));
+                    }
+                    if (steps == 0) break;                        // the range's end
+                    if (starts && !ends && lane == 0) {
+                        // the CTA whose range holds the unit's last step
+                        const int last = static_cast<int>(((static_cast<long long>(unit_f) + cost) * W - 1) / T);
+                        p.records[cta] = CombineRecord{u.nq * G, row0, head * G, solo ? 1 : 0, last, {0, 0, 0}};
+                    }
+                }
+                // ---- its copies ----
+                const int32_t* bt = p.block_tables + static_cast<size_t>(seq) * p.max_blocks;
+                const int c_lo = u.klo >> rsh, c_hi = (u.khi - 1) >> rsh;     // pieces that hold keys
                 // the lane's piece of a step: its row in the cache, -1 for none
                 auto entry = [&](int i) -> int {
-                    const int c = (g.step + i) * per_step + lane;
-                    if (i >= g.steps || lane >= per_step || c < c_lo || c > c_hi) return -1;
+                    const int c = (step0 + i) * per_step + lane;
+                    if (i >= steps || lane >= per_step || c < c_lo || c > c_hi) return -1;
                     const int key = c << rsh;
                     int phys = __ldg(bt + (key >> bsh));
                     if (static_cast<unsigned>(phys) >= static_cast<unsigned>(p.num_blocks)) {
                         atomicOr(p.status, kDevErrRange);
                         phys = 0;
                     }
-                    return ((phys * p.num_kv_heads + g.h) << bsh) + (key & (p.block_size - 1));
+                    return ((phys * p.num_kv_heads + head) << bsh) + (key & (p.block_size - 1));
                 };
                 auto copy = [&](const CUtensorMap* map, int y) {
                     constexpr int kRing = kFp8 ? C::kRaw : NS;
                     constexpr int kF = kFp8 ? static_cast<int>(kRawFull) : static_cast<int>(kFull);
                     constexpr int kE = kFp8 ? static_cast<int>(kRawEmpty) : static_cast<int>(kEmpty);
                     const int st = r % kRing;
-                    if (r >= kRing && !warp_wait(bar(kE + st), ((r / kRing) - 1) & 1, p.timeout_ns)) {
+                    if (!ok || (r >= kRing && !warp_wait(bar(kE + st), ((r / kRing) - 1) & 1, p.timeout_ns))) {
                         ok = false;
                         return;
                     }
@@ -451,18 +531,39 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                     }
                     ++r;
                 };
-                // K0, K1, then V(i), K(i + 2); the table's entries a step ahead of their use
-                int y0 = entry(0), y1 = entry(1);
+                // K0, the queries, K1, then V(i), K(i + 2); the table's entries ahead of their use
+                int y0 = entry(0), y1 = entry(1), y2 = entry(2);
                 copy(&kmap, y0);
-                if (ok && g.steps > 1) copy(&kmap, y1);
-                for (int i = 0; i < g.steps && ok; ++i) {
-                    const int y2 = entry(i + 2);
+                for (int x = 0; x < (solo ? 1 : 2) && ok; ++x) {
+                    // one copy of QT queries x G heads; those past the unit's are other rows or zeros and
+                    // end in rows of S that nothing reads
+                    const int b = solo ? (k - 1) & 1 : x;
+                    if (q_used >> b & 1) {
+                        if (!warp_wait(bar(kQEmpty + b), q_par >> b & 1, p.timeout_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        q_par ^= 1u << b;
+                    }
+                    q_used |= 1u << b;
+                    const uint32_t landed = bar((kFp8 && QBf16 ? kQLand : kQFull) + b), dst = sbase + b * kTileBytes;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(landed, static_cast<uint32_t>(QT * G) * 256);
+                        tma_load_3d(dst, &qmap, 0, head * G, row0 + x * QT, landed);
+                        tma_load_3d(dst + kHalfBytes, &qmap, 64, head * G, row0 + x * QT, landed);
+                    }
+                    __syncwarp();
+                }
+                if (steps > 1) copy(&kmap, y1);
+                for (int i = 0; i < steps && ok; ++i) {
+                    const int y3 = entry(i + 3);
                     copy(&vmap, y0);
                     // (the tile's barrier is in its phase from here until the zeroing is done)
-                    if (!kFp8 && ok && lane == 0 && edge_step(g.flags, g.tail, i)) mbar_arrive(bar(kIssued + (r - 1) % NS));
-                    if (ok && i + 2 < g.steps) copy(&kmap, y2);
+                    if (!kFp8 && ok && lane == 0 && edge_step(flags, tail, i)) mbar_arrive(bar(kIssued + (r - 1) % NS));
+                    if (i + 2 < steps) copy(&kmap, y2);
                     y0 = y1;
                     y1 = y2;
+                    y2 = y3;
                 }
             }
             if (!ok) {
@@ -486,26 +587,24 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                     return ok;
                 };
                 auto tile_ready = [&](int r) -> bool { return wait(bar(kFull + r % NS), (r / NS) & 1); };
+                // a tile's descriptor, and those of its parts by adding to the address field
                 auto issue_s = [&](int x, uint32_t qbase, int r) {
-                    const uint32_t kbase = stage(r);
+                    const uint64_t a = umma_desc_sw128(qbase, 16, 1024), b = umma_desc_sw128(stage(r), 16, 1024);
 #pragma unroll
                     for (int kk = 0; kk < kHeadDim / 16; ++kk) {
-                        const uint64_t a = umma_desc_sw128(qbase + (kk >> 2) * kHalfBytes + (kk & 3) * 32, 16, 1024);
-                        const uint64_t b = umma_desc_sw128(kbase + (kk >> 2) * kHalfBytes + (kk & 3) * 32, 16, 1024);
-                        umma_f16(tS(x), a, b, idS, kk > 0 ? 1u : 0u);
+                        const uint32_t at = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
+                        umma_f16(tS(x), a + at, b + at, idS, kk > 0 ? 1u : 0u);
                     }
                     umma_commit(bar(kSFull + x));
                 };
                 // P.V over the step's keys 64 half .. 64 half + 63
                 auto issue_pv = [&](int x, int r, int half, bool first) {
-                    const uint32_t vbase = stage(r);
+                    // V is MN-major: d-halves kHalfBytes apart, 16 keys = 2 KiB
+                    const uint64_t b = umma_desc_sw128(stage(r) + half * (kKeys / 32) * 2048, kHalfBytes, 1024);
 #pragma unroll
-                    for (int e = 0; e < kKeys / 32; ++e) {
-                        const int kk = half * (kKeys / 32) + e;
-                        // V is MN-major: d-halves kHalfBytes apart, 16 keys = 2 KiB
-                        const uint64_t b = umma_desc_sw128(vbase + kk * 2048, kHalfBytes, 1024);
-                        umma_f16_ts(tO(x), tS(x) + 8 * kk, b, idPV, (!first || kk > 0) ? 1u : 0u);
-                    }
+                    for (int e = 0; e < kKeys / 32; ++e)
+                        umma_f16_ts(tO(x), tS(x) + 8 * (half * (kKeys / 32) + e), b + (e * 2048 >> 4), idPV,
+                                    (!first || half > 0 || e > 0) ? 1u : 0u);
                 };
                 int r0 = 0, seg = 0;
                 // parities as bits: an array indexed at run time would live in local memory, whose
@@ -599,193 +698,151 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                 if (!ok) atomicOr(p.status, kDevErrTimeout);
             }
             __syncwarp();
-        } else if (warp == 2) {
-            // ================= the walk over the range =================
-            CombineRecord rec = {};
-            int seg = 0;
-            while (true) {
-                const int sl = seg % kSegs;
-                if (seg >= kSegs && !warp_wait(bar(kSegEmpty + sl), ((seg / kSegs) - 1) & 1, p.timeout_ns)) {
-                    if (lane == 0) atomicOr(p.status, kDevErrTimeout);
-                    break;
-                }
-                int* d = segs + sl * kSegInts;
-                if (left == 0) {
-                    if (lane == 0) {
-                        d[kSegSteps] = 0;
-                        mbar_arrive(bar(kSegFull + sl));
-                    }
-                    break;
-                }
-                // the range's part of the unit, places [coff, coff + take) of its cost, of which the
-                // first `lead` stand for its start: steps [a, b)
-                const Unit u = unit_of(p, sv_cur, ct);
-                const int lead = unit_lead(p, u), cost = u.steps + lead;
-                const int take = min(left, cost - coff);
-                const int a = max(coff - lead, 0), b = coff + take - lead;
-                const bool starts = a == 0, ends = b == u.steps;
-                const bool solo = u.nq <= QT;
-                const int unit_f = f - coff;
-                f += take;
-                left -= take;
-                coff = 0;
-                const int at_s = cs, at_h = ch;
-                const SeqView at_v = sv_cur;
-                if (left > 0 && ++ch == p.num_kv_heads) {
-                    ch = 0;
-                    if (++ct == units_per_head(p, sv_cur)) {
-                        ct = 0;
-                        do {
-                            sv_cur = seq_view(p, ++cs, false);
-                        } while (sv_cur.q_len == 0);
-                    }
-                }
-                if (b <= 0) continue;            // nothing but the start: the next CTA has the steps
-                if (lane == 0) {
-                    // a partial that continues another CTA's unit goes to the CTA's first slot,
-                    // one that starts a unit to its second: the range has one of each at most
-                    d[kSegHead] = at_h;
-                    d[kSegRow0] = at_v.q0 + u.ja;
-                    d[kSegNq] = u.nq;
-                    d[kSegStep] = u.step0 + a;
-                    d[kSegSteps] = b - a;
-                    d[kSegKlo] = u.klo;
-                    d[kSegKhi] = u.khi;
-                    d[kSegCtx] = p.masks ? at_v.n - at_v.q_len : INT_MAX;
-                    d[kSegJ0] = u.ja;
-                    {
-                        // the first step that reaches behind the last key, or the first node
-                        const int end = p.masks ? at_v.n - at_v.q_len : u.khi;
-                        d[kSegTail] = max(end / kKeys - u.step0 - a, 0);
-                    }
-                    d[kSegQLen] = at_v.q_len;
-                    d[kSegN] = at_v.n;
-                    d[kSegPrefix] = at_v.prefix;
-                    d[kSegSeq] = at_s;
-                    d[kSegFlags] = (solo ? 1 : 0) | (starts && ends ? 2 : 0) | ((u.step0 + a) * kKeys < u.klo ? 4 : 0);
-                    d[kSegSlot] = 2 * cta + (starts ? 1 : 0);
-                    mbar_arrive(bar(kSegFull + sl));
-                }
-                if (starts && !ends) {
-                    rec.rows = u.nq * G;
-                    rec.row0 = at_v.q0 + u.ja;
-                    rec.head0 = at_h * G;
-                    rec.solo = solo ? 1 : 0;
-                    // the CTA whose range holds the unit's last step
-                    rec.last = static_cast<int>(((static_cast<long long>(unit_f) + cost) * W - 1) / T);
-                }
-                ++seg;
-            }
-            if (lane == 0) p.records[cta] = rec;
-        } else {
-            // ================= queries, and V rows that no row sees =================
-            int r0 = 0;
-            unsigned q_used = 0, q_par = 0;          // bit b: the buffer was filled, parity of its releases
-            [[maybe_unused]] unsigned q_fills = 0;   // bit b: parity of its copies
-            unsigned issued = 0;                     // bit st: parity of the stage's edge copies
+        } else if (kFp8) {
+            // ================= FP8: e4m3 rows to fp16 tiles, two of a tile's rows a thread =================
+            const int part = warp - 2;
+            int r = 0;
+            [[maybe_unused]] unsigned q_fills = 0;   // bit b: parity of the Q buffer's copies
             Seg g;
             while (ok && next_seg(g)) {
                 const bool solo = g.flags & 1;
-                const int qb = solo ? (k - 1) & 1 : 0;
-                for (int x = 0; x < (solo ? 1 : 2) && ok; ++x) {
-                    const int b = solo ? qb : x;
-                    if (q_used >> b & 1) {
-                        if (!warp_wait(bar(kQEmpty + b), q_par >> b & 1, p.timeout_ns)) {
-                            ok = false;
-                            break;
-                        }
-                        q_par ^= 1u << b;
+                const int two = min(2, g.steps), both = 2 * max(g.steps - 2, 0);
+                for (int it = 0; it < 2 * g.steps && ok; ++it, ++r) {
+                    // the item's step, and whether it is V
+                    int i = it;
+                    bool is_v = false;
+                    if (it >= two) {
+                        const int e = it - two;
+                        is_v = e >= both || !(e & 1);
+                        i = (e < both ? e >> 1 : e - both / 2) + (is_v ? 0 : 2);
                     }
-                    q_used |= 1u << b;
-                    // one copy of QT queries x G heads; those past the unit's are other rows or zeros
-                    // and end in rows of S that nothing reads
-                    constexpr bool kWiden = kFp8 && QBf16;
-                    const uint32_t landed = bar((kWiden ? kQLand : kQFull) + b), dst = sbase + b * kTileBytes;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(landed, static_cast<uint32_t>(QT * G) * 256);
-                        tma_load_3d(dst, &qmap, 0, g.h * G, g.row0 + x * QT, landed);
-                        tma_load_3d(dst + kHalfBytes, &qmap, 64, g.h * G, g.row0 + x * QT, landed);
+                    uint32_t seen[2] = {0xffffffffu, 0xffffffffu};     // keys 32 (2 e + part) .. that some row sees
+                    const int key0 = (g.step + i) * kKeys;
+                    if (is_v && edge_step(g.flags, g.tail, i)) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) seen[e] = seen_keys(p, g, key0 + 32 * (2 * e + part), lane);
                     }
-                    __syncwarp();
-                    if constexpr (kWiden) {
-                        // bf16 to fp16, as the widened codes: exact for magnitudes 2^-14 to 65504, 2^-25
-                        // off below, infinite above
-                        if (!warp_wait(landed, q_fills >> b & 1, p.timeout_ns)) {
-                            ok = false;
-                            break;
-                        }
-                        q_fills ^= 1u << b;
-                        uint4* q = reinterpret_cast<uint4*>(sm + b * kTileBytes);
-                        const int chunks = min(QT, g.nq - x * QT) * G * 8;      // of 16 bytes, in each half
-                        for (int i = lane; i < chunks; i += 32) {
+                    const int rs = r % C::kRaw, st = r % NS;
+                    if (!warp_wait(bar(kRawFull + rs), (r / C::kRaw) & 1, p.timeout_ns) ||
+                        (r >= NS && !warp_wait(bar(kEmpty + st), ((r / NS) - 1) & 1, p.timeout_ns))) {
+                        ok = false;
+                        break;
+                    }
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        const int row = 32 * (2 * h + part) + lane;
+                        const uint8_t* src = sm + C::kOffRaw + rs * kHalfBytes + row * 128;
+                        uint8_t* dst = sm + C::kOffStage + st * kTileBytes;
+                        const bool zero = !((h ? seen[1] : seen[0]) >> lane & 1);
+#pragma unroll 1
+                        for (int q = 0; q < 2; ++q) {                  // 64 components: a d-half
+                            uint4 x4[4];
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                uint4& v = q[e * (kHalfBytes / 16) + i];
-                                uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                            for (int e = 0; e < 4; ++e)
+                                x4[e] = zero ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(src + (((4 * q + e) ^ (row & 7)) << 4));
 #pragma unroll
-                                for (int a = 0; a < 4; ++a)
-                                    w[a] = pack2<false>(to_float<true>(w[a] & 0xffffu), to_float<true>(w[a] >> 16));
-                                v = make_uint4(w[0], w[1], w[2], w[3]);
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t w[4] = {x4[e].x, x4[e].y, x4[e].z, x4[e].w};
+                                uint32_t f16[8];
+#pragma unroll
+                                for (int a = 0; a < 4; ++a) {
+                                    f16[2 * a] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[a] & 0xffffu));
+                                    f16[2 * a + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[a] >> 16));
+                                }
+                                *reinterpret_cast<uint4*>(dst + q * kHalfBytes + sw128_offset(row, 16 * e)) = make_uint4(f16[0], f16[1], f16[2], f16[3]);
+                                *reinterpret_cast<uint4*>(dst + q * kHalfBytes + sw128_offset(row, 16 * e + 8)) = make_uint4(f16[4], f16[5], f16[6], f16[7]);
                             }
                         }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(kQFull + b));
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bar(kFull + st));
+                        mbar_arrive(bar(kRawEmpty + rs));
+                    }
+                    if constexpr (QBf16) {
+                        // behind the first K tile the queries, bf16 to fp16 as the widened codes: exact for
+                        // magnitudes 2^-14 to 65504, 2^-25 off below, infinite above
+                        for (int x = 0; x < (solo ? 1 : 2) && it == 0; ++x) {
+                            const int b = solo ? (k - 1) & 1 : x;
+                            if (!warp_wait(bar(kQLand + b), q_fills >> b & 1, p.timeout_ns)) {
+                                ok = false;
+                                break;
+                            }
+                            q_fills ^= 1u << b;
+                            uint4* q = reinterpret_cast<uint4*>(sm + b * kTileBytes);
+                            const int chunks = min(QT, g.nq - x * QT) * G * 8;      // of 16 bytes, in each half
+#pragma unroll 1
+                            for (int c0 = 32 * part + lane; c0 < chunks; c0 += 2 * 64) {
+                                uint4 v[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const int c = c0 + 64 * (e >> 1);
+                                    if (c < chunks) v[e] = q[(e & 1) * (kHalfBytes / 16) + c];
+                                }
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const int c = c0 + 64 * (e >> 1);
+                                    uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
+#pragma unroll
+                                    for (int a = 0; a < 4; ++a)
+                                        w[a] = pack2<false>(to_float<true>(w[a] & 0xffffu), to_float<true>(w[a] >> 16));
+                                    if (c < chunks) q[(e & 1) * (kHalfBytes / 16) + c] = make_uint4(w[0], w[1], w[2], w[3]);
+                                }
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(bar(kQFull + b));
+                        }
                     }
                 }
-                if constexpr (!kFp8) {
-                    for (int i = 0; i < g.steps && ok; ++i) {
-                        const int key0 = (g.step + i) * kKeys;
-                        if (!edge_step(g.flags, g.tail, i)) continue;
-                        const int r = r0 + item_v(g.steps, i);
-                        // nodes that some row of the unit sees (lane w: keys 32 w .. of the step)
-                        uint32_t seen[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
-                        if (key0 + kKeys > g.ctx) {
+            }
+            if (!ok && lane == 0) atomicOr(p.status, kDevErrTimeout);
+        } else if (warp == 3) {
+            // ================= 16-bit caches: V rows that no row sees =================
+            int r0 = 0;
+            unsigned issued = 0;                     // bit st: parity of the stage's edge copies
+            Seg g;
+            while (ok && next_seg(g)) {
+                for (int i = 0; i < g.steps && ok; ++i) {
+                    const int key0 = (g.step + i) * kKeys;
+                    if (!edge_step(g.flags, g.tail, i)) continue;
+                    const int r = r0 + item_v(g.steps, i);
+                    uint32_t seen[4];
 #pragma unroll
-                            for (int w = 0; w < 4; ++w) {
-                                const int at = key0 + 32 * w - g.ctx;
-                                uint32_t any = 0;
-                                if (at > -32 && at < g.q_len)
-                                    for (int j = lane; j < g.nq; j += 32)
-                                        any |= tree_bits(p.masks + static_cast<size_t>(g.row0 + j) * p.mask_words, g.q_len, at);
-                                any = __reduce_or_sync(0xffffffffu, any);
-                                // tokens before the tree
-                                seen[w] = at >= 0 ? any : at <= -32 ? 0xffffffffu : any | ((1u << -at) - 1);
-                            }
-                        }
-                        // not before its copy is issued: the stage may still be a phase or two behind
-                        if (!warp_wait(bar(kIssued + r % NS), issued >> (r % NS) & 1, p.timeout_ns) ||
-                            !warp_wait(bar(kFull + r % NS), (r / NS) & 1, p.timeout_ns)) {
-                            ok = false;
-                            break;
-                        }
-                        issued ^= 1u << (r % NS);
-                        uint8_t* vst = sm + C::kOffStage + (r % NS) * kTileBytes;
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            const int row = 32 * w + lane;
-                            if (key0 + row >= g.klo && key0 + row < g.khi && (seen[w] >> lane & 1)) continue;
-#pragma unroll
-                            for (int c = 0; c < 8; ++c) {
-                                *reinterpret_cast<uint4*>(vst + row * 128 + 16 * c) = make_uint4(0, 0, 0, 0);
-                                *reinterpret_cast<uint4*>(vst + kHalfBytes + row * 128 + 16 * c) = make_uint4(0, 0, 0, 0);
-                            }
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(kFixed + r % NS));
+                    for (int w = 0; w < 4; ++w) seen[w] = seen_keys(p, g, key0 + 32 * w, lane);
+                    // not before its copy is issued: the stage may still be a phase or two behind
+                    if (!warp_wait(bar(kIssued + r % NS), issued >> (r % NS) & 1, p.timeout_ns) ||
+                        !warp_wait(bar(kFull + r % NS), (r / NS) & 1, p.timeout_ns)) {
+                        ok = false;
+                        break;
                     }
+                    issued ^= 1u << (r % NS);
+                    uint8_t* vst = sm + C::kOffStage + (r % NS) * kTileBytes;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const int row = 32 * w + lane;
+                        if (seen[w] >> lane & 1) continue;
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            *reinterpret_cast<uint4*>(vst + row * 128 + 16 * c) = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4*>(vst + kHalfBytes + row * 128 + 16 * c) = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kFixed + r % NS));
                 }
                 r0 += 2 * g.steps;
             }
             if (!ok && lane == 0) atomicOr(p.status, kDevErrTimeout);
         }
-    } else if (warp < 4 + C::kSoftmaxWarps) {
-        setmaxnreg_inc<C::kRegsSoftmax>();
-        // ================= softmax: tile A's warps, then tile B's; H threads for a row =================
-        constexpr int NC = C::kCols;
-        const int x = (warp - 4) / (4 * H);
-        const int half = (warp - 4) / 4 % H;           // the thread's keys of a step: NC half ..
+    } else {
+        setmaxnreg_inc<kRegsSoftmax>();
+        // ================= softmax: tile A's warps, then tile B's; two threads to a row =================
+        constexpr int NC = kCols;
+        const int x = (warp - 4) / 8;
+        const int half = (warp - 4) / 4 % 2;           // the thread's keys of a step: NC half ..
         const int quarter = warp & 3;                  // tensor-memory lanes 32 quarter .. + 31
         const int r = quarter * 32 + lane;
         const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
@@ -843,7 +900,7 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                 if (!warp_live) {                       // rows past the unit's: nothing reads their P
                     if (lane == 0) {
                         mbar_arrive(bar(kPHalf + x));
-                        if (half == H - 1) mbar_arrive(bar(kPFull + x));
+                        if (half) mbar_arrive(bar(kPFull + x));
                     }
                     continue;
                 }
@@ -952,12 +1009,10 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                     }
                     mx *= mul;
                 }
-                if constexpr (H == 2) {
-                    // with the row's other thread, which has read its scores too: P may go over them
-                    row_smem[exch] = mx;
-                    if (!meet()) break;
-                    mx = fmaxf(mx, row_smem[exch ^ kRows]);
-                }
+                // with the row's other thread, which has read its scores too: P may go over them
+                row_smem[exch] = mx;
+                if (!meet()) break;
+                mx = fmaxf(mx, row_smem[exch ^ kRows]);
                 const bool need = live && mx > m_used + kRescale;
                 const bool resc = __any_sync(0xffffffffu, need);
                 const float m_new = need ? mx : m_used;
@@ -969,8 +1024,8 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                 // before any of P(i) is released, since P.V(i) accumulates into it.
                 if (!first && resc) {
 #pragma unroll 1
-                    for (int c = 0; c < kHeadDim / 16 / H; ++c) {       // few registers beside the scores
-                        const uint32_t o_addr = tO(x) + lane_off + kHeadDim / H * half + 16 * c;
+                    for (int c = 0; c < kHeadDim / 32; ++c) {       // few registers beside the scores
+                        const uint32_t o_addr = tO(x) + lane_off + kHeadDim / 2 * half + 16 * c;
                         uint32_t ov[16];
                         tmem_ld16(o_addr, ov);
                         tmem_wait_ld();
@@ -978,10 +1033,10 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                         for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
                         tmem_st16(o_addr, ov);
                     }
-                    if (H == 2 && half == 1) tmem_wait_st();
+                    if (half == 1) tmem_wait_st();
                 }
                 // the products of the first 64 keys wait for this half of O as well
-                if (H == 2 && half == 1) {
+                if (half == 1) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(kPHalf + x));
@@ -1008,13 +1063,6 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                         pw[e >> 1] = pack2<kMmaBf16>(p0, p1);
                     }
                     tmem_st8(p_addr + 8 * c, pw);
-                    if (H == 1 && c == kKeys / 32 - 1) {
-                        // the first 64 keys' P (and any rescale of O) is in tensor memory
-                        tmem_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(kPHalf + x));
-                    }
                 }
                 tmem_wait_st();
                 float s0, s1, s2, s3;
@@ -1023,18 +1071,16 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                 l = l * alpha + ((s0 + s1) + (s2 + s3));
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar((half == H - 1 ? kPFull : kPHalf) + x));
+                if (lane == 0) mbar_arrive(bar((half ? kPFull : kPHalf) + x));
             }
             // ---- the segment's outputs ----
             if (!ok) break;
-            if constexpr (H == 2) {
-                if (warp_live) {                       // the row's sum
-                    row_smem[exch] = l;
-                    if (!meet()) break;
-                    const float l2 = row_smem[exch ^ kRows];
-                    l = half ? l2 + l : l + l2;
-                    if (solo && !meet()) break;        // both have read: the places are free
-                }
+            if (warp_live) {                           // the row's sum
+                row_smem[exch] = l;
+                if (!meet()) break;
+                const float l2 = row_smem[exch ^ kRows];
+                l = half ? l2 + l : l + l2;
+                if (solo && !meet()) break;            // both have read: the places are free
             }
             if (!warp_wait(bar(kSegDone), (k - 1) & 1, p.timeout_ns)) {
                 ok = false;
@@ -1083,7 +1129,7 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                 if (warp_live) {
                     const float inv = l == 0.f ? 0.f : vscale / l;
 #pragma unroll 1
-                    for (int c = 4 / H * half; c < 4 / H * (half + 1); ++c) {
+                    for (int c = 2 * half; c < 2 * half + 2; ++c) {
                         uint32_t ov[32];
                         tmem_ld32(tO(x) + lane_off + 32 * c, ov);
                         tmem_wait_ld();
@@ -1092,8 +1138,8 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                     if (!whole && live && half == 0) *ml = make_float2(m_used, l);
                 }
             } else {
-                // A's steps and B's: both tiles hold the row in this lane; each of the row's 2 H threads
-                // writes its share of the components
+                // A's steps and B's: both tiles hold the row in this lane; each of the row's four threads
+                // writes a quarter of the components
                 if (half == 0) {
                     row_smem[2 * x * kRows + r] = m_used;
                     row_smem[(2 * x + 1) * kRows + r] = l;
@@ -1112,23 +1158,20 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
                     const float sum = la * wa + lb * wb;
                     const float inv = sum == 0.f ? 0.f : vscale / sum;
                     const bool two = d[kSegSteps] > 1;  // else B has no products
-                    const int share = x * H + half;
-#pragma unroll 1
-                    for (int c = 2 / H * share; c < 2 / H * (share + 1); ++c) {
-                        uint32_t ov[32];
-                        tmem_ld32(tO(0) + lane_off + 32 * c, ov);
+                    const int c = 2 * x + half;
+                    uint32_t ov[32];
+                    tmem_ld32(tO(0) + lane_off + 32 * c, ov);
+                    tmem_wait_ld();
+                    if (two) {
+                        uint32_t ob[32];
+                        tmem_ld32(tO(1) + lane_off + 32 * c, ob);
                         tmem_wait_ld();
-                        if (two) {
-                            uint32_t ob[32];
-                            tmem_ld32(tO(1) + lane_off + 32 * c, ob);
-                            tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                ov[e] = __float_as_uint(fmaf(__uint_as_float(ov[e]), wa, __uint_as_float(ob[e]) * wb));
-                        }
-                        put(c, ov, inv);
+                        for (int e = 0; e < 32; ++e)
+                            ov[e] = __float_as_uint(fmaf(__uint_as_float(ov[e]), wa, __uint_as_float(ob[e]) * wb));
                     }
-                    if (!whole && live && share == 0) *ml = make_float2(m, sum);
+                    put(c, ov, inv);
+                    if (!whole && live && c == 0) *ml = make_float2(m, sum);
                 }
                 par ^= 2u;
                 tc_fence_before();
@@ -1142,73 +1185,6 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
             if (lane == 0) mbar_arrive(bar(kSegEmpty + (k - 1) % kSegs));
         }
         if (!ok && lane == 0) atomicOr(p.status, kDevErrTimeout);
-    } else {
-        setmaxnreg_dec<C::kRegsFront>();
-        // ================= FP8: e4m3 rows to fp16 tiles; thread = one key's row =================
-        if constexpr (kFp8) {
-            const int row = (warp - 4 - C::kSoftmaxWarps) * 32 + lane;
-            int r = 0;
-            Seg g;
-            while (ok && next_seg(g)) {
-                for (int it = 0; it < 2 * g.steps && ok; ++it, ++r) {
-                    // the item's step, and whether it is V
-                    const int two = min(2, g.steps);
-                    int i = it;
-                    bool is_v = false;
-                    if (it >= two) {
-                        const int e = it - two, both = 2 * max(g.steps - 2, 0);
-                        i = e < both ? e >> 1 : e - both / 2;
-                        is_v = e >= both || !(e & 1);
-                        if (!is_v) i += 2;
-                    }
-                    const int key0 = (g.step + i) * kKeys;
-                    bool zero = false;
-                    if (is_v && edge_step(g.flags, g.tail, i)) {
-                        zero = key0 + row < g.klo || key0 + row >= g.khi;
-                        const int at = key0 + row - lane - g.ctx;        // of the warp's first key
-                        if (at > -32 && key0 + kKeys > g.ctx) {
-                            uint32_t any = 0;
-                            for (int j = lane; j < g.nq; j += 32)
-                                any |= tree_bits(p.masks + static_cast<size_t>(g.row0 + j) * p.mask_words, g.q_len, at);
-                            any = __reduce_or_sync(0xffffffffu, any);
-                            if (at + lane >= 0 && !(any >> lane & 1)) zero = true;
-                        }
-                    }
-                    const int rs = r % C::kRaw, st = r % NS;
-                    if (!warp_wait(bar(kRawFull + rs), (r / C::kRaw) & 1, p.timeout_ns) ||
-                        (r >= NS && !warp_wait(bar(kEmpty + st), ((r / NS) - 1) & 1, p.timeout_ns))) {
-                        ok = false;
-                        break;
-                    }
-                    const uint8_t* src = sm + C::kOffRaw + rs * kHalfBytes + row * 128;
-                    uint8_t* dst = sm + C::kOffStage + st * kTileBytes;
-                    uint4 x8[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        x8[e] = zero ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(src + ((e ^ (row & 7)) << 4));
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const uint32_t w[4] = {x8[e].x, x8[e].y, x8[e].z, x8[e].w};
-                        uint32_t h[8];
-#pragma unroll
-                        for (int a = 0; a < 4; ++a) {
-                            h[2 * a] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[a] & 0xffffu));
-                            h[2 * a + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[a] >> 16));
-                        }
-                        uint8_t* d = dst + (e >> 2) * kHalfBytes;
-                        *reinterpret_cast<uint4*>(d + sw128_offset(row, 16 * (e & 3))) = make_uint4(h[0], h[1], h[2], h[3]);
-                        *reinterpret_cast<uint4*>(d + sw128_offset(row, 16 * (e & 3) + 8)) = make_uint4(h[4], h[5], h[6], h[7]);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(bar(kFull + st));
-                        mbar_arrive(bar(kRawEmpty + rs));
-                    }
-                }
-            }
-            if (!ok && lane == 0) atomicOr(p.status, kDevErrTimeout);
-        }
     }
 
     // ---- teardown ----
@@ -1224,7 +1200,7 @@ __global__ void __launch_bounds__(Cfg<Kind>::kWarps * 32, 1)
 //   out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,   M = max_i m_i,
 // over the partials (o_i, m_i in log2 units, l_i).  CTA (w, y) takes parts of the unit that main
 // CTA w began and did not finish; its partials lie in w's second slot and in the first slots of
-// the CTAs behind it up to `last`.  A part is up to 32 rows and four quads of their components;
+// the CTAs behind it up to `last`.  A part is up to 32 rows and 4 or 8 quads of their components;
 // the threads that are left when the rows are few share out the partials, and their sums meet
 // in shared memory.
 template <bool OutBf16, bool Fp8>
@@ -1241,12 +1217,13 @@ __global__ void __launch_bounds__(256) scored_combine_kernel(const ScoredParams 
     // threads: row (a power of two of them up to 32) x 4 quads x share of the partials
     int shift = 0;
     while (shift < 5 && (1 << shift) < rec.rows) ++shift;
-    const int row = threadIdx.x & ((1 << shift) - 1), quad = threadIdx.x >> shift & 3, share = threadIdx.x >> (shift + 2);
-    const int shares = 64 >> shift;
-    const int tasks = ((rec.rows + (1 << shift) - 1) >> shift) * 8;
+    const int qs = parts <= 8 && shift == 5 ? 3 : 2;         // 8 quads where nothing is left to share out
+    const int row = threadIdx.x & ((1 << shift) - 1), quad = threadIdx.x >> shift & ((1 << qs) - 1);
+    const int share = threadIdx.x >> (shift + qs), shares = 256 >> (shift + qs);
+    const int tasks = ((rec.rows + (1 << shift) - 1) >> shift) * (32 >> qs);
     for (int task = blockIdx.y; task < tasks; task += gridDim.y) {
-        const int i = ((task >> 3) << shift) + row;
-        const int q4 = (task & 7) * 4 + quad;
+        const int i = ((task >> (5 - qs)) << shift) + row;
+        const int q4 = ((task & ((32 >> qs) - 1)) << qs) + quad;
         const bool live = i < rec.rows;
         const int query = i / G;
         const int at = rec.solo ? i : (query / QT) * kRows + (query % QT) * G + i % G;
@@ -1285,7 +1262,7 @@ __global__ void __launch_bounds__(256) scored_combine_kernel(const ScoredParams 
             __syncthreads();
             if (share == 0)
                 for (int e = 1; e < min(shares, parts); ++e)
-                    fold(ml_smem[threadIdx.x + (e << (shift + 2))], acc_smem[threadIdx.x + (e << (shift + 2))]);
+                    fold(ml_smem[threadIdx.x + (e << (shift + qs))], acc_smem[threadIdx.x + (e << (shift + qs))]);
         }
         if (live && share == 0) {
             const int head = rec.head0 + i % G;
@@ -1344,7 +1321,7 @@ cudaError_t launch_scored(CacheKind kind, bool q_bf16, bool mod, const CUtensorM
                           const CUtensorMap& qmap, const ScoredParams& p, int sms, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(sms));
-    cfg.blockDim = dim3(static_cast<unsigned>(32 * (kind == kKindFp8 ? Cfg<kKindFp8>::kWarps : Cfg<kKindBf16>::kWarps)));
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = scored_smem(kind);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -1359,7 +1336,7 @@ cudaError_t launch_scored(CacheKind kind, bool q_bf16, bool mod, const CUtensorM
 
 cudaError_t launch_scored_combine(bool out_bf16, bool fp8, const ScoredParams& p, int sms, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(sms), 8);
+    cfg.gridDim = dim3(static_cast<unsigned>(sms), 16);
     cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
