@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // every role follows the segments in order
     int k = 0;                               // segments taken so far
     auto next_seg = [&](Seg& g) -> bool {
-        if (!warp_wait(bar(kSegFull + k % kSegs), (k / kSegs) & 1, p.timeout_ns)) {
+        if (!warp_wait_all(bar(kSegFull + k % kSegs), (k / kSegs) & 1, p.timeout_ns)) {
             ok = false;
             return false;
         }
@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // ---- its description ----
                 {
                     const int sl = k % kSegs;
-                    if (k >= kSegs && !warp_wait(bar(kSegEmpty + sl), ((k / kSegs) - 1) & 1, p.timeout_ns)) {
+                    if (k >= kSegs && !warp_wait_all(bar(kSegEmpty + sl), ((k / kSegs) - 1) & 1, p.timeout_ns)) {
                         ok = false;
                         break;
                     }
@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     constexpr int kF = kFp8 ? static_cast<int>(kRawFull) : static_cast<int>(kFull);
                     constexpr int kE = kFp8 ? static_cast<int>(kRawEmpty) : static_cast<int>(kEmpty);
                     const int st = r % kRing;
-                    if (!ok || (r >= kRing && !warp_wait(bar(kE + st), ((r / kRing) - 1) & 1, p.timeout_ns))) {
+                    if (!ok || (r >= kRing && !warp_wait_all(bar(kE + st), ((r / kRing) - 1) & 1, p.timeout_ns))) {
                         ok = false;
                         return;
                     }
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // end in rows of S that nothing reads
                     const int b = solo ? (k - 1) & 1 : x;
                     if (q_used >> b & 1) {
-                        if (!warp_wait(bar(kQEmpty + b), q_par >> b & 1, p.timeout_ns)) {
+                        if (!warp_wait_all(bar(kQEmpty + b), q_par >> b & 1, p.timeout_ns)) {
                             ok = false;
                             break;
                         }
@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // let the copies still in flight land before the CTA leaves
                 constexpr int kRing = kFp8 ? C::kRaw : NS;
                 constexpr int kF = kFp8 ? static_cast<int>(kRawFull) : static_cast<int>(kFull);
-                for (int i = max(0, r - kRing); i < r; ++i) warp_wait(bar(kF + i % kRing), (i / kRing) & 1, p.timeout_ns);
+                for (int i = max(0, r - kRing); i < r; ++i) warp_wait_all(bar(kF + i % kRing), (i / kRing) & 1, p.timeout_ns);
             }
         } else if (warp == 1) {
             // ================= MMA issuer =================
@@ -723,8 +723,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int e = 0; e < 2; ++e) seen[e] = seen_keys(p, g, key0 + 32 * (2 * e + part), lane);
                     }
                     const int rs = r % C::kRaw, st = r % NS;
-                    if (!warp_wait(bar(kRawFull + rs), (r / C::kRaw) & 1, p.timeout_ns) ||
-                        (r >= NS && !warp_wait(bar(kEmpty + st), ((r / NS) - 1) & 1, p.timeout_ns))) {
+                    if (!warp_wait_all(bar(kRawFull + rs), (r / C::kRaw) & 1, p.timeout_ns) ||
+                        (r >= NS && !warp_wait_all(bar(kEmpty + st), ((r / NS) - 1) & 1, p.timeout_ns))) {
                         ok = false;
                         break;
                     }
@@ -765,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // magnitudes 2^-14 to 65504, 2^-25 off below, infinite above
                         for (int x = 0; x < (solo ? 1 : 2) && it == 0; ++x) {
                             const int b = solo ? (k - 1) & 1 : x;
-                            if (!warp_wait(bar(kQLand + b), q_fills >> b & 1, p.timeout_ns)) {
+                            if (!warp_wait_all(bar(kQLand + b), q_fills >> b & 1, p.timeout_ns)) {
                                 ok = false;
                                 break;
                             }
@@ -812,8 +812,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int w = 0; w < 4; ++w) seen[w] = seen_keys(p, g, key0 + 32 * w, lane);
                     // not before its copy is issued: the stage may still be a phase or two behind
-                    if (!warp_wait(bar(kIssued + r % NS), issued >> (r % NS) & 1, p.timeout_ns) ||
-                        !warp_wait(bar(kFull + r % NS), (r / NS) & 1, p.timeout_ns)) {
+                    if (!warp_wait_all(bar(kIssued + r % NS), issued >> (r % NS) & 1, p.timeout_ns) ||
+                        !warp_wait_all(bar(kFull + r % NS), (r / NS) & 1, p.timeout_ns)) {
                         ok = false;
                         break;
                     }
@@ -853,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto meet = [&]() -> bool {                    // both threads of the row
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kPair + 4 * x + quarter));
-            if (!warp_wait(bar(kPair + 4 * x + quarter), par >> 2 & 1, p.timeout_ns)) ok = false;
+            if (!warp_wait_all(bar(kPair + 4 * x + quarter), par >> 2 & 1, p.timeout_ns)) ok = false;
             par ^= 4u;
             return ok;
         };
@@ -861,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // L1 that is left): a segment's fields are read from shared memory where they are used,
         // and its slot is given back when its outputs are written.
         while (ok) {
-            if (!warp_wait(bar(kSegFull + k % kSegs), (k / kSegs) & 1, p.timeout_ns)) {
+            if (!warp_wait_all(bar(kSegFull + k % kSegs), (k / kSegs) & 1, p.timeout_ns)) {
                 ok = false;
                 break;
             }
@@ -892,7 +892,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool first = true;
             for (int left_steps = solo ? (d[kSegSteps] + 1 - x) >> 1 : d[kSegSteps]; left_steps > 0;
                  --left_steps, key0 += stride * kKeys, first = false) {
-                if (!warp_wait(bar(kSFull + x), par & 1, p.timeout_ns)) {
+                if (!warp_wait_all(bar(kSFull + x), par & 1, p.timeout_ns)) {
                     ok = false;
                     break;
                 }
@@ -1082,7 +1082,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l = half ? l2 + l : l + l2;
                 if (solo && !meet()) break;            // both have read: the places are free
             }
-            if (!warp_wait(bar(kSegDone), (k - 1) & 1, p.timeout_ns)) {
+            if (!warp_wait_all(bar(kSegDone), (k - 1) & 1, p.timeout_ns)) {
                 ok = false;
                 break;
             }
@@ -1146,7 +1146,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kMlReady));
-                if (!warp_wait(bar(kMlReady), par >> 1 & 1, p.timeout_ns)) {
+                if (!warp_wait_all(bar(kMlReady), par >> 1 & 1, p.timeout_ns)) {
                     ok = false;
                     break;
                 }
@@ -1178,7 +1178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kOFree));
             }
-            if (!warp_wait(bar(kOFree), (k - 1) & 1, p.timeout_ns)) {
+            if (!warp_wait_all(bar(kOFree), (k - 1) & 1, p.timeout_ns)) {
                 ok = false;
                 break;
             }
