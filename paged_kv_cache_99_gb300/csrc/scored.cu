@@ -239,6 +239,12 @@ __device__ __forceinline__ uint32_t seen_keys(const ScoredParams& p, const Seg& 
     return seen;
 }
 
+// Four e4m3 codes to fp16, exactly (free to be scheduled: the two warps that widen live by it).
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(w));
+}
+
 // Tile order in the ring: K0, K1, V0, K2, V1, K3, ...: each K two steps ahead of its use, V as
 // its step begins.
 __device__ __forceinline__ int item_v(int steps, int i) { return min(2, steps) + i + min(i, max(steps - 2, 0)); }
@@ -728,30 +734,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = false;
                         break;
                     }
+                    // a row's eight 16-byte chunks are read and its sixteen written at places that differ
+                    // from row to row by an exclusive or with the row's low bits
 #pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
                         const int row = 32 * (2 * h + part) + lane;
-                        const uint8_t* src = sm + C::kOffRaw + rs * kHalfBytes + row * 128;
-                        uint8_t* dst = sm + C::kOffStage + st * kTileBytes;
-                        const bool zero = !((h ? seen[1] : seen[0]) >> lane & 1);
-#pragma unroll 1
-                        for (int q = 0; q < 2; ++q) {                  // 64 components: a d-half
-                            uint4 x4[4];
+                        const uint32_t swz = (row & 7) << 4;
+                        const uint32_t src = sbase + C::kOffRaw + rs * kHalfBytes + row * 128;
+                        const uint32_t dst = stage(r) + row * 128;
+                        uint4 x8[8];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                x4[e] = zero ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(src + (((4 * q + e) ^ (row & 7)) << 4));
+                        for (int e = 0; e < 8; ++e) x8[e] = ld_shared_16(src + ((e << 4) ^ swz));
+                        if (!((h ? seen[1] : seen[0]) >> lane & 1)) {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const uint32_t w[4] = {x4[e].x, x4[e].y, x4[e].z, x4[e].w};
-                                uint32_t f16[8];
+                            for (int e = 0; e < 8; ++e) x8[e] = make_uint4(0, 0, 0, 0);
+                        }
 #pragma unroll
-                                for (int a = 0; a < 4; ++a) {
-                                    f16[2 * a] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[a] & 0xffffu));
-                                    f16[2 * a + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[a] >> 16));
-                                }
-                                *reinterpret_cast<uint4*>(dst + q * kHalfBytes + sw128_offset(row, 16 * e)) = make_uint4(f16[0], f16[1], f16[2], f16[3]);
-                                *reinterpret_cast<uint4*>(dst + q * kHalfBytes + sw128_offset(row, 16 * e + 8)) = make_uint4(f16[4], f16[5], f16[6], f16[7]);
-                            }
+                        for (int e = 0; e < 8; ++e) {
+                            const uint32_t w[4] = {x8[e].x, x8[e].y, x8[e].z, x8[e].w};
+                            uint32_t f16[8];
+#pragma unroll
+                            for (int a = 0; a < 4; ++a) widen4(w[a], f16[2 * a], f16[2 * a + 1]);
+                            const uint32_t d = dst + (e >> 2) * kHalfBytes;
+                            st_shared_16(d + ((((e & 3) * 2) << 4) ^ swz), make_uint4(f16[0], f16[1], f16[2], f16[3]));
+                            st_shared_16(d + ((((e & 3) * 2 + 1) << 4) ^ swz), make_uint4(f16[4], f16[5], f16[6], f16[7]));
                         }
                     }
                     fence_proxy_async_smem();
