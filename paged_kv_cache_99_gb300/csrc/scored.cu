@@ -239,16 +239,35 @@ __device__ __forceinline__ uint32_t seen_keys(const ScoredParams& p, const Seg& 
     return seen;
 }
 
+// tcgen05.mma by descriptors' low words (address and leading offset, in 16 bytes); the high
+// word is the same for every tile: 8-row groups 1024 bytes apart, version 1, 128-byte swizzle.
+constexpr uint32_t kDescHigh = (1024 >> 4) | (1u << 14) | (2u << 29);
+
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tmov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a), "r"(b), "r"(kDescHigh), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+        : "memory");
+}
+// the same with A from tensor memory
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tmov.b64 db, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b), "r"(kDescHigh), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+        : "memory");
+}
+
 // Four e4m3 codes to fp16, exactly (free to be scheduled: the two warps that widen live by it).
 __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
         : "=r"(lo), "=r"(hi) : "r"(w));
 }
 
-// Tile order in the ring: K0, K1, V0, K2, V1, K3, ...: each K two steps ahead of its use, V as
-// its step begins.
+// Tile order in the ring: K0, K1, V0, K2, V1, K3, ...: each K two steps ahead of its V.  Place of
+// V(i) among a segment's tiles.
 __device__ __forceinline__ int item_v(int steps, int i) { return min(2, steps) + i + min(i, max(steps - 2, 0)); }
-__device__ __forceinline__ int item_k(int steps, int i) { return i < 2 ? i : item_v(steps, i - 2) + 1; }
 
 // tanh(x) / x on |x| <= kCapSmall as a polynomial in x^2 (interpolated at Chebyshev nodes):
 // within 2^-23.7 of it.
@@ -277,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto bar = [&](int i) -> uint32_t { return sbase + C::kOffBars + 8u * i; };
     auto stage = [&](int r) -> uint32_t { return sbase + C::kOffStage + static_cast<uint32_t>(r % NS) * kTileBytes; };
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0);
     const int lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
@@ -393,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     auto tS = [&](int x) -> uint32_t { return tmem + 128u * x; };          // S, then P over its first 64 columns
     auto tO = [&](int x) -> uint32_t { return tmem + 256u + 128u * x; };
     const int G = p.group;
@@ -581,128 +600,151 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp == 1) {
             // ================= MMA issuer =================
-            if (lane == 0) {
-                constexpr uint32_t idS = umma_idesc_f16<kMmaBf16>(kRows, kKeys, false);
-                constexpr uint32_t idPV = umma_idesc_f16<kMmaBf16>(kRows, kHeadDim, true);
-                auto wait = [&](uint32_t b, uint32_t par) -> bool {
-                    if (ok && !mbar_wait_bounded(b, par, p.timeout_ns)) ok = false;
-                    return ok;
-                };
-                auto poll = [&](uint32_t b, uint32_t par) -> bool {
-                    if (ok && !mbar_poll_bounded(b, par, p.timeout_ns)) ok = false;
-                    return ok;
-                };
-                auto tile_ready = [&](int r) -> bool { return wait(bar(kFull + r % NS), (r / NS) & 1); };
-                // a tile's descriptor, and those of its parts by adding to the address field
-                auto issue_s = [&](int x, uint32_t qbase, int r) {
-                    const uint64_t a = umma_desc_sw128(qbase, 16, 1024), b = umma_desc_sw128(stage(r), 16, 1024);
+            // The whole warp walks along, so that addresses stay uniform and need no moves, and one
+            // lane issues.  What it does between two products is time in which the tensor cores run
+            // dry: places in the ring are counted on, not divided out, and the tiles of the next step
+            // are waited for behind the last product of this one.
+            constexpr uint32_t idS = umma_idesc_f16<kMmaBf16>(kRows, kKeys, false);
+            constexpr uint32_t idPV = umma_idesc_f16<kMmaBf16>(kRows, kHeadDim, true);
+            const bool leader = lane == 0;
+            const uint32_t tiles = (sbase + C::kOffStage) >> 4, q_tiles = sbase >> 4;      // in units of 16 bytes
+            int st = 0;                              // the next tile's stage, and the parity of its filling
+            uint32_t ph = 0;
+            auto wait = [&](uint32_t b, uint32_t par) -> bool {
+                if (!warp_wait_all(b, par, p.timeout_ns)) ok = false;
+                return ok;
+            };
+            auto advance = [&]() {
+                if (++st == NS) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+            };
+            auto issue_s = [&](int x, int q, int stage_k) {
+                if (leader) {
+                    const uint32_t a = (q_tiles + q * (kTileBytes >> 4)) | (1u << 16);
+                    const uint32_t b = (tiles + stage_k * (kTileBytes >> 4)) | (1u << 16);
 #pragma unroll
                     for (int kk = 0; kk < kHeadDim / 16; ++kk) {
                         const uint32_t at = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
-                        umma_f16(tS(x), a + at, b + at, idS, kk > 0 ? 1u : 0u);
+                        mma_ss(tS(x), a + at, b + at, idS, kk > 0);
                     }
                     umma_commit(bar(kSFull + x));
-                };
-                // P.V over the step's keys 64 half .. 64 half + 63
-                auto issue_pv = [&](int x, int r, int half, bool first) {
-                    // V is MN-major: d-halves kHalfBytes apart, 16 keys = 2 KiB
-                    const uint64_t b = umma_desc_sw128(stage(r) + half * (kKeys / 32) * 2048, kHalfBytes, 1024);
+                }
+            };
+            // P.V over the step's keys 64 half .. 64 half + 63; V is MN-major: d-halves kHalfBytes
+            // apart, 16 keys = 2 KiB
+            auto issue_pv = [&](int x, int stage_v, int half, bool first) {
+                if (leader) {
+                    const uint32_t b = (tiles + stage_v * (kTileBytes >> 4) + half * (kKeys / 32) * 128) | ((kHalfBytes >> 4) << 16);
 #pragma unroll
                     for (int e = 0; e < kKeys / 32; ++e)
-                        umma_f16_ts(tO(x), tS(x) + 8 * (half * (kKeys / 32) + e), b + (e * 2048 >> 4), idPV,
-                                    (!first || half > 0 || e > 0) ? 1u : 0u);
-                };
-                int r0 = 0, seg = 0;
-                // parities as bits: an array indexed at run time would live in local memory, whose
-                // loads miss the little L1 that is left (prompt 8k: 5 times the time)
-                unsigned fixes = 0;                  // bit st: of the stage's zeroings
-                unsigned q_par = 0, p_par = 0;       // bit x: of the buffer's fills, of the tile's P
-                while (ok) {
-                    if (!wait(bar(kSegFull + seg % kSegs), (seg / kSegs) & 1)) break;
-                    const int* d = segs + (seg % kSegs) * kSegInts;
-                    const int n = d[kSegSteps], flags = d[kSegFlags], tail = d[kSegTail];
-                    mbar_arrive(bar(kSegEmpty + seg % kSegs));
-                    if (n == 0) break;
-                    const bool solo = flags & 1;
-                    const int qb = solo ? seg & 1 : 0;
-                    const uint32_t q_a = sbase + qb * kTileBytes, q_b = solo ? q_a : sbase + kTileBytes;
-                    if (!wait(bar(kQFull + qb), q_par >> qb & 1)) break;
-                    q_par ^= 1u << qb;
-                    if (!solo) {
-                        if (!wait(bar(kQFull + 1), q_par >> 1 & 1)) break;
-                        q_par ^= 2u;
-                    }
-                    auto q_free = [&]() {            // behind the segment's last S
-                        umma_commit(bar(kQEmpty + qb));
-                        if (!solo) umma_commit(bar(kQEmpty + 1));
-                    };
-                    // P(i) of tile x, in two halves, into O_x
-                    auto pv = [&](int x, int i, bool first) -> bool {
-                        const int r = r0 + item_v(n, i);
-                        if (!poll(bar(kPHalf + x), p_par >> x & 1)) return false;
-                        tc_fence_after();
-                        issue_pv(x, r, 0, first);
-                        if (!poll(bar(kPFull + x), p_par >> x & 1)) return false;
-                        tc_fence_after();
-                        issue_pv(x, r, 1, first);
-                        p_par ^= 1u << x;
-                        return true;
-                    };
-                    auto v_ready = [&](int i) -> bool {
-                        const int st = (r0 + item_v(n, i)) % NS;
-                        if (!tile_ready(r0 + item_v(n, i))) return false;
-                        if (!kFp8 && edge_step(flags, tail, i)) {
-                            if (!wait(bar(kFixed + st), fixes >> st & 1)) return false;
-                            fixes ^= 1u << st;
-                        }
-                        return true;
-                    };
-                    if (!tile_ready(r0)) break;
-                    tc_fence_after();
-                    issue_s(0, q_a, r0);
-                    if (!solo) issue_s(1, q_b, r0);
-                    umma_commit(bar(kEmpty + r0 % NS));
-                    if (n == 1) q_free();
-                    if (solo && n > 1) {
-                        if (!tile_ready(r0 + 1)) break;
-                        tc_fence_after();
-                        issue_s(1, q_b, r0 + 1);
-                        umma_commit(bar(kEmpty + (r0 + 1) % NS));
-                        if (n == 2) q_free();
-                    }
-                    for (int i = 0; i < n && ok; ++i) {
-                        if (!v_ready(i)) break;
-                        if (solo) {
-                            if (!pv(i & 1, i, i < 2)) break;
-                            umma_commit(bar(kEmpty + (r0 + item_v(n, i)) % NS));
-                            if (i + 2 < n) {
-                                const int rk = r0 + item_k(n, i + 2);
-                                if (!tile_ready(rk)) break;
-                                tc_fence_after();
-                                issue_s(i & 1, q_a, rk);
-                                umma_commit(bar(kEmpty + rk % NS));
-                                if (i + 3 == n) q_free();
-                            }
-                        } else {
-                            const int rk = r0 + item_k(n, i + 1);
-                            if (i + 1 < n && !tile_ready(rk)) break;
-                            for (int x = 0; x < 2; ++x) {
-                                if (!pv(x, i, i == 0)) break;
-                                if (i + 1 < n) issue_s(x, x ? q_b : q_a, rk);
-                            }
-                            if (!ok) break;
-                            umma_commit(bar(kEmpty + (r0 + item_v(n, i)) % NS));
-                            if (i + 1 < n) umma_commit(bar(kEmpty + rk % NS));
-                            if (i + 2 == n) q_free();
-                        }
-                    }
-                    if (!ok) break;
-                    umma_commit(bar(kSegDone));
-                    r0 += 2 * n;
-                    ++seg;
+                        mma_ts(tO(x), tS(x) + 8 * (half * (kKeys / 32) + e), b + e * 128, idPV, !first || half > 0 || e > 0);
                 }
-                if (!ok) atomicOr(p.status, kDevErrTimeout);
+            };
+            auto commit = [&](int b) {
+                if (leader) umma_commit(bar(b));
+            };
+            // parities as bits: an array indexed at run time would live in local memory
+            unsigned fixes = 0;                      // bit st: of the stage's zeroings
+            unsigned q_par = 0, p_par = 0;           // bit x: of the buffer's fills, of the tile's P
+            auto pv = [&](int x, int stage_v, bool first) -> bool {
+                if (!wait(bar(kPHalf + x), p_par >> x & 1)) return false;
+                tc_fence_after();
+                issue_pv(x, stage_v, 0, first);
+                if (!wait(bar(kPFull + x), p_par >> x & 1)) return false;
+                tc_fence_after();
+                issue_pv(x, stage_v, 1, first);
+                p_par ^= 1u << x;
+                return true;
+            };
+            int seg = 0;
+            while (ok) {
+                if (!wait(bar(kSegFull + seg % kSegs), (seg / kSegs) & 1)) break;
+                const int* d = segs + (seg % kSegs) * kSegInts;
+                const int n = __shfl_sync(0xffffffffu, d[kSegSteps], 0), flags = __shfl_sync(0xffffffffu, d[kSegFlags], 0);
+                const int tail = __shfl_sync(0xffffffffu, d[kSegTail], 0);
+                if (leader) mbar_arrive(bar(kSegEmpty + seg % kSegs));
+                if (n == 0) break;
+                const bool solo = flags & 1;
+                const int qa = solo ? seg & 1 : 0, qb = solo ? qa : 1;
+                if (!wait(bar(kQFull + qa), q_par >> qa & 1)) break;
+                q_par ^= 1u << qa;
+                if (!solo) {
+                    if (!wait(bar(kQFull + 1), q_par >> 1 & 1)) break;
+                    q_par ^= 2u;
+                }
+                auto q_free = [&]() {                // behind the segment's last S
+                    commit(kQEmpty + qa);
+                    if (!solo) commit(kQEmpty + 1);
+                };
+                // V of step i at the next place: landed, and its unseen rows zeroed
+                auto v_ready = [&](int i) -> bool {
+                    if (!wait(bar(kFull + st), ph)) return false;
+                    if (!kFp8 && edge_step(flags, tail, i)) {
+                        if (!wait(bar(kFixed + st), fixes >> st & 1)) return false;
+                        fixes ^= 1u << st;
+                    }
+                    return true;
+                };
+                if (!wait(bar(kFull + st), ph)) break;
+                tc_fence_after();
+                issue_s(0, qa, st);
+                if (!solo) issue_s(1, qb, st);
+                commit(kEmpty + st);
+                if (n == 1) q_free();
+                advance();
+                if (solo) {
+                    if (n > 1) {
+                        if (!wait(bar(kFull + st), ph)) break;
+                        tc_fence_after();
+                        issue_s(1, qa, st);
+                        commit(kEmpty + st);
+                        if (n == 2) q_free();
+                        advance();
+                    }
+                    for (int i = 0; i < n; ++i) {
+                        // V(i), then K(i + 2) for the same tile
+                        if (!v_ready(i)) break;
+                        const int v_st = st, x = i & 1;
+                        advance();
+                        if (!pv(x, v_st, i < 2)) break;
+                        commit(kEmpty + v_st);
+                        if (i + 2 < n) {
+                            if (!wait(bar(kFull + st), ph)) break;
+                            tc_fence_after();
+                            issue_s(x, qa, st);
+                            commit(kEmpty + st);
+                            if (i + 3 == n) q_free();
+                            advance();
+                        }
+                    }
+                } else {
+                    for (int i = 0; i < n; ++i) {
+                        // K(i + 1) and V(i), for both tiles
+                        const bool more = i + 1 < n;
+                        const int k_st = st;
+                        if (more) {
+                            if (!wait(bar(kFull + st), ph)) break;
+                            advance();
+                        }
+                        if (!v_ready(i)) break;
+                        const int v_st = st;
+                        advance();
+                        if (!pv(0, v_st, i == 0)) break;
+                        if (more) issue_s(0, 0, k_st);
+                        if (!pv(1, v_st, i == 0)) break;
+                        if (more) issue_s(1, 1, k_st);
+                        commit(kEmpty + v_st);
+                        if (more) commit(kEmpty + k_st);
+                        if (i + 2 == n) q_free();
+                    }
+                }
+                if (!ok) break;
+                commit(kSegDone);
+                ++seg;
             }
+            if (!ok && leader) atomicOr(p.status, kDevErrTimeout);
             __syncwarp();
         } else if (kFp8) {
             // ================= FP8: e4m3 rows to fp16 tiles, two of a tile's rows a thread =================
