@@ -27,7 +27,7 @@ struct DeviceState {
     bool decode_prepared[3][2][3][2][2] = {};
     bool chunk_prepared[3][2] = {};
     bool evict_prepared = false;
-    bool scored_prepared[3][2][2] = {};
+    bool scored_prepared[3][2][3] = {};
 };
 
 std::mutex g_mu;
@@ -495,13 +495,13 @@ pa_status scored_impl(ScoredParams p, void* out, const void* q, const int32_t* q
     if (workspace_bytes < lay.total) return PA_ERR_WORKSPACE;
     const CacheKind kind = kind_of(cache_dtype);
     const bool q_bf16 = q_dtype == PA_BF16, fp8 = kind == kKindFp8;
-    const bool mod = cap > 0.f || p.slopes != nullptr;
+    const ScoreForm form = p.slopes ? kBiasedScores : cap > 0.f ? kCappedScores : kPlainScores;
     {
         std::lock_guard<std::mutex> lock(g_mu);
-        if (!st->scored_prepared[kind][q_bf16][mod]) {
-            cudaError_t e = scored_prepare(kind, q_bf16, mod);
+        if (!st->scored_prepared[kind][q_bf16][form]) {
+            cudaError_t e = scored_prepare(kind, q_bf16, form);
             if (e != cudaSuccess) return fail("cudaFuncSetAttribute(scored)", e);
-            st->scored_prepared[kind][q_bf16][mod] = true;
+            st->scored_prepared[kind][q_bf16][form] = true;
         }
     }
     CUtensorMap kmap, vmap;
@@ -530,8 +530,10 @@ pa_status scored_impl(ScoredParams p, void* out, const void* q, const int32_t* q
     p.num_blocks = num_blocks;
     p.block_size = block_size;
     p.block_shift = block_shift_of(block_size);
-    p.scale = scale;
+    p.scale_log2 = scale * 1.4426950408889634f;
     p.cap = cap;
+    p.cap_scale = cap > 0.f ? scale / cap : 0.f;
+    p.cap_log2 = cap * 1.4426950408889634f;
     p.queries_per_tile = scored_rows() / group;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.records = reinterpret_cast<CombineRecord*>(ws + lay.records_off);
@@ -542,7 +544,7 @@ pa_status scored_impl(ScoredParams p, void* out, const void* q, const int32_t* q
     CUtensorMap qmap;
     s = encode_query_map(&qmap, q, total_q, num_q_heads, group, p.queries_per_tile);
     if (s != PA_OK) return s;
-    s = launched(launch_scored(kind, q_bf16, mod, kmap, vmap, qmap, p, st->sms, stream), "launch(scored)");
+    s = launched(launch_scored(kind, q_bf16, form, kmap, vmap, qmap, p, st->sms, stream), "launch(scored)");
     // tables of one step: no unit is ever shared
     if (s != PA_OK || static_cast<long long>(max_blocks_per_seq) * block_size <= scored_rows()) return s;
     return launched(launch_scored_combine(q_bf16, fp8, p, st->sms, stream), "launch(scored combine)");

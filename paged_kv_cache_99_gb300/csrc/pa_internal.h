@@ -355,8 +355,10 @@ struct ScoredParams {
     int block_size;                   // tokens per physical block: 8, 16 or 32
     int block_shift;                  // log2(block_size)
     int queries_per_tile;             // queries of a 128-row tile
-    float scale;
+    float scale_log2;                 // softmax scale * log2(e)
     float cap;                        // 0: none
+    float cap_scale;                  // scale / cap
+    float cap_log2;                   // cap * log2(e)
     CombineRecord* records;           // [CTAs]
     float2* ml;                       // [CTAs][2][256]: maximum (log2 units), sum
     float4* partial;                  // [CTAs][2][32 quads][256]: unnormalised outputs
@@ -371,9 +373,10 @@ struct ScoredLayout {
 
 ScoredLayout scored_layout(int sms);
 int scored_rows();                    // rows of one tile
-// mod: the kernel that caps and biases scores
-cudaError_t scored_prepare(CacheKind kind, bool q_bf16, bool mod);
-cudaError_t launch_scored(CacheKind kind, bool q_bf16, bool mod, const CUtensorMap& kmap, const CUtensorMap& vmap,
+// Forms of the kernel: scores as they are, capped, or biased (and perhaps capped).
+enum ScoreForm { kPlainScores = 0, kCappedScores = 1, kBiasedScores = 2 };
+cudaError_t scored_prepare(CacheKind kind, bool q_bf16, ScoreForm form);
+cudaError_t launch_scored(CacheKind kind, bool q_bf16, ScoreForm form, const CUtensorMap& kmap, const CUtensorMap& vmap,
                           const CUtensorMap& qmap, const ScoredParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_scored_combine(bool out_bf16, bool fp8, const ScoredParams& p, int sms, cudaStream_t stream);
 

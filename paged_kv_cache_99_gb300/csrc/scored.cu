@@ -53,7 +53,6 @@ constexpr int kCols = kKeys / 2;             // a softmax thread's keys of a ste
 // registers per thread at launch, and the shares of warps 0-3 and the softmax after setmaxnreg
 constexpr int kRegsLaunch = 96, kRegsFront = 64, kRegsSoftmax = 104;
 constexpr float kRescale = 8.0f;             // lazy rescale threshold (factor 256)
-constexpr float kCapSmall = 0.6f;            // |x / cap| up to which the tanh is a polynomial
 
 template <int Kind>
 struct Cfg {
@@ -269,14 +268,21 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
 // V(i) among a segment's tiles.
 __device__ __forceinline__ int item_v(int steps, int i) { return min(2, steps) + i + min(i, max(steps - 2, 0)); }
 
-// tanh(x) / x on |x| <= kCapSmall as a polynomial in x^2 (interpolated at Chebyshev nodes):
-// within 2^-23.7 of it.
+// c2 tanh(y) = c2 - 2 c2 / (1 + e^2y), by the exponential unit: within 2^-21 of c2.
+__device__ __forceinline__ float capped(float y, float c2) {
+    return fmaf(-2.f * c2, rcp_approx(1.f + ex2_approx(y * 2.8853900817779268f)), c2);
+}
+
+// tanh(x) / x as polynomials in x^2 (interpolated at Chebyshev nodes): on |x| <= kCapTiny within
+// 2^-19.7 of it, on |x| <= kCapSmall within 2^-23.7.
+constexpr float kCapTiny = 0.3f, kCapSmall = 0.6f;
+constexpr float kTiny0 = 0.999998835f, kTiny1 = -0.333099888f, kTiny2 = 0.126335824f;
 constexpr float kTanh0 = 0.999999926f, kTanh1 = -0.33332302f, kTanh2 = 0.133100644f, kTanh3 = -0.0520966534f,
                 kTanh4 = 0.0154687513f;
 
 }  // namespace
 
-template <int Kind, bool QBf16, bool Mod>
+template <int Kind, bool QBf16, int Form>
 __global__ void __launch_bounds__(kThreads, 1)
     scored_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                   const __grid_constant__ CUtensorMap qmap, const ScoredParams p) {
@@ -925,15 +931,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 live = r < QT * G && jq < d[kSegNq];
                 if (live) view = row_view(p, SeqView{d[kSegRow0] - d[kSegJ0], d[kSegQLen], d[kSegN], d[kSegPrefix]}, d[kSegJ0] + jq);
                 if (kFp8) kscale = __ldg(p.k_scale + d[kSegHead] * p.scale_stride);
-                if (Mod && p.slopes && live) slope2 = __ldg(p.slopes + d[kSegHead] * G + r % G) * 1.4426950408889634f;
+                if (Form == kBiasedScores && p.slopes && live) slope2 = __ldg(p.slopes + d[kSegHead] * G + r % G) * 1.4426950408889634f;
             }
             const bool warp_live = __any_sync(0xffffffffu, live);
             const int lo_max = __reduce_max_sync(0xffffffffu, view.lo);
             const int hi_min = __reduce_min_sync(0xffffffffu, view.hi);
+            [[maybe_unused]] const int pos_min = __reduce_min_sync(0xffffffffu, live ? view.pos : INT_MAX);
             // never 0: hidden scores are infinite, and stay so under it
-            const float s_raw = p.scale * 1.4426950408889634f * kscale;
+            const float s_raw = p.scale_log2 * kscale;
             const float s_log2 = s_raw == 0.f ? 1e-30f : s_raw;
-            const bool pos_scale = s_log2 >= 0.f;
             float m_used = -INFINITY, l = 0.f;
             const int stride = solo ? 2 : 1;
             int key0 = (d[kSegStep] + (solo ? x : 0)) * kKeys + NC * half;
@@ -977,72 +983,58 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < NC / 32; ++c)
                     tmem_ld32(s_addr + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * c));
                 tmem_wait_ld();
-                if constexpr (Mod) {
-                    // scores in log2 units, capped and biased (what stands in hidden places, keys that
-                    // were never copied, must not choose the form of the tanh)
-                    if (need_mask) {
-#pragma unroll
-                        for (int e = 0; e < NC; ++e) sv[e] = vis[e >> 5] >> (e & 31) & 1 ? sv[e] : 0u;
-                    }
+                // The row's maximum, of what the maximum of the scores follows: a cap is monotone, so that
+                // of the raw scores will do; biased scores are computed first.  (A negative scale turns
+                // the order round.)  Hidden scores are infinite on the far side.
+                const float mul = Form == kBiasedScores ? 1.0f : s_log2;
+                const bool upward = Form == kBiasedScores || s_log2 >= 0.f;
+                if constexpr (Form == kBiasedScores) {
+                    // a cap first: a rare pair, so by the exponential unit alone (what stands in hidden
+                    // places, keys that were never copied, stays there)
                     if (p.cap > 0.f) {
-                        // |x / cap| small in the whole warp (nearly always: caps lie far above most
-                        // scores): the polynomial, 3.5 packed instructions a score; else 1 - 2 / (1 +
-                        // e^2x), two steps of the exponential unit, which the softmax waits for too.
-                        // tanh.approx is 2^-11 off, 0.02 of a score at a cap of 50.
-                        const float k1 = p.scale * kscale / p.cap;
-                        float a4[4] = {0.f, 0.f, 0.f, 0.f};
+                        const float c2 = p.cap_log2, k1 = p.cap_scale * kscale;
 #pragma unroll
-                        for (int e = 0; e < NC; e += 2)
-                            a4[(e >> 1) & 3] = max3f(a4[(e >> 1) & 3], fabsf(__uint_as_float(sv[e])), fabsf(__uint_as_float(sv[e + 1])));
-                        const float am = fmaxf(fmaxf(a4[0], a4[1]), fmaxf(a4[2], a4[3]));
-                        if (!__any_sync(0xffffffffu, live && am * fabsf(k1) > kCapSmall)) {
-                            const uint64_t k12 = f2_pack(k1, k1), sc2 = f2_pack(s_log2, s_log2);
-                            const uint64_t c0 = f2_pack(kTanh0, kTanh0), c1 = f2_pack(kTanh1, kTanh1),
-                                           c2 = f2_pack(kTanh2, kTanh2), c3 = f2_pack(kTanh3, kTanh3),
-                                           c4 = f2_pack(kTanh4, kTanh4);
+                        for (int e = 0; e < NC; ++e)
+                            sv[e] = __float_as_uint(capped(__uint_as_float(sv[e]) * k1, c2));
+                    }
+                    const float by = p.cap > 0.f ? 1.0f : s_log2;
+                    const uint64_t by2 = f2_pack(by, by);
+                    if (key0 + NC - 1 <= pos_min) {
+                        // every key at or before every row: the bias grows by slope2 from key to key, and
+                        // is counted on for four pairs from a place that is computed
+                        const uint64_t step2 = f2_pack(2.f * slope2, 2.f * slope2);
+                        const float base = static_cast<float>(key0 - view.pos);
 #pragma unroll
-                            for (int e = 0; e < NC; e += 2) {
-                                const uint64_t v = f2_pack(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
-                                const uint64_t y = f2_mul(v, k12), u = f2_mul(y, y);
-                                uint64_t q = f2_fma(u, c4, c3);
-                                q = f2_fma(u, q, c2);
-                                q = f2_fma(u, q, c1);
-                                q = f2_fma(u, q, c0);
+                        for (int c = 0; c < NC / 8; ++c) {
+                            const float b0 = slope2 * (base + static_cast<float>(8 * c));
+                            uint64_t b2 = f2_pack(b0, b0 + slope2);
+#pragma unroll
+                            for (int e = 8 * c; e < 8 * c + 8; e += 2) {
                                 float a0, a1;
-                                f2_unpack(f2_mul(f2_mul(v, sc2), q), a0, a1);
+                                f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), by2, b2), a0, a1);
                                 sv[e] = __float_as_uint(a0);
                                 sv[e + 1] = __float_as_uint(a1);
+                                b2 = f2_add(b2, step2);
                             }
-                        } else {
-                            const float c2 = p.cap * 1.4426950408889634f, k2 = k1 * 2.8853900817779268f;
-#pragma unroll
-                            for (int e = 0; e < NC; ++e)
-                                sv[e] = __float_as_uint(fmaf(-2.f * c2, rcp_approx(1.f + ex2_approx(__uint_as_float(sv[e]) * k2)), c2));
                         }
                     } else {
-#pragma unroll
-                        for (int e = 0; e < NC; ++e) sv[e] = __float_as_uint(__uint_as_float(sv[e]) * s_log2);
-                    }
-                    if (p.slopes) {
                         const float base = static_cast<float>(key0 - view.pos);
 #pragma unroll
                         for (int e = 0; e < NC; ++e)
-                            sv[e] = __float_as_uint(fmaf(-slope2, fabsf(base + static_cast<float>(e)), __uint_as_float(sv[e])));
+                            sv[e] = __float_as_uint(fmaf(__uint_as_float(sv[e]), by, -slope2 * fabsf(base + static_cast<float>(e))));
                     }
                 }
-                // row maximum of s * scale = max(s) * scale for scale >= 0, min(s) * scale
-                // otherwise; four independent chains
-                const float mul = Mod ? 1.0f : s_log2;
-                float mx;
                 if (need_mask) {
-                    const float hidden = Mod || pos_scale ? -INFINITY : INFINITY;
+                    const float hidden = upward ? -INFINITY : INFINITY;
 #pragma unroll
                     for (int e = 0; e < NC; ++e)
                         sv[e] = vis[e >> 5] >> (e & 31) & 1 ? sv[e] : __float_as_uint(hidden);
                 }
+                float mx;
                 {
+                    // four independent chains
                     float e4[4];
-                    if (Mod || pos_scale) {
+                    if (upward) {
                         e4[0] = e4[1] = e4[2] = e4[3] = -INFINITY;
 #pragma unroll
                         for (int e = 0; e < NC; e += 2)
@@ -1055,12 +1047,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                             e4[(e >> 1) & 3] = min3f(e4[(e >> 1) & 3], __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
                         mx = fminf(fminf(e4[0], e4[1]), fminf(e4[2], e4[3]));
                     }
-                    mx *= mul;
+                    mx *= Form == kCappedScores ? p.cap_scale * kscale : mul;
+                }
+                // The form of the tanh, one for the warp's part of the step: the shortest polynomial where
+                // the largest x / cap of every row lies in [-0.1, 0.3] and the cap is 40 or more: what lies
+                // below -0.3 then weighs e^-7.7 at most, and beyond the polynomial's range, where it falls
+                // faster than the tanh, next to nothing.  Else by the largest |x / cap|.
+                int tanh_form = 0;
+                if constexpr (Form == kCappedScores) {
+                    const float k1 = p.cap_scale * kscale;
+                    if (__any_sync(0xffffffffu, live && !(mx >= -0.1f && mx <= kCapTiny)) || p.cap < 40.f || fabsf(k1) < 1e-8f) {
+                        float am = 0.f;
+#pragma unroll
+                        for (int e = 0; e < NC; ++e) {
+                            const float v = fabsf(__uint_as_float(sv[e]));
+                            am = fmaxf(am, v < INFINITY ? v : 0.f);
+                        }
+                        am = live ? fmaxf(am * fabsf(k1), mx) : 0.f;        // mx: an infinite score that is seen
+                        tanh_form = __any_sync(0xffffffffu, am > kCapSmall) ? 2
+                                    : __any_sync(0xffffffffu, am > kCapTiny || fabsf(k1) < 1e-8f) ? 1 : 0;
+                    }
                 }
                 // with the row's other thread, which has read its scores too: P may go over them
                 row_smem[exch] = mx;
                 if (!meet()) break;
                 mx = fmaxf(mx, row_smem[exch ^ kRows]);
+                if constexpr (Form == kCappedScores) {
+                    // the row's maximum capped (a reference: what matters is that both threads take the same)
+                    const float c2 = p.cap_log2;
+                    if (__any_sync(0xffffffffu, live && !(fabsf(mx) <= kCapTiny))) {
+                        mx = mx == -INFINITY ? mx : capped(mx, c2);
+                    } else {
+                        const float u = mx * mx;
+                        mx *= c2 * fmaf(u, fmaf(u, kTiny2, kTiny1), kTiny0);
+                    }
+                }
                 const bool need = live && mx > m_used + kRescale;
                 const bool resc = __any_sync(0xffffffffu, need);
                 const float m_new = need ? mx : m_used;
@@ -1093,30 +1114,73 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // (bf16 2^-8 of it at most, fp16, FP8 caches' type too, 2^-11; their sum is of the
                 // unrounded ones), written over the columns of S (keys 32 c .. +31 -> columns 16 c
                 // .. +15).  P in two 16-bit parts would double the products of P.V.
-                uint64_t sum2[2] = {0ull, 0ull};
-                const uint64_t scale2 = f2_pack(mul, mul);
-                const uint64_t negm2 = f2_pack(-m_at, -m_at);
+                float sum;
+                if constexpr (Form != kCappedScores) {
+                    uint64_t sum2[2] = {0ull, 0ull};
+                    const uint64_t negm2 = f2_pack(-m_at, -m_at), scale2 = f2_pack(mul, mul);
 #pragma unroll
-                for (int c = 0; c < NC / 16; ++c) {
-                    uint32_t pw[8];
+                    for (int c = 0; c < NC / 16; ++c) {
+                        uint32_t pw[8];
 #pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        const int kk = 16 * c + e;
-                        const uint64_t v = f2_pack(__uint_as_float(sv[kk]), __uint_as_float(sv[kk + 1]));
-                        float a0, a1;
-                        if constexpr (Mod) f2_unpack(f2_add(v, negm2), a0, a1);
-                        else f2_unpack(f2_fma(v, scale2, negm2), a0, a1);
-                        const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);     // hidden: 0
-                        sum2[(e >> 1) & 1] = f2_add(sum2[(e >> 1) & 1], f2_pack(p0, p1));
-                        pw[e >> 1] = pack2<kMmaBf16>(p0, p1);
+                        for (int e = 0; e < 16; e += 2) {
+                            const uint64_t v = f2_pack(__uint_as_float(sv[16 * c + e]), __uint_as_float(sv[16 * c + e + 1]));
+                            float a0, a1;
+                            f2_unpack(Form == kPlainScores ? f2_fma(v, scale2, negm2) : f2_add(v, negm2), a0, a1);
+                            const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);     // hidden: 0
+                            sum2[(e >> 1) & 1] = f2_add(sum2[(e >> 1) & 1], f2_pack(p0, p1));
+                            pw[e >> 1] = pack2<kMmaBf16>(p0, p1);
+                        }
+                        tmem_st8(p_addr + 8 * c, pw);
                     }
-                    tmem_st8(p_addr + 8 * c, pw);
+                    float s0, s1, s2, s3;
+                    f2_unpack(sum2[0], s0, s1);
+                    f2_unpack(sum2[1], s2, s3);
+                    sum = (s0 + s1) + (s2 + s3);
+                } else {
+                    // cap tanh(x / cap) less the maximum, x a score before the scale: a polynomial where |x /
+                    // cap| is small, nearly always (caps lie far above most scores), four operations with
+                    // the scale and the maximum folded in, or eight with its coefficients in the
+                    // instructions; else by the exponential unit, which the softmax waits for too
+                    // (tanh.approx is 2^-11 off, 0.02 of a score at a cap of 50).  One score at a time:
+                    // packed pairs take twice the registers for what is the same in both, and spilled.
+                    float sums[2] = {0.f, 0.f};
+                    auto store_p = [&](auto exponent) {
+#pragma unroll
+                        for (int c = 0; c < NC / 16; ++c) {
+                            uint32_t pw[8];
+#pragma unroll
+                            for (int e = 0; e < 16; e += 2) {
+                                const float p0 = ex2_approx(exponent(__uint_as_float(sv[16 * c + e])));      // hidden: 0
+                                const float p1 = ex2_approx(exponent(__uint_as_float(sv[16 * c + e + 1])));
+                                sums[0] += p0;
+                                sums[1] += p1;
+                                pw[e >> 1] = pack2<kMmaBf16>(p0, p1);
+                            }
+                            tmem_st8(p_addr + 8 * c, pw);
+                        }
+                    };
+                    const float k1 = p.cap_scale * kscale;
+                    if (tanh_form == 0) {
+                        const float d0 = kTiny0 * s_log2, d1 = kTiny1 * s_log2 * (k1 * k1), d2 = kTiny2 * s_log2 * (k1 * k1) * (k1 * k1);
+                        store_p([&](float v) {
+                            const float u = v * v;
+                            return fmaf(v, fmaf(u, fmaf(u, d2, d1), d0), -m_at);
+                        });
+                    } else if (tanh_form == 1) {
+                        store_p([&](float v) {
+                            const float y = v * k1, u = y * y;
+                            return fmaf(y * p.cap_log2, fmaf(u, fmaf(u, fmaf(u, fmaf(u, kTanh4, kTanh3), kTanh2), kTanh1), kTanh0), -m_at);
+                        });
+                    } else {
+                        store_p([&](float v) {
+                            const float t = capped(v * k1, p.cap_log2) - m_at;
+                            return v * k1 == -INFINITY ? -INFINITY : t;
+                        });
+                    }
+                    sum = sums[0] + sums[1];
                 }
                 tmem_wait_st();
-                float s0, s1, s2, s3;
-                f2_unpack(sum2[0], s0, s1);
-                f2_unpack(sum2[1], s2, s3);
-                l = l * alpha + ((s0 + s1) + (s2 + s3));
+                l = l * alpha + sum;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar((half ? kPFull : kPHalf) + x));
@@ -1330,16 +1394,20 @@ __global__ void __launch_bounds__(256) scored_combine_kernel(const ScoredParams 
 namespace {
 
 template <int Kind, bool QBf16>
-const void* scored_fn(bool mod) {
-    return mod ? reinterpret_cast<const void*>(&scored_kernel<Kind, QBf16, true>)
-               : reinterpret_cast<const void*>(&scored_kernel<Kind, QBf16, false>);
+const void* scored_fn(ScoreForm form) {
+    switch (form) {
+        case kPlainScores: return reinterpret_cast<const void*>(&scored_kernel<Kind, QBf16, kPlainScores>);
+        case kCappedScores: return reinterpret_cast<const void*>(&scored_kernel<Kind, QBf16, kCappedScores>);
+        case kBiasedScores: return reinterpret_cast<const void*>(&scored_kernel<Kind, QBf16, kBiasedScores>);
+    }
+    return nullptr;
 }
 
-const void* scored_fn(CacheKind kind, bool q_bf16, bool mod) {
+const void* scored_fn(CacheKind kind, bool q_bf16, ScoreForm form) {
     switch (kind) {
-        case kKindBf16: return scored_fn<kKindBf16, true>(mod);
-        case kKindFp16: return scored_fn<kKindFp16, false>(mod);
-        case kKindFp8: return q_bf16 ? scored_fn<kKindFp8, true>(mod) : scored_fn<kKindFp8, false>(mod);
+        case kKindBf16: return scored_fn<kKindBf16, true>(form);
+        case kKindFp16: return scored_fn<kKindFp16, false>(form);
+        case kKindFp8: return q_bf16 ? scored_fn<kKindFp8, true>(form) : scored_fn<kKindFp8, false>(form);
     }
     return nullptr;
 }
@@ -1360,12 +1428,12 @@ ScoredLayout scored_layout(int sms) {
 
 int scored_rows() { return kRows; }
 
-cudaError_t scored_prepare(CacheKind kind, bool q_bf16, bool mod) {
-    return cudaFuncSetAttribute(scored_fn(kind, q_bf16, mod), cudaFuncAttributeMaxDynamicSharedMemorySize,
+cudaError_t scored_prepare(CacheKind kind, bool q_bf16, ScoreForm form) {
+    return cudaFuncSetAttribute(scored_fn(kind, q_bf16, form), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(scored_smem(kind)));
 }
 
-cudaError_t launch_scored(CacheKind kind, bool q_bf16, bool mod, const CUtensorMap& kmap, const CUtensorMap& vmap,
+cudaError_t launch_scored(CacheKind kind, bool q_bf16, ScoreForm form, const CUtensorMap& kmap, const CUtensorMap& vmap,
                           const CUtensorMap& qmap, const ScoredParams& p, int sms, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(sms));
@@ -1379,7 +1447,7 @@ cudaError_t launch_scored(CacheKind kind, bool q_bf16, bool mod, const CUtensorM
     cfg.numAttrs = 1;
     void* args[] = {const_cast<CUtensorMap*>(&kmap), const_cast<CUtensorMap*>(&vmap), const_cast<CUtensorMap*>(&qmap),
                     const_cast<ScoredParams*>(&p)};
-    return cudaLaunchKernelExC(&cfg, scored_fn(kind, q_bf16, mod), args);
+    return cudaLaunchKernelExC(&cfg, scored_fn(kind, q_bf16, form), args);
 }
 
 cudaError_t launch_scored_combine(bool out_bf16, bool fp8, const ScoredParams& p, int sms, cudaStream_t stream) {
