@@ -1150,8 +1150,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             uint32_t pw[8];
 #pragma unroll
                             for (int e = 0; e < 16; e += 2) {
-                                const float p0 = ex2_approx(exponent(__uint_as_float(sv[16 * c + e])));      // hidden: 0
-                                const float p1 = ex2_approx(exponent(__uint_as_float(sv[16 * c + e + 1])));
+                                float a0, a1;
+                                exponent(__uint_as_float(sv[16 * c + e]), __uint_as_float(sv[16 * c + e + 1]), a0, a1);
+                                const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);     // hidden: 0
                                 sums[0] += p0;
                                 sums[1] += p1;
                                 pw[e >> 1] = pack2<kMmaBf16>(p0, p1);
@@ -1162,19 +1163,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float k1 = p.cap_scale * kscale;
                     if (tanh_form == 0) {
                         const float d0 = kTiny0 * s_log2, d1 = kTiny1 * s_log2 * (k1 * k1), d2 = kTiny2 * s_log2 * (k1 * k1) * (k1 * k1);
-                        store_p([&](float v) {
-                            const float u = v * v;
-                            return fmaf(v, fmaf(u, fmaf(u, d2, d1), d0), -m_at);
+                        const uint64_t c0 = f2_pack(d0, d0), c1 = f2_pack(d1, d1), c2 = f2_pack(d2, d2), negm2 = f2_pack(-m_at, -m_at);
+                        store_p([&](float v0, float v1, float& a0, float& a1) {
+                            const uint64_t v = f2_pack(v0, v1), u = f2_mul(v, v);
+                            f2_unpack(f2_fma(v, f2_fma(u, f2_fma(u, c2, c1), c0), negm2), a0, a1);
                         });
                     } else if (tanh_form == 1) {
-                        store_p([&](float v) {
+                        auto one = [&](float v) {
                             const float y = v * k1, u = y * y;
                             return fmaf(y * p.cap_log2, fmaf(u, fmaf(u, fmaf(u, fmaf(u, kTanh4, kTanh3), kTanh2), kTanh1), kTanh0), -m_at);
+                        };
+                        store_p([&](float v0, float v1, float& a0, float& a1) {
+                            a0 = one(v0);
+                            a1 = one(v1);
                         });
                     } else {
-                        store_p([&](float v) {
+                        auto one = [&](float v) {
                             const float t = capped(v * k1, p.cap_log2) - m_at;
                             return v * k1 == -INFINITY ? -INFINITY : t;
+                        };
+                        store_p([&](float v0, float v1, float& a0, float& a1) {
+                            a0 = one(v0);
+                            a1 = one(v1);
                         });
                     }
                     sum = sums[0] + sums[1];
