@@ -27,6 +27,7 @@ struct DeviceState {
     bool decode_prepared[3][2][3][2][2] = {};
     bool chunk_prepared[3][2] = {};
     bool evict_prepared = false;
+    bool norm_rope_prepared = false;
     bool scored_prepared[3][2][3] = {};
 };
 
@@ -767,6 +768,14 @@ pa_status pa_norm_rope_and_cache(void* q_out, long long q_out_stride, const void
     if (num_tokens == 0) return PA_OK;
     DeviceState* st = device_state(nullptr);
     if (!st) return PA_ERR_CUDA;
+    {
+        std::lock_guard<std::mutex> lock(g_mu);
+        if (!st->norm_rope_prepared) {
+            cudaError_t e = norm_rope_prepare();
+            if (e != cudaSuccess) return fail("cudaFuncSetAttribute(norm_rope)", e);
+            st->norm_rope_prepared = true;
+        }
+    }
     p.q_weight = static_cast<const uint16_t*>(q_weight);
     p.k_weight = static_cast<const uint16_t*>(k_weight);
     p.eps = eps;

@@ -255,7 +255,8 @@ struct NormRopeParams {
     unsigned one_axis;                // bit c: pairs 8 c .. 8 c + 7 follow one axis
 };
 
-cudaError_t launch_norm_rope_cache(NormRopeParams p, bool src_bf16, bool fp8, bool interleaved, int sms,
+cudaError_t norm_rope_prepare();
+cudaError_t launch_norm_rope_cache(const NormRopeParams& p, bool src_bf16, bool fp8, bool interleaved, int sms,
                                    cudaStream_t stream);
 
 // Eviction: selection of the places that stay and the copy of their rows, by a cluster of

@@ -192,3 +192,58 @@ def test_captured():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, ref)
+
+
+@pytest.mark.parametrize("kind,cache,per_head", [("bf16", "bf16", False), ("fp16", "fp16", False), ("bf16", "fp8", False),
+                                                 ("fp16", "fp8", True)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_many_tokens(kind, cache, per_head, interleaved):
+    """More tokens than every SM has a few of: rotations of part of a head and several axes."""
+    for T, hq, hkv, rot, sections in ((3001, 28, 4, 128, (24, 20, 20)), (9000, 8, 2, 64, (5, 3, 0, 24)), (2500, 40, 8, 112, None)):
+        axes = pa.rope_axes(sections, in_turns=True) if sections else None
+        go(Case(T, T, hq, hkv, rot, kind, cache, axes=axes, per_head=per_head), interleaved=interleaved)
+
+
+def test_many_tokens_with_padding():
+    c = Case(8, 4000, 28, 4, 128, axes=list(pa.rope_axes((16, 24, 24))))
+    ws = torch.zeros(256, dtype=torch.uint8, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    pad = torch.rand(4000, generator=g, device=DEV) < 0.1
+    far = torch.rand(4000, generator=g, device=DEV) < 0.05
+    none = torch.rand(4000, generator=g, device=DEV) < 0.1
+    c.pos[1, pad] = -1
+    c.pos[2, far & ~pad] = 600
+    c.slots[none] = -1
+    q = c.run(workspace=ws)
+    assert pa.pa_read_device_status(ws) == pa.PA_ERR_OUT_OF_RANGE
+    skipped = pad | far
+    assert bool((q[skipped] == 5.0).all())
+    c.pos[:, skipped] = 0
+    want, err = c.turned(c.parts()[0], c.wq, 1e-6, 0.0, False)
+    assert bool(((q.double() - want).abs() <= err + 2.0 ** -8 * (want.abs() + err))[~skipped].all())
+    want, err = c.turned(c.parts()[1], c.wk, 1e-6, 0.0, False)
+    live = ~skipped & ~none
+    rows = c.kc[c.slots[live] // c.bs, :, c.slots[live] % c.bs].double()
+    assert bool(((rows - want[live]).abs() <= err[live] + 2.0 ** -8 * (want[live].abs() + err[live])).all())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+def test_stored_values_are_those_of_the_slot_write(kind):
+    """V in an FP8 cache: the codes that pa_reshape_and_cache writes, bit for bit, NaNs and
+    infinities, zeros of both signs and scales of any size among them."""
+    T, hq, hkv = 5000, 12, 2
+    g = torch.Generator(device=DEV).manual_seed(9)
+    bits = torch.randint(-32768, 32768, (T, hq + 2 * hkv, 128), generator=g, device=DEV, dtype=torch.int16)
+    qkv = bits.view(TYPES[kind])
+    slots = torch.randperm(5008, generator=g, device=DEV)[:T]
+    table = torch.ones(16, 128, device=DEV)
+    for scale in (1.0, 0.013, 3e-3, 2.0 ** -70, 1e-38, 2.0 ** 66):
+        ks = torch.full((1,), scale, device=DEV)
+        kc, vc, k2, v2 = (torch.zeros(313, hkv, 16, 128, dtype=torch.uint8, device=DEV) for _ in range(4))
+        q = torch.empty(T, hq, 128, dtype=qkv.dtype, device=DEV)
+        for t in (T, 40):
+            pa.pa_norm_rope_and_cache(q[:t], qkv[:t, :hq], qkv[:t, hq:hq + hkv], qkv[:t, hq + hkv:], kc, vc, slots[:t],
+                                      torch.zeros(t, dtype=torch.int64, device=DEV), table, k_scale=ks, v_scale=ks)
+            v = qkv[:t, hq + hkv:].contiguous()
+            pa.pa_reshape_and_cache(v, v, k2, v2, slots[:t].contiguous(), ks, ks)
+            assert torch.equal(vc, v2), scale
