@@ -3,6 +3,8 @@ calls over it (csrc/binding.c) with the C compiler."""
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.metadata
+import importlib.util
 import os
 import platform
 import shutil
@@ -21,7 +23,13 @@ HEADERS = ["pa_device.cuh", "pa_internal.h"]
 BUILD_DIR = os.path.join(HERE, "_build", platform.machine())
 LIB_PATH = os.path.join(BUILD_DIR, "libpa.so")
 BINDING = "binding.c"
-BINDING_PATH = os.path.join(BUILD_DIR, "_binding" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+TENSOR_INFO = "tensor_info.cpp"
+try:
+    _TORCH = importlib.metadata.version("torch")
+except importlib.metadata.PackageNotFoundError:
+    _TORCH = "unknown"
+# named by the torch it is built against, whose tensors it reads
+BINDING_PATH = os.path.join(BUILD_DIR, f"_binding-{_TORCH}" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -46,7 +54,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     that go through it raise ImportError; the library and all other calls do not need it."""
     if force or _stale(LIB_PATH, SOURCES + HEADERS):
         _build_lib(verbose)
-    if force or _stale(BINDING_PATH, [BINDING]):
+    if force or _stale(BINDING_PATH, [BINDING, TENSOR_INFO, "tensor_info.h"]):
         try:
             _build_binding()
         except (OSError, RuntimeError) as e:
@@ -84,15 +92,35 @@ def _build_lib(verbose: bool) -> None:
     os.replace(tmp, LIB_PATH)
 
 
-def _build_binding() -> None:
-    """The extension module of the calls in csrc/binding.c, beside libpa.so and linked to it."""
-    tmp = BINDING_PATH + f".{os.getpid()}.tmp"
-    cmd = [shutil.which("gcc") or shutil.which("cc") or "cc", "-O2", "-shared", "-fPIC", "-I", INCLUDE,
-           "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, BINDING), "-o", tmp,
-           "-L", BUILD_DIR, "-l:libpa.so", "-Wl,-rpath,$ORIGIN"]
+def _run(cmd, what: str) -> None:
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
-        raise RuntimeError(f"building {BINDING} failed:\n{res.stdout}\n{res.stderr}")
+        raise RuntimeError(f"building {what} failed:\n{res.stdout}\n{res.stderr}")
+
+
+def _build_binding() -> None:
+    """The extension module of the calls in csrc/binding.c, beside libpa.so and linked to it, with
+    csrc/tensor_info.cpp if torch's headers and a C++ compiler are there (else tensors are asked
+    through their Python methods)."""
+    tmp = BINDING_PATH + f".{os.getpid()}.tmp"
+    cc = shutil.which("gcc") or shutil.which("cc") or "cc"
+    flags = ["-O2", "-fPIC", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"]]
+    objs, libs = [os.path.join(BUILD_DIR, f"binding.{os.getpid()}.o")], []
+    _run([cc, *flags, "-c", os.path.join(CSRC, BINDING), "-o", objs[0]], BINDING)
+    try:
+        torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+        info = os.path.join(BUILD_DIR, f"tensor_info.{os.getpid()}.o")
+        _run([shutil.which("g++") or shutil.which("c++") or "c++", *flags, "-std=c++17",
+              "-I", os.path.join(torch_dir, "include"),
+              "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+              "-c", os.path.join(CSRC, TENSOR_INFO), "-o", info], TENSOR_INFO)
+        objs.append(info)
+        libs = ["-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lstdc++"]
+    except (OSError, RuntimeError) as e:
+        warnings.warn(f"{TENSOR_INFO} was not built, calls take longer: {e}", RuntimeWarning, stacklevel=2)
+    _run([cc, "-shared", *objs, "-o", tmp, "-L", BUILD_DIR, "-l:libpa.so", "-Wl,-rpath,$ORIGIN", *libs], BINDING)
+    for obj in objs:
+        os.remove(obj)
     os.replace(tmp, BINDING_PATH)
 
 

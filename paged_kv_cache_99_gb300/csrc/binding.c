@@ -12,6 +12,10 @@
 #include <Python.h>
 
 #include "pa.h"
+#include "tensor_info.h"
+
+/* absent where tensor_info.cpp could not be built */
+#pragma weak pa_tensor_info
 
 enum { BF16 = 1, FP16 = 2, U8 = 4, E4M3 = 8, F32 = 16, I32 = 32, I64 = 64 };
 enum { HALVES = BF16 | FP16, CACHES = BF16 | FP16 | U8 | E4M3 };
@@ -38,8 +42,12 @@ static int as_int(PyObject* o, long long* out) {
     return *out == -1 && PyErr_Occurred() ? -1 : 0;
 }
 
+static int info_of(PyObject* t, TensorInfo* info) { return pa_tensor_info && pa_tensor_info(t, info) == 0; }
+
 static int device_of(PyObject* t, const char* name, long long* device) {
-    if (!PyObject_TypeCheck(t, tensor_type)) *device = -1;
+    TensorInfo info;
+    if (info_of(t, &info)) *device = info.device;
+    else if (!PyObject_TypeCheck(t, tensor_type)) *device = -1;
     else if (as_int(PyObject_CallMethodNoArgs(t, s_get_device), device)) return -1;
     if (*device >= 0) return 0;
     PyErr_Format(PyExc_TypeError, "%s must be a CUDA tensor", name);
@@ -49,35 +57,57 @@ static int device_of(PyObject* t, const char* name, long long* device) {
 /* Reads a tensor of one of `allowed` types on `device` with ndim dimensions (0: any).  rows: each
  * token's heads are contiguous, with any stride between tokens; otherwise it is contiguous. */
 static int take(PyObject* t, const char* name, int allowed, int ndim, long long device, int rows, Tensor* out) {
-    long long dev, ptr;
-    if (device_of(t, name, &dev)) return -1;
-    PyObject* dtype = PyObject_GetAttr(t, s_dtype);
-    if (!dtype) return -1;
-    out->type = 0;
-    for (int i = 0; i < NUM_TYPES; ++i)
-        if (dtype == types[i]) out->type = 1 << i;
-    if (!(out->type & allowed)) {
-        PyErr_Format(PyExc_TypeError, "%s: dtype %S is not one it can have", name, dtype);
-        Py_DECREF(dtype);
+    long long dev, ptr = 0, strides[3];
+    TensorInfo info;
+    const int known = info_of(t, &info);
+    if (known) {
+        dev = info.device;
+        if (dev < 0) {
+            PyErr_Format(PyExc_TypeError, "%s must be a CUDA tensor", name);
+            return -1;
+        }
+        out->type = info.type < 0 ? 0 : 1 << info.type;
+    } else if (device_of(t, name, &dev)) {
         return -1;
     }
-    Py_DECREF(dtype);
+    if (!known || !(out->type & allowed)) {
+        PyObject* dtype = PyObject_GetAttr(t, s_dtype);
+        if (!dtype) return -1;
+        out->type = 0;
+        for (int i = 0; i < NUM_TYPES; ++i)
+            if (dtype == types[i]) out->type = 1 << i;
+        if (!(out->type & allowed)) {
+            PyErr_Format(PyExc_TypeError, "%s: dtype %S is not one it can have", name, dtype);
+            Py_DECREF(dtype);
+            return -1;
+        }
+        Py_DECREF(dtype);
+    }
     if (dev != device) {
         PyErr_Format(PyExc_ValueError, "%s is on cuda:%lld, not on cuda:%lld", name, dev, device);
         return -1;
     }
-    PyObject* shape = PyObject_GetAttr(t, s_shape);
-    if (!shape) return -1;
-    const Py_ssize_t n = PyTuple_Check(shape) ? PyTuple_GET_SIZE(shape) : -1;
-    out->ndim = (int)n;
+    Py_ssize_t n;
     out->numel = 1;
-    for (Py_ssize_t i = 0; i < n; ++i) {
-        const long long d = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, i));
-        out->numel *= d;
-        if (i < 4) out->shape[i] = d;
+    if (known) {
+        n = info.ndim;
+        for (Py_ssize_t i = 0; i < n; ++i) {
+            out->numel *= info.shape[i];
+            if (i < 4) out->shape[i] = info.shape[i];
+        }
+    } else {
+        PyObject* shape = PyObject_GetAttr(t, s_shape);
+        if (!shape) return -1;
+        n = PyTuple_Check(shape) ? PyTuple_GET_SIZE(shape) : -1;
+        for (Py_ssize_t i = 0; i < n; ++i) {
+            const long long d = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, i));
+            out->numel *= d;
+            if (i < 4) out->shape[i] = d;
+        }
+        Py_DECREF(shape);
+        if (PyErr_Occurred()) return -1;
     }
-    Py_DECREF(shape);
-    if (PyErr_Occurred()) return -1;
+    out->ndim = (int)n;
     if (ndim && n != ndim) {
         PyErr_Format(PyExc_ValueError, "%s must have %d dimensions, not %zd", name, ndim, n);
         return -1;
@@ -90,27 +120,40 @@ static int take(PyObject* t, const char* name, int allowed, int ndim, long long 
     }
     if (rows) {
         const long long heads = out->shape[1], d = out->shape[2];
-        PyObject* st = PyObject_CallMethodNoArgs(t, s_stride);
-        if (!st) return -1;
-        const long long s0 = PyLong_AsLongLong(PyTuple_GET_ITEM(st, 0)), s1 = PyLong_AsLongLong(PyTuple_GET_ITEM(st, 1)),
-                        s2 = PyLong_AsLongLong(PyTuple_GET_ITEM(st, 2));
-        Py_DECREF(st);
-        if (out->shape[0] && ((s2 != 1 && d > 1) || (s1 != d && heads > 1))) {
+        if (known) {
+            for (int i = 0; i < 3; ++i) strides[i] = info.stride[i];
+        } else {
+            PyObject* st = PyObject_CallMethodNoArgs(t, s_stride);
+            if (!st) return -1;
+            for (int i = 0; i < 3; ++i) strides[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(st, i));
+            Py_DECREF(st);
+        }
+        if (out->shape[0] && ((strides[2] != 1 && d > 1) || (strides[1] != d && heads > 1))) {
             PyErr_Format(PyExc_ValueError, "%s: the heads of a token must be contiguous", name);
             return -1;
         }
-        out->step = out->shape[0] > 1 ? s0 : heads * d;     /* a single token's stride means nothing */
+        out->step = out->shape[0] > 1 ? strides[0] : heads * d;     /* a single token's stride means nothing */
     } else {
-        PyObject* c = PyObject_CallMethodNoArgs(t, s_is_contiguous);
-        if (!c) return -1;
-        Py_DECREF(c);
-        if (c != Py_True) {
+        int contiguous;
+        if (known) {
+            contiguous = info.contiguous;
+        } else {
+            PyObject* c = PyObject_CallMethodNoArgs(t, s_is_contiguous);
+            if (!c) return -1;
+            contiguous = c == Py_True;
+            Py_DECREF(c);
+        }
+        if (!contiguous) {
             PyErr_Format(PyExc_ValueError, "%s must be contiguous", name);
             return -1;
         }
     }
-    if (as_int(PyObject_CallMethodNoArgs(t, s_data_ptr), &ptr)) return -1;
-    out->ptr = (void*)ptr;
+    if (known) {
+        out->ptr = info.ptr;
+    } else {
+        if (as_int(PyObject_CallMethodNoArgs(t, s_data_ptr), &ptr)) return -1;
+        out->ptr = (void*)ptr;
+    }
     return 0;
 }
 

@@ -1,0 +1,34 @@
+// What binding.c asks about a tensor, read from the tensor itself: five calls of its Python
+// methods cost 0.3 us on the Grace cores, and a call checks up to sixty tensors.  Built against
+// the headers of the torch that is installed; without them binding.c calls the methods.
+#include <torch/csrc/autograd/python_variable.h>
+
+#include "tensor_info.h"
+
+// 0: *out is filled.  -1: not an exact tensor (or one without storage), ask its methods.
+extern "C" int pa_tensor_info(PyObject* o, TensorInfo* out) noexcept {
+    try {
+        if (!THPVariable_CheckExact(o)) return -1;
+        const c10::TensorImpl* t = THPVariable_Unpack(o).unsafeGetTensorImpl();
+        if (!t->has_storage() || t->layout() != c10::kStrided) return -1;
+        switch (c10::typeMetaToScalarType(t->dtype())) {
+            case c10::ScalarType::BFloat16: out->type = 0; break;
+            case c10::ScalarType::Half: out->type = 1; break;
+            case c10::ScalarType::Byte: out->type = 2; break;
+            case c10::ScalarType::Float8_e4m3fn: out->type = 3; break;
+            case c10::ScalarType::Float: out->type = 4; break;
+            case c10::ScalarType::Int: out->type = 5; break;
+            case c10::ScalarType::Long: out->type = 6; break;
+            default: out->type = -1;
+        }
+        out->device = t->device().is_cuda() ? t->device().index() : -1;
+        out->ptr = const_cast<void*>(t->data());
+        out->ndim = static_cast<int>(t->dim());
+        out->shape = t->sizes().data();
+        out->stride = t->strides().data();
+        out->contiguous = t->is_contiguous();
+        return 0;
+    } catch (...) {
+        return -1;
+    }
+}
