@@ -22,11 +22,15 @@
 // ahead across segments.  Rows past the unit's are not computed: a warp whose 32 rows are all
 // past them only passes the barriers.
 //
-// Warps: 0 copies K and V (TMA, 128-byte swizzle, a lane per 8 or 16 rows of a block), 1 issues
-// tcgen05.mma, 2 walks the range and describes the segments to the others, 3 copies
-// the queries (TMA) and zeroes V rows that no row sees (0 x NaN is NaN), 4-7 and 8-11 are
-// the softmax of tiles A and B, a thread per row; with an FP8 cache 12-15 widen the copied e4m3
-// rows exactly to fp16, which costs them about as long as the copies take.
+// Warps: 0 walks the range, describes its segments to the others and issues every copy (TMA,
+// 128-byte swizzle: a lane per 8 or 16 rows of a block of K and V, one box of queries); 1 issues
+// tcgen05.mma; with a 16-bit cache 3 zeroes V rows that no row sees (0 x NaN is NaN), with an FP8
+// cache 2 and 3 widen the copied e4m3 rows exactly to fp16, which costs them about as long as a
+// step's products take; 4-11 and 12-19 are the softmax of tiles A and B, two threads to a row,
+// each with 64 of a step's keys.  The two tiles go from segment to segment on their own (a pair's
+// A ends half a step before B), and read the next segment's masks and scales, and with FP8 caches
+// turn its bf16 queries to fp16, while the last products run: 8192 tokens of one prompt, 32/8
+// heads, plain scores 484 -> 437 us, FP8 509 -> 488.
 // Every wait is bounded.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -58,7 +62,7 @@ template <int Kind>
 struct Cfg {
     static constexpr bool kFp8 = Kind == kKindFp8;
     static constexpr bool kMmaBf16 = Kind == kKindBf16;
-    static constexpr int kStages = kFp8 ? 3 : 5;         // K and V tiles of 16-bit elements
+    static constexpr int kStages = kFp8 ? 3 : 4;         // K and V tiles of 16-bit elements
     static constexpr int kRaw = kFp8 ? 4 : 1;            // FP8: e4m3 tiles as copied
     static constexpr uint32_t kOffStage = 2 * kTileBytes;                    // behind Q_A, Q_B
     static constexpr uint32_t kOffRaw = kOffStage + kStages * kTileBytes;
@@ -83,14 +87,13 @@ enum {                                       // barriers, 8 bytes each
     kQFull = kSegEmpty + kSegs,              // [Q buffer]
     kQEmpty = kQFull + 2,                    // [Q buffer]
     kSFull = kQEmpty + 2,                    // [tile]
-    kPHalf = kSFull + 2,                     // [tile] P of the step's first 64 keys is stored
-    kPFull = kPHalf + 2,                     // [tile]
-    kSegDone = kPFull + 2,                   // every product of the segment is done
-    kMlReady,                                // solo: both tiles' (maximum, sum) are in shared memory
-    kOFree,                                  // the segment's outputs are read
+    kPFull = kSFull + 2,                     // [tile] P is stored, O rescaled where it had to be
+    kSegDone = kPFull + 2,                   // [tile] every product of the segment is done
+    kMlReady = kSegDone + 2,                             // solo: both tiles' (maximum, sum) are in shared memory
+    kOFree,                                  // solo: the segment's outputs are read
     kFixed,                                  // [stage] V rows that no row sees are zeroed (edge steps)
     kIssued = kFixed + 5,                    // [stage] the copy of an edge step's V is under way
-    kQLand = kIssued + 5,                    // [Q buffer] a bf16 query of an FP8 cache has landed
+    kQLand = kIssued + 5,                    // [Q buffer] an FP8 cache's bf16 queries have landed
     kPair = kQLand + 2,                      // [tile][warp's rows] the two threads of a row have met
     kNumBars = kPair + 8
 };
@@ -320,14 +323,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bar(kSegEmpty + i), kSegReaders);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(kQFull + i), kFp8 && QBf16 ? 2 : 1);
+            mbar_init(bar(kQFull + i), kFp8 && QBf16 ? kSoftmaxWarps : 1);
             mbar_init(bar(kQEmpty + i), 1);
             mbar_init(bar(kQLand + i), 1);
             mbar_init(bar(kSFull + i), 1);
-            mbar_init(bar(kPHalf + i), 8);
-            mbar_init(bar(kPFull + i), 4);
+            mbar_init(bar(kPFull + i), 8);
+            mbar_init(bar(kSegDone + i), 1);
         }
-        mbar_init(bar(kSegDone), 1);
         mbar_init(bar(kMlReady), kSoftmaxWarps);
         mbar_init(bar(kOFree), kSoftmaxWarps);
         for (int i = 0; i < 8; ++i) mbar_init(bar(kPair + i), 2);
@@ -447,22 +449,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int rsh = min(bsh, 4);                          // log2 of a piece's rows
             const int per_step = kKeys >> rsh;                    // pieces per step: 8 or 16
             if (lane == 0) p.records[cta].rows = 0;
+            SeqView at = sv_cur;
             int r = 0;                                            // tiles copied so far
-            unsigned q_used = 0, q_par = 0;                       // bit b: the Q buffer was filled, parity of its releases
+            // bit b: the Q buffer was filled, parity of its fills, of its releases
+            unsigned q_used = 0, q_sent = 0, q_par = 0;
             while (ok) {
                 // the range's part of the next unit, places [coff, coff + take) of its cost, of which
                 // the first `lead` stand for its start: steps [a, b)
                 Unit u = {};
-                SeqView sv = sv_cur;
+                SeqView sv = at;
                 int a = 0, steps = 0, seq = cs, head = ch, cost = 0, unit_f = f;
                 while (left > 0 && steps == 0) {
-                    u = unit_of(p, sv_cur, ct);
+                    u = unit_of(p, at, ct);
                     const int lead = unit_lead(p, u);
                     cost = u.steps + lead;
                     const int take = min(left, cost - coff);
                     a = max(coff - lead, 0);
                     steps = max(coff + take - lead, 0) - a;       // 0: nothing but the start, the next CTA has the steps
-                    sv = sv_cur;
+                    sv = at;
                     seq = cs;
                     head = ch;
                     unit_f = f - coff;
@@ -471,11 +475,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     coff = 0;
                     if (left > 0 && ++ch == p.num_kv_heads) {
                         ch = 0;
-                        if (++ct == units_per_head(p, sv_cur)) {
+                        if (++ct == units_per_head(p, at)) {
                             ct = 0;
                             do {
-                                sv_cur = seq_view(p, ++cs, false);
-                            } while (sv_cur.q_len == 0);
+                                at = seq_view(p, ++cs, false);
+                            } while (at.q_len == 0);
                         }
                     }
                 }
@@ -524,6 +528,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 // ---- its copies ----
+                // a solo's keys are read once, beside partials and tables that are read again: they leave
+                // L2 first (16 x 8192 tokens, trees of 24: 70.6 -> 66.6 us)
+                const uint64_t policy = solo ? l2_policy_evict_first() : l2_policy_evict_normal();
                 const int32_t* bt = p.block_tables + static_cast<size_t>(seq) * p.max_blocks;
                 const int c_lo = u.klo >> rsh, c_hi = (u.khi - 1) >> rsh;     // pieces that hold keys
                 // the lane's piece of a step: its row in the cache, -1 for none
@@ -553,11 +560,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (y >= 0) {
                         if constexpr (kFp8) {
-                            tma_load_2d(sbase + C::kOffRaw + st * kHalfBytes + (lane << rsh) * 128, map, 0, y, full);
+                            tma_load_2d_hint(sbase + C::kOffRaw + st * kHalfBytes + (lane << rsh) * 128, map, 0, y, full, policy);
                         } else {
                             const uint32_t dst = sbase + C::kOffStage + st * kTileBytes + (lane << rsh) * 128;
-                            tma_load_2d(dst, map, 0, y, full);
-                            tma_load_2d(dst + kHalfBytes, map, 64, y, full);
+                            tma_load_2d_hint(dst, map, 0, y, full, policy);
+                            tma_load_2d_hint(dst + kHalfBytes, map, 64, y, full, policy);
                         }
                     }
                     ++r;
@@ -577,6 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         q_par ^= 1u << b;
                     }
                     q_used |= 1u << b;
+                    q_sent ^= 1u << b;
                     const uint32_t landed = bar((kFp8 && QBf16 ? kQLand : kQFull) + b), dst = sbase + b * kTileBytes;
                     if (lane == 0) {
                         mbar_arrive_expect_tx(landed, static_cast<uint32_t>(QT * G) * 256);
@@ -603,6 +611,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 constexpr int kRing = kFp8 ? C::kRaw : NS;
                 constexpr int kF = kFp8 ? static_cast<int>(kRawFull) : static_cast<int>(kFull);
                 for (int i = max(0, r - kRing); i < r; ++i) warp_wait_all(bar(kF + i % kRing), (i / kRing) & 1, p.timeout_ns);
+                for (int b = 0; b < 2; ++b)
+                    if (q_used >> b & 1) warp_wait_all(bar((kFp8 && QBf16 ? kQLand : kQFull) + b), (q_sent >> b & 1) ^ 1u, p.timeout_ns);
             }
         } else if (warp == 1) {
             // ================= MMA issuer =================
@@ -638,14 +648,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     umma_commit(bar(kSFull + x));
                 }
             };
-            // P.V over the step's keys 64 half .. 64 half + 63; V is MN-major: d-halves kHalfBytes
-            // apart, 16 keys = 2 KiB
-            auto issue_pv = [&](int x, int stage_v, int half, bool first) {
+            // P.V over the step's keys; V is MN-major: d-halves kHalfBytes apart, 16 keys = 2 KiB
+            auto issue_pv = [&](int x, int stage_v, bool first) {
                 if (leader) {
-                    const uint32_t b = (tiles + stage_v * (kTileBytes >> 4) + half * (kKeys / 32) * 128) | ((kHalfBytes >> 4) << 16);
+                    const uint32_t b = (tiles + stage_v * (kTileBytes >> 4)) | ((kHalfBytes >> 4) << 16);
 #pragma unroll
-                    for (int e = 0; e < kKeys / 32; ++e)
-                        mma_ts(tO(x), tS(x) + 8 * (half * (kKeys / 32) + e), b + e * 128, idPV, !first || half > 0 || e > 0);
+                    for (int e = 0; e < kKeys / 16; ++e) mma_ts(tO(x), tS(x) + 8 * e, b + e * 128, idPV, !first || e > 0);
                 }
             };
             auto commit = [&](int b) {
@@ -654,14 +662,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             // parities as bits: an array indexed at run time would live in local memory
             unsigned fixes = 0;                      // bit st: of the stage's zeroings
             unsigned q_par = 0, p_par = 0;           // bit x: of the buffer's fills, of the tile's P
-            auto pv = [&](int x, int stage_v, bool first) -> bool {
-                if (!wait(bar(kPHalf + x), p_par >> x & 1)) return false;
-                tc_fence_after();
-                issue_pv(x, stage_v, 0, first);
-                if (!wait(bar(kPFull + x), p_par >> x & 1)) return false;
-                tc_fence_after();
-                issue_pv(x, stage_v, 1, first);
+            // P of tile x and whatever else the products need, asked for together: each test takes a
+            // hundred cycles or so, side by side no more than one
+            auto p_and = [&](int x, uint32_t b1, uint32_t par1, uint32_t b2, uint32_t par2) -> bool {
+                const bool p0 = mbar_test(bar(kPFull + x), p_par >> x & 1), p1 = mbar_test(b1, par1), p2 = mbar_test(b2, par2);
+                if (!__all_sync(0xffffffffu, p0 && p1 && p2) &&
+                    !(wait(b1, par1) && wait(b2, par2) && wait(bar(kPFull + x), p_par >> x & 1)))
+                    return false;
                 p_par ^= 1u << x;
+                tc_fence_after();
                 return true;
             };
             int seg = 0;
@@ -684,12 +693,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     commit(kQEmpty + qa);
                     if (!solo) commit(kQEmpty + 1);
                 };
-                // V of step i at the next place: landed, and its unseen rows zeroed
-                auto v_ready = [&](int i) -> bool {
-                    if (!wait(bar(kFull + st), ph)) return false;
+                // V of step i is at place v_st: its unseen rows have to be zeroed
+                auto v_fixed = [&](int i, int v_st) -> bool {
                     if (!kFp8 && edge_step(flags, tail, i)) {
-                        if (!wait(bar(kFixed + st), fixes >> st & 1)) return false;
-                        fixes ^= 1u << st;
+                        if (!wait(bar(kFixed + v_st), fixes >> v_st & 1)) return false;
+                        fixes ^= 1u << v_st;
                     }
                     return true;
                 };
@@ -711,11 +719,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     for (int i = 0; i < n; ++i) {
                         // V(i), then K(i + 2) for the same tile
-                        if (!v_ready(i)) break;
                         const int v_st = st, x = i & 1;
-                        advance();
-                        if (!pv(x, v_st, i < 2)) break;
+                        const uint32_t v_bar = bar(kFull + st);
+                        if (!v_fixed(i, v_st) || !p_and(x, v_bar, ph, v_bar, ph)) break;
+                        issue_pv(x, v_st, i < 2);
                         commit(kEmpty + v_st);
+                        advance();
                         if (i + 2 < n) {
                             if (!wait(bar(kFull + st), ph)) break;
                             tc_fence_after();
@@ -725,29 +734,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                             advance();
                         }
                     }
+                    // (B's warps are in this segment too, if it has no step for them)
+                    if (n == 1) {
+                        if (!wait(bar(kPFull + 1), p_par >> 1 & 1)) break;
+                        p_par ^= 2u;
+                    }
+                    if (!ok) break;
+                    commit(kSegDone);
                 } else {
                     for (int i = 0; i < n; ++i) {
                         // K(i + 1) and V(i), for both tiles
                         const bool more = i + 1 < n;
                         const int k_st = st;
-                        if (more) {
-                            if (!wait(bar(kFull + st), ph)) break;
-                            advance();
-                        }
-                        if (!v_ready(i)) break;
+                        const uint32_t k_bar = bar(kFull + st), k_ph = ph;
+                        if (more) advance();
                         const int v_st = st;
-                        advance();
-                        if (!pv(0, v_st, i == 0)) break;
+                        const uint32_t v_bar = bar(kFull + st);
+                        if (!v_fixed(i, v_st) || !p_and(0, more ? k_bar : v_bar, more ? k_ph : ph, v_bar, ph)) break;
+                        issue_pv(0, v_st, i == 0);
                         if (more) issue_s(0, 0, k_st);
-                        if (!pv(1, v_st, i == 0)) break;
+                        else commit(kSegDone);
+                        if (!p_and(1, v_bar, ph, v_bar, ph)) break;
+                        issue_pv(1, v_st, i == 0);
                         if (more) issue_s(1, 1, k_st);
                         commit(kEmpty + v_st);
                         if (more) commit(kEmpty + k_st);
                         if (i + 2 == n) q_free();
+                        advance();
                     }
                 }
                 if (!ok) break;
-                commit(kSegDone);
+                commit(kSegDone + 1);
                 ++seg;
             }
             if (!ok && leader) atomicOr(p.status, kDevErrTimeout);
@@ -756,10 +773,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ================= FP8: e4m3 rows to fp16 tiles, two of a tile's rows a thread =================
             const int part = warp - 2;
             int r = 0;
-            [[maybe_unused]] unsigned q_fills = 0;   // bit b: parity of the Q buffer's copies
             Seg g;
             while (ok && next_seg(g)) {
-                const bool solo = g.flags & 1;
                 const int two = min(2, g.steps), both = 2 * max(g.steps - 2, 0);
                 for (int it = 0; it < 2 * g.steps && ok; ++it, ++r) {
                     // the item's step, and whether it is V
@@ -813,41 +828,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) {
                         mbar_arrive(bar(kFull + st));
                         mbar_arrive(bar(kRawEmpty + rs));
-                    }
-                    if constexpr (QBf16) {
-                        // behind the first K tile the queries, bf16 to fp16 as the widened codes: exact for
-                        // magnitudes 2^-14 to 65504, 2^-25 off below, infinite above
-                        for (int x = 0; x < (solo ? 1 : 2) && it == 0; ++x) {
-                            const int b = solo ? (k - 1) & 1 : x;
-                            if (!warp_wait_all(bar(kQLand + b), q_fills >> b & 1, p.timeout_ns)) {
-                                ok = false;
-                                break;
-                            }
-                            q_fills ^= 1u << b;
-                            uint4* q = reinterpret_cast<uint4*>(sm + b * kTileBytes);
-                            const int chunks = min(QT, g.nq - x * QT) * G * 8;      // of 16 bytes, in each half
-#pragma unroll 1
-                            for (int c0 = 32 * part + lane; c0 < chunks; c0 += 2 * 64) {
-                                uint4 v[4];
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const int c = c0 + 64 * (e >> 1);
-                                    if (c < chunks) v[e] = q[(e & 1) * (kHalfBytes / 16) + c];
-                                }
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const int c = c0 + 64 * (e >> 1);
-                                    uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
-#pragma unroll
-                                    for (int a = 0; a < 4; ++a)
-                                        w[a] = pack2<false>(to_float<true>(w[a] & 0xffffu), to_float<true>(w[a] >> 16));
-                                    if (c < chunks) q[(e & 1) * (kHalfBytes / 16) + c] = make_uint4(w[0], w[1], w[2], w[3]);
-                                }
-                            }
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(bar(kQFull + b));
-                        }
                     }
                 }
             }
@@ -903,7 +883,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t s_addr = tS(x) + lane_off + NC * half;               // its scores
         const uint32_t p_addr = s_addr - NC / 2 * half;                     // its P, 16 bits each
         const int exch = (2 * x + half) * kRows + r;   // in row_smem; the row's other thread: exch ^ kRows
-        unsigned par = 0;                              // parities: 1 of S, 2 of the solos, 4 of the meetings
+        // parities: 1 of S, 2 of the solos, 4 of the meetings, 8 and 16 of the Q buffers' copies
+        unsigned par = 0;
         auto meet = [&]() -> bool {                    // both threads of the row
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kPair + 4 * x + quarter));
@@ -914,52 +895,86 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Registers are short (a thread's scores take most of them, and a spill misses the little
         // L1 that is left): a segment's fields are read from shared memory where they are used,
         // and its slot is given back when its outputs are written.
-        while (ok) {
+        // What a segment's row needs from global memory is read ahead, while the products of the
+        // segment before it end.
+        RowView next_view;
+        float next_kscale = 1.0f, next_slope2 = 0.f;
+        bool next_live = false, more = false;
+        auto look_ahead = [&]() {
             if (!warp_wait_all(bar(kSegFull + k % kSegs), (k / kSegs) & 1, p.timeout_ns)) {
-                ok = false;
-                break;
+                ok = more = false;
+                return;
             }
             const int* d = segs + (k % kSegs) * kSegInts;
-            ++k;
-            if (d[kSegSteps] == 0) break;
-            const bool solo = d[kSegFlags] & 1;
-            RowView view = {0, 0, INT_MAX};
-            float kscale = 1.0f, slope2 = 0.f;
-            bool live;
-            {
-                const int jq = (solo ? 0 : x * QT) + r / G;
-                live = r < QT * G && jq < d[kSegNq];
-                if (live) view = row_view(p, SeqView{d[kSegRow0] - d[kSegJ0], d[kSegQLen], d[kSegN], d[kSegPrefix]}, d[kSegJ0] + jq);
-                if (kFp8) kscale = __ldg(p.k_scale + d[kSegHead] * p.scale_stride);
-                if (Form == kBiasedScores && p.slopes && live) slope2 = __ldg(p.slopes + d[kSegHead] * G + r % G) * 1.4426950408889634f;
+            more = d[kSegSteps] != 0;
+            if (!more) return;
+            const int jq = (d[kSegFlags] & 1 ? 0 : x * QT) + r / G;
+            next_live = r < QT * G && jq < d[kSegNq];
+            next_view = RowView{0, 0, INT_MAX};
+            if (next_live)
+                next_view = row_view(p, SeqView{d[kSegRow0] - d[kSegJ0], d[kSegQLen], d[kSegN], d[kSegPrefix]}, d[kSegJ0] + jq);
+            if (kFp8) next_kscale = __ldg(p.k_scale + d[kSegHead] * p.scale_stride);
+            if (Form == kBiasedScores && p.slopes)
+                next_slope2 = next_live ? __ldg(p.slopes + d[kSegHead] * G + r % G) * 1.4426950408889634f : 0.f;
+            if constexpr (kFp8 && QBf16) {
+                // its queries, bf16 to fp16 as the widened codes: exact for magnitudes 2^-14 to 65504, 2^-25
+                // off below, infinite above.  A pair's tile by its own warps, a solo's by all.
+                const bool solo = d[kSegFlags] & 1;
+                const int b = solo ? k & 1 : x;
+                if (!warp_wait_all(bar(kQLand + b), par >> (3 + b) & 1, p.timeout_ns)) {
+                    ok = more = false;
+                    return;
+                }
+                par ^= solo ? 8u << b : 24u;
+                uint4* q = reinterpret_cast<uint4*>(sm + b * kTileBytes);
+                const int chunks = min(QT, d[kSegNq] - (solo ? 0 : x * QT)) * G * 8;      // of 16 bytes, in each half
+#pragma unroll 1
+                for (int c = (warp - 4 - (solo ? 0 : 8 * x)) * 32 + lane; c < chunks; c += solo ? 512 : 256) {
+                    uint4 v[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) v[e] = q[e * (kHalfBytes / 16) + c];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
+#pragma unroll
+                        for (int a = 0; a < 4; ++a)
+                            w[a] = pack2<false>(to_float<true>(w[a] & 0xffffu), to_float<true>(w[a] >> 16));
+                        q[e * (kHalfBytes / 16) + c] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_n(bar(kQFull + b), solo ? 1 : 2);
             }
+        };
+        look_ahead();
+        while (more) {
+            const int* d = segs + (k % kSegs) * kSegInts;
+            ++k;
+            const bool solo = d[kSegFlags] & 1;
+            const RowView view = next_view;
+            const float kscale = next_kscale;
+            [[maybe_unused]] const float slope2 = next_slope2;
+            const bool live = next_live;
             const bool warp_live = __any_sync(0xffffffffu, live);
-            const int lo_max = __reduce_max_sync(0xffffffffu, view.lo);
-            const int hi_min = __reduce_min_sync(0xffffffffu, view.hi);
-            [[maybe_unused]] const int pos_min = __reduce_min_sync(0xffffffffu, live ? view.pos : INT_MAX);
             // never 0: hidden scores are infinite, and stay so under it
             const float s_raw = p.scale_log2 * kscale;
             const float s_log2 = s_raw == 0.f ? 1e-30f : s_raw;
             float m_used = -INFINITY, l = 0.f;
-            const int stride = solo ? 2 : 1;
             int key0 = (d[kSegStep] + (solo ? x : 0)) * kKeys + NC * half;
-            bool first = true;
             for (int left_steps = solo ? (d[kSegSteps] + 1 - x) >> 1 : d[kSegSteps]; left_steps > 0;
-                 --left_steps, key0 += stride * kKeys, first = false) {
+                 --left_steps, key0 += (d[kSegFlags] & 1 ? 2 : 1) * kKeys) {
                 if (!warp_wait_all(bar(kSFull + x), par & 1, p.timeout_ns)) {
                     ok = false;
                     break;
                 }
                 par ^= 1u;
                 if (!warp_live) {                       // rows past the unit's: nothing reads their P
-                    if (lane == 0) {
-                        mbar_arrive(bar(kPHalf + x));
-                        if (half) mbar_arrive(bar(kPFull + x));
-                    }
+                    if (lane == 0) mbar_arrive(bar(kPFull + x));
                     continue;
                 }
                 tc_fence_after();
-                const bool need_mask = key0 < lo_max || key0 + NC > hi_min;
+                const bool need_mask = __any_sync(0xffffffffu, key0 < view.lo || key0 + NC > view.hi);
                 // what the row sees of the thread's keys
                 uint32_t vis[NC / 32];
 #pragma unroll
@@ -999,7 +1014,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const float by = p.cap > 0.f ? 1.0f : s_log2;
                     const uint64_t by2 = f2_pack(by, by);
-                    if (key0 + NC - 1 <= pos_min) {
+                    if (__all_sync(0xffffffffu, !live || key0 + NC - 1 <= view.pos)) {
                         // every key at or before every row: the bias grows by slope2 from key to key, and
                         // is counted on for four pairs from a place that is computed
                         const uint64_t step2 = f2_pack(2.f * slope2, 2.f * slope2);
@@ -1083,7 +1098,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const bool need = live && mx > m_used + kRescale;
-                const bool resc = __any_sync(0xffffffffu, need);
+                const bool resc = __any_sync(0xffffffffu, need && m_used > -INFINITY);
                 const float m_new = need ? mx : m_used;
                 // a row that has seen nothing yet: exponents against 0, all of hidden scores
                 const float m_at = m_new == -INFINITY ? 0.f : m_new;
@@ -1091,7 +1106,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 m_used = m_new;
                 // O is final for the products before: S(i) was issued behind them.  Rescaled
                 // before any of P(i) is released, since P.V(i) accumulates into it.
-                if (!first && resc) {
+                if (resc) {
 #pragma unroll 1
                     for (int c = 0; c < kHeadDim / 32; ++c) {       // few registers beside the scores
                         const uint32_t o_addr = tO(x) + lane_off + kHeadDim / 2 * half + 16 * c;
@@ -1102,14 +1117,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
                         tmem_st16(o_addr, ov);
                     }
-                    if (half == 1) tmem_wait_st();
                 }
-                // the products of the first 64 keys wait for this half of O as well
-                if (half == 1) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(kPHalf + x));
-                }
+                __syncwarp();          // (and nothing below is begun above: it would spill)
                 // p = 2^(s * scale - m), rounded to the 16 bits that the tensor cores take beside V's
                 // (bf16 2^-8 of it at most, fp16, FP8 caches' type too, 2^-11; their sum is of the
                 // unrounded ones), written over the columns of S (keys 32 c .. +31 -> columns 16 c
@@ -1193,23 +1202,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l = l * alpha + sum;
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar((half ? kPFull : kPHalf) + x));
+                if (lane == 0) mbar_arrive(bar(kPFull + x));
             }
             // ---- the segment's outputs ----
+            if (solo && x == 1 && d[kSegSteps] == 1 && lane == 0) mbar_arrive(bar(kPFull + 1));
+            const float vscale = kFp8 ? __ldg(p.v_scale + d[kSegHead] * p.scale_stride) : 1.0f;
+            if (ok) look_ahead();
             if (!ok) break;
             if (warp_live) {                           // the row's sum
                 row_smem[exch] = l;
                 if (!meet()) break;
                 const float l2 = row_smem[exch ^ kRows];
                 l = half ? l2 + l : l + l2;
-                if (solo && !meet()) break;            // both have read: the places are free
+                if (!meet()) break;                    // both have read: the places are free
             }
-            if (!warp_wait_all(bar(kSegDone), (k - 1) & 1, p.timeout_ns)) {
+            if (!warp_wait_all(bar(kSegDone + x), (k - 1) & 1, p.timeout_ns)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            const float vscale = kFp8 ? __ldg(p.v_scale + d[kSegHead] * p.scale_stride) : 1.0f;
             const bool whole = d[kSegFlags] & 2;
             const size_t slot = static_cast<size_t>(d[kSegSlot]);
             const size_t orow = (static_cast<size_t>(d[kSegRow0] + (solo ? 0 : x * QT) + r / G) * p.num_q_heads + d[kSegHead] * G + r % G) * kHeadDim;
@@ -1242,12 +1253,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
             };
             float2* ml = p.ml + slot * (2 * kRows) + at_row;
-            // A warp goes on to the next segment once all have seen this one's end: its products
-            // (solo: also read by the other tile's warps) are overwritten, and no barrier can get
-            // two phases ahead of a warp.
+            // No barrier gets two phases ahead of a warp: a segment's end waits for P, or as much, of
+            // all of the tile's warps.
             if (!solo) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(kOFree));
                 if (warp_live) {
                     const float inv = l == 0.f ? 0.f : vscale / l;
 #pragma unroll 1
@@ -1295,15 +1303,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     put(c, ov, inv);
                     if (!whole && live && c == 0) *ml = make_float2(m, sum);
                 }
-                par ^= 2u;
+                // its products were read by both tiles' warps: the next may go over them when all are done
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kOFree));
+                if (!warp_wait_all(bar(kOFree), par >> 1 & 1, p.timeout_ns)) {
+                    ok = false;
+                    break;
+                }
+                par ^= 2u;
             }
-            if (!warp_wait_all(bar(kOFree), (k - 1) & 1, p.timeout_ns)) {
-                ok = false;
-                break;
-            }
+            tc_fence_before();
+            __syncwarp();
             if (lane == 0) mbar_arrive(bar(kSegEmpty + (k - 1) % kSegs));
         }
         if (!ok && lane == 0) atomicOr(p.status, kDevErrTimeout);
