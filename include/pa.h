@@ -507,7 +507,7 @@ PA_API size_t pa_workspace_size_scored(int num_seqs, int num_q_heads, int num_kv
  *   prefix_lens    device, int32 [num_seqs]: the sequence's first tokens that all its rows
  *                  see, those behind them too; NULL: none
  *   slopes         device, float32 [num_q_heads]; NULL: no bias
- *   cap            >= 0 and finite
+ *   cap            0, or from 1e-6 to 1e6 with scale / cap finite
  *   window         >= 0; 0: none.  Table entries of blocks that no row of a call sees through
  *                  the window need not name a block (they are not read)
  *   workspace      pa_workspace_size_scored bytes

@@ -480,13 +480,15 @@ pa_status scored_impl(ScoredParams p, void* out, const void* q, const int32_t* q
                                        cache_dtype, k_scale, v_scale, workspace);
     if (s != PA_OK) return s;
     if (!std::isfinite(cap) || !(cap >= 0.f) || window < 0) return PA_ERR_INVALID_ARG;
+    // what is computed with scale / cap and cap / ln 2 stays in float's range
+    if (cap > 0.f && (cap < 1e-6f || cap > 1e6f || !std::isfinite(scale / cap))) return PA_ERR_UNSUPPORTED;
     if (num_seqs > 0 && (!query_start_loc || !aligned(query_start_loc, 4))) return PA_ERR_INVALID_ARG;
     const int group = num_q_heads / num_kv_heads;
     if (group > scored_rows()) return PA_ERR_UNSUPPORTED;
     // rows, and steps of 128 keys of all units, in 32 bits
     const long long pair = 2ll * (scored_rows() / group);
     const long long units = (num_seqs + (total_q + pair - 1) / pair) * num_kv_heads;
-    const long long steps = static_cast<long long>(max_blocks_per_seq) * block_size / scored_rows() + 1;
+    const long long steps = static_cast<long long>(max_blocks_per_seq) * block_size / scored_rows() + 3;      // and a unit's start
     if (static_cast<long long>(total_q) * num_q_heads >= (1ll << 31) || units * steps >= (1ll << 31))
         return PA_ERR_UNSUPPORTED;
     if (num_seqs == 0) return PA_OK;

@@ -183,8 +183,9 @@ __device__ __forceinline__ Unit unit_of(const ScoredParams& p, const SeqView& s,
 }
 
 // A unit's share of the ranges: its steps, and what beginning a unit costs in steps (the
-// queries, the first scores and the last products run alone): about 4.8 us of a pair, whose step
-// takes 2.5, and 1 to 2 us of a solo, whose step takes 2.
+// queries, the first scores and the last products run alone): two steps of a pair, one of a solo.
+// With 1, 2, 3, 4 steps a pair, 8192 tokens of one prompt (32/8 heads) took 513, 439, 441, 447 us;
+// with 1, 2 a solo, 64 decode rows of up to 8192 tokens 99.7, 101.2.
 __device__ __forceinline__ int unit_lead(const ScoredParams& p, const Unit& u) { return u.nq <= p.queries_per_tile ? 1 : 2; }
 __device__ __forceinline__ int unit_cost(const ScoredParams& p, const Unit& u) { return u.steps + unit_lead(p, u); }
 
@@ -198,7 +199,7 @@ __device__ __forceinline__ int seq_cost(const ScoredParams& p, int s, bool repor
     const int np = units_per_head(p, v);
     int sum = 0;
     for (int t = 0; t < np; ++t) sum += unit_cost(p, unit_of(p, v, t));
-    return sum * p.num_kv_heads;
+    return sum * p.num_kv_heads;             // (one sequence's: the host has checked that it fits)
 }
 
 // A segment as its CTA's warps see it: steps [step, step + steps) of a unit.
@@ -343,35 +344,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     grid_launch_dependents();
 
     // ---- cost per sequence: exclusive scan into cum ----
+    // (Sums stop at 2^31 - 1, which no batch reaches whose rows are q's, each in one sequence.)
     const int B = p.num_seqs;
     {
+        auto add = [](int a, int b) { return static_cast<int>(min(static_cast<unsigned>(a) + static_cast<unsigned>(b), 0x7fffffffu)); };
         const int per = (B + kThreads - 1) / kThreads;
         const int beg = min(B, static_cast<int>(threadIdx.x) * per), end = min(B, beg + per);
         int local = 0;
         for (int s = beg; s < end; ++s) {
             const int w = seq_cost(p, s, blockIdx.x == 0);
             cum[s] = w;
-            local += w;
+            local = add(local, w);
         }
         int incl = local;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
+            if (lane >= o) incl = add(incl, y);
         }
         if (lane == 31) scan[warp] = incl;
         __syncthreads();
-        int run = incl - local;
-        for (int w = 0; w < warp; ++w) run += scan[w];
+        const int behind = __shfl_up_sync(0xffffffffu, incl, 1);
+        int run = lane ? behind : 0;
+        for (int w = 0; w < warp; ++w) run = add(run, scan[w]);
         for (int s = beg; s < end; ++s) {
             const int w = cum[s];
             cum[s] = run;
-            run += w;
+            run = add(run, w);
         }
         if (threadIdx.x == kThreads - 1) cum[B] = run;
         __syncthreads();
     }
-    const int T = cum[B];
+    const int sum = cum[B];
+    if (sum == INT_MAX && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.status, kDevErrRange);
+    const int T = sum == INT_MAX ? 0 : sum;
     const int W = min(static_cast<int>(gridDim.x), T);
     const int cta = blockIdx.x;
     if (cta >= W) {
@@ -960,6 +966,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // never 0: hidden scores are infinite, and stay so under it
             const float s_raw = p.scale_log2 * kscale;
             const float s_log2 = s_raw == 0.f ? 1e-30f : s_raw;
+            [[maybe_unused]] auto k_cap = [&]() {       // of a score, to x / cap
+                const float k = p.cap_scale * kscale;
+                return k == 0.f ? 1e-30f : k;
+            };
             float m_used = -INFINITY, l = 0.f;
             int key0 = (d[kSegStep] + (solo ? x : 0)) * kKeys + NC * half;
             for (int left_steps = solo ? (d[kSegSteps] + 1 - x) >> 1 : d[kSegSteps]; left_steps > 0;
@@ -1062,7 +1072,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             e4[(e >> 1) & 3] = min3f(e4[(e >> 1) & 3], __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
                         mx = fminf(fminf(e4[0], e4[1]), fminf(e4[2], e4[3]));
                     }
-                    mx *= Form == kCappedScores ? p.cap_scale * kscale : mul;
+                    mx *= Form == kCappedScores ? k_cap() : mul;
                 }
                 // The form of the tanh, one for the warp's part of the step: the shortest polynomial where
                 // the largest x / cap of every row lies in [-0.1, 0.3] and the cap is 40 or more: what lies
@@ -1070,7 +1080,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // faster than the tanh, next to nothing.  Else by the largest |x / cap|.
                 int tanh_form = 0;
                 if constexpr (Form == kCappedScores) {
-                    const float k1 = p.cap_scale * kscale;
+                    const float k1 = k_cap();
                     if (__any_sync(0xffffffffu, live && !(mx >= -0.1f && mx <= kCapTiny)) || p.cap < 40.f || fabsf(k1) < 1e-8f) {
                         float am = 0.f;
 #pragma unroll
@@ -1169,7 +1179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tmem_st8(p_addr + 8 * c, pw);
                         }
                     };
-                    const float k1 = p.cap_scale * kscale;
+                    const float k1 = k_cap();
                     if (tanh_form == 0) {
                         const float d0 = kTiny0 * s_log2, d1 = kTiny1 * s_log2 * (k1 * k1), d2 = kTiny2 * s_log2 * (k1 * k1) * (k1 * k1);
                         const uint64_t c0 = f2_pack(d0, d0), c1 = f2_pack(d1, d1), c2 = f2_pack(d2, d2), negm2 = f2_pack(-m_at, -m_at);

@@ -126,10 +126,10 @@ def reference(b, sight, cap=0.0, slopes=None):
             continue
         q = b.q[r0:r0 + m].double().view(m, b.hkv, grp, 128)
         x = torch.einsum("mhgd,nhd->mhgn", q, b.k[s]) * b.scale
-        size = torch.einsum("mhgd,nhd->mhgn", q.abs(), b.k[s].abs()) * b.scale
+        size = torch.einsum("mhgd,nhd->mhgn", q.abs(), b.k[s].abs()) * abs(b.scale)
         e = 128 * 2.0 ** -23 * size + 2.0 ** -18 * x.abs()
         if b.cache == "fp8":                # the query as fp16: below its normal range 2^-25 off
-            e = e + 2.0 ** -25 * b.k[s].abs().sum(-1).T[None, :, None] * b.scale
+            e = e + 2.0 ** -25 * b.k[s].abs().sum(-1).T[None, :, None] * abs(b.scale)
         if cap:
             x = cap * torch.tanh(x / cap)
         if slopes is not None:

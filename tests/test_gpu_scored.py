@@ -50,7 +50,7 @@ def test_groups(G, cache):
     one(b, 20.0, slopes_of(b.hq), 0, [0, 690, 131])
 
 
-@pytest.mark.parametrize("cap", [0.5, 3.0, 1000.0, 3e4])
+@pytest.mark.parametrize("cap", [1e-6, 0.5, 3.0, 1000.0, 3e4, 1e6])
 def test_caps_from_tight_to_wide(cap):
     # scores far beyond the cap, near it and far below
     for size in (0.05, 2.0, 40.0):
@@ -193,3 +193,77 @@ def test_empty_calls():
     i0, i1 = torch.zeros(0, dtype=torch.int32, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
     ws = pa.new_workspace_scored(0, 8, 2)
     pa.pa_mixed_scored(e, e, i1, *b.caches, torch.zeros(0, 4, dtype=torch.int32, device=DEV), i0, 0.1, ws)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+@pytest.mark.parametrize("scale", [-0.1, 0.0])
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (30.0, False), (0.0, True), (4.0, True)])
+def test_scales_that_turn_or_flatten_the_scores(cache, scale, cap, bias):
+    b = Batch(60, [300, 129, 700, 1], [1, 100, 7, 1], 8, 2, cache)
+    b.scale = scale
+    one(b, cap, slopes_of(8) if bias else None, 64 if bias else 0)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+def test_outputs_on_any_16_bytes(cache):
+    b = Batch(61, [5000, 129, 700], [1, 100, 7], 8, 2, cache)
+    flat = torch.full((b.q.numel() + 64,), 7.0, dtype=b.q.dtype, device=DEV)
+    for at in (0, 8, 16):
+        out = flat[at:at + b.q.numel()].view_as(b.q)
+        assert out.data_ptr() % 32 == 2 * at % 32
+        call(b, out, cap=30.0)
+        check(out, *reference(b, causal(b), 30.0), f"at {at}")
+    assert bool((flat[b.q.numel() + 16:] == 7).all())
+
+
+def test_query_rows_that_the_output_replaces():
+    b = Batch(62, [5000, 129, 700, 2600], [1, 100, 7, 30], 8, 2)
+    want = call(b, cap=30.0)
+    q = b.q.clone()
+    call(b, q, q, cap=30.0)
+    assert torch.equal(q, want)
+
+
+def test_starts_that_go_back_and_forth():
+    # rows that several sequences name, or none: recorded, or their last writer's
+    b = Batch(63, [300] * 6, [10] * 6, 8, 2)
+    good = call(b)
+    ws = pa.new_workspace_scored(6, 8, 2)
+    b.start = torch.tensor([0, 60, 10, 60, 20, 25, 60], dtype=torch.int32, device=DEV)
+    out = torch.full_like(b.q, 7.0)
+    pa.pa_mixed_scored(out, b.q, b.start, *b.caches, b.tables, b.lens, b.scale, ws)
+    assert pa.pa_read_device_status(ws) == pa.PA_ERR_OUT_OF_RANGE
+    assert bool(torch.isfinite(out).all()) and torch.equal(call(Batch(63, [300] * 6, [10] * 6, 8, 2)), good)
+
+
+def test_a_cache_past_four_gib():
+    bs, hkv, blocks = 16, 8, 200000                  # 6.5 GB each
+    if torch.cuda.mem_get_info()[0] < 20 << 30:
+        pytest.skip("needs 20 GB")
+    b = Batch(64, [300, 129], [1, 100], 16, hkv, bs=bs)
+    first = blocks - b.caches[0].shape[0]
+    big = [torch.empty(blocks, hkv, bs, 128, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    for x, c in zip(big, b.caches):
+        x[first:] = c
+    b.caches = big
+    b.tables = torch.where(b.tables >= 0, b.tables + first, b.tables)
+    got = one(b, 30.0)
+    # and rows written and moved there
+    c = torch.randn(3, 32, 128, device=DEV).bfloat16()
+    slots = torch.tensor([(blocks - 1) * bs + 3, blocks * bs - 1, (blocks - 2) * bs], device=DEV)
+    table = torch.tensor([[1.0] * 8 + [0.0] * 8], device=DEV)
+    q = torch.empty(3, 16, 128, dtype=torch.bfloat16, device=DEV)
+    pa.pa_norm_rope_and_cache(q, c[:, :16], c[:, 16:24], c[:, 24:], *big, slots, torch.zeros(3, dtype=torch.int64, device=DEV),
+                              table)
+    for i, x in enumerate(slots.tolist()):
+        assert torch.equal(big[0][x // bs, :, x % bs], c[i, 16:24]) and torch.equal(big[1][x // bs, :, x % bs], c[i, 24:])
+    lens = torch.tensor([2 * bs], dtype=torch.int32, device=DEV)
+    tables = torch.tensor([[blocks - 2, blocks - 1]], dtype=torch.int32, device=DEV)
+    new = torch.zeros_like(lens)
+    pa.pa_tree_commit(new, big[:1], big[1:], torch.tensor([[3, 15]], dtype=torch.int32, device=DEV),
+                      torch.tensor([2], dtype=torch.int32, device=DEV), torch.tensor([0, bs], dtype=torch.int32, device=DEV),
+                      tables, lens)
+    assert new.tolist() == [bs + 2]
+    for i in range(2):
+        assert torch.equal(big[0][blocks - 1, :, i], c[i, 16:24]) and torch.equal(big[1][blocks - 1, :, i], c[i, 24:])
+    assert got.shape == b.q.shape

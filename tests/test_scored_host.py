@@ -68,7 +68,8 @@ def _tree(lib, **kw):
 def test_scored_and_tree_refusals(lib, call):
     odd = ctypes.c_void_p(0x10002)
     for kw in (dict(d=64), dict(bs=64), dict(qd=2), dict(cd=1), dict(hq=258, hkv=2), dict(T=1 << 29),
-               dict(maxb=1 << 28, B=64), dict(nb=1 << 28)):
+               dict(maxb=1 << 28, B=64), dict(nb=1 << 28), dict(cap=F(9e-7)), dict(cap=F(1.1e6)),
+               dict(cap=F(1e-6), scale=F(1e34))):
         assert call(lib, **kw) == 2, kw
     for kw in (dict(q=None), dict(out=None), dict(qsl=None), dict(kc=None), dict(sl=None), dict(bt=None), dict(ws=None),
                dict(hq=7), dict(B=-1), dict(B=9000), dict(T=-1), dict(cap=F(-1)), dict(cap=F(float("nan"))),
