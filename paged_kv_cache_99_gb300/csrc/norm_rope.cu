@@ -250,8 +250,9 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_co
 // positions and slots fetched 32 at a time before; the other warps norm, turn and write one
 // stage after the other, eight threads to a row.  So nothing waits for a chain of loads, and
 // the table's rows are read once for a token whatever axes its pairs follow: 16384 tokens of
-// 32/8 heads in bf16 (0.41 GB) take 76 us with three axes, 5.4 TB/s, as one row per group 110;
-// 1040 of 64/8 heads into an FP8 cache 10.4 against 13.9.  Four CTAs of four warps: three of
+// 32/8 heads in bf16 (0.41 GB) take 78 us with three axes, 5.3 TB/s, as one row per group 110
+// (interleaved pairs 75, with the weights in the components' order 80: banks met); 1040 of 64/8
+// heads into an FP8 cache 10.3 against 13.9.  Four CTAs of four warps: three of
 // six take 70 to 76 and 12.8 (fewer heads left over in a token's last pass against more
 // tokens at once).  Two rows of a thread at a time spill.
 constexpr int kStreamWarps = 4;                             // that work on rows
@@ -271,7 +272,9 @@ __global__ void __launch_bounds__(kStreamThreads, 4)
     extern __shared__ __align__(128) uint8_t sm[];
     __shared__ __align__(8) uint64_t bars[2 * kMaxStages];
     __shared__ long long slots[kMaxStages];                 // of a stage's token; -2: nothing of it is written
-    __shared__ __align__(16) float weights[2 * kHeadDim];   // of q and k, the offset added
+    // of q and k, the offset added: [four of a thread's components][thread of a row][4], so that a
+    // row's threads read side by side
+    __shared__ __align__(16) float weights[2 * kHeadDim];
     const RopeParams& p = np.rope;
     const uint32_t full = smem_addr(bars), empty = full + 8 * kMaxStages;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -355,7 +358,9 @@ __global__ void __launch_bounds__(kStreamThreads, 4)
     const int heads = p.num_q_heads + p.num_kv_heads;
     for (int i = threadIdx.x; i < 2 * kHeadDim; i += 32 * kStreamWarps) {
         const uint16_t* w = i < kHeadDim ? np.q_weight : np.k_weight;
-        weights[i] = w ? np.weight_offset + to_float<SrcBf16>(w[i & (kHeadDim - 1)]) : 1.0f;
+        const RowPieces of = RowPieces::of<Interleaved>(i >> 2 & 7, p.rot_dim);
+        const int e = (i >> 5 & 3) * 4 + (i & 3);
+        weights[i] = w ? np.weight_offset + to_float<SrcBf16>(w[e < 8 ? of.o0 + e : of.o1 + e - 8]) : 1.0f;
     }
     named_barrier_sync(1, 32 * kStreamWarps);
     for (int i = 0; i < mine; ++i) {
@@ -383,11 +388,11 @@ __global__ void __launch_bounds__(kStreamThreads, 4)
                 unpack_pieces<SrcBf16>(x0, x1, f);
                 const float r = norm_factor(np, f, row_lanes);      // of every row: a branch here costs 8%
                 if (norm) {
-                    const float* g = weights + (is_q ? 0 : kHeadDim);
+                    const float* g = weights + (is_q ? 0 : kHeadDim) + 4 * rp.c;
                     const uint64_t r2 = f2_pack(r, r);
 #pragma unroll
                     for (int e = 0; e < 16; e += 4) {
-                        const float4 w = *reinterpret_cast<const float4*>(g + (e < 8 ? rp.o0 + e : rp.o1 + e - 8));
+                        const float4 w = *reinterpret_cast<const float4*>(g + 8 * e);
                         f2_unpack(f2_mul(f2_mul(f2_pack(f[e], f[e + 1]), r2), f2_pack(w.x, w.y)), f[e], f[e + 1]);
                         f2_unpack(f2_mul(f2_mul(f2_pack(f[e + 2], f[e + 3]), r2), f2_pack(w.z, w.w)), f[e + 2], f[e + 3]);
                     }
