@@ -247,16 +247,19 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_co
 // ---- many tokens: copies run ahead ----
 // A CTA takes every gridDim-th token.  Its last warp copies a token's q, k and v and its rows
 // of the table (bulk copies) into a ring of stages, several tokens ahead, with the tokens'
-// positions and slots fetched 32 at a time before; the other warps norm, turn and write one
-// stage after the other, eight threads to a row.  So nothing waits for a chain of loads, and
-// the table's rows are read once for a token whatever axes its pairs follow: 16384 tokens of
-// 32/8 heads in bf16 (0.41 GB) take 78 us with three axes, 5.3 TB/s, as one row per group 110
-// (interleaved pairs 75, with the weights in the components' order 80: banks met); 1040 of 64/8
-// heads into an FP8 cache 10.3 against 13.9.  Four CTAs of four warps: three of
-// six take 70 to 76 and 12.8 (fewer heads left over in a token's last pass against more
-// tokens at once).  Two rows of a thread at a time spill.
-constexpr int kStreamWarps = 4;                             // that work on rows
-constexpr int kStreamThreads = 32 * (kStreamWarps + 1);
+// positions and slots fetched 32 at a time before; the other warps norm and turn one stage
+// after the other in place, eight threads to a row, and the copying warp brings the worked rows
+// back (bulk copies again; FP8 codes are written by their threads).  So nothing waits for a
+// chain of loads, and the table's rows are read once for a token whatever axes its pairs
+// follow: 16384 tokens of 32/8 heads in bf16 (0.41 GB) take 66 us with three axes, 6.2 TB/s,
+// as one row per group 110, with rows stored by their threads 78.
+//
+// Four CTAs of four working warps to an SM, or three of six: the fewer tokens are in flight, the
+// less HBM turns between reading and writing, so the three for 16-bit caches whose data do not fit L2
+// (16384 tokens 66 against 74 us, 8192 34.1 against 38.0, but 4096 18.1 against 16.7); FP8
+// codes are bound by the work, which four CTAs spread better (1040 tokens of 64/8 heads 10.3
+// against 12.4; a row per group 13.9).
+constexpr int stream_ctas(int warps) { return warps == 4 ? 4 : 3; }
 constexpr int kMaxStages = 8;
 constexpr unsigned long long kStreamTimeoutNs = 1000ull * 1000ull * 1000ull;    // bound of every wait
 
@@ -266,8 +269,8 @@ struct StreamShape {
     int stages;
 };
 
-template <bool SrcBf16, bool Fp8, bool Interleaved>
-__global__ void __launch_bounds__(kStreamThreads, 4)
+template <bool SrcBf16, bool Fp8, bool Interleaved, int Warps>
+__global__ void __launch_bounds__(32 * (Warps + 1), stream_ctas(Warps))
     norm_rope_stream_kernel(const __grid_constant__ NormRopeParams np, const StreamShape sh) {
     extern __shared__ __align__(128) uint8_t sm[];
     __shared__ __align__(8) uint64_t bars[2 * kMaxStages];
@@ -281,7 +284,7 @@ __global__ void __launch_bounds__(kStreamThreads, 4)
     if (threadIdx.x == 0) {
         for (int i = 0; i < sh.stages; ++i) {
             mbar_init(full + 8 * i, 1);
-            mbar_init(empty + 8 * i, kStreamWarps);
+            mbar_init(empty + 8 * i, Warps);
         }
         fence_barrier_init();
     }
@@ -299,10 +302,26 @@ __global__ void __launch_bounds__(kStreamThreads, 4)
             ph ^= 1u;
         }
     };
-    if (warp == kStreamWarps) {
+    if (warp == Warps) {
         const int row_bytes = p.rot_dim * 4;
         long long pos[kMaxAxes], slot = 0;
         int done = 0;
+        // the worked rows of the CTA's i-th token, in stage st, to where they belong
+        auto flush = [&](int i) {
+            const long long s = slots[st];
+            const uint32_t src = smem_addr(sm) + st * sh.stage_bytes;
+            if (s >= -1 && lane == 0)
+                bulk_store(p.q_out + (first + static_cast<long long>(i) * step) * p.q_out_stride, src, p.num_q_heads * 256);
+            if (!Fp8 && s >= 0) {
+                for (int r = lane; r < 2 * p.num_kv_heads; r += 32) {
+                    const bool is_v = r >= p.num_kv_heads;
+                    uint16_t* cache = static_cast<uint16_t*>(is_v ? p.v_cache : p.k_cache);
+                    bulk_store(cache + slot_row(p, s, is_v ? r - p.num_kv_heads : r), src + (p.num_q_heads + r) * 256, 256);
+                }
+            }
+            bulk_store_wait_read();
+            __syncwarp();
+        };
         for (; done < mine; ++done) {
             if ((done & 31) == 0) {
                 // the next 32 tokens' places, a lane each
@@ -312,7 +331,10 @@ __global__ void __launch_bounds__(kStreamThreads, 4)
                     pos[a] = a < np.num_axes ? p.positions[static_cast<size_t>(a) * p.num_tokens + t] : 0;
                 slot = p.slots[t];
             }
-            if (done >= sh.stages && !warp_wait_all(empty + 8 * st, ph ^ 1u, kStreamTimeoutNs)) break;
+            if (done >= sh.stages) {
+                if (!warp_wait_all(empty + 8 * st, ph ^ 1u, kStreamTimeoutNs)) break;
+                flush(done - sh.stages);
+            }
             const int src = done & 31;
             const int t = first + done * step;
             const long long s = __shfl_sync(0xffffffffu, slot, src);
@@ -327,7 +349,7 @@ __global__ void __launch_bounds__(kStreamThreads, 4)
             if (lane == 0) {
                 if (!padding && (beyond || s >= limit) && p.status) atomicOr(p.status, kDevErrRange);
                 const bool skip = padding || beyond;
-                slots[st] = skip ? -2 : s >= limit ? -1 : s;
+                slots[st] = skip ? -2 : s < 0 || s >= limit ? -1 : s;
                 if (skip) {
                     mbar_arrive(full + 8 * st);
                 } else {
@@ -345,7 +367,17 @@ __global__ void __launch_bounds__(kStreamThreads, 4)
             __syncwarp();
             advance();
         }
-        if (done < mine) {
+        bool ok = done == mine;
+        for (int i = max(0, mine - sh.stages); i < mine && ok; ++i) {
+            if (mine < sh.stages) {
+                st = i;
+                ph = 1u;
+            }
+            ok = warp_wait_all(empty + 8 * st, ph ^ 1u, kStreamTimeoutNs);
+            if (ok) flush(i);
+            advance();
+        }
+        if (!ok) {
             // a wait gave up: let the copies in flight land before the CTA leaves
             if (lane == 0 && p.status) atomicOr(p.status, kDevErrTimeout);
             for (int i = max(0, done - sh.stages); i < done; ++i)
@@ -356,13 +388,13 @@ __global__ void __launch_bounds__(kStreamThreads, 4)
     const RowPieces rp = RowPieces::of<Interleaved>(threadIdx.x & 7, p.rot_dim);
     const unsigned row_lanes = 0xffu << (threadIdx.x & 24);
     const int heads = p.num_q_heads + p.num_kv_heads;
-    for (int i = threadIdx.x; i < 2 * kHeadDim; i += 32 * kStreamWarps) {
+    for (int i = threadIdx.x; i < 2 * kHeadDim; i += 32 * Warps) {
         const uint16_t* w = i < kHeadDim ? np.q_weight : np.k_weight;
         const RowPieces of = RowPieces::of<Interleaved>(i >> 2 & 7, p.rot_dim);
         const int e = (i >> 5 & 3) * 4 + (i & 3);
         weights[i] = w ? np.weight_offset + to_float<SrcBf16>(w[e < 8 ? of.o0 + e : of.o1 + e - 8]) : 1.0f;
     }
-    named_barrier_sync(1, 32 * kStreamWarps);
+    named_barrier_sync(1, 32 * Warps);
     for (int i = 0; i < mine; ++i) {
         if (!warp_wait_all(full + 8 * st, ph, kStreamTimeoutNs)) {
             if (lane == 0 && p.status) atomicOr(p.status, kDevErrTimeout);
@@ -370,18 +402,18 @@ __global__ void __launch_bounds__(kStreamThreads, 4)
         }
         const long long slot = slots[st];
         if (slot >= -1) {
-            const size_t tok = static_cast<size_t>(first + static_cast<long long>(i) * step);
-            const uint8_t* stage = sm + st * sh.stage_bytes;
+            uint8_t* stage = sm + st * sh.stage_bytes;
             float cs[8], sn[8];
             if (rp.turned) {
                 const float* table = reinterpret_cast<const float*>(stage + sh.table_off);
                 load_turns(np, rp.c, p.rot_dim >> 1, [&](unsigned axis) { return table + axis * p.rot_dim; }, cs, sn);
             }
-            for (int row = threadIdx.x >> 3; row < sh.rows; row += 4 * kStreamWarps) {
+            // (16-bit values stay as they came)
+            for (int row = threadIdx.x >> 3; row < (Fp8 ? sh.rows : heads); row += 4 * Warps) {
                 const bool is_q = row < p.num_q_heads, is_v = row >= heads;
                 if (!is_q && slot < 0) break;
                 const int h = row - (is_q ? 0 : is_v ? heads : p.num_q_heads);
-                const uint16_t* src = reinterpret_cast<const uint16_t*>(stage) + row * kHeadDim;
+                uint16_t* src = reinterpret_cast<uint16_t*>(stage) + row * kHeadDim;
                 const uint4 x0 = *reinterpret_cast<const uint4*>(src + rp.o0), x1 = *reinterpret_cast<const uint4*>(src + rp.o1);
                 const bool norm = !is_v && (is_q ? np.q_weight : np.k_weight) != nullptr, turns = rp.turned && !is_v;
                 float f[16];
@@ -398,44 +430,48 @@ __global__ void __launch_bounds__(kStreamThreads, 4)
                     }
                 }
                 if (turns) turn_pieces<Interleaved>(cs, sn, f);
-                if (is_q) {
-                    store_halves<SrcBf16>(p.q_out + tok * p.q_out_stride + h * kHeadDim, rp, norm || turns, x0, x1, f);
-                } else if constexpr (!Fp8) {
-                    store_halves<SrcBf16>(static_cast<uint16_t*>(is_v ? p.v_cache : p.k_cache) + slot_row(p, slot, h), rp,
-                                          norm || turns, x0, x1, f);
-                } else {
+                if (!Fp8 || is_q) {
+                    if (norm || turns) store_halves<SrcBf16>(src, rp, true, x0, x1, f);
+                } else if constexpr (Fp8) {
                     store_codes(static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + slot_row(p, slot, h), rp, norm || turns,
                                 x0, x1, f, __ldg((is_v ? p.v_scale : p.k_scale) + h * p.scale_stride));
                 }
             }
         }
+        fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(empty + 8 * st);
         advance();
     }
 }
 
+// warps: of the kernel for many tokens, 0 for the one for few
+template <bool SrcBf16, bool Fp8, bool Interleaved>
+const void* norm_rope_fn(int warps) {
+    if (warps == 0) return reinterpret_cast<const void*>(&norm_rope_kernel<SrcBf16, Fp8, Interleaved>);
+    if constexpr (!Fp8) {
+        if (warps == 6) return reinterpret_cast<const void*>(&norm_rope_stream_kernel<SrcBf16, Fp8, Interleaved, 6>);
+    }
+    return reinterpret_cast<const void*>(&norm_rope_stream_kernel<SrcBf16, Fp8, Interleaved, 4>);
+}
+
 template <bool SrcBf16, bool Fp8>
-const void* norm_rope_fn(bool interleaved, bool stream) {
-    if (stream)
-        return interleaved ? reinterpret_cast<const void*>(&norm_rope_stream_kernel<SrcBf16, Fp8, true>)
-                           : reinterpret_cast<const void*>(&norm_rope_stream_kernel<SrcBf16, Fp8, false>);
-    return interleaved ? reinterpret_cast<const void*>(&norm_rope_kernel<SrcBf16, Fp8, true>)
-                       : reinterpret_cast<const void*>(&norm_rope_kernel<SrcBf16, Fp8, false>);
+const void* norm_rope_fn(bool interleaved, int warps) {
+    return interleaved ? norm_rope_fn<SrcBf16, Fp8, true>(warps) : norm_rope_fn<SrcBf16, Fp8, false>(warps);
 }
 
-const void* norm_rope_fn(bool src_bf16, bool fp8, bool interleaved, bool stream) {
-    if (src_bf16) return fp8 ? norm_rope_fn<true, true>(interleaved, stream) : norm_rope_fn<true, false>(interleaved, stream);
-    return fp8 ? norm_rope_fn<false, true>(interleaved, stream) : norm_rope_fn<false, false>(interleaved, stream);
+const void* norm_rope_fn(bool src_bf16, bool fp8, bool interleaved, int warps) {
+    if (src_bf16) return fp8 ? norm_rope_fn<true, true>(interleaved, warps) : norm_rope_fn<true, false>(interleaved, warps);
+    return fp8 ? norm_rope_fn<false, true>(interleaved, warps) : norm_rope_fn<false, false>(interleaved, warps);
 }
 
-constexpr int kStreamSmem = 54 * 1024;                      // of a CTA's stages: four CTAs to an SM
+constexpr int kStreamSmem = 54 * 1024;                      // of a CTA's stages: four CTAs to an SM (three: the same)
 
 }  // namespace
 
 cudaError_t norm_rope_prepare() {
-    for (int i = 0; i < 8; ++i) {
-        const cudaError_t e = cudaFuncSetAttribute(norm_rope_fn(i & 1, i & 2, i & 4, true),
+    for (int i = 0; i < 16; ++i) {
+        const cudaError_t e = cudaFuncSetAttribute(norm_rope_fn(i & 1, i & 2, i & 4, i & 8 ? 6 : 4),
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem);
         if (e != cudaSuccess) return e;
     }
@@ -453,10 +489,13 @@ cudaError_t launch_norm_rope_cache(const NormRopeParams& p, bool src_bf16, bool 
     // the streaming kernel where there are a few tokens for each of its CTAs and stages to run ahead
     // (1024 tokens of 32/8 heads 7.7 us against 7.2, 2048 10.3 against 11.8)
     const bool many = sh.stages >= 2 && total > 512ll * sms;
+    // rows that take 512 bytes of L2 each, in and out (130 MB in all)
+    const int warps = !many ? 0 : !fp8 && total > (160ll << 20) / 512 ? 6 : 4;
     cudaLaunchConfig_t cfg = {};
     if (many) {
-        cfg.gridDim = dim3(static_cast<unsigned>(p.rope.num_tokens < 4 * sms ? p.rope.num_tokens : 4 * sms));
-        cfg.blockDim = dim3(kStreamThreads);
+        const int ctas = stream_ctas(warps) * sms;
+        cfg.gridDim = dim3(static_cast<unsigned>(p.rope.num_tokens < ctas ? p.rope.num_tokens : ctas));
+        cfg.blockDim = dim3(32 * (warps + 1));
         cfg.dynamicSmemBytes = static_cast<size_t>(sh.stages) * sh.stage_bytes;
     } else {
         constexpr int kPerCta = kNormThreads / 8;
@@ -470,7 +509,7 @@ cudaError_t launch_norm_rope_cache(const NormRopeParams& p, bool src_bf16, bool 
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     void* args[] = {const_cast<NormRopeParams*>(&p), &sh};
-    return cudaLaunchKernelExC(&cfg, norm_rope_fn(src_bf16, fp8, interleaved, many), args);
+    return cudaLaunchKernelExC(&cfg, norm_rope_fn(src_bf16, fp8, interleaved, warps), args);
 }
 
 }  // namespace pa

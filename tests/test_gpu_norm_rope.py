@@ -247,3 +247,24 @@ def test_stored_values_are_those_of_the_slot_write(kind):
             v = qkv[:t, hq + hkv:].contiguous()
             pa.pa_reshape_and_cache(v, v, k2, v2, slots[:t].contiguous(), ks, ks)
             assert torch.equal(vc, v2), scale
+
+
+@pytest.mark.parametrize("kind,cache", [("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "fp8")])
+def test_more_tokens_than_l2_holds(kind, cache):
+    # 8,000 x 48 rows of 512 bytes in and out; every thirteenth token has no slot, some of them another
+    # negative number than -1: q is written all the same
+    c = Case(21, 8000, 32, 8, 128, kind, cache, axes=pa.rope_axes((24, 20, 20)))
+    keep = torch.ones(8000, dtype=torch.bool, device=DEV)
+    keep[::13] = False
+    before = c.kc.clone(), c.vc.clone()
+    slots = c.slots.clone()
+    c.slots[::13] = -torch.arange(1, len(c.slots[::13]) + 1, device=DEV)
+    q = c.run()
+    for cache_, old in zip((c.kc, c.vc), before):
+        lost = slots[~keep]
+        assert torch.equal(cache_[lost // c.bs, :, lost % c.bs], old[lost // c.bs, :, lost % c.bs])
+    want, err = c.turned(c.parts()[0], c.wq, 1e-6, 0.0, False)
+    u = torch.finfo(c.qkv.dtype).eps / 2
+    assert bool(((q.double() - want).abs() <= err + u * (want.abs() + err) + (2.0 ** -25 if kind == "fp16" else 0.0)).all())
+    c.slots, c.qkv, c.pos, c.T = c.slots[keep], c.qkv[keep], c.pos[:, keep], int(keep.sum())
+    c.check(q[keep], before)
