@@ -92,7 +92,7 @@ def tree_sight(b, parents, window=0, blind=()):
                 masks[row, at // 64] |= np.uint64(1) << np.uint64(at % 64)
                 at = int(parents[s][at])
                 depth += 1
-            pos[j] = n - m + depth
+            pos[j] = n - m + max(depth, 0)      # a row that sees no node: the first one's place
             low = max(0, pos[j] - window + 1) if window else 0
             see[j, min(low, n - m):n - m] = True
         out.append((torch.from_numpy(see).to(DEV), torch.from_numpy(pos).to(DEV)))

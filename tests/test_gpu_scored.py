@@ -267,3 +267,30 @@ def test_a_cache_past_four_gib():
     for i in range(2):
         assert torch.equal(big[0][blocks - 1, :, i], c[i, 16:24]) and torch.equal(big[1][blocks - 1, :, i], c[i, 24:])
     assert got.shape == b.q.shape
+
+
+@pytest.mark.parametrize("cache,kind,per_head", FORMATS)
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (30.0, False), (0.0, True)])
+def test_many_short_units_of_all_sizes(cache, kind, per_head, cap, bias):
+    # every SM goes through solos and pairs of one step and of a few, in any order
+    g = torch.Generator().manual_seed(65)
+    rows = [int(x) for x in torch.randint(0, 4, (400,), generator=g)]
+    rows = [r if r < 3 else int(torch.randint(1, 90, (1,), generator=g)) for r in rows]
+    lens = [r + int(torch.randint(0, 300, (1,), generator=g)) * int(torch.rand(1, generator=g) < 0.6) for r in rows]
+    b = Batch(66, lens, rows, 24, 3, cache, kind, 16, per_head)
+    one(b, cap, slopes_of(24) if bias else None)
+
+
+def test_two_streams_at_once():
+    batches = [Batch(67, [5000, 129, 2000], [1, 100, 7], 8, 2), Batch(68, [40] * 200, [1] * 200, 16, 2, "fp8")]
+    want = [call(b, cap=30.0) for b in batches]
+    spaces = [pa.new_workspace_scored(len(b.lens_h), b.hq, b.hkv) for b in batches]
+    outs = [torch.zeros_like(b.q) for b in batches]
+    streams = [torch.cuda.Stream() for _ in batches]
+    torch.cuda.synchronize()
+    for _ in range(50):
+        for b, out, ws, st in zip(batches, outs, spaces, streams):
+            pa.pa_mixed_scored(out, b.q, b.start, *b.caches, b.tables, b.lens, b.scale, ws, cap=30.0, stream=st, **b.args())
+    torch.cuda.synchronize()
+    for out, ws, w in zip(outs, spaces, want):
+        assert pa.pa_read_device_status(ws) == pa.PA_OK and torch.equal(out, w)
