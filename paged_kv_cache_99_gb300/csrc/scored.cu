@@ -891,12 +891,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int exch = (2 * x + half) * kRows + r;   // in row_smem; the row's other thread: exch ^ kRows
         // parities: 1 of S, 2 of the solos, 4 of the meetings, 8 and 16 of the Q buffers' copies
         unsigned par = 0;
-        auto meet = [&]() -> bool {                    // both threads of the row
+        auto come = [&]() {                            // to a meeting of both threads of the row
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kPair + 4 * x + quarter));
+        };
+        auto met = [&]() -> bool {
             if (!warp_wait_all(bar(kPair + 4 * x + quarter), par >> 2 & 1, p.timeout_ns)) ok = false;
             par ^= 4u;
             return ok;
+        };
+        auto meet = [&]() -> bool {
+            come();
+            return met();
         };
         // Registers are short (a thread's scores take most of them, and a spill misses the little
         // L1 that is left): a segment's fields are read from shared memory where they are used,
@@ -1217,9 +1223,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---- the segment's outputs ----
             if (solo && x == 1 && d[kSegSteps] == 1 && lane == 0) mbar_arrive(bar(kPFull + 1));
             const float vscale = kFp8 ? __ldg(p.v_scale + d[kSegHead] * p.scale_stride) : 1.0f;
-            if (ok) look_ahead();
+            if (!ok) break;
+            // The sum goes where the maximum of the last step stood: not before the row's other thread has
+            // read that.  (Between two steps the scores are waited for, which come behind both threads' P.)
+            if (warp_live) come();
+            look_ahead();
             if (!ok) break;
             if (warp_live) {                           // the row's sum
+                if (!met()) break;
                 row_smem[exch] = l;
                 if (!meet()) break;
                 const float l2 = row_smem[exch ^ kRows];
