@@ -1101,7 +1101,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 // with the row's other thread, which has read its scores too: P may go over them
                 row_smem[exch] = mx;
+                tc_fence_before();
                 if (!meet()) break;
+                tc_fence_after();
                 mx = fmaxf(mx, row_smem[exch ^ kRows]);
                 if constexpr (Form == kCappedScores) {
                     // the row's maximum capped (a reference: what matters is that both threads take the same)
