@@ -28,7 +28,7 @@ struct DeviceState {
     bool chunk_prepared[3][2] = {};
     bool evict_prepared = false;
     bool norm_rope_prepared = false;
-    bool scored_prepared[3][2][3] = {};
+    bool scored_prepared[3][2][kScoreForms] = {};
 };
 
 std::mutex g_mu;
@@ -498,7 +498,9 @@ pa_status scored_impl(ScoredParams p, void* out, const void* q, const int32_t* q
     if (workspace_bytes < lay.total) return PA_ERR_WORKSPACE;
     const CacheKind kind = kind_of(cache_dtype);
     const bool q_bf16 = q_dtype == PA_BF16, fp8 = kind == kKindFp8;
-    const ScoreForm form = p.slopes ? kBiasedScores : cap > 0.f ? kCappedScores : kPlainScores;
+    const bool wide = cap > kWideCap;
+    const ScoreForm form = p.slopes ? (wide ? kWideBiasedScores : kBiasedScores)
+                           : cap > 0.f ? (wide ? kWideCappedScores : kCappedScores) : kPlainScores;
     {
         std::lock_guard<std::mutex> lock(g_mu);
         if (!st->scored_prepared[kind][q_bf16][form]) {

@@ -374,8 +374,10 @@ struct ScoredLayout {
 
 ScoredLayout scored_layout(int sms);
 int scored_rows();                    // rows of one tile
-// Forms of the kernel: scores as they are, capped, or biased (and perhaps capped).
-enum ScoreForm { kPlainScores = 0, kCappedScores = 1, kBiasedScores = 2 };
+// Forms of the kernel: scores as they are, capped, or biased (and perhaps capped), the latter two for
+// caps above kWideCap too.
+enum ScoreForm { kPlainScores = 0, kCappedScores, kBiasedScores, kWideCappedScores, kWideBiasedScores, kScoreForms };
+constexpr float kWideCap = 256.f;
 cudaError_t scored_prepare(CacheKind kind, bool q_bf16, ScoreForm form);
 cudaError_t launch_scored(CacheKind kind, bool q_bf16, ScoreForm form, const CUtensorMap& kmap, const CUtensorMap& vmap,
                           const CUtensorMap& qmap, const ScoredParams& p, int sms, cudaStream_t stream);

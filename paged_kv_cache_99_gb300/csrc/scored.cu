@@ -272,17 +272,34 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
 // V(i) among a segment's tiles.
 __device__ __forceinline__ int item_v(int steps, int i) { return min(2, steps) + i + min(i, max(steps - 2, 0)); }
 
-// c2 tanh(y) = c2 - 2 c2 / (1 + e^2y), by the exponential unit: within 2^-21 of c2.
-__device__ __forceinline__ float capped(float y, float c2) {
-    return fmaf(-2.f * c2, rcp_approx(1.f + ex2_approx(y * 2.8853900817779268f)), c2);
-}
-
 // tanh(x) / x as polynomials in x^2 (interpolated at Chebyshev nodes): on |x| <= kCapTiny within
 // 2^-19.7 of it, on |x| <= kCapSmall within 2^-23.7.
 constexpr float kCapTiny = 0.3f, kCapSmall = 0.6f;
 constexpr float kTiny0 = 0.999998835f, kTiny1 = -0.333099888f, kTiny2 = 0.126335824f;
 constexpr float kTanh0 = 0.999999926f, kTanh1 = -0.33332302f, kTanh2 = 0.133100644f, kTanh3 = -0.0520966534f,
                 kTanh4 = 0.0154687513f;
+
+// c2 tanh(y) = c2 - 2 c2 / (1 + e^2y), by the exponential unit: within 2^-21 of c2.
+__device__ __forceinline__ float capped_far(float y, float c2) {
+    return fmaf(-2.f * c2, rcp_approx(1.f + ex2_approx(y * 2.8853900817779268f)), c2);
+}
+
+// c2 tanh(y) + add for |y| <= kCapSmall.
+__device__ __forceinline__ float capped_near(float y, float c2, float add) {
+    const float u = y * y;
+    return fmaf(y * c2, fmaf(u, fmaf(u, fmaf(u, fmaf(u, kTanh4, kTanh3), kTanh2), kTanh1), kTanh0), add);
+}
+
+// c2 tanh(y) by the exponential unit.  Far above a score a cap rounds it to what fits the cap (at 1e6
+// a tenth of a score): up to kWideCap that is 2^-13 of a score at most, half of what fp16 weights
+// are rounded by; wider caps take the polynomial for scores that are small beside them, in forms of
+// the kernel that only they pay for (8192 tokens of one prompt, 32/8 heads, a cap of 300: 527 -> 531 us
+// where no score passes 0.6 of it, 921 -> 1829 where some do everywhere, 799 -> 1207 with a bias; at run
+// time the choice cost the FP8 trees with a cap of 50 8%).
+template <bool Wide>
+__device__ __forceinline__ float capped(float y, float c2) {
+    return Wide && fabsf(y) <= kCapSmall ? capped_near(y, c2, 0.f) : capped_far(y, c2);
+}
 
 }  // namespace
 
@@ -293,6 +310,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     using C = Cfg<Kind>;
     constexpr bool kFp8 = C::kFp8;
     constexpr bool kMmaBf16 = C::kMmaBf16;
+    constexpr bool kCapped = Form == kCappedScores || Form == kWideCappedScores;
+    constexpr bool kBiased = Form == kBiasedScores || Form == kWideBiasedScores;
+    constexpr bool kWide = Form == kWideCappedScores || Form == kWideBiasedScores;
     constexpr int NS = C::kStages;
     constexpr int kSegReaders = kSoftmaxWarps + (kFp8 ? 3 : 2);      // and warps 1, 3, with FP8 caches 2
 
@@ -926,7 +946,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (next_live)
                 next_view = row_view(p, SeqView{d[kSegRow0] - d[kSegJ0], d[kSegQLen], d[kSegN], d[kSegPrefix]}, d[kSegJ0] + jq);
             if (kFp8) next_kscale = __ldg(p.k_scale + d[kSegHead] * p.scale_stride);
-            if (Form == kBiasedScores && p.slopes)
+            if (kBiased && p.slopes)
                 next_slope2 = next_live ? __ldg(p.slopes + d[kSegHead] * G + r % G) * 1.4426950408889634f : 0.f;
             if constexpr (kFp8 && QBf16) {
                 // its queries, bf16 to fp16 as the widened codes: exact for magnitudes 2^-14 to 65504, 2^-25
@@ -1017,16 +1037,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // The row's maximum, of what the maximum of the scores follows: a cap is monotone, so that
                 // of the raw scores will do; biased scores are computed first.  (A negative scale turns
                 // the order round.)  Hidden scores are infinite on the far side.
-                const float mul = Form == kBiasedScores ? 1.0f : s_log2;
-                const bool upward = Form == kBiasedScores || s_log2 >= 0.f;
-                if constexpr (Form == kBiasedScores) {
-                    // a cap first: a rare pair, so by the exponential unit alone (what stands in hidden
+                const float mul = kBiased ? 1.0f : s_log2;
+                const bool upward = kBiased || s_log2 >= 0.f;
+                if constexpr (kBiased) {
+                    // a cap first: a rare pair, so without the short polynomials (what stands in hidden
                     // places, keys that were never copied, stays there)
                     if (p.cap > 0.f) {
                         const float c2 = p.cap_log2, k1 = p.cap_scale * kscale;
 #pragma unroll
                         for (int e = 0; e < NC; ++e)
-                            sv[e] = __float_as_uint(capped(__uint_as_float(sv[e]) * k1, c2));
+                            sv[e] = __float_as_uint(capped<kWide>(__uint_as_float(sv[e]) * k1, c2));
                     }
                     const float by = p.cap > 0.f ? 1.0f : s_log2;
                     const uint64_t by2 = f2_pack(by, by);
@@ -1078,14 +1098,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                             e4[(e >> 1) & 3] = min3f(e4[(e >> 1) & 3], __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
                         mx = fminf(fminf(e4[0], e4[1]), fminf(e4[2], e4[3]));
                     }
-                    mx *= Form == kCappedScores ? k_cap() : mul;
+                    mx *= kCapped ? k_cap() : mul;
                 }
                 // The form of the tanh, one for the warp's part of the step: the shortest polynomial where
                 // the largest x / cap of every row lies in [-0.1, 0.3] and the cap is 40 or more: what lies
                 // below -0.3 then weighs e^-7.7 at most, and beyond the polynomial's range, where it falls
                 // faster than the tanh, next to nothing.  Else by the largest |x / cap|.
                 int tanh_form = 0;
-                if constexpr (Form == kCappedScores) {
+                if constexpr (kCapped) {
                     const float k1 = k_cap();
                     if (__any_sync(0xffffffffu, live && !(mx >= -0.1f && mx <= kCapTiny)) || p.cap < 40.f || fabsf(k1) < 1e-8f) {
                         float am = 0.f;
@@ -1105,11 +1125,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!meet()) break;
                 tc_fence_after();
                 mx = fmaxf(mx, row_smem[exch ^ kRows]);
-                if constexpr (Form == kCappedScores) {
+                if constexpr (kCapped) {
                     // the row's maximum capped (a reference: what matters is that both threads take the same)
                     const float c2 = p.cap_log2;
                     if (__any_sync(0xffffffffu, live && !(fabsf(mx) <= kCapTiny))) {
-                        mx = mx == -INFINITY ? mx : capped(mx, c2);
+                        mx = mx == -INFINITY ? mx : capped_far(mx, c2);
                     } else {
                         const float u = mx * mx;
                         mx *= c2 * fmaf(u, fmaf(u, kTiny2, kTiny1), kTiny0);
@@ -1142,7 +1162,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // unrounded ones), written over the columns of S (keys 32 c .. +31 -> columns 16 c
                 // .. +15).  P in two 16-bit parts would double the products of P.V.
                 float sum;
-                if constexpr (Form != kCappedScores) {
+                if constexpr (!kCapped) {
                     uint64_t sum2[2] = {0ull, 0ull};
                     const uint64_t negm2 = f2_pack(-m_at, -m_at), scale2 = f2_pack(mul, mul);
 #pragma unroll
@@ -1196,17 +1216,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                             f2_unpack(f2_fma(v, f2_fma(u, f2_fma(u, c2, c1), c0), negm2), a0, a1);
                         });
                     } else if (tanh_form == 1) {
-                        auto one = [&](float v) {
-                            const float y = v * k1, u = y * y;
-                            return fmaf(y * p.cap_log2, fmaf(u, fmaf(u, fmaf(u, fmaf(u, kTanh4, kTanh3), kTanh2), kTanh1), kTanh0), -m_at);
-                        };
+                        auto one = [&](float v) { return capped_near(v * k1, p.cap_log2, -m_at); };
                         store_p([&](float v0, float v1, float& a0, float& a1) {
                             a0 = one(v0);
                             a1 = one(v1);
                         });
                     } else {
                         auto one = [&](float v) {
-                            const float t = capped(v * k1, p.cap_log2) - m_at;
+                            const float t = capped<kWide>(v * k1, p.cap_log2) - m_at;
                             return v * k1 == -INFINITY ? -INFINITY : t;
                         };
                         store_p([&](float v0, float v1, float& a0, float& a1) {
@@ -1443,6 +1460,8 @@ const void* scored_fn(ScoreForm form) {
         case kPlainScores: return reinterpret_cast<const void*>(&scored_kernel<Kind, QBf16, kPlainScores>);
         case kCappedScores: return reinterpret_cast<const void*>(&scored_kernel<Kind, QBf16, kCappedScores>);
         case kBiasedScores: return reinterpret_cast<const void*>(&scored_kernel<Kind, QBf16, kBiasedScores>);
+        case kWideCappedScores: return reinterpret_cast<const void*>(&scored_kernel<Kind, QBf16, kWideCappedScores>);
+        case kWideBiasedScores: return reinterpret_cast<const void*>(&scored_kernel<Kind, QBf16, kWideBiasedScores>);
     }
     return nullptr;
 }
