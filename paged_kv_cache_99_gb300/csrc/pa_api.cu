@@ -539,6 +539,7 @@ pa_status scored_impl(ScoredParams p, void* out, const void* q, const int32_t* q
     p.cap = cap;
     p.cap_scale = cap > 0.f ? scale / cap : 0.f;
     p.cap_log2 = cap * 1.4426950408889634f;
+    p.cap_flat = cap > 0.f ? std::pow(1e-36f / p.cap_log2, 0.2f) : 0.f;
     p.queries_per_tile = scored_rows() / group;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.records = reinterpret_cast<CombineRecord*>(ws + lay.records_off);

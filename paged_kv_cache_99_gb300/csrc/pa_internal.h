@@ -360,6 +360,7 @@ struct ScoredParams {
     float cap;                        // 0: none
     float cap_scale;                  // scale / cap
     float cap_log2;                   // cap * log2(e)
+    float cap_flat;                   // scores' factor to x / cap below which cap_log2 times its fifth power nears 0
     CombineRecord* records;           // [CTAs]
     float2* ml;                       // [CTAs][2][256]: maximum (log2 units), sum
     float4* partial;                  // [CTAs][2][32 quads][256]: unnormalised outputs

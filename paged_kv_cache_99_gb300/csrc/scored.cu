@@ -1103,11 +1103,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // The form of the tanh, one for the warp's part of the step: the shortest polynomial where
                 // the largest x / cap of every row lies in [-0.1, 0.3] and the cap is 40 or more: what lies
                 // below -0.3 then weighs e^-7.7 at most, and beyond the polynomial's range, where it falls
-                // faster than the tanh, next to nothing.  Else by the largest |x / cap|.
+                // faster than the tanh, next to nothing.  Else by the largest |x / cap|.  Not the shortest where its
+                // highest coefficient would leave float's range: 0 does not hide an infinite score.
                 int tanh_form = 0;
                 if constexpr (kCapped) {
                     const float k1 = k_cap();
-                    if (__any_sync(0xffffffffu, live && !(mx >= -0.1f && mx <= kCapTiny)) || p.cap < 40.f || fabsf(k1) < 1e-8f) {
+                    if (__any_sync(0xffffffffu, live && !(mx >= -0.1f && mx <= kCapTiny)) || p.cap < 40.f || fabsf(k1) < p.cap_flat) {
                         float am = 0.f;
 #pragma unroll
                         for (int e = 0; e < NC; ++e) {
@@ -1116,7 +1117,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         am = live ? fmaxf(am * fabsf(k1), mx) : 0.f;        // mx: an infinite score that is seen
                         tanh_form = __any_sync(0xffffffffu, am > kCapSmall) ? 2
-                                    : __any_sync(0xffffffffu, am > kCapTiny || fabsf(k1) < 1e-8f) ? 1 : 0;
+                                    : __any_sync(0xffffffffu, am > kCapTiny || fabsf(k1) < p.cap_flat) ? 1 : 0;
                     }
                 }
                 // with the row's other thread, which has read its scores too: P may go over them
