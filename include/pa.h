@@ -560,7 +560,7 @@ PA_API pa_status pa_tree(void* out, const void* q, const int32_t* query_start_lo
  *   seq_lens_out[s] = seq_lens[s] - q_len_s + path_lens[s].
  * Rows behind the accepted ones keep what they hold.
  *
- *   seq_lens_out   device, int32 [num_seqs]; not seq_lens itself
+ *   seq_lens_out   device, int32 [num_seqs]; shares no memory with the arrays below
  *   k_caches, v_caches
  *                  host, num_layers pointers each to a cache (layout as pa_decode); all
  *                  distinct.  Read during the call
@@ -667,7 +667,7 @@ PA_API pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int32_t* src
  *   weights_out    the same layout; may be weights itself (up to 393216 tokens of table:
  *                  beyond that PA_ERR_UNSUPPORTED), otherwise must not overlap it
  *   kept           device, int32 [num_seqs][num_kv_heads][budget]
- *   seq_lens_out   device, int32 [num_seqs]; not seq_lens itself
+ *   seq_lens_out   device, int32 [num_seqs]; shares no memory with the arrays below
  *   new_tables     device, int32 [num_seqs][max_new_blocks_per_seq], not block_tables itself, with
  *                  max_new_blocks_per_seq * block_size >= min(budget, max_blocks_per_seq *
  *                  block_size); entries past ceil(left / block_size) are never read.  Its

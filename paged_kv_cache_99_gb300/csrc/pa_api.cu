@@ -138,6 +138,12 @@ pa_status encode_query_map(CUtensorMap* map, const void* base, int rows, int hea
     return PA_OK;
 }
 
+// Whether na int32 from a on and nb from b on share memory.
+bool share(const int32_t* a, long long na, const int32_t* b, long long nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y ? y - x < 4ull * na : x - y < 4ull * nb;
+}
+
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Tokens per physical block: 8, 16 or 32 (the kernels work in 16-key units).
@@ -1204,8 +1210,7 @@ pa_status pa_tree_commit(int32_t* seq_lens_out, void* const* k_caches, void* con
                 return PA_ERR_INVALID_ARG;
     }
     if (num_seqs == 0 || num_layers == 0) return PA_OK;
-    if (!seq_lens_out || !path_lens || !query_start_loc || !block_tables || !seq_lens || seq_lens_out == seq_lens ||
-        (max_path > 0 && !paths))
+    if (!seq_lens_out || !path_lens || !query_start_loc || !block_tables || !seq_lens || (max_path > 0 && !paths))
         return PA_ERR_INVALID_ARG;
     if (!aligned(seq_lens_out, 4) || !aligned(paths, 4) || !aligned(path_lens, 4) || !aligned(query_start_loc, 4) ||
         !aligned(block_tables, 4) || !aligned(seq_lens, 4) || (workspace && !aligned(workspace, 256)))
@@ -1215,6 +1220,12 @@ pa_status pa_tree_commit(int32_t* seq_lens_out, void* const* k_caches, void* con
     if (static_cast<long long>(max_blocks_per_seq) * block_size >= (1ll << 31) ||
         static_cast<long long>(num_seqs) * num_kv_heads * 2 * group >= (1ll << 31))
         return PA_ERR_UNSUPPORTED;
+    // the lengths are read by every warp of a sequence, and again for later layers
+    const long long B = num_seqs;
+    if (share(seq_lens_out, B, seq_lens, B) || share(seq_lens_out, B, path_lens, B) ||
+        share(seq_lens_out, B, query_start_loc, B + 1) || share(seq_lens_out, B, paths, B * max_path) ||
+        share(seq_lens_out, B, block_tables, B * max_blocks_per_seq))
+        return PA_ERR_INVALID_ARG;
     for (int first = 0; first < num_layers; first += kCommitLayers) {
         CommitParams p = {};
         p.num_layers = num_layers - first < kCommitLayers ? num_layers - first : kCommitLayers;
