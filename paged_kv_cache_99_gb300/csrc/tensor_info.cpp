@@ -9,7 +9,7 @@
 extern "C" int pa_tensor_info(PyObject* o, TensorInfo* out) noexcept {
     try {
         if (!THPVariable_CheckExact(o)) return -1;
-        const c10::TensorImpl* t = THPVariable_Unpack(o).unsafeGetTensorImpl();
+        c10::TensorImpl* t = THPVariable_Unpack(o).unsafeGetTensorImpl();
         if (!t->has_storage() || t->layout() != c10::kStrided) return -1;
         switch (c10::typeMetaToScalarType(t->dtype())) {
             case c10::ScalarType::BFloat16: out->type = 0; break;
@@ -22,7 +22,7 @@ extern "C" int pa_tensor_info(PyObject* o, TensorInfo* out) noexcept {
             default: out->type = -1;
         }
         out->device = t->device().is_cuda() ? t->device().index() : -1;
-        out->ptr = const_cast<void*>(t->data());
+        out->ptr = t->mutable_data();      // as data_ptr(): storage that is shared until it is written becomes the tensor's own
         out->ndim = static_cast<int>(t->dim());
         out->shape = t->sizes().data();
         out->stride = t->strides().data();
