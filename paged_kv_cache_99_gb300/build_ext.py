@@ -100,28 +100,34 @@ def _run(cmd, what: str) -> None:
 
 def _build_binding() -> None:
     """The extension module of the calls in csrc/binding.c, beside libpa.so and linked to it, with
-    csrc/tensor_info.cpp if torch's headers and a C++ compiler are there (else tensors are asked
-    through their Python methods)."""
+    csrc/tensor_info.cpp if torch's headers, its libraries and a C++ compiler are there (else tensors
+    are asked through their Python methods)."""
     tmp = BINDING_PATH + f".{os.getpid()}.tmp"
+    obj, info = (os.path.join(BUILD_DIR, f"{name}.{os.getpid()}.o") for name in ("binding", "tensor_info"))
     cc = shutil.which("gcc") or shutil.which("cc") or "cc"
     flags = ["-O2", "-fPIC", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"]]
-    objs, libs = [os.path.join(BUILD_DIR, f"binding.{os.getpid()}.o")], []
-    _run([cc, *flags, "-c", os.path.join(CSRC, BINDING), "-o", objs[0]], BINDING)
+    link = [cc, "-shared", obj, "-o", tmp, "-L", BUILD_DIR, "-l:libpa.so", "-Wl,-rpath,$ORIGIN"]
     try:
-        torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
-        info = os.path.join(BUILD_DIR, f"tensor_info.{os.getpid()}.o")
-        _run([shutil.which("g++") or shutil.which("c++") or "c++", *flags, "-std=c++17",
-              "-I", os.path.join(torch_dir, "include"),
-              "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
-              "-c", os.path.join(CSRC, TENSOR_INFO), "-o", info], TENSOR_INFO)
-        objs.append(info)
-        libs = ["-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lstdc++"]
-    except (OSError, RuntimeError) as e:
-        warnings.warn(f"{TENSOR_INFO} was not built, calls take longer: {e}", RuntimeWarning, stacklevel=2)
-    _run([cc, "-shared", *objs, "-o", tmp, "-L", BUILD_DIR, "-l:libpa.so", "-Wl,-rpath,$ORIGIN", *libs], BINDING)
-    for obj in objs:
-        os.remove(obj)
-    os.replace(tmp, BINDING_PATH)
+        _run([cc, *flags, "-c", os.path.join(CSRC, BINDING), "-o", obj], BINDING)
+        try:
+            spec = importlib.util.find_spec("torch")
+            if spec is None or spec.origin is None:
+                raise RuntimeError("torch is not installed")
+            torch_dir = os.path.dirname(spec.origin)
+            _run([shutil.which("g++") or shutil.which("c++") or "c++", *flags, "-std=c++17",
+                  "-I", os.path.join(torch_dir, "include"),
+                  "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+                  "-c", os.path.join(CSRC, TENSOR_INFO), "-o", info], TENSOR_INFO)
+            _run([*link, info, "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10",
+                  "-lstdc++"], TENSOR_INFO)
+        except (OSError, RuntimeError) as e:
+            warnings.warn(f"{TENSOR_INFO} was not built, calls take longer: {e}", RuntimeWarning, stacklevel=2)
+            _run(link, BINDING)
+        os.replace(tmp, BINDING_PATH)
+    finally:
+        for path in (obj, info, tmp):
+            if os.path.exists(path):
+                os.remove(path)
 
 
 if __name__ == "__main__":
