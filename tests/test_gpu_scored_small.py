@@ -1,10 +1,9 @@
 """What is small in the attention with scores that are not plain: scales and caps near the ends
 of their ranges, and weights far below a row's largest."""
 import pytest
-import torch
 
-from tests._scored import Batch, causal, reference
-from tests.test_gpu_scored import call, one
+from tests._scored import Batch
+from tests.test_gpu_scored import one
 
 pytestmark = pytest.mark.gpu
 
