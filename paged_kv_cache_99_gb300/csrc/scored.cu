@@ -57,6 +57,10 @@ constexpr int kCols = kKeys / 2;             // a softmax thread's keys of a ste
 // registers per thread at launch, and the shares of warps 0-3 and the softmax after setmaxnreg
 constexpr int kRegsLaunch = 96, kRegsFront = 64, kRegsSoftmax = 104;
 constexpr float kRescale = 8.0f;             // lazy rescale threshold (factor 256)
+// fp16 weights stand this far above the row's reference, in log2 units: the largest is then 2^14 at most,
+// and what falls below fp16's range is 2^-31 of the row's largest rather than 2^-25, which would add up
+// over a long context whose largest weight is a sink's
+constexpr float kLift = 6.0f;
 
 template <int Kind>
 struct Cfg {
@@ -1142,6 +1146,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // a row that has seen nothing yet: exponents against 0, all of hidden scores
                 const float m_at = m_new == -INFINITY ? 0.f : m_new;
                 const float alpha = ex2_approx(m_used - m_at);    // 0 before the row's first key, 1 when kept
+                const float neg_m = (kMmaBf16 ? 0.f : kLift) - m_at;
                 m_used = m_new;
                 // O is final for the products before: S(i) was issued behind them.  Rescaled
                 // before any of P(i) is released, since P.V(i) accumulates into it.
@@ -1159,13 +1164,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();          // (and nothing below is begun above: it would spill)
                 // p = 2^(s * scale - m), rounded to the 16 bits that the tensor cores take beside V's
-                // (bf16 2^-8 of it at most, fp16, FP8 caches' type too, 2^-11; their sum is of the
-                // unrounded ones), written over the columns of S (keys 32 c .. +31 -> columns 16 c
+                // (bf16 2^-8 of it at most, fp16, FP8 caches' type too, 2^-11, times 2^kLift; their sum is of
+                // the unrounded ones), written over the columns of S (keys 32 c .. +31 -> columns 16 c
                 // .. +15).  P in two 16-bit parts would double the products of P.V.
                 float sum;
                 if constexpr (!kCapped) {
                     uint64_t sum2[2] = {0ull, 0ull};
-                    const uint64_t negm2 = f2_pack(-m_at, -m_at), scale2 = f2_pack(mul, mul);
+                    const uint64_t negm2 = f2_pack(neg_m, neg_m), scale2 = f2_pack(mul, mul);
 #pragma unroll
                     for (int c = 0; c < NC / 16; ++c) {
                         uint32_t pw[8];
@@ -1211,20 +1216,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float k1 = k_cap();
                     if (tanh_form == 0) {
                         const float d0 = kTiny0 * s_log2, d1 = kTiny1 * s_log2 * (k1 * k1), d2 = kTiny2 * s_log2 * (k1 * k1) * (k1 * k1);
-                        const uint64_t c0 = f2_pack(d0, d0), c1 = f2_pack(d1, d1), c2 = f2_pack(d2, d2), negm2 = f2_pack(-m_at, -m_at);
+                        const uint64_t c0 = f2_pack(d0, d0), c1 = f2_pack(d1, d1), c2 = f2_pack(d2, d2), negm2 = f2_pack(neg_m, neg_m);
                         store_p([&](float v0, float v1, float& a0, float& a1) {
                             const uint64_t v = f2_pack(v0, v1), u = f2_mul(v, v);
                             f2_unpack(f2_fma(v, f2_fma(u, f2_fma(u, c2, c1), c0), negm2), a0, a1);
                         });
                     } else if (tanh_form == 1) {
-                        auto one = [&](float v) { return capped_near(v * k1, p.cap_log2, -m_at); };
+                        auto one = [&](float v) { return capped_near(v * k1, p.cap_log2, neg_m); };
                         store_p([&](float v0, float v1, float& a0, float& a1) {
                             a0 = one(v0);
                             a1 = one(v1);
                         });
                     } else {
                         auto one = [&](float v) {
-                            const float t = capped<kWide>(v * k1, p.cap_log2) - m_at;
+                            const float t = capped<kWide>(v * k1, p.cap_log2) + neg_m;
                             return v * k1 == -INFINITY ? -INFINITY : t;
                         };
                         store_p([&](float v0, float v1, float& a0, float& a1) {
