@@ -232,7 +232,8 @@ PA_API pa_status pa_rope_and_cache(void* q_out, long long q_out_stride, const vo
  *   q_weight, k_weight  device, [128] of src_dtype, 16-byte aligned; NULL: those heads are
  *                  not normed
  *   eps            >= 0 and finite (the sum of squares is float32: with eps == 0 a head whose
- *                  squares vanish there becomes NaN)
+ *                  squares vanish there becomes NaN, and one whose squares pass its range,
+ *                  components of 1e18 and more, zeros)
  *   weight_offset  added to the weights (1 for checkpoints that store weight - 1)
  *   positions      device, int64 [num_axes][num_tokens]; a token any of whose positions is
  *                  negative is padding (nothing of it is written); one with a position >=
@@ -515,7 +516,8 @@ PA_API size_t pa_workspace_size_scored(int num_seqs, int num_q_heads, int num_kv
  * the table) is recorded as PA_ERR_OUT_OF_RANGE and its rows are left as they were.  What a
  * token that no row of its sequence sees holds does not matter (it may be NaN); one that some
  * of its rows see must be finite for the others.  Other arguments, and the precision, as
- * pa_mixed; at most 128 query heads per KV head.
+ * pa_mixed (over fp16 and FP8 caches a key that weighs less than 2^-31 of its row's largest
+ * adds nothing beside V); at most 128 query heads per KV head.
  */
 PA_API pa_status pa_mixed_scored(void* out, const void* q, const int32_t* query_start_loc, const void* k_cache,
                                  const void* v_cache, const int32_t* block_tables, int max_blocks_per_seq,
@@ -561,6 +563,7 @@ PA_API pa_status pa_tree(void* out, const void* q, const int32_t* query_start_lo
  * Rows behind the accepted ones keep what they hold.
  *
  *   seq_lens_out   device, int32 [num_seqs]; shares no memory with the arrays below
+ *   num_layers     0: nothing is done (the lengths are not written either)
  *   k_caches, v_caches
  *                  host, num_layers pointers each to a cache (layout as pa_decode); all
  *                  distinct.  Read during the call
