@@ -17,7 +17,7 @@ def path(monkeypatch):
     path = os.path.join(build_ext.BUILD_DIR, f"_binding-fallback-{os.getpid()}.so")
     monkeypatch.setattr(build_ext, "BINDING_PATH", path)
     yield path
-    left = glob.glob(os.path.join(build_ext.BUILD_DIR, f"*{os.getpid()}*"))
+    left = glob.glob(path + "*") + glob.glob(os.path.join(build_ext.BUILD_DIR, f"*.{os.getpid()}.o"))
     for f in left:
         os.remove(f)
     assert set(left) <= {path}
